@@ -583,6 +583,130 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
                             void *gather_dev, int32_t gather_dtype, int64_t offset,
                             const zero_hparams *hp, zero_ctrl *ctrl_dev, void *stream);
 
+/* ---- Matrices: orthogonalised updates ---------------------------------------
+ * For parameters that are whole matrices inside a shard.  A stack is `count`
+ * row-major matrices of rows x cols elements.
+ *
+ * The orthogonalisation of G is k steps of an odd quintic iteration on the
+ * normalised matrix, on whichever side is smaller:
+ *     X <- G / (||G||_F + eps)
+ *     X <- (a I + b S + c S^2) X,  S = X X^T      (rows <= cols)
+ *     X <- X (a I + b S + c S^2),  S = X^T X      (rows >  cols)
+ * which drives every singular value of X towards 1 and keeps the singular
+ * vectors.  A zero matrix gives zeros; a matrix holding inf or NaN gives NaN.
+ * Between steps X is fp32; the products take fp16 operands (power-of-two
+ * scaled, fp32 sums) whose diagonals are kept apart in fp32.  The result is
+ * within about 1e-3 (relative, Frobenius norm; 1e-5 where the smaller side is at
+ * most 128) of the iteration in 64 bits,
+ * so it is returned in 16 bits.  The scales are chosen for coefficients that
+ * keep the singular values below about 1.3, as the usual ones do. */
+#define ZERO_F32 3 /* a dtype of the matrix calls below, where they say so */
+
+typedef struct zero_newton_schulz {
+    float a, b, c; /* the polynomial's coefficients, finite */
+    float eps;     /* added to the Frobenius norm, >= 0 */
+    int32_t steps; /* k, 0..64 */
+} zero_newton_schulz;
+
+/* Bytes of device workspace for zero_orthogonalize and zero_muon_step over
+ * such a stack (16-byte aligned; 0 where one workgroup holds a whole matrix:
+ * up to 32 x 1024, 64 x 512 or 128 x 256).  0 for sizes the calls refuse. */
+size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
+
+/* dst[b] = orthogonalisation of src[b].  src: src_dtype ZERO_F16, ZERO_BF16
+ * or ZERO_F32; row r of matrix b starts at element b * src_stride + r * src_ld.
+ * dst: dst_dtype ZERO_F16 or ZERO_BF16, laid out likewise; it may be src when
+ * type and layout agree.  count, rows or cols of 0: nothing is enqueued.
+ * Errors: EINVAL (null pointer, dtype, coefficients, steps, eps), EALIGN (a
+ * pointer not aligned to its elements, workspace not to 16 bytes), ERANGE
+ * (rows or cols above 65536, negative sizes, count above 65535, ld below
+ * cols, stride below the matrix), ESPACE (workspace too small). */
+int zero_orthogonalize(const void *src_dev, int32_t src_dtype, int32_t count, int64_t rows,
+                       int64_t cols, int64_t src_ld, int64_t src_stride, void *dst_dev,
+                       int32_t dst_dtype, int64_t dst_ld, int64_t dst_stride,
+                       const zero_newton_schulz *ns, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* How the orthogonalised update is scaled before it meets lr. */
+enum {
+    ZERO_MUON_SCALE_SHAPE = 0, /* sqrt(max(1, rows / cols)) */
+    ZERO_MUON_SCALE_RMS = 1    /* 0.2 sqrt(max(rows, cols)): the root mean square of an AdamW update */
+};
+
+typedef struct zero_muon_hparams {
+    float lr, momentum, weight_decay;
+    int32_t nesterov; /* 0 or 1 */
+    int32_t scale;    /* ZERO_MUON_SCALE_* */
+    zero_newton_schulz ns;
+} zero_muon_hparams;
+
+/* One optimizer step for a stack of matrices of a shard, in place, beside
+ * zero_adam_step for the shard's other parameters (two-pass path: g comes from
+ * zero_reduce_grads, the decisions from zero_grad_norm_overflow):
+ *     g' = clip g;  mom = mu mom + (1 - mu) g'
+ *     u = nesterov ? (1 - mu) g' + mu mom : mom
+ *     p = (p - lr wd p) - lr s NS(u);  slot = RNE16(p)
+ * momentum, the decay and the final update round each operation to fp32 in
+ * that order.  master_dev, mom_dev, g_dev: fp32; matrix b is the rows * cols
+ * elements from b * stride.  ctrl_dev may be NULL (no clipping, no skip); on a
+ * skipped step nothing is written.  gather_dev may be NULL (no slot), else
+ * element i of master goes to gather[offset + i].  Errors: as
+ * zero_orthogonalize's, and EINVAL for lr, momentum (0 <= mu < 1),
+ * weight_decay or scale out of range. */
+int zero_muon_step(float *master_dev, float *mom_dev, const float *g_dev, int32_t count,
+                   int64_t rows, int64_t cols, int64_t stride, const zero_muon_hparams *hp,
+                   const zero_ctrl *ctrl_dev, void *gather_dev, int32_t gather_dtype,
+                   int64_t offset, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* ---- Matrices: MXFP4 (OCP microscaling) operands -----------------------------
+ * A matrix quantised along its rows: every 32 consecutive elements of a row
+ * share a scale 2^(s - 127) (one byte s, E8M0) and hold 4-bit codes (E2M1:
+ * 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives; sign in bit 3).  For a
+ * block whose largest magnitude is x, s - 127 = floor(log2 x) - 2 (not below
+ * -127; x = 0: -127), each element is rounded to the nearest code, ties to
+ * the even code, and saturates at 6.  A block holding inf or NaN has s = 255
+ * (NaN) and codes 0.  Columns are padded with zeros to P = a multiple of 128.
+ * codes: [rows][P / 2] bytes, the even element in the low four bits;
+ * scales: [rows][P / 32] bytes; both 16-byte aligned. */
+int64_t zero_mx4_padded(int64_t cols);
+size_t zero_mx4_code_bytes(int64_t rows, int64_t cols);
+size_t zero_mx4_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantises src (rows x cols, row stride ld elements; ZERO_F16, ZERO_BF16 or
+ * ZERO_F32) along its rows into codes/scales and, from the same read, along its
+ * columns into codes_t/scales_t: the quantisation of the transposed matrix
+ * (cols x rows).  Either pair may be NULL, not both.  Errors: EINVAL, EALIGN
+ * (src to its elements, outputs to 16 bytes), ERANGE (negative sizes, rows or
+ * cols above 2^24, ld below cols). */
+int zero_mx4_quantize(const void *src_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                      void *codes_dev, void *scales_dev, void *codes_t_dev, void *scales_t_dev,
+                      void *stream);
+
+/* The values: dst (rows x cols, row stride ld; ZERO_F16, ZERO_BF16 or
+ * ZERO_F32, rounded to nearest even from the exact product). */
+int zero_mx4_dequantize(const void *codes_dev, const void *scales_dev, int64_t rows, int64_t cols,
+                        void *dst_dev, int32_t dtype, int64_t ld, void *stream);
+
+/* c[i][j] = sum over k of A[i][k] B[j][k] (+ c[i][j] when accumulate is 1 and
+ * c is ZERO_F32), A m x k and B n x k quantised along k, sums in fp32; c is
+ * m x n, row stride ldc, ZERO_F16, ZERO_BF16 or ZERO_F32.  k = 0 gives zeros
+ * (or c unchanged).  ws: zero_mx4_matmul_workspace_bytes, 16-byte aligned. */
+size_t zero_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int zero_mx4_matmul(const void *a_codes_dev, const void *a_scales_dev, const void *b_codes_dev,
+                    const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,
+                    int32_t c_dtype, int64_t ldc, int32_t accumulate, void *ws_dev,
+                    size_t ws_bytes, void *stream);
+
+/* zero_mx4_matmul with A given as values (ZERO_F16, ZERO_BF16 or ZERO_F32, row
+ * stride lda) and quantised on the way in, for the few rows of single tokens:
+ * equal to zero_mx4_quantize and zero_mx4_matmul.  m is at most
+ * ZERO_MX4_ROWS_MAX. */
+#define ZERO_MX4_ROWS_MAX 64
+size_t zero_mx4_matmul_rows_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int zero_mx4_matmul_rows(const void *a_dev, int32_t a_dtype, int64_t lda, const void *b_codes_dev,
+                         const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,
+                         int32_t c_dtype, int64_t ldc, void *ws_dev, size_t ws_bytes,
+                         void *stream);
+
 /* Message for the last nonzero return on the calling thread ("" if none). */
 const char *zero_last_error(void);
 

@@ -1,0 +1,136 @@
+"""The matrix calls' sizes and refusals, on the host: every argument error is
+returned before anything is enqueued, so no GPU is needed."""
+import ctypes
+
+import pytest
+
+EINVAL, EALIGN, ERANGE, ESPACE = -1, -2, -3, -4
+F16, BF16, F32 = 1, 2, 3
+P = 0x10000  # an aligned address that no refused call touches
+
+
+@pytest.fixture(scope="module")
+def Z():
+    import zero_partitioned_mixed_amd as Z
+    return Z
+
+
+def ns(Z, **kw):
+    return ctypes.byref(Z.newton_schulz(**kw))
+
+
+def test_struct_sizes(Z):
+    assert ctypes.sizeof(Z.NewtonSchulz) == 20 and ctypes.sizeof(Z.MuonHparams) == 40
+
+
+def test_sizes(Z):
+    assert [Z._lib.zero_mx4_padded(c) for c in (-1, 0, 1, 128, 129)] == [0, 0, 128, 128, 256]
+    assert Z._lib.zero_mx4_code_bytes(3, 129) == 3 * 128 and Z._lib.zero_mx4_scale_bytes(3, 129) == 3 * 8
+    assert Z._lib.zero_mx4_code_bytes(0, 5) == 0 == Z._lib.zero_mx4_scale_bytes(5, 0)
+    ws = Z._lib.zero_ns_workspace_bytes
+    assert ws(5, 128, 128) == 0 and ws(0, 500, 500) == 0 and ws(1, 0, 9) == 0 and ws(1, 70000, 9) == 0
+    one = ws(1, 129, 400)
+    assert one > 129 * 400 * 4 and ws(7, 129, 400) == 7 * one and ws(1, 400, 129) == one
+    assert ws(1, 65536, 65536) > 0
+
+
+def ortho(Z, src=P, sdt=F32, count=1, rows=200, cols=300, sld=300, sst=60000, dst=P, ddt=BF16, dld=300, dst_st=60000,
+          s=None, ws=P, ws_bytes=1 << 40):
+    return Z._lib.zero_orthogonalize(src, sdt, count, rows, cols, sld, sst, dst, ddt, dld, dst_st,
+                                     s if s is not None else ns(Z), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(sdt=0), EINVAL), (dict(sdt=4), EINVAL), (dict(ddt=F32), EINVAL), (dict(src=None), EINVAL), (dict(dst=None), EINVAL),
+    (dict(src=P + 2), EALIGN), (dict(dst=P + 1), EALIGN), (dict(sdt=F16, src=P + 1), EALIGN), (dict(count=-1), ERANGE),
+    (dict(count=65536), ERANGE), (dict(rows=-1), ERANGE), (dict(cols=65537, sld=70000, dld=70000), ERANGE),
+    (dict(sld=299), ERANGE), (dict(dld=299), ERANGE), (dict(count=2, sst=59999), ERANGE), (dict(count=2, dst_st=100), ERANGE),
+    (dict(ws=None), EINVAL), (dict(ws=P + 8), EALIGN), (dict(ws_bytes=1000), ESPACE)])
+def test_orthogonalize_refuses(Z, kw, code):
+    assert ortho(Z, **kw) == code
+    assert "zero_orthogonalize" in Z.zero_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(steps=-1), dict(steps=65), dict(eps=-1.0), dict(eps=float("nan")),
+                                dict(coeffs=(float("inf"), 0, 0)), dict(coeffs=(1, float("nan"), 0))])
+def test_settings_refused(Z, kw):
+    assert ortho(Z, s=ns(Z, **kw)) == EINVAL
+
+
+def test_nothing_to_do(Z):
+    for kw in (dict(count=0), dict(rows=0), dict(cols=0, sld=0, dld=0)):
+        assert ortho(Z, src=None, dst=None, ws=None, **kw) == 0
+    assert Z.zero_last_error() == ""
+
+
+def muon(Z, master=P, mom=P, g=P, count=1, rows=200, cols=300, stride=60000, ctrl=None, gather=P, gdt=F16, offset=0, ws=P,
+         ws_bytes=1 << 40, **hp):
+    h = Z.muon_hparams(**hp)
+    return Z._lib.zero_muon_step(master, mom, g, count, rows, cols, stride, ctypes.byref(h), ctrl, gather, gdt, offset, ws,
+                                 ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(momentum=1.0), EINVAL), (dict(momentum=-0.1), EINVAL), (dict(momentum=float("nan")), EINVAL),
+    (dict(lr=float("inf")), EINVAL), (dict(weight_decay=float("nan")), EINVAL), (dict(scale=2), EINVAL), (dict(steps=100), EINVAL),
+    (dict(gdt=F32), EINVAL), (dict(master=None), EINVAL), (dict(mom=None), EINVAL), (dict(g=None), EINVAL),
+    (dict(master=P + 2), EALIGN), (dict(gather=P + 1), EALIGN), (dict(ctrl=P + 4), EALIGN), (dict(offset=-1), ERANGE),
+    (dict(count=2, stride=59999), ERANGE), (dict(rows=70000), ERANGE), (dict(ws_bytes=16), ESPACE)])
+def test_muon_refuses(Z, kw, code):
+    assert muon(Z, **kw) == code
+    assert "zero_muon_step" in Z.zero_last_error()
+
+
+def quant(Z, src=P, dt=BF16, rows=4, cols=64, ld=64, c=P, s=P, ct=P, st=P):
+    return Z._lib.zero_mx4_quantize(src, dt, rows, cols, ld, c, s, ct, st, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=7), EINVAL), (dict(c=None), EINVAL), (dict(st=None), EINVAL), (dict(c=None, s=None, ct=None, st=None), EINVAL),
+    (dict(src=None), EINVAL), (dict(src=P + 1), EALIGN), (dict(c=P + 8), EALIGN), (dict(st=P + 4), EALIGN), (dict(rows=-1), ERANGE),
+    (dict(cols=(1 << 24) + 1, ld=1 << 25), ERANGE), (dict(ld=63), ERANGE)])
+def test_quantize_refuses(Z, kw, code):
+    assert quant(Z, **kw) == code
+    assert "zero_mx4_quantize" in Z.zero_last_error()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=0), EINVAL), (dict(c=None), EINVAL), (dict(d=None), EINVAL), (dict(c=P + 1), EALIGN), (dict(d=P + 1), EALIGN),
+    (dict(rows=-2), ERANGE), (dict(ld=10), ERANGE)])
+def test_dequantize_refuses(Z, kw, code):
+    a = dict(c=P, s=P, rows=4, cols=64, d=P, dt=F16, ld=64)
+    a.update(kw)
+    assert Z._lib.zero_mx4_dequantize(a["c"], a["s"], a["rows"], a["cols"], a["d"], a["dt"], a["ld"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(cdt=9), EINVAL), (dict(acc=2, cdt=F32), EINVAL), (dict(acc=1, cdt=F16), EINVAL), (dict(a=None), EINVAL),
+    (dict(sb=None), EINVAL), (dict(c=None), EINVAL), (dict(a=P + 8), EALIGN), (dict(b=P + 1), EALIGN), (dict(c=P + 1), EALIGN),
+    (dict(ldc=7), ERANGE), (dict(m=-1), ERANGE), (dict(k=1 << 25), ERANGE)])
+def test_matmul_refuses(Z, kw, code):
+    a = dict(a=P, sa=P, b=P, sb=P, m=8, n=8, k=64, c=P, cdt=BF16, ldc=8, acc=0)
+    a.update(kw)
+    assert Z._lib.zero_mx4_matmul(a["a"], a["sa"], a["b"], a["sb"], a["m"], a["n"], a["k"], a["c"], a["cdt"], a["ldc"],
+                                  a["acc"], P, 1 << 40, None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(adt=0), EINVAL), (dict(a=None), EINVAL), (dict(b=None), EINVAL), (dict(ws=None), EINVAL), (dict(a=P + 1), EALIGN),
+    (dict(ws=P + 4), EALIGN), (dict(m=65), ERANGE), (dict(lda=63), ERANGE), (dict(wsb=1), ESPACE)])
+def test_matmul_rows_refuses(Z, kw, code):
+    a = dict(a=P, adt=BF16, lda=64, b=P, sb=P, m=8, n=8, k=64, c=P, cdt=BF16, ldc=8, ws=P, wsb=1 << 40)
+    a.update(kw)
+    assert Z._lib.zero_mx4_matmul_rows(a["a"], a["adt"], a["lda"], a["b"], a["sb"], a["m"], a["n"], a["k"], a["c"], a["cdt"],
+                                       a["ldc"], a["ws"], a["wsb"], None) == code
+
+
+def test_cpu_tensors_refused(Z):
+    import torch
+    x = torch.zeros(4, 64)
+    for call in (lambda: Z.orthogonalize(x, torch.float16), lambda: Z.mx4_quantize(x),
+                 lambda: Z.muon_step(x, x, x, Z.muon_hparams()), lambda: Z.mx4_linear(x, x),
+                 lambda: Z.mx4_matmul(x, Z.MX4.alloc(4, 64, "cpu"))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(ValueError):
+        Z.MX4(torch.zeros(4, 31, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 4, 64)

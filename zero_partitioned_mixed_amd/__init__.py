@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(HERE, "libzero_shard.so")
 
 F16 = 1
 BF16 = 2
+F32 = 3  # ZERO_F32: the matrix calls only
 SCALER_NONE, SCALER_STATIC, SCALER_DYNAMIC = 0, 1, 2
 MAX_RANKS = 64
 
@@ -68,6 +69,8 @@ LAUNCH_MIN_TILES = 2048  # ZERO_LAUNCH_MIN_TILES
 LAUNCH_PAYLOAD_TILES = 16384  # ZERO_LAUNCH_PAYLOAD_TILES
 NOALLOC_MAX_LEN = 1 << 31  # ZERO_NOALLOC_MAX_LEN
 BATCH_SHARDS = 32  # ZERO_BATCH_SHARDS
+MUON_SCALE_SHAPE, MUON_SCALE_RMS = 0, 1  # ZERO_MUON_SCALE_*
+MX4_ROWS_MAX = 64  # ZERO_MX4_ROWS_MAX
 
 
 def launch_tiles(nranks: int = 0, payload: bool = False) -> int:
@@ -94,6 +97,17 @@ class Shard(ctypes.Structure):
     _fields_ = [("contrib", _vp), ("stride", _i64), ("pair", _vp), ("valid_len", _i64),
                 ("offset", _i64), ("ctrl", _vp), ("ws", _vp), ("ws_bytes", ctypes.c_size_t),
                 ("state", State), ("g", _vp)]
+
+
+class NewtonSchulz(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float), ("steps", _i32)]
+
+
+class MuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("nesterov", _i32), ("scale", _i32),
+                ("ns", NewtonSchulz)]
 
 
 _sig = {
@@ -161,6 +175,24 @@ _sig = {
     "zero_adam_step_shards": (ctypes.c_int, [ctypes.POINTER(Shard), _i32, ctypes.POINTER(Hparams),
                                              _vp, _i32, _vp]),
     "zero_launch_tiles": (ctypes.c_int64, [_i32]),
+    "zero_ns_workspace_bytes": (ctypes.c_size_t, [_i32, _i64, _i64]),
+    "zero_orthogonalize": (ctypes.c_int, [_vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _i64,
+                                          _i64, ctypes.POINTER(NewtonSchulz), _vp,
+                                          ctypes.c_size_t, _vp]),
+    "zero_muon_step": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                                      ctypes.POINTER(MuonHparams), _vp, _vp, _i32, _i64, _vp,
+                                      ctypes.c_size_t, _vp]),
+    "zero_mx4_padded": (_i64, [_i64]),
+    "zero_mx4_code_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_mx4_scale_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_mx4_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "zero_mx4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "zero_mx4_matmul_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "zero_mx4_matmul": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _i64, _i32,
+                                       _vp, ctypes.c_size_t, _vp]),
+    "zero_mx4_matmul_rows_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "zero_mx4_matmul_rows": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i32,
+                                            _i64, _vp, ctypes.c_size_t, _vp]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 for _name, (_res, _args) in _sig.items():
@@ -804,3 +836,7 @@ class MultiShardStep:
                 self.step(contribs, gather, qgathers, pool)
         torch.cuda.current_stream().wait_stream(side)
         return graph
+
+
+from .matrices import (MX4, muon_hparams, muon_step, mx4_dequantize, mx4_linear,  # noqa: E402,F401
+                       mx4_matmul, mx4_quantize, newton_schulz, orthogonalize)

@@ -15,10 +15,11 @@ import os
 import re
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "zero_shard.hip")
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("zero_shard.hip", "newton_schulz.hip", "mx4.hip")]
 LIB = os.path.join(HERE, "libzero_shard.so")
 ISA_JSON = os.path.join(HERE, "libzero_shard.isa.json")
 INCLUDE = os.path.join(ROOT, "include")
@@ -27,7 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 # -packed-fp32-ops: no packed fp32 instructions in any generated code.
 CODEGEN_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
                  "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-HIPCC_FLAGS = CODEGEN_FLAGS + ["-fPIC", "-shared", "-Wall", "-Wextra", "-I", INCLUDE]
+HOST_FLAGS = ["-fPIC", "-Wall", "-Wextra", "-I", INCLUDE]
 
 
 def kernel_name(demangled: str) -> str:
@@ -64,16 +65,30 @@ def _run(cmd):
     return r
 
 
-def build() -> str:
-    tmp = LIB + ".tmp"
-    _run(["hipcc", *HIPCC_FLAGS, "-o", tmp, SRC])
-    asm = ISA_JSON + ".s.tmp"
+def _compile(src: str, obj: str, asm: str):
+    """One source: its object, and the digests of its kernels' machine code."""
     try:
-        _run(["hipcc", *CODEGEN_FLAGS, "-I", INCLUDE, "--cuda-device-only", "-S", "-o", asm, SRC])
-        digests = isa_digests(open(asm).read())
+        _run(["hipcc", *CODEGEN_FLAGS, *HOST_FLAGS, "-c", "-o", obj, src])
+        _run(["hipcc", *CODEGEN_FLAGS, "-I", INCLUDE, "--cuda-device-only", "-S", "-o", asm, src])
+        return isa_digests(open(asm).read())
     finally:
         if os.path.exists(asm):
             os.remove(asm)
+
+
+def build() -> str:
+    tmp = LIB + ".tmp"
+    stems = [os.path.join(HERE, os.path.basename(s)[:-len(".hip")]) for s in SRCS]
+    objs = [s + ".o" for s in stems]
+    try:
+        with ThreadPoolExecutor(len(SRCS)) as pool:
+            parts = list(pool.map(_compile, SRCS, objs, [s + ".s.tmp" for s in stems]))
+        _run(["hipcc", "--offload-arch=gfx950", "-shared", "-o", tmp, *objs])
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
+    digests = {k: v for part in parts for k, v in part.items()}
     names = subprocess.run(["c++filt"], input="\n".join(digests), stdout=subprocess.PIPE,
                            text=True, check=True).stdout.splitlines()
     table = {kernel_name(d): h for d, h in zip(names, digests.values())}

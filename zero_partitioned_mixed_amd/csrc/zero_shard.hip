@@ -43,7 +43,13 @@
 #include <cstdio>
 #include <mutex>
 
+#include "zero_internal.h"
 #include "zero_shard.h"
+
+char* zero_error_text() {
+    static thread_local char text[kErrorText];
+    return text;
+}
 
 namespace {
 
@@ -1469,18 +1475,16 @@ __global__ void __launch_bounds__(kBlock) dequantize_kernel(DequantArgs a) {
 }
 
 // ---------------------------------------------------------------- host side
-thread_local char g_err[512];
-
 int fail(int code, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    vsnprintf(zero_error_text(), kErrorText, fmt, ap);
     va_end(ap);
     return code;
 }
 
 int ok() {
-    g_err[0] = '\0';
+    zero_error_text()[0] = '\0';
     return ZERO_OK;
 }
 
@@ -2582,6 +2586,6 @@ int zero_fused_step_noalloc(const void* contrib, int32_t contrib_dtype, int32_t 
     return zero_fused_restore(pair, valid_len, gather, gather_dtype, offset, ctrl, stream);
 }
 
-const char* zero_last_error(void) { return g_err; }
+const char* zero_last_error(void) { return zero_error_text(); }
 
 }  // extern "C"
