@@ -4,15 +4,20 @@
 // The product.  A workgroup computes a TILE x TILE tile of A B^T, both
 // operands stored row-major along k, from "slabs" of 128 bytes of every row
 // (64 fp16 or 256 4-bit elements).  A slab of both operands is copied to LDS by
-// direct global-to-LDS loads of 16 bytes per lane, double-buffered, while the
-// previous one feeds the matrix cores: one barrier per slab.  A fragment of
+// direct global-to-LDS loads of 16 bytes per lane, one to three slabs ahead of the
+// one that feeds the matrix cores: one barrier per slab.  Within a slab a k step's
+// fragments are read while the one before multiplies, and a quarter of the next
+// loads goes out with each k step: issued together they hold up their wave for as
+// long as the memory pipeline takes them (4096^3, fp16: 900 TFLOP/s with neither,
+// 1050 with both; the library's product 1220 at 8192^3).  A fragment of
 // the 32x32 matrix instructions is 16 bytes per lane, so fp16 (k = 16) and
 // 4-bit (k = 64) operands move alike and share this code; which 16-byte
 // pieces of a slab meet in one instruction does not matter as long as both
 // operands agree, and lane group h takes pieces 4h..4h+3 (for the 4-bit
 // operands its four block scales are then one dword).  Direct loads write LDS
 // in lane order, so the bank swizzle is put into the addresses they read:
-// piece q of row r sits in slot q ^ (r mod 8).
+// piece q of row r sits in slot q ^ (r / 2 mod 8) (16 lanes then read all 64 banks;
+// q ^ (r mod 8) measured 1-3% slower).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -72,16 +77,18 @@ __device__ __forceinline__ typename Elem<DT>::type from_float(float x) {
 // ---------------------------------------------------------------- the product
 constexpr int kSlab = 128;  // bytes of every row per slab
 
-// A tile of TILE x TILE outputs by waves of WM x WN outputs each.
-template <int TILE_, int WM_, int WN_>
+// A tile of TILE x TILE outputs by waves of WM x WN outputs each, with STAGES slabs
+// in LDS: STAGES - 1 on their way while one is used.
+template <int TILE_, int WM_, int WN_, int STAGES_>
 struct Shape {
-    static constexpr int TILE = TILE_, WM = WM_, WN = WN_;
+    static constexpr int TILE = TILE_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr int WAVES = (TILE / WM) * (TILE / WN);
     static constexpr int THREADS = WAVES * 64;
     static constexpr int MT = WM / 32, NT = WN / 32;
-    static constexpr int LOADS = 2 * TILE / 8 / WAVES;  // direct loads (8 rows each) per wave and slab
-    static constexpr int BUFFER = 2 * TILE * kSlab;     // bytes of one slab of both operands
-    static constexpr int LDS = 2 * BUFFER;
+    static constexpr int LOADS = 2 * TILE / 8 / WAVES;    // direct loads (8 rows each) per wave and slab
+    static constexpr int SCALES = 4 * TILE / 64 / WAVES;  // direct loads of block scales, 4-bit operands
+    static constexpr int ROWS = 2 * TILE * kSlab;         // bytes of a slab of both operands
+    static_assert((TILE / 8) % LOADS == 0 && (4 * TILE / 64) % WAVES == 0, "whole loads per wave");
 };
 
 // Rows of an operand from a tile's first row on: row r starts at base + r * ld
@@ -99,45 +106,82 @@ struct Lane {
           c(lane & 31) {}
 };
 
-__device__ __forceinline__ void load_to_lds(const char* from, char* to) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+// Bytes straight to LDS: lane l's 16 (or 4) go to `to` + 16 l (or 4 l).
+typedef const __attribute__((address_space(1))) void* GlobalPtr;
+typedef __attribute__((address_space(3))) void* LdsPtr;
+__device__ __forceinline__ void load_to_lds16(const char* from, char* to) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)to, 16, 0, 0);
+}
+__device__ __forceinline__ void load_to_lds4(const char* from, char* to) {
+    __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)to, 4, 0, 0);
+}
+
+// Until at most N of this wave's loads are on their way and its LDS reads are
+// done; then all waves of the workgroup.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // fp16 operands: four k = 16 instructions a slab.
 struct MmF16 {
-    static constexpr bool kHalfSlabs = false;
-    __device__ void begin(int, int) {}
-    __device__ void next(int) {}
+    static constexpr bool kScaled = false;
     template <int KK>
-    __device__ __forceinline__ f32x16 mma(const i32x4& a, const i32x4& b, f32x16 c, int, int) const {
+    static __device__ __forceinline__ f32x16 mma(const i32x4& a, const i32x4& b, f32x16 c, uint32_t, uint32_t) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b),
                                                       c, 0, 0, 0);
     }
 };
 
-template <class S, class MM, int KK>
-__device__ __forceinline__ void slab_step(MM& mm, f32x16 (&acc)[S::MT][S::NT], const char* ra, const char* rb,
-                                          int slot) {
-    const int at = (slot ^ KK) << 4;
+// 4-bit operands under block scales: four k = 64 instructions a slab.  The scales
+// of a row's eight blocks go to LDS as two dwords, one per lane group.
+struct MmFp4 {
+    static constexpr bool kScaled = true;
+    template <int KK>
+    static __device__ __forceinline__ f32x16 mma(const i32x4& a, const i32x4& b, f32x16 c, uint32_t sa, uint32_t sb) {
+        const i32x8 u = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+        const i32x8 v = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(u, v, c, 4, 4, KK, (int)sa, KK, (int)sb);
+    }
+};
+
+// Bytes of LDS of a product.
+template <class S, class MM>
+constexpr int product_lds() {
+    return S::STAGES * (S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0));
+}
+
+// One k step's fragments of a wave's rows and columns.
+template <class S>
+struct Frags {
     i32x4 a[S::MT], b[S::NT];
+    __device__ __forceinline__ void load(const char* ra, const char* rb, int at) {
 #pragma unroll
-    for (int i = 0; i < S::MT; ++i) a[i] = *(const i32x4*)(ra + i * 32 * kSlab + at);
+        for (int i = 0; i < S::MT; ++i) a[i] = *(const i32x4*)(ra + i * 32 * kSlab + at);
 #pragma unroll
-    for (int j = 0; j < S::NT; ++j) b[j] = *(const i32x4*)(rb + j * 32 * kSlab + at);
+        for (int j = 0; j < S::NT; ++j) b[j] = *(const i32x4*)(rb + j * 32 * kSlab + at);
+    }
+};
+
+template <class S, class MM, int KK>
+__device__ __forceinline__ void multiply(f32x16 (&acc)[S::MT][S::NT], const Frags<S>& f,
+                                         const uint32_t (&sa)[S::MT], const uint32_t (&sb)[S::NT]) {
 #pragma unroll
     for (int i = 0; i < S::MT; ++i)
 #pragma unroll
-        for (int j = 0; j < S::NT; ++j) acc[i][j] = mm.template mma<KK>(a[i], b[j], acc[i][j], i, j);
+        for (int j = 0; j < S::NT; ++j) acc[i][j] = MM::template mma<KK>(f.a[i], f.b[j], acc[i][j], sa[i], sb[j]);
 }
 
 // acc = the wave's part of the tile over `slabs` whole slabs, then (4-bit
 // operands) half a slab if `half`.  Element r of acc[i][j] is output row
 // wm * WM + 32 i + 8 (r / 4) + 4 h + r % 4, column wn * WN + 32 j + c.
-// lds: S::LDS bytes.
+// SA and SB: the scales' rows (4-bit operands).  lds: product_lds bytes, free for
+// other use once every wave has returned.
 template <class S, class MM>
-__device__ __forceinline__ void tile_product(const Operand& A, const Operand& B, int slabs, bool half, MM& mm,
-                                             char* lds, f32x16 (&acc)[S::MT][S::NT]) {
+__device__ __forceinline__ void tile_product(const Operand& A, const Operand& B, const Operand& SA, const Operand& SB,
+                                             int slabs, bool half, char* lds, f32x16 (&acc)[S::MT][S::NT]) {
     const Lane L;
     const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
 #pragma unroll
@@ -147,8 +191,7 @@ __device__ __forceinline__ void tile_product(const Operand& A, const Operand& B,
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-    const int total = slabs + (half ? 1 : 0);
-    if (total == 0) return;
+    const int total = slabs + (MM::kScaled && half ? 1 : 0);
     // this wave's direct loads: groups of 8 rows, all of one operand
     const int g0 = L.wave * S::LOADS;
     const bool is_a = g0 < S::TILE / 8;
@@ -156,48 +199,147 @@ __device__ __forceinline__ void tile_product(const Operand& A, const Operand& B,
     const uint32_t ld = is_a ? A.ld : B.ld;
     const int last = (is_a ? A.rows : B.rows) - 1;
     const int row0 = (is_a ? g0 : g0 - S::TILE / 8) * 8 + (L.lane >> 3);
-    const uint32_t piece = (L.lane & 7) ^ (L.lane >> 3);
     uint32_t off[S::LOADS];
+    bool upper[S::LOADS];  // a piece of the slab's second half
 #pragma unroll
     for (int i = 0; i < S::LOADS; ++i) {
         const int row = row0 + i * 8;
+        const uint32_t piece = (L.lane & 7) ^ ((row >> 1) & 7);
         off[i] = (uint32_t)(row < last ? row : last) * ld + piece * 16;
+        upper[i] = piece >= 4;
     }
-    auto stage = [&](int slab, int buf) {
-        const char* from = base + (int64_t)slab * kSlab;
-        // past a half slab lies the next row: its second half is not read
-        const uint32_t back = MM::kHalfSlabs && slab >= slabs ? (piece & 4) * 16 : 0;
-        char* to = lds + buf * S::BUFFER + g0 * 1024;
+    // and of scales: dword h * 2 TILE + row of the two operands' rows
+    constexpr int kScaleLoads = MM::kScaled ? S::SCALES : 0;
+    const char* scale_base[kScaleLoads + 1];
+    uint32_t scale_off[kScaleLoads + 1], scale_h[kScaleLoads + 1];
 #pragma unroll
-        for (int i = 0; i < S::LOADS; ++i) load_to_lds(from + (off[i] - back), to + i * 1024);
+    for (int i = 0; i < kScaleLoads; ++i) {
+        const int first = (L.wave * S::SCALES + i) * 64, h = first / (2 * S::TILE), r = first % (2 * S::TILE);
+        const Operand& O = r < S::TILE ? SA : SB;
+        const int row = (r < S::TILE ? r : r - S::TILE) + L.lane;
+        scale_base[i] = O.base;
+        scale_off[i] = (uint32_t)(row < O.rows - 1 ? row : O.rows - 1) * O.ld;
+        scale_h[i] = 4 * h;
+    }
+    constexpr int kStage = S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0);
+    // quarter q of the loads of a slab (q = 4: all)
+    auto stage = [&](int slab, char* buf, int q) {
+        const bool cut = MM::kScaled && slab >= slabs;  // past a half slab lies the next row
+        const char* from = base + (int64_t)slab * kSlab;
+        char* to = buf + g0 * 1024;
+#pragma unroll
+        for (int i = 0; i < S::LOADS; ++i)
+            if (q == 4 || i * 4 / S::LOADS == q)
+                load_to_lds16(from + (off[i] - (cut && upper[i] ? 64u : 0u)), to + i * 1024);
+        if (q >= 3) {
+#pragma unroll
+            for (int i = 0; i < kScaleLoads; ++i)
+                load_to_lds4(scale_base[i] + (int64_t)slab * 8 + (scale_off[i] + (cut ? 0u : scale_h[i])),
+                             buf + S::ROWS + (L.wave * S::SCALES + i) * 256);
+        }
     };
     const int fa = (wm * S::WM + L.c) * kSlab, fb = (S::TILE + wn * S::WN + L.c) * kSlab;
-    const int slot = (4 * L.h) ^ (L.c & 7);
+    const int turn = (L.c >> 1) & 7;
+    auto scales = [&](const char* buf, int shift, uint32_t (&sa)[S::MT], uint32_t (&sb)[S::NT]) {
+        if constexpr (MM::kScaled) {
+            const uint32_t* at = (const uint32_t*)(buf + S::ROWS) + L.h * 2 * S::TILE + L.c;
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i) sa[i] = at[wm * S::WM + 32 * i] >> shift;
+#pragma unroll
+            for (int j = 0; j < S::NT; ++j) sb[j] = at[S::TILE + wn * S::WN + 32 * j] >> shift;
+        }
+    };
 
-    stage(0, 0);
-    mm.begin(wm, wn);
+    for (int s = 0; s < S::STAGES - 1 && s < total; ++s) stage(s, lds + s * kStage, 4);
+    char* const end = lds + S::STAGES * kStage;
+    char *buf = lds, *fill = lds + (S::STAGES - 1) * kStage;
+    auto after = [&](char* b) { return b + kStage == end ? lds : b + kStage; };
     for (int s = 0; s < slabs; ++s) {
-        __syncthreads();  // slab s has landed; the other buffer's readers are done
-        const char* buf = lds + (s & 1) * S::BUFFER;
-        if (s + 1 < total) stage(s + 1, (s + 1) & 1);
-        mm.next(s + 1 < total ? s + 1 : s);
+        // slab s has landed in every wave's part, and the buffer used before it is free
+        if (s + S::STAGES - 2 < total)
+            wait_and_meet<(S::STAGES - 2) * (S::LOADS + kScaleLoads)>();
+        else
+            wait_and_meet<0>();
+        const bool more = s + S::STAGES - 1 < total;
+        const int ahead = s + S::STAGES - 1;
+        uint32_t sa[S::MT], sb[S::NT];
+        scales(buf, 0, sa, sb);
         const char *ra = buf + fa, *rb = buf + fb;
-        slab_step<S, MM, 0>(mm, acc, ra, rb, slot);
-        slab_step<S, MM, 1>(mm, acc, ra, rb, slot);
-        slab_step<S, MM, 2>(mm, acc, ra, rb, slot);
-        slab_step<S, MM, 3>(mm, acc, ra, rb, slot);
+        const int slot = (4 * L.h) ^ turn;
+        Frags<S> f[2];
+        f[0].load(ra, rb, (slot ^ 0) << 4);
+        if (more) stage(ahead, fill, 0);
+        f[1].load(ra, rb, (slot ^ 1) << 4);
+        multiply<S, MM, 0>(acc, f[0], sa, sb);
+        if (more) stage(ahead, fill, 1);
+        f[0].load(ra, rb, (slot ^ 2) << 4);
+        multiply<S, MM, 1>(acc, f[1], sa, sb);
+        if (more) stage(ahead, fill, 2);
+        f[1].load(ra, rb, (slot ^ 3) << 4);
+        multiply<S, MM, 2>(acc, f[0], sa, sb);
+        if (more) stage(ahead, fill, 3);
+        multiply<S, MM, 3>(acc, f[1], sa, sb);
+        buf = after(buf);
+        fill = after(fill);
     }
-    if constexpr (MM::kHalfSlabs) {
+    if constexpr (MM::kScaled) {
         if (!half) return;
-        __syncthreads();
-        const char* buf = lds + (slabs & 1) * S::BUFFER;
-        mm.half();
+        wait_and_meet<0>();
+        uint32_t sa[S::MT], sb[S::NT];
+        scales(buf, 16 * L.h, sa, sb);  // group h takes blocks 2h and 2h + 1 of four
         const char *ra = buf + fa, *rb = buf + fb;
-        const int hslot = (2 * L.h) ^ (L.c & 7);
-        slab_step<S, MM, 0>(mm, acc, ra, rb, hslot);
-        slab_step<S, MM, 1>(mm, acc, ra, rb, hslot);
+        const int slot = (2 * L.h) ^ turn;
+        Frags<S> f[2];
+        f[0].load(ra, rb, (slot ^ 0) << 4);
+        f[1].load(ra, rb, (slot ^ 1) << 4);
+        multiply<S, MM, 0>(acc, f[0], sa, sb);
+        multiply<S, MM, 1>(acc, f[1], sa, sb);
     }
 }
+
+// Turns the 4 x 4 values of four neighbouring lanes: v[r] of lane t <-> v[t] of lane r.
+template <int CTRL>
+__device__ __forceinline__ float quad_swap(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ void quad_turn(float (&v)[4]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+    for (int p = 0; p < 4; p += 2) {
+        const float o = quad_swap<0xB1>(odd ? v[p] : v[p + 1]);  // with lane ^ 1
+        v[p] = odd ? o : v[p];
+        v[p + 1] = odd ? v[p + 1] : o;
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const float o = quad_swap<0x4E>(high ? v[p] : v[p + 2]);  // with lane ^ 2
+        v[p] = high ? o : v[p];
+        v[p + 2] = high ? v[p + 2] : o;
+    }
+}
+
+// A wave's fp16 results on their way to the transposed place: 32 columns by WM rows
+// at a time, through this wave's own part of LDS, so that a column's WM values
+// leave as one run.
+template <class S>
+struct Turner {
+    static constexpr int kLd = S::WM * 2 + 16;  // bytes a column
+    static constexpr int kBytes = 32 * kLd;     // per wave
+    char* lds;
+    __device__ Turner(char* all, const Lane& L) : lds(all + L.wave * kBytes) {}
+    // rows i..i+3 (i within WM) of this lane's column
+    __device__ __forceinline__ void put(const Lane& L, int i, f16x4 v) { *(f16x4*)(lds + L.c * kLd + i * 2) = v; }
+    // out[(j0 + c) * ld + i0 ..], columns below cols, rows below rows (a multiple of 8)
+    __device__ __forceinline__ void flush(const Lane& L, _Float16* out, int64_t ld, int j0, int i0, int cols, int rows) {
+        constexpr int kRun = S::WM / 8;  // 16-byte pieces a column
+#pragma unroll
+        for (int t = 0; t < 32 * kRun / 64; ++t) {
+            const int p = t * 64 + L.lane, c = p / kRun, i = p % kRun * 8;
+            const f16x8 v = *(const f16x8*)(lds + c * kLd + i * 2);
+            if (j0 + c < cols && i0 + i < rows) *(f16x8*)(out + (int64_t)(j0 + c) * ld + i0 + i) = v;
+        }
+    }
+};
 
 // Workgroup number -> tile number: consecutive workgroups go to different XCDs,
 // each with its own L2, so every XCD gets a contiguous range of tiles.
@@ -249,6 +391,46 @@ int launch(void (*kernel)(Args), dim3 grid, int block, hipStream_t s, const Args
         return fail(ZERO_EHIP, "%s: launch failed: %s", what, hipGetErrorString(e));
     }
     return ok();
+}
+
+// The shapes in use: (tile, wave rows, wave columns, slabs in LDS).
+typedef Shape<256, 64, 128, 2> Tile256;
+typedef Shape<192, 96, 96, 3> Tile192;
+typedef Shape<128, 64, 64, 2> Tile128;      // two workgroups on a CU
+typedef Shape<128, 64, 64, 3> Tile128Few;   // at most one workgroup for a CU
+typedef Shape<64, 32, 32, 2> Tile64;
+typedef Shape<64, 32, 32, 4> Tile64Few;
+
+// The shape that a product takes, by the tiles it has at each: microseconds a slab
+// as measured (fp16, 256 CUs, tiles of 4096 long rows) times the rounds that the
+// tiles need.  Which of 192 and 256 wins at large sizes is mostly a matter of how
+// whole the last round is: 136 tiles of 256 leave half of the CUs idle
+// where 253 of 192 fill them.
+template <class F>
+int pick_tile(F tiles) {
+    const int64_t t256 = tiles(256), t192 = tiles(192), t128 = tiles(128), t64 = tiles(64);
+    const double cost[6] = {2.05 * (double)ceil_div(t256, 256),
+                            1.20 * (double)ceil_div(t192, 256),
+                            1.14 * (double)ceil_div(t128, 512),
+                            0.61 * (double)ceil_div(t128, 256),
+                            0.81 * (double)ceil_div(t64, 1024),
+                            0.31 * (double)ceil_div(t64, 256)};
+    int k = 0;
+    for (int i = 1; i < 6; ++i)
+        if (cost[i] < cost[k]) k = i;
+    return k;
+}
+
+template <class F>
+int with_tile(int pick, F f) {
+    switch (pick) {
+        case 0: return f(Tile256());
+        case 1: return f(Tile192());
+        case 2: return f(Tile128());
+        case 3: return f(Tile128Few());
+        case 4: return f(Tile64());
+        default: return f(Tile64Few());
+    }
 }
 
 }  // namespace

@@ -194,61 +194,6 @@ __global__ void __launch_bounds__(kThreads) mx4_values_kernel(DequantArgs a) {
 }
 
 // ---------------------------------------------------------------- the product
-// 4-bit operands: the four block scales that lane group h needs of a slab's
-// row are the dword 4h of that row's eight; it is fetched a slab ahead.
-template <class S>
-struct MmFp4 {
-    static constexpr bool kHalfSlabs = true;
-    const uint8_t *sa, *sb;  // scales of the tile's first rows
-    uint32_t ld;             // bytes a row
-    int rows_a, rows_b, slabs;
-    uint32_t off_a[S::MT], off_b[S::NT];
-    uint32_t a[S::MT], b[S::NT], na[S::MT], nb[S::NT];
-
-    __device__ __forceinline__ void fetch(int slab) {
-        const int h = (threadIdx.x & 63) >> 5;
-        const uint32_t at = slab * 8 + (slab < slabs ? 4 * h : 0);
-#pragma unroll
-        for (int i = 0; i < S::MT; ++i) na[i] = *(const uint32_t*)(sa + (off_a[i] + at));
-#pragma unroll
-        for (int j = 0; j < S::NT; ++j) nb[j] = *(const uint32_t*)(sb + (off_b[j] + at));
-    }
-    __device__ __forceinline__ void begin(int wm, int wn) {
-        const int c = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < S::MT; ++i) {
-            const int r = wm * S::WM + 32 * i + c;
-            off_a[i] = (uint32_t)(r < rows_a ? r : rows_a - 1) * ld;
-        }
-#pragma unroll
-        for (int j = 0; j < S::NT; ++j) {
-            const int r = wn * S::WN + 32 * j + c;
-            off_b[j] = (uint32_t)(r < rows_b ? r : rows_b - 1) * ld;
-        }
-        fetch(0);
-    }
-    __device__ __forceinline__ void next(int slab) {
-#pragma unroll
-        for (int i = 0; i < S::MT; ++i) a[i] = na[i];
-#pragma unroll
-        for (int j = 0; j < S::NT; ++j) b[j] = nb[j];
-        fetch(slab);
-    }
-    __device__ __forceinline__ void half() {  // group h takes blocks 2h and 2h + 1 of four
-        const int shift = ((threadIdx.x & 63) >> 5) * 16;
-#pragma unroll
-        for (int i = 0; i < S::MT; ++i) a[i] = na[i] >> shift;
-#pragma unroll
-        for (int j = 0; j < S::NT; ++j) b[j] = nb[j] >> shift;
-    }
-    template <int KK>
-    __device__ __forceinline__ f32x16 mma(const i32x4& x, const i32x4& y, f32x16 c, int i, int j) const {
-        const i32x8 u = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
-        const i32x8 v = __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1);
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(u, v, c, 4, 4, KK, (int)a[i], KK, (int)b[j]);
-    }
-};
-
 struct MatmulArgs {
     const uint8_t *a, *sa, *b, *sb;
     int64_t m, n, p;  // p: padded k
@@ -256,56 +201,66 @@ struct MatmulArgs {
     int64_t ldc;
     int tiles_m, tiles_n;
     int accumulate;
+    int vector;  // rows of c aligned to four elements
 };
 
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS) mx4_matmul_kernel(MatmulArgs g) {
-    __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+    __shared__ __attribute__((aligned(16))) char lds[product_lds<S, MmFp4>()];
     int ti, tj;
     band_tile(xcd_tile(blockIdx.x, gridDim.x), g.tiles_m, g.tiles_n, ti, tj);
     const int64_t i0 = (int64_t)ti * S::TILE, j0 = (int64_t)tj * S::TILE;
     const int64_t left_m = g.m - i0, left_n = g.n - j0;
     const int rows_a = (int)(left_m < S::TILE ? left_m : S::TILE), rows_b = (int)(left_n < S::TILE ? left_n : S::TILE);
-    const Operand A{(const char*)g.a + i0 * (g.p / 2), (uint32_t)(g.p / 2), rows_a};
-    const Operand B{(const char*)g.b + j0 * (g.p / 2), (uint32_t)(g.p / 2), rows_b};
-    MmFp4<S> mm;
-    mm.sa = g.sa + i0 * (g.p / kMxBlock);
-    mm.sb = g.sb + j0 * (g.p / kMxBlock);
-    mm.ld = (uint32_t)(g.p / kMxBlock);
-    mm.rows_a = rows_a;
-    mm.rows_b = rows_b;
-    mm.slabs = (int)(g.p / 256);
+    const uint32_t ld = (uint32_t)(g.p / 2), ls = (uint32_t)(g.p / kMxBlock);
+    const Operand A{(const char*)g.a + i0 * ld, ld, rows_a}, B{(const char*)g.b + j0 * ld, ld, rows_b};
+    const Operand SA{(const char*)g.sa + i0 * ls, ls, rows_a}, SB{(const char*)g.sb + j0 * ls, ls, rows_b};
     f32x16 acc[S::MT][S::NT];
-    tile_product<S>(A, B, mm.slabs, g.p % 256 != 0, mm, lds, acc);
+    tile_product<S, MmFp4>(A, B, SA, SB, (int)(g.p / 256), g.p % 256 != 0, lds, acc);
 
     typedef typename Elem<DT>::type T;
-    T* out = (T*)g.c;
     const Lane L;
-    const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
+    const int64_t iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
 #pragma unroll
     for (int ii = 0; ii < S::MT; ++ii)
 #pragma unroll
-        for (int jj = 0; jj < S::NT; ++jj) {
-            const int64_t j = j0 + wn * S::WN + jj * 32 + L.c;
+        for (int jj = 0; jj < S::NT; ++jj)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t i = i0 + wm * S::WM + ii * 32 + 8 * (r / 4) + 4 * L.h + r % 4;
-                if (i < g.m && j < g.n) {
-                    float v = acc[ii][jj][r];
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
+                quad_turn(v);  // four columns of one row
+                const int64_t i = iw + ii * 32 + 8 * q + 4 * L.h + (L.c & 3), j = jw + jj * 32 + (L.c & ~3);
+                if (i >= g.m || j >= g.n) continue;
+                T* out = (T*)g.c + i * g.ldc + j;
+                if (g.vector && j + 4 <= g.n) {
+                    typedef T T4 __attribute__((ext_vector_type(4)));
+                    T4 w;
                     if constexpr (DT == ZERO_F32) {
-                        if (g.accumulate) v += out[i * g.ldc + j];
+                        if (g.accumulate) {
+                            w = *(const T4*)out;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] += w[e];
+                        }
                     }
-                    out[i * g.ldc + j] = from_float<DT>(v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = from_float<DT>(v[e]);
+                    *(T4*)out = w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (j + e >= g.n) break;
+                        if constexpr (DT == ZERO_F32) {
+                            if (g.accumulate) v[e] += out[e];
+                        }
+                        out[e] = from_float<DT>(v[e]);
+                    }
                 }
             }
-        }
 }
 
 // ---------------------------------------------------------------- host side
-typedef Shape<256, 128, 64> Big;
-typedef Shape<128, 64, 64> Mid;
-typedef Shape<64, 32, 32> Low;
-
 int check_sides(int64_t rows, int64_t cols, const char* what) {
     if (rows < 0 || cols < 0 || rows > kMaxSide || cols > kMaxSide)
         return fail(ZERO_ERANGE, "%s: %lld x %lld out of range", what, (long long)rows, (long long)cols);
@@ -347,6 +302,7 @@ int matmul_with(MatmulArgs g, int32_t c_dtype, hipStream_t s, const char* what) 
     if (tm * tn > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many tiles for one launch", what);
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
+    g.vector = aligned(g.c, 4 * elem_bytes(c_dtype)) && g.ldc % 4 == 0;
     const dim3 grid((unsigned)(tm * tn));
     switch (c_dtype) {
         case ZERO_F16: return launch(mx4_matmul_kernel<S, ZERO_F16>, grid, S::THREADS, s, g, what);
@@ -356,11 +312,8 @@ int matmul_with(MatmulArgs g, int32_t c_dtype, hipStream_t s, const char* what) 
 }
 
 int matmul(const MatmulArgs& g, int32_t c_dtype, hipStream_t s, const char* what) {
-    const int64_t side = g.m < g.n ? g.m : g.n;
-    auto tiles = [&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); };
-    if (side > 128 && tiles(256) >= 256) return matmul_with<Big>(g, c_dtype, s, what);
-    if (side > 64 && tiles(128) >= 256) return matmul_with<Mid>(g, c_dtype, s, what);
-    return matmul_with<Low>(g, c_dtype, s, what);
+    const int pick = pick_tile([&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); });
+    return with_tile(pick, [&](auto shape) { return matmul_with<decltype(shape)>(g, c_dtype, s, what); });
 }
 
 // The checks shared by the products; 1: nothing to do.
@@ -454,7 +407,7 @@ int zero_mx4_matmul(const void* a, const void* sa, const void* b, const void* sb
     if (k > 0 && (a == nullptr || sa == nullptr)) return fail(ZERO_EINVAL, "%s: null operand", what);
     if (!aligned(a, 16) || !aligned(sa, 16)) return fail(ZERO_EALIGN, "%s: operands not 16-byte aligned", what);
     const MatmulArgs g{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb,
-                       m, n, padded(k), c, ldc, 0, 0, accumulate};
+                       m, n, padded(k), c, ldc, 0, 0, accumulate, 0};
     return matmul(g, c_dtype, (hipStream_t)stream, what);
 }
 
@@ -485,7 +438,7 @@ int zero_mx4_matmul_rows(const void* a, int32_t a_dtype, int64_t lda, const void
     uint8_t* scales = codes + round_up(m * (padded(k) / 2), 256);
     if (k > 0 && (rc = quantize(a, a_dtype, m, k, lda, codes, scales, nullptr, nullptr, (hipStream_t)stream, what)) != ZERO_OK)
         return rc;
-    const MatmulArgs g{codes, scales, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, 0};
+    const MatmulArgs g{codes, scales, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, 0, 0};
     return matmul(g, c_dtype, (hipStream_t)stream, what);
 }
 

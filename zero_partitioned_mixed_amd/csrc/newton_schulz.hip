@@ -35,6 +35,7 @@ struct Coeffs {
 // (multiples of 64, the padding zero).
 struct Work {
     int m, n, mp, np;
+    int kp;                  // row length of M and X^T: mp, or 2 mp where X^T is kept in two parts
     int64_t stride;  // bytes from one matrix's block to the next
     char* base;
     int64_t x16, xt0, xt1, s16, m16, ds, dm, sums;  // byte offsets; X in fp32 at 0
@@ -126,23 +127,24 @@ __device__ __forceinline__ double block_sum(double v, double* red, int waves) {
 // which makes the iteration as exact as fp32: 1e-5 against 64 bits.
 //
 // A workgroup holds a strip of X in registers, in the layout of the matrix
-// cores' results: blocks of T x T, each by a group of (T / 32)^2 waves with
+// cores' results: blocks of T x T, each by a group of waves with CT tiles of
 // 32 x 32 elements per wave; G groups side by side and NB blocks after each other,
-// so a strip is G * NB * T columns.  A matrix of one strip takes one
+// so a strip is G * NB * T columns.  Eight waves, so that a wave has 256 registers:
+// sixteen with half of them spilled a hundred and took twice as long.  A matrix of one strip takes one
 // launch for all its steps; a longer one takes, per step, one workgroup that
 // makes M from the strips' parts of S, and one workgroup per strip that
 // applies M and makes its part of the next S.
-template <int T_, int G_, int NB_>
+template <int T_, int CT_, int G_, int NB_>
 struct Strip {
-    static constexpr int T = T_, G = G_, NB = NB_;
-    static constexpr int TILES = T / 32, GROUP = TILES * TILES, WAVES = G * GROUP, THREADS = WAVES * 64;
+    static constexpr int T = T_, CT = CT_, G = G_, NB = NB_;
+    static constexpr int TILES = T / 32 / CT, GROUP = T / 32 * TILES, WAVES = G * GROUP, THREADS = WAVES * 64;
     static constexpr int COLS = G * NB * T;
     static constexpr int ARRAY = T * T * 2;  // bytes of a T x T fp16 array
     static constexpr int SIZE = COLS * T;    // elements of a strip
 };
-typedef Strip<32, 8, 4> Strip32;
-typedef Strip<64, 4, 2> Strip64;
-typedef Strip<128, 1, 2> Strip128;
+typedef Strip<32, 1, 8, 4> Strip32;
+typedef Strip<64, 1, 2, 4> Strip64;
+typedef Strip<128, 2, 1, 2> Strip128;
 
 struct Pair {  // high part and rest, arrays in LDS
     char *hi, *lo;
@@ -159,42 +161,51 @@ __device__ __forceinline__ f16x8 small_frag(const char* a, int row, int kk, int 
     return *(const f16x8*)(a + small_at<T>(row, kk * 16 + h * 8));
 }
 
-// acc += A B^T of two pairs, the product of the two rests left out.
-template <int T>
-__device__ __forceinline__ void small_product(const Pair& A, const Pair& B, int i0, int j0, const Lane& L, f32x16& acc) {
+// acc += A B^T of two pairs, the product of the two rests left out: a wave's CT tiles
+// from row i0, columns j0, + 32, ...
+template <int T, int CT>
+__device__ __forceinline__ void small_product(const Pair& A, const Pair& B, int i0, int j0, const Lane& L,
+                                              f32x16 (&acc)[CT]) {
 #pragma unroll
     for (int kk = 0; kk < T / 16; ++kk) {
         const f16x8 ah = small_frag<T>(A.hi, i0 + L.c, kk, L.h), al = small_frag<T>(A.lo, i0 + L.c, kk, L.h);
-        const f16x8 bh = small_frag<T>(B.hi, j0 + L.c, kk, L.h), bl = small_frag<T>(B.lo, j0 + L.c, kk, L.h);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh, acc, 0, 0, 0);
+        f16x8 bh[CT], bl[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            bh[t] = small_frag<T>(B.hi, j0 + 32 * t + L.c, kk, L.h);
+            bl[t] = small_frag<T>(B.lo, j0 + 32 * t + L.c, kk, L.h);
+        }
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh[t], acc[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl[t], acc[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh[t], acc[t], 0, 0, 0);
     }
 }
 
-// A wave's 32 x 32 elements into a pair; TURNED: into its transpose.
-template <int T, bool TURNED>
-__device__ __forceinline__ void small_store(const Pair& P, int i0, int j0, const Lane& L, const float* v) {
+// A wave's tiles into a pair; TURNED: into its transpose.
+template <int T, int CT, bool TURNED>
+__device__ __forceinline__ void small_store(const Pair& P, int i0, int j0, const Lane& L, const float (&v)[CT][16]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int i = i0 + 8 * q + 4 * L.h, j = j0 + L.c;
-        f16x4 h, l;
+    for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            h[r] = (_Float16)v[4 * q + r];
-            l[r] = (_Float16)(v[4 * q + r] - (float)h[r]);
-        }
-        if constexpr (TURNED) {
-            *(f16x4*)(P.hi + small_at<T>(j, i)) = h;
-            *(f16x4*)(P.lo + small_at<T>(j, i)) = l;
-        } else {
+        for (int q = 0; q < 4; ++q) {
+            float x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = v[t][4 * q + r];
+            if constexpr (!TURNED) quad_turn(x);  // four columns of one row
+            f16x4 h, l;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                *(_Float16*)(P.hi + small_at<T>(i + r, j)) = h[r];
-                *(_Float16*)(P.lo + small_at<T>(i + r, j)) = l[r];
+                h[r] = (_Float16)x[r];
+                l[r] = (_Float16)(x[r] - (float)h[r]);
             }
+            const int i = i0 + 8 * q + 4 * L.h, j = j0 + 32 * t;
+            const int at = TURNED ? small_at<T>(j + L.c, i) : small_at<T>(i + (L.c & 3), j + (L.c & ~3));
+            *(f16x4*)(P.hi + at) = h;
+            *(f16x4*)(P.lo + at) = l;
         }
-    }
 }
 
 // LDS of a strip's workgroup: a pair per group for its current block of X (or the
@@ -209,98 +220,135 @@ struct StripLds {
 
 template <class P>
 struct StripWave {
-    static constexpr int T = P::T;
+    static constexpr int T = P::T, CT = P::CT;
+    typedef float Tiles[CT][16];
     Lane L;
-    int group, i0, j0;  // this wave's group, and its tile's place in a block
+    int group, i0, j0;  // this wave's group, and its tiles' place in a block
     StripLds<P>& lds;
     Pair mine, square;
 
     __device__ StripWave(StripLds<P>& s) : lds(s) {
         group = L.wave / P::GROUP;
         i0 = L.wave % P::GROUP / P::TILES * 32;
-        j0 = L.wave % P::TILES * 32;
+        j0 = L.wave % P::TILES * 32 * CT;
         mine = {s.block + group * 2 * P::ARRAY, s.block + (group * 2 + 1) * P::ARRAY};
         square = {s.square, s.square + P::ARRAY};
     }
-    __device__ int row(int r) const { return i0 + 8 * (r / 4) + 4 * L.h + r % 4; }
-    __device__ int col(int b) const { return (b * P::G + group) * T + j0 + L.c; }  // within the strip
+    __device__ __forceinline__ int row(int r) const { return i0 + 8 * (r / 4) + 4 * L.h + r % 4; }
+    __device__ __forceinline__ int at(int t) const { return j0 + 32 * t + L.c; }  // column within a block
+    __device__ __forceinline__ int col(int b, int t) const { return (b * P::G + group) * T + at(t); }  // within the strip
 
-    // This wave's tile of S = X X^T of the strip's first nb blocks of every group.
-    __device__ void gram(const float (&x)[P::NB][16], int nb, float (&s)[16]) {
-        f32x16 acc;
+    __device__ __forceinline__ void product(const Pair& A, const Pair& B, f32x16 (&acc)[CT]) const {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[t][r] = 0.0f;
+        small_product<T, CT>(A, B, i0, j0, L, acc);
+    }
+
+    // This wave's tiles of S = X X^T of the strip's first nb blocks of every group.
+    __device__ __forceinline__ void gram(const Tiles (&x)[P::NB], int nb, Tiles& s) {
+        f32x16 acc[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[t][r] = 0.0f;
 #pragma unroll
         for (int b = 0; b < P::NB; ++b) {
             if (b >= nb) break;
             __syncthreads();  // the block's last readers are done
-            small_store<T, false>(mine, i0, j0, L, x[b]);
+            small_store<T, CT, false>(mine, i0, j0, L, x[b]);
             __syncthreads();
-            small_product<T>(mine, mine, i0, j0, L, acc);
+            small_product<T, CT>(mine, mine, i0, j0, L, acc);
         }
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = acc[r] * (1.0f / (kXScale * kXScale));
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[t][r] = acc[t][r] * (1.0f / (kXScale * kXScale));
         if constexpr (P::G > 1) {
             float* parts = (float*)lds.block;
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) parts[group * T * T + row(r) * T + j0 + L.c] = s[r];
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) parts[group * T * T + row(r) * T + at(t)] = s[t][r];
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float v = 0.0f;
-                for (int g = 0; g < P::G; ++g) v += parts[g * T * T + row(r) * T + j0 + L.c];
-                s[r] = v;
-            }
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int g = 0; g < P::G; ++g) v += parts[g * T * T + row(r) * T + at(t)];
+                    s[t][r] = v;
+                }
         }
     }
 
-    // M from S, which every group holds: m[] this wave's tile off the diagonal
+    // M from S, which every group holds: m this wave's tiles off the diagonal
     // (times mscale), lds.dm the diagonal.
-    __device__ void poly(const Coeffs& k, float (&s)[16], float (&m)[16]) {
+    __device__ __forceinline__ void poly(const Coeffs& k, Tiles& s, Tiles& m) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const bool diag = row(r) == j0 + L.c;
-            if (diag && group == 0) lds.ds[row(r)] = s[r];
-            s[r] = diag ? 0.0f : s[r];
-            m[r] = s[r] * kSScale;
-        }
-        if (group == 0) small_store<T, true>(square, i0, j0, L, m);  // symmetric
-        __syncthreads();
-        f32x16 acc;
+        for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
-        small_product<T>(square, square, i0, j0, L, acc);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int i = row(r), j = j0 + L.c;
-            const float di = lds.ds[i];
-            float s2 = acc[r] * (1.0f / (kSScale * kSScale)) + s[r] * (di + lds.ds[j]);
-            if (i == j) {
-                s2 += di * di;
-                if (group == 0) lds.dm[i] = k.a + k.b * di + k.c * s2;
+            for (int r = 0; r < 16; ++r) {
+                const bool diag = row(r) == at(t);
+                if (diag && group == 0) lds.ds[row(r)] = s[t][r];
+                s[t][r] = diag ? 0.0f : s[t][r];
+                m[t][r] = s[t][r] * kSScale;
             }
-            m[r] = i == j ? 0.0f : (k.b * s[r] + k.c * s2) * k.mscale;
-        }
+        if (group == 0) small_store<T, CT, true>(square, i0, j0, L, m);  // symmetric
+        __syncthreads();
+        f32x16 acc[CT];
+        product(square, square, acc);
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int i = row(r), j = at(t);
+                const float di = lds.ds[i];
+                float s2 = acc[t][r] * (1.0f / (kSScale * kSScale)) + s[t][r] * (di + lds.ds[j]);
+                if (i == j) {
+                    s2 += di * di;
+                    if (group == 0) lds.dm[i] = k.a + k.b * di + k.c * s2;
+                }
+                m[t][r] = i == j ? 0.0f : (k.b * s[t][r] + k.c * s2) * k.mscale;
+            }
         __syncthreads();  // the readers of S are done
     }
 
     // X <- M X; M's pair is written by the caller before, without a barrier.
-    __device__ void apply(const Coeffs& k, int nb, float (&x)[P::NB][16]) {
+    __device__ __forceinline__ void apply(const Coeffs& k, int nb, Tiles (&x)[P::NB]) {
         const float un = 1.0f / k.mscale;
 #pragma unroll
         for (int b = 0; b < P::NB; ++b) {
             if (b >= nb) break;
             if (b > 0) __syncthreads();
-            small_store<T, true>(mine, i0, j0, L, x[b]);
+            small_store<T, CT, true>(mine, i0, j0, L, x[b]);
             __syncthreads();
-            f32x16 acc;
+            f32x16 acc[CT];
+            product(square, mine, acc);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
-            small_product<T>(square, mine, i0, j0, L, acc);
+            for (int t = 0; t < CT; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[b][r] = lds.dm[row(r)] * x[b][r] + acc[r] * un;
+                for (int r = 0; r < 16; ++r) x[b][t][r] = lds.dm[row(r)] * x[b][t][r] + acc[t][r] * un;
         }
+    }
+
+    // Forgets what the compiler knows of the lane's place, so that it works addresses
+    // and bounds out again rather than keep them in registers across the steps (a
+    // hundred spilled registers otherwise).
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(L.c), "+v"(L.h)); }
+
+    // every value of a strip: f(block, tile, value's number, row, column in the strip)
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+        for (int b = 0; b < P::NB; ++b)
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) f(b, t, r, row(r), col(b, t));
     }
 };
 
@@ -331,58 +379,46 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
     const int nb = (n + P::G * P::T - 1) / (P::G * P::T);
     const float clip = io.clip();
-    float x[P::NB][16];
+    typename StripWave<P>::Tiles x[P::NB], s, mv;
     double ss = 0.0;
-#pragma unroll
-    for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int i = w.row(r), j = w.col(bl);
-            const float v = i < m && j < n ? io.first(b, tall ? j : i, tall ? i : j, clip) : 0.0f;
-            ss += (double)v * (double)v;
-            x[bl][r] = v;
-        }
+    w.each([&](int bl, int t, int r, int i, int j) {
+        const float v = i < m && j < n ? io.first(b, tall ? j : i, tall ? i : j, clip) : 0.0f;
+        ss += (double)v * (double)v;
+        x[bl][t][r] = v;
+    });
     const double scale = scale_of(sqrt(block_sum(ss, lds.red, P::WAVES)), a.k.eps);
-#pragma unroll
-    for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[bl][r] = (float)(x[bl][r] * scale);
+    w.each([&](int bl, int t, int r, int, int) { x[bl][t][r] = (float)(x[bl][t][r] * scale); });
+    w.forget();
+#pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
-        float s[16], mv[16];
         w.gram(x, nb, s);
         w.poly(a.k, s, mv);
-        if (w.group == 0) small_store<P::T, true>(w.square, w.i0, w.j0, w.L, mv);
+        if (w.group == 0) small_store<P::T, P::CT, true>(w.square, w.i0, w.j0, w.L, mv);
         w.apply(a.k, nb, x);
     }
-#pragma unroll
-    for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int i = w.row(r), j = w.col(bl);
-            if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, x[bl][r] * (1.0f / kXScale));
-        }
+    w.forget();
+    w.each([&](int bl, int t, int r, int i, int j) {
+        if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, x[bl][t][r] * (1.0f / kXScale));
+    });
 }
 
 // M of a matrix of several strips: fp32 [T][T] off the diagonal, then the diagonal.
 template <class P, class IO>
 __global__ void __launch_bounds__(P::GROUP * 64) ns_poly_kernel(StripArgs<IO> a) {
-    typedef Strip<P::T, 1, 1> One;
+    typedef Strip<P::T, P::CT, 1, 1> One;
     __shared__ StripLds<One> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
     StripWave<One> w(lds);
     char* ws = a.ws + blockIdx.x * a.stride;
     const float* parts = (const float*)(ws + a.parts);
-    float s[16], mv[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+    typename StripWave<One>::Tiles s, mv;
+    w.each([&](int, int t, int r, int, int) { s[t][r] = 0.0f; });
     for (int p = 0; p < a.strips; ++p)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] += parts[(int64_t)p * P::T * P::T + w.row(r) * P::T + w.j0 + w.L.c];
+        w.each([&](int, int t, int r, int i, int j) { s[t][r] += parts[(int64_t)p * P::T * P::T + i * P::T + j]; });
     w.poly(a.k, s, mv);
     float* mat = (float*)(ws + a.mat);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) mat[w.row(r) * P::T + w.j0 + w.L.c] = mv[r];
-    if ((int)threadIdx.x < P::T) mat[P::T * P::T + threadIdx.x] = lds.dm[threadIdx.x];
+    w.each([&](int, int t, int r, int i, int j) { mat[i * P::T + j] = mv[t][r]; });
+    for (int i = threadIdx.x; i < P::T; i += One::THREADS) mat[P::T * P::T + i] = lds.dm[i];
 }
 
 // One strip: step 0 makes X; step k applies the k-th M; the last one writes the
@@ -398,55 +434,44 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
     const int left = n - j0 < P::COLS ? n - j0 : P::COLS, nb = (left + P::G * P::T - 1) / (P::G * P::T);
     char* ws = a.ws + b * a.stride;
-    float* mine = (float*)ws + (int64_t)strip * P::SIZE + w.L.wave * 1024 + w.L.lane;
-    float x[P::NB][16];
+    float* mine = (float*)ws + (int64_t)strip * P::SIZE + w.L.wave * (P::NB * P::CT * 1024) + w.L.lane;
+    typename StripWave<P>::Tiles x[P::NB], s;
     if (a.step == 0) {
         double ss = 0.0;
         for (int p = threadIdx.x; p < a.sum_parts; p += P::THREADS) ss += ((const double*)(ws + a.sums))[p];
         const double scale = scale_of(sqrt(block_sum(ss, lds.red, P::WAVES)), a.k.eps);
         const float clip = io.clip();
-#pragma unroll
-        for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int i = w.row(r), j = j0 + w.col(bl);
-                x[bl][r] = i < m && j < n ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
-            }
+        w.each([&](int bl, int t, int r, int i, int jj) {
+            const int j = j0 + jj;
+            x[bl][t][r] = i < m && j < n ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
+        });
     } else {
-#pragma unroll
-        for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) x[bl][r] = mine[bl * P::WAVES * 1024 + r * 64];
+        w.each([&](int bl, int t, int r, int, int) { x[bl][t][r] = mine[((bl * P::CT + t) * 16 + r) * 64]; });
         const float* mat = (const float*)(ws + a.mat);
         if (w.group == 0) {
-            float mv[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) mv[r] = mat[w.row(r) * P::T + w.j0 + w.L.c];
-            small_store<P::T, true>(w.square, w.i0, w.j0, w.L, mv);
+            w.each([&](int bl, int t, int r, int i, int) {
+                if (bl == 0) s[t][r] = mat[i * P::T + w.at(t)];
+            });
+            small_store<P::T, P::CT, true>(w.square, w.i0, w.j0, w.L, s);
         }
-        if ((int)threadIdx.x < P::T) lds.dm[threadIdx.x] = mat[P::T * P::T + threadIdx.x];
+        for (int i = threadIdx.x; i < P::T; i += P::THREADS) lds.dm[i] = mat[P::T * P::T + i];
         w.apply(a.k, nb, x);
     }
     if (a.step == a.steps) {
-#pragma unroll
-        for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int i = w.row(r), j = j0 + w.col(bl);
-                if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, x[bl][r] * (1.0f / kXScale));
-            }
+        w.each([&](int bl, int t, int r, int i, int jj) {
+            const int j = j0 + jj;
+            if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, x[bl][t][r] * (1.0f / kXScale));
+        });
         return;
     }
-#pragma unroll
-    for (int bl = 0; bl < P::NB; ++bl)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mine[bl * P::WAVES * 1024 + r * 64] = x[bl][r];
-    float s[16];
+    w.each([&](int bl, int t, int r, int, int) { mine[((bl * P::CT + t) * 16 + r) * 64] = x[bl][t][r]; });
     w.gram(x, nb, s);
     float* part = (float*)(ws + a.parts) + (int64_t)strip * P::T * P::T;
     if (w.group == 0) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) part[w.row(r) * P::T + w.j0 + w.L.c] = s[r];
+        for (int t = 0; t < P::CT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) part[w.row(r) * P::T + w.at(t)] = s[t][r];
     }
 }
 
@@ -520,7 +545,11 @@ __global__ void __launch_bounds__(256) ns_begin_kernel(IoArgs<IO> a) {
             x32[(int64_t)(i0 + i) * w.np + j0 + x] = v;
             x16[(int64_t)(i0 + i) * w.np + j0 + x] = (_Float16)v;
         }
-        if (j0 + i < w.n && i0 + x < w.mp) xt[(int64_t)(j0 + i) * w.mp + i0 + x] = (_Float16)vt;
+        if (j0 + i < w.n && i0 + x < w.mp) {
+            const int64_t at = (int64_t)(j0 + i) * w.kp + i0 + x;
+            xt[at] = (_Float16)vt;
+            if (w.kp > w.mp) xt[at + w.mp] = (_Float16)(vt - (float)(_Float16)vt);
+        }
     }
 }
 
@@ -561,10 +590,19 @@ __device__ __forceinline__ void triangle_tile(int t, int& i, int& j) {
     i = t - j * (j + 1) / 2;
 }
 
+// Results leave through two doors.  Four lanes turn their 4 x 4 values, so a
+// lane then has four neighbouring columns of one row: row-major reads and writes
+// are vectors.  The transposed copy goes through the wave's part of LDS.
+template <class S>
+constexpr int ns_lds() {
+    const int a = product_lds<S, MmF16>(), b = 2 * S::WAVES * Turner<S>::kBytes;
+    return a > b ? a : b;
+}
+
 // S (POLY false) or M (POLY true): tiles on and above the diagonal, mirrored.
 template <class S, bool POLY>
 __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
-    __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+    __shared__ __attribute__((aligned(16))) char lds[ns_lds<S>()];
     const Work& w = a.w;
     if (w.skipped()) return;
     char* base = w.of(blockIdx.y);
@@ -576,61 +614,95 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     const Operand A{from + (int64_t)i0 * ld * 2, (uint32_t)ld * 2, w.m - i0};
     const Operand B{from + (int64_t)j0 * ld * 2, (uint32_t)ld * 2, w.m - j0};
     f32x16 acc[S::MT][S::NT];
-    MmF16 mm;
-    tile_product<S>(A, B, ld / 64, false, mm, lds, acc);
+    tile_product<S, MmF16>(A, B, A, B, ld / 64, false, lds, acc);
+    __syncthreads();  // LDS is free
 
     const Lane L;
-    const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
+    const int iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
     const Coeffs& k = a.k;
     float* diag = (float*)(base + (POLY ? w.dm : w.ds));
     const float* ds = (const float*)(base + w.ds);
     const _Float16* s16 = (const _Float16*)(base + w.s16);
     _Float16* out = (_Float16*)(base + (POLY ? w.m16 : w.s16));
+    const int ldo = POLY ? w.kp : w.mp;
+    const bool twice = POLY && w.kp > w.mp;  // M meets both parts of X^T
+    Turner<S> turner(lds, L);
 #pragma unroll
-    for (int ii = 0; ii < S::MT; ++ii)
+    for (int jj = 0; jj < S::NT; ++jj) {
+        const int j = jw + jj * 32 + (L.c & ~3);  // and the three after it
+        // what the tile needs from memory, all of a column block before its first use
+        float dj[4], di4[S::MT * 4];
+        f16x4 old[S::MT * 4];
+        if constexpr (POLY) {
 #pragma unroll
-        for (int jj = 0; jj < S::NT; ++jj) {
-            const int j = j0 + wn * S::WN + jj * 32 + L.c;
+            for (int e = 0; e < 4; ++e) dj[e] = ds[j + e < w.m ? j + e : w.m - 1];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int ib = i0 + wm * S::WM + ii * 32 + 8 * q + 4 * L.h;
-                f16x4 h;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = ib + r;
-                    float v = 0.0f;
-                    if (i < w.m && j < w.m) {
-                        if constexpr (POLY) {
-                            const float di = ds[i];
-                            const float e = (float)s16[(int64_t)i * w.mp + j] * (1.0f / kSScale);
-                            float s2 = acc[ii][jj][4 * q + r] * (1.0f / (kSScale * kSScale)) + e * (di + ds[j]);
-                            if (i == j) {
-                                s2 += di * di;
-                                diag[i] = k.a + k.b * di + k.c * s2;
-                            } else {
-                                v = (k.b * e + k.c * s2) * k.mscale;
-                            }
-                        } else {
-                            v = acc[ii][jj][4 * q + r] * (1.0f / (kXScale * kXScale));
-                            if (i == j) {
-                                diag[i] = v;
-                                v = 0.0f;
-                            }
-                            v *= kSScale;
-                        }
-                    }
-                    h[r] = (_Float16)v;
-                    if (i < w.m && j < w.mp) out[(int64_t)i * w.mp + j] = h[r];
-                }
-                if (ti != tj && j < w.m && ib < w.mp) *(f16x4*)(out + (int64_t)j * w.mp + ib) = h;
+            for (int t = 0; t < S::MT * 4; ++t) {
+                const int i = iw + t / 4 * 32 + 8 * (t % 4) + 4 * L.h + (L.c & 3), ic = i < w.m ? i : w.m - 1;
+                old[t] = *(const f16x4*)(s16 + (int64_t)ic * w.mp + (j < w.mp ? j : w.mp - 4));
+                di4[t] = ds[ic];
             }
         }
+#pragma unroll
+        for (int ii = 0; ii < S::MT; ++ii)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = ii * 32 + 8 * q + 4 * L.h, i = iw + row + (L.c & 3);
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
+                quad_turn(v);
+                const bool inside = i < w.m && j < w.mp;
+                f16x4 h;
+                if constexpr (POLY) {
+                    const float di = di4[ii * 4 + q];
+                    const f16x4 e16 = old[ii * 4 + q];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = (float)e16[e] * (1.0f / kSScale);
+                        float s2 = v[e] * (1.0f / (kSScale * kSScale)) + x * (di + dj[e]);
+                        if (i == j + e) {
+                            s2 += di * di;
+                            if (i < w.m) diag[i] = k.a + k.b * di + k.c * s2;
+                        }
+                        v[e] = i == j + e ? 0.0f : (k.b * x + k.c * s2) * k.mscale;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] *= 1.0f / (kXScale * kXScale);
+                        if (i == j + e) {
+                            if (i < w.m) diag[i] = v[e];
+                            v[e] = 0.0f;
+                        }
+                        v[e] *= kSScale;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (i >= w.m || j + e >= w.m) v[e] = 0.0f;  // rows repeated past the end
+                    h[e] = (_Float16)v[e];
+                }
+                if (inside) *(f16x4*)(out + (int64_t)i * ldo + j) = h;
+                if (inside && twice) *(f16x4*)(out + (int64_t)i * ldo + w.mp + j) = h;
+                if (ti != tj) {
+                    quad_turn(v);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = (_Float16)v[r];
+                    turner.put(L, row, h);
+                }
+            }
+        if (ti != tj) {
+            turner.flush(L, out, ldo, jw + jj * 32, iw, w.m, w.mp);
+            if (twice) turner.flush(L, out + w.mp, ldo, jw + jj * 32, iw, w.m, w.mp);
+        }
+    }
 }
 
 // X <- diag(M) X + (M - diag(M)) X, with its fp16 copies for the next step.
 template <class S>
 __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
-    __shared__ __attribute__((aligned(16))) char lds[S::LDS];
+    __shared__ __attribute__((aligned(16))) char lds[ns_lds<S>()];
     const Work& w = a.w;
     if (w.skipped()) return;
     char* base = w.of(blockIdx.y);
@@ -638,53 +710,85 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     band_tile(xcd_tile(blockIdx.x, gridDim.x), a.tiles_m, a.tiles_n, ti, tj);
     const int i0 = ti * S::TILE, j0 = tj * S::TILE;
     const char* xt = base + (a.odd ? w.xt1 : w.xt0);
-    const Operand A{base + w.m16 + (int64_t)i0 * w.mp * 2, (uint32_t)w.mp * 2, w.m - i0};
-    const Operand B{xt + (int64_t)j0 * w.mp * 2, (uint32_t)w.mp * 2, w.n - j0};
+    const Operand A{base + w.m16 + (int64_t)i0 * w.kp * 2, (uint32_t)w.kp * 2, w.m - i0};
+    const Operand B{xt + (int64_t)j0 * w.kp * 2, (uint32_t)w.kp * 2, w.n - j0};
     f32x16 acc[S::MT][S::NT];
-    MmF16 mm;
-    tile_product<S>(A, B, w.mp / 64, false, mm, lds, acc);
+    tile_product<S, MmF16>(A, B, A, B, w.kp / 64, false, lds, acc);
+    __syncthreads();  // LDS is free
 
     const Lane L;
-    const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
+    const int iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
     const float un = 1.0f / a.k.mscale;
     const float* dm = (const float*)(base + w.dm);
     float* x32 = (float*)base;
     _Float16 *x16 = (_Float16*)(base + w.x16), *next = (_Float16*)(base + (a.odd ? w.xt0 : w.xt1));
+    const bool two = w.kp > w.mp;
+    Turner<S> turner(lds, L), rest(lds + S::WAVES * Turner<S>::kBytes, L);
 #pragma unroll
-    for (int ii = 0; ii < S::MT; ++ii)
+    for (int jj = 0; jj < S::NT; ++jj) {
+        const int j = jw + jj * 32 + (L.c & ~3);
+        // X of the column block, all of it before its first use
+        f32x4 old[S::MT * 4];
+        float dm4[S::MT * 4];
 #pragma unroll
-        for (int jj = 0; jj < S::NT; ++jj) {
-            const int j = j0 + wn * S::WN + jj * 32 + L.c;
+        for (int t = 0; t < S::MT * 4; ++t) {
+            const int i = iw + t / 4 * 32 + 8 * (t % 4) + 4 * L.h + (L.c & 3), ic = i < w.m ? i : w.m - 1;
+            old[t] = *(const f32x4*)(x32 + (int64_t)ic * w.np + (j < w.np ? j : w.np - 4));
+            dm4[t] = dm[ic];
+        }
+#pragma unroll
+        for (int ii = 0; ii < S::MT; ++ii)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int ib = i0 + wm * S::WM + ii * 32 + 8 * q + 4 * L.h;
+                const int row = ii * 32 + 8 * q + 4 * L.h, i = iw + row + (L.c & 3);
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
+                quad_turn(v);
+                const bool inside = i < w.m && j < w.np;
+                const int64_t at = (int64_t)i * w.np + j;
+                f32x4 x = old[ii * 4 + q];
+                const float d = dm4[ii * 4 + q];
                 f16x4 h;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = ib + r;
-                    float v = 0.0f;
-                    if (i < w.m && j < w.np) {
-                        const int64_t at = (int64_t)i * w.np + j;
-                        // columns from n on are zero: their X^T row repeats row n - 1
-                        if (j < w.n) v = dm[i] * x32[at] + acc[ii][jj][4 * q + r] * un;
-                        x32[at] = v;
-                        if (!a.last) x16[at] = (_Float16)v;
-                    }
-                    h[r] = (_Float16)v;
+                for (int e = 0; e < 4; ++e) {
+                    // past the ends of both sides: rows repeated
+                    v[e] = inside && j + e < w.n ? d * x[e] + v[e] * un : 0.0f;
+                    x[e] = v[e];
+                    h[e] = (_Float16)v[e];
                 }
-                if (!a.last && j < w.n && ib < w.mp) *(f16x4*)(next + (int64_t)j * w.mp + ib) = h;
+                if (inside) {
+                    *(f32x4*)(x32 + at) = x;
+                    if (!a.last) *(f16x4*)(x16 + at) = h;
+                }
+                if (!a.last) {
+                    quad_turn(v);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = (_Float16)v[r];
+                    turner.put(L, row, h);
+                    if (two) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) h[r] = (_Float16)(v[r] - (float)h[r]);
+                        rest.put(L, row, h);
+                    }
+                }
             }
+        if (!a.last) {
+            turner.flush(L, next, w.kp, jw + jj * 32, iw, w.n, w.mp);
+            if (two) rest.flush(L, next + w.mp, w.kp, jw + jj * 32, iw, w.n, w.mp);
         }
+    }
 }
 
 // ---------------------------------------------------------------- host side
 constexpr int64_t kMaxSide = 65536;
 constexpr int32_t kMaxCount = 65535;
 constexpr int kNarrow = 128;  // smaller sides up to this take the strip kernels
-
-typedef Shape<256, 128, 64> Big;
-typedef Shape<128, 64, 64> Mid;
-typedef Shape<64, 32, 32> Low;
+// Up to this smaller side the product with M takes X in two fp16 parts.  The rounding
+// of X puts noise into directions that X lacks, which grows 140-fold over the
+// steps after; it averages out over a long side only (a matrix of rank one was 4e-3
+// off at 130 x 200 with one part, 2e-3 at 256 x 700).
+constexpr int kTwoParts = 512;
 
 bool narrow(int64_t rows, int64_t cols) { return rows <= kNarrow || cols <= kNarrow; }
 
@@ -700,6 +804,7 @@ Work work_of(int64_t rows, int64_t cols) {
     w.n = (int)(rows < cols ? cols : rows);
     w.mp = (int)round_up(w.m, 64);
     w.np = (int)round_up(w.n, 64);
+    w.kp = w.m <= kTwoParts ? 2 * w.mp : w.mp;
     w.parts = sum_parts(rows, cols);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -709,10 +814,10 @@ Work work_of(int64_t rows, int64_t cols) {
     };
     take((int64_t)w.m * w.np * 4);
     w.x16 = take((int64_t)w.m * w.np * 2);
-    w.xt0 = take((int64_t)w.n * w.mp * 2);
-    w.xt1 = take((int64_t)w.n * w.mp * 2);
+    w.xt0 = take((int64_t)w.n * w.kp * 2);
+    w.xt1 = take((int64_t)w.n * w.kp * 2);
     w.s16 = take((int64_t)w.m * w.mp * 2);
-    w.m16 = take((int64_t)w.m * w.mp * 2);
+    w.m16 = take((int64_t)w.m * w.kp * 2);
     w.ds = take((int64_t)w.m * 4);
     w.dm = take((int64_t)w.m * 4);
     w.sums = take((int64_t)w.parts * 8);
@@ -781,26 +886,34 @@ Coeffs coeffs_of(const zero_newton_schulz& ns) {
     return k;
 }
 
-template <class S>
-int steps_with(const Work& w, const Coeffs& k, int32_t count, int steps, hipStream_t s, const char* what) {
-    int rc = ZERO_OK;
-    const int tm = (int)ceil_div(w.m, S::TILE), tn = (int)ceil_div(w.np, S::TILE);
-    StepArgs a{w, k, tm, tn, 0, 0};
-    const dim3 square((unsigned)(tm * (tm + 1) / 2), (unsigned)count), whole((unsigned)(tm * tn), (unsigned)count);
+// The steps of a large stack: three launches each.
+int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStream_t s, const char* what) {
+    auto square_tiles = [&](int64_t t) { return count * (ceil_div(w.m, t) * (ceil_div(w.m, t) + 1) / 2); };
+    auto whole_tiles = [&](int64_t t) { return count * ceil_div(w.m, t) * ceil_div(w.np, t); };
+    const int square = pick_tile(square_tiles), whole = pick_tile(whole_tiles);
+    StepArgs a{w, k, 0, 0, 0, 0};
+    auto squares = [&](auto poly) {
+        return with_tile(square, [&](auto shape) {
+            typedef decltype(shape) S;
+            const dim3 grid((unsigned)(square_tiles(S::TILE) / count), (unsigned)count);
+            return launch(ns_square_kernel<S, decltype(poly)::value>, grid, S::THREADS, s, a, what);
+        });
+    };
     for (int i = 0; i < steps; ++i) {
         a.odd = i & 1;
         a.last = i + 1 == steps;
-        if ((rc = launch(ns_square_kernel<S, false>, square, S::THREADS, s, a, what)) != ZERO_OK) return rc;
-        if ((rc = launch(ns_square_kernel<S, true>, square, S::THREADS, s, a, what)) != ZERO_OK) return rc;
-        if ((rc = launch(ns_apply_kernel<S>, whole, S::THREADS, s, a, what)) != ZERO_OK) return rc;
+        int rc;
+        if ((rc = squares(std::false_type())) != ZERO_OK || (rc = squares(std::true_type())) != ZERO_OK) return rc;
+        rc = with_tile(whole, [&](auto shape) {
+            typedef decltype(shape) S;
+            a.tiles_m = (int)ceil_div(w.m, S::TILE);
+            a.tiles_n = (int)ceil_div(w.np, S::TILE);
+            return launch(ns_apply_kernel<S>, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)count), S::THREADS, s, a,
+                          what);
+        });
+        if (rc != ZERO_OK) return rc;
     }
-    return rc;
-}
-
-// Tiles of a stack's symmetric products at a tile side.
-int64_t square_tiles(const Work& w, int32_t count, int tile) {
-    const int64_t t = ceil_div(w.m, tile);
-    return count * (t * (t + 1) / 2);
+    return ZERO_OK;
 }
 
 template <class IO>
@@ -848,13 +961,7 @@ int run_stack(const IO& io, int32_t count, const zero_newton_schulz& ns, const i
     // patches cover the padding of both orientations
     const dim3 patches((unsigned)ceil_div(io.cols, kPatch), (unsigned)ceil_div(io.rows, kPatch), (unsigned)count);
     if ((rc = launch(ns_begin_kernel<IO>, patches, 256, s, a, what)) != ZERO_OK) return rc;
-    if (square_tiles(w, count, 256) >= 256)
-        rc = steps_with<Big>(w, k, count, ns.steps, s, what);
-    else if (square_tiles(w, count, 128) >= 256)
-        rc = steps_with<Mid>(w, k, count, ns.steps, s, what);
-    else
-        rc = steps_with<Low>(w, k, count, ns.steps, s, what);
-    if (rc != ZERO_OK) return rc;
+    if ((rc = run_steps(w, k, count, ns.steps, s, what)) != ZERO_OK) return rc;
     return launch(ns_end_kernel<IO>, patches, 256, s, a, what);
 }
 
