@@ -161,26 +161,42 @@ __device__ __forceinline__ f16x8 small_frag(const char* a, int row, int kk, int 
     return *(const f16x8*)(a + small_at<T>(row, kk * 16 + h * 8));
 }
 
-// acc += A B^T of two pairs, the product of the two rests left out: a wave's CT tiles
-// from row i0, columns j0, + 32, ...
+// acc += A B^T of two pairs over the first `pieces` 16 columns, the product of the
+// two rests left out: a wave's CT tiles from row i0, columns j0, + 32, ...  The next
+// k step's fragments are read while one multiplies.
 template <int T, int CT>
-__device__ __forceinline__ void small_product(const Pair& A, const Pair& B, int i0, int j0, const Lane& L,
-                                              f32x16 (&acc)[CT]) {
-#pragma unroll
-    for (int kk = 0; kk < T / 16; ++kk) {
-        const f16x8 ah = small_frag<T>(A.hi, i0 + L.c, kk, L.h), al = small_frag<T>(A.lo, i0 + L.c, kk, L.h);
-        f16x8 bh[CT], bl[CT];
+struct SmallFrags {
+    f16x8 ah, al, bh[CT], bl[CT];
+    __device__ __forceinline__ void load(const Pair& A, const Pair& B, int i0, int j0, int kk, const Lane& L) {
+        ah = small_frag<T>(A.hi, i0 + L.c, kk, L.h);
+        al = small_frag<T>(A.lo, i0 + L.c, kk, L.h);
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             bh[t] = small_frag<T>(B.hi, j0 + 32 * t + L.c, kk, L.h);
             bl[t] = small_frag<T>(B.lo, j0 + 32 * t + L.c, kk, L.h);
         }
+    }
+    __device__ __forceinline__ void multiply(f32x16 (&acc)[CT]) const {
 #pragma unroll
         for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh[t], acc[t], 0, 0, 0);
 #pragma unroll
         for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl[t], acc[t], 0, 0, 0);
 #pragma unroll
         for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh[t], acc[t], 0, 0, 0);
+    }
+};
+
+template <int T, int CT>
+__device__ __forceinline__ void small_product(const Pair& A, const Pair& B, int i0, int j0, int pieces, const Lane& L,
+                                              f32x16 (&acc)[CT]) {
+    SmallFrags<T, CT> f, g;
+    f.load(A, B, i0, j0, 0, L);
+#pragma unroll 1
+    for (int kk = 0; kk < pieces; kk += 2) {  // an odd one more meets zeros; past the end the first is read again
+        g.load(A, B, i0, j0, kk + 1, L);
+        f.multiply(acc);
+        f.load(A, B, i0, j0, (kk + 2) % (T / 16), L);
+        g.multiply(acc);
     }
 }
 
@@ -227,12 +243,16 @@ struct StripWave {
     StripLds<P>& lds;
     Pair mine, square;
 
-    __device__ StripWave(StripLds<P>& s) : lds(s) {
+    int side, live;  // 16-column pieces of the smaller side; whether this wave's rows have any
+
+    __device__ StripWave(StripLds<P>& s, int m) : lds(s) {
         group = L.wave / P::GROUP;
         i0 = L.wave % P::GROUP / P::TILES * 32;
         j0 = L.wave % P::TILES * 32 * CT;
         mine = {s.block + group * 2 * P::ARRAY, s.block + (group * 2 + 1) * P::ARRAY};
         square = {s.square, s.square + P::ARRAY};
+        side = (m + 15) / 16;
+        live = i0 < m;
     }
     __device__ __forceinline__ int row(int r) const { return i0 + 8 * (r / 4) + 4 * L.h + r % 4; }
     __device__ __forceinline__ int at(int t) const { return j0 + 32 * t + L.c; }  // column within a block
@@ -243,11 +263,12 @@ struct StripWave {
         for (int t = 0; t < CT; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[t][r] = 0.0f;
-        small_product<T, CT>(A, B, i0, j0, L, acc);
+        if (live) small_product<T, CT>(A, B, i0, j0, side, L, acc);
     }
 
     // This wave's tiles of S = X X^T of the strip's first nb blocks of every group.
-    __device__ __forceinline__ void gram(const Tiles (&x)[P::NB], int nb, Tiles& s) {
+    // cols: the strip's columns.
+    __device__ __forceinline__ void gram(const Tiles (&x)[P::NB], int nb, int cols, Tiles& s) {
         f32x16 acc[CT];
 #pragma unroll
         for (int t = 0; t < CT; ++t)
@@ -259,7 +280,8 @@ struct StripWave {
             __syncthreads();  // the block's last readers are done
             small_store<T, CT, false>(mine, i0, j0, L, x[b]);
             __syncthreads();
-            small_product<T, CT>(mine, mine, i0, j0, L, acc);
+            const int left = cols - (b * P::G + group) * T, k = left < T ? left : T;
+            if (live && k > 0) small_product<T, CT>(mine, mine, i0, j0, (k + 15) / 16, L, acc);
         }
 #pragma unroll
         for (int t = 0; t < CT; ++t)
@@ -373,10 +395,10 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     __shared__ StripLds<P> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
     const IO& io = a.io;
-    StripWave<P> w(lds);
     const int b = blockIdx.x;
     const bool tall = io.rows > io.cols;
     const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
+    StripWave<P> w(lds, m);
     const int nb = (n + P::G * P::T - 1) / (P::G * P::T);
     const float clip = io.clip();
     typename StripWave<P>::Tiles x[P::NB], s, mv;
@@ -391,7 +413,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     w.forget();
 #pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
-        w.gram(x, nb, s);
+        w.gram(x, nb, n, s);
         w.poly(a.k, s, mv);
         if (w.group == 0) small_store<P::T, P::CT, true>(w.square, w.i0, w.j0, w.L, mv);
         w.apply(a.k, nb, x);
@@ -408,7 +430,7 @@ __global__ void __launch_bounds__(P::GROUP * 64) ns_poly_kernel(StripArgs<IO> a)
     typedef Strip<P::T, P::CT, 1, 1> One;
     __shared__ StripLds<One> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
-    StripWave<One> w(lds);
+    StripWave<One> w(lds, a.io.rows < a.io.cols ? a.io.rows : a.io.cols);
     char* ws = a.ws + blockIdx.x * a.stride;
     const float* parts = (const float*)(ws + a.parts);
     typename StripWave<One>::Tiles s, mv;
@@ -428,10 +450,10 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     __shared__ StripLds<P> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
     const IO& io = a.io;
-    StripWave<P> w(lds);
     const int b = blockIdx.y, strip = blockIdx.x, j0 = strip * P::COLS;
     const bool tall = io.rows > io.cols;
     const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
+    StripWave<P> w(lds, m);
     const int left = n - j0 < P::COLS ? n - j0 : P::COLS, nb = (left + P::G * P::T - 1) / (P::G * P::T);
     char* ws = a.ws + b * a.stride;
     float* mine = (float*)ws + (int64_t)strip * P::SIZE + w.L.wave * (P::NB * P::CT * 1024) + w.L.lane;
@@ -465,7 +487,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
         return;
     }
     w.each([&](int bl, int t, int r, int, int) { mine[((bl * P::CT + t) * 16 + r) * 64] = x[bl][t][r]; });
-    w.gram(x, nb, s);
+    w.gram(x, nb, left, s);
     float* part = (float*)(ws + a.parts) + (int64_t)strip * P::T * P::T;
     if (w.group == 0) {
 #pragma unroll
