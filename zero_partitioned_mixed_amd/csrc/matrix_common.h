@@ -78,12 +78,15 @@ __device__ __forceinline__ typename Elem<DT>::type from_float(float x) {
 constexpr int kSlab = 128;  // bytes of every row per slab
 
 // A tile of TILE x TILE outputs by waves of WM x WN outputs each, with STAGES slabs
-// in LDS: STAGES - 1 on their way while one is used.
-template <int TILE_, int WM_, int WN_, int STAGES_>
+// in LDS: STAGES - 1 on their way while one is used.  KS such groups of waves take
+// the slabs in turn, each with its own slabs in LDS, and add their sums at the
+// end: for tiles that have a CU to themselves, where one group leaves
+// the matrix cores waiting for LDS half of the time.
+template <int TILE_, int WM_, int WN_, int STAGES_, int KS_ = 1>
 struct Shape {
-    static constexpr int TILE = TILE_, WM = WM_, WN = WN_, STAGES = STAGES_;
-    static constexpr int WAVES = (TILE / WM) * (TILE / WN);
-    static constexpr int THREADS = WAVES * 64;
+    static constexpr int TILE = TILE_, WM = WM_, WN = WN_, STAGES = STAGES_, KS = KS_;
+    static constexpr int WAVES = (TILE / WM) * (TILE / WN);  // of a group
+    static constexpr int THREADS = KS * WAVES * 64;
     static constexpr int MT = WM / 32, NT = WN / 32;
     static constexpr int LOADS = 2 * TILE / 8 / WAVES;    // direct loads (8 rows each) per wave and slab
     static constexpr int SCALES = 4 * TILE / 64 / WAVES;  // direct loads of block scales, 4-bit operands
@@ -104,6 +107,7 @@ struct Lane {
     __device__ Lane()
         : lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), h(lane >> 5),
           c(lane & 31) {}
+    __device__ explicit Lane(int of) : Lane() { wave %= of; }  // wave within a group of `of`
 };
 
 // Bytes straight to LDS: lane l's 16 (or 4) go to `to` + 16 l (or 4 l).
@@ -150,7 +154,7 @@ struct MmFp4 {
 // Bytes of LDS of a product.
 template <class S, class MM>
 constexpr int product_lds() {
-    return S::STAGES * (S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0));
+    return S::KS * S::STAGES * (S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0));
 }
 
 // One k step's fragments of a wave's rows and columns.
@@ -178,11 +182,14 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MT][S::NT], const Frag
 // operands) half a slab if `half`.  Element r of acc[i][j] is output row
 // wm * WM + 32 i + 8 (r / 4) + 4 h + r % 4, column wn * WN + 32 j + c.
 // SA and SB: the scales' rows (4-bit operands).  lds: product_lds bytes, free for
-// other use once every wave has returned.
+// other use once every wave has returned and met.  True for the waves that hold
+// the result (the first group).
 template <class S, class MM>
-__device__ __forceinline__ void tile_product(const Operand& A, const Operand& B, const Operand& SA, const Operand& SB,
+__device__ __forceinline__ bool tile_product(const Operand& A, const Operand& B, const Operand& SA, const Operand& SB,
                                              int slabs, bool half, char* lds, f32x16 (&acc)[S::MT][S::NT]) {
-    const Lane L;
+    const Lane L(S::WAVES);
+    const int group = S::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (S::WAVES * 64));
+    char* const all = lds;
     const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
 #pragma unroll
     for (int i = 0; i < S::MT; ++i)
@@ -250,51 +257,96 @@ __device__ __forceinline__ void tile_product(const Operand& A, const Operand& B,
         }
     };
 
-    for (int s = 0; s < S::STAGES - 1 && s < total; ++s) stage(s, lds + s * kStage, 4);
+    lds += group * S::STAGES * kStage;
+    // round t of this group: slab t * KS + group
+    const int rounds = (slabs + S::KS - 1) / S::KS;
+    auto slab_of = [&](int t) { return t * S::KS + group; };
+    for (int t = 0; t < S::STAGES - 1; ++t)
+        if (slab_of(t) < total) stage(slab_of(t), lds + t * kStage, 4);
     char* const end = lds + S::STAGES * kStage;
     char *buf = lds, *fill = lds + (S::STAGES - 1) * kStage;
     auto after = [&](char* b) { return b + kStage == end ? lds : b + kStage; };
-    for (int s = 0; s < slabs; ++s) {
-        // slab s has landed in every wave's part, and the buffer used before it is free
-        if (s + S::STAGES - 2 < total)
+    for (int t = 0; t < rounds; ++t) {
+        // this round's slab has landed in every wave's part, and the buffer used before it is free
+        if (slab_of(t + S::STAGES - 2) < total)
             wait_and_meet<(S::STAGES - 2) * (S::LOADS + kScaleLoads)>();
         else
             wait_and_meet<0>();
-        const bool more = s + S::STAGES - 1 < total;
-        const int ahead = s + S::STAGES - 1;
-        uint32_t sa[S::MT], sb[S::NT];
-        scales(buf, 0, sa, sb);
-        const char *ra = buf + fa, *rb = buf + fb;
-        const int slot = (4 * L.h) ^ turn;
-        Frags<S> f[2];
-        f[0].load(ra, rb, (slot ^ 0) << 4);
-        if (more) stage(ahead, fill, 0);
-        f[1].load(ra, rb, (slot ^ 1) << 4);
-        multiply<S, MM, 0>(acc, f[0], sa, sb);
-        if (more) stage(ahead, fill, 1);
-        f[0].load(ra, rb, (slot ^ 2) << 4);
-        multiply<S, MM, 1>(acc, f[1], sa, sb);
-        if (more) stage(ahead, fill, 2);
-        f[1].load(ra, rb, (slot ^ 3) << 4);
-        multiply<S, MM, 2>(acc, f[0], sa, sb);
-        if (more) stage(ahead, fill, 3);
-        multiply<S, MM, 3>(acc, f[1], sa, sb);
+        const int slab = slab_of(t), ahead = slab_of(t + S::STAGES - 1);
+        const bool more = ahead < total;
+        if (S::KS == 1 || slab < slabs) {
+            uint32_t sa[S::MT], sb[S::NT];
+            scales(buf, 0, sa, sb);
+            const char *ra = buf + fa, *rb = buf + fb;
+            const int slot = (4 * L.h) ^ turn;
+            Frags<S> f[2];
+            f[0].load(ra, rb, (slot ^ 0) << 4);
+            if (more) stage(ahead, fill, 0);
+            f[1].load(ra, rb, (slot ^ 1) << 4);
+            multiply<S, MM, 0>(acc, f[0], sa, sb);
+            if (more) stage(ahead, fill, 1);
+            f[0].load(ra, rb, (slot ^ 2) << 4);
+            multiply<S, MM, 1>(acc, f[1], sa, sb);
+            if (more) stage(ahead, fill, 2);
+            f[1].load(ra, rb, (slot ^ 3) << 4);
+            multiply<S, MM, 2>(acc, f[0], sa, sb);
+            if (more) stage(ahead, fill, 3);
+            multiply<S, MM, 3>(acc, f[1], sa, sb);
+        }
         buf = after(buf);
         fill = after(fill);
     }
     if constexpr (MM::kScaled) {
-        if (!half) return;
-        wait_and_meet<0>();
-        uint32_t sa[S::MT], sb[S::NT];
-        scales(buf, 16 * L.h, sa, sb);  // group h takes blocks 2h and 2h + 1 of four
-        const char *ra = buf + fa, *rb = buf + fb;
-        const int slot = (2 * L.h) ^ turn;
-        Frags<S> f[2];
-        f[0].load(ra, rb, (slot ^ 0) << 4);
-        f[1].load(ra, rb, (slot ^ 1) << 4);
-        multiply<S, MM, 0>(acc, f[0], sa, sb);
-        multiply<S, MM, 1>(acc, f[1], sa, sb);
+        if (half) {
+            wait_and_meet<0>();
+            if (S::KS == 1 || group == slabs % S::KS) {
+                buf = lds + slabs / S::KS % S::STAGES * kStage;
+                uint32_t sa[S::MT], sb[S::NT];
+                scales(buf, 16 * L.h, sa, sb);  // group h takes blocks 2h and 2h + 1 of four
+                const char *ra = buf + fa, *rb = buf + fb;
+                const int slot = (2 * L.h) ^ turn;
+                Frags<S> f[2];
+                f[0].load(ra, rb, (slot ^ 0) << 4);
+                f[1].load(ra, rb, (slot ^ 1) << 4);
+                multiply<S, MM, 0>(acc, f[0], sa, sb);
+                multiply<S, MM, 1>(acc, f[1], sa, sb);
+            }
+        }
     }
+    if constexpr (S::KS > 1) {
+        static_assert((S::KS - 1) * S::TILE * S::TILE * 4 <= product_lds<S, MM>(), "the groups' sums fit");
+        __syncthreads();
+        float* mine = (float*)all + (group - 1) * S::TILE * S::TILE + L.wave * S::MT * S::NT * 1024 + L.lane * 4;
+#pragma unroll
+        for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f32x4 v;
+                    float* at = mine + ((i * S::NT + j) * 4 + q) * 256;
+                    if (group > 0) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r];
+                        *(f32x4*)at = v;
+                    }
+                }
+        __syncthreads();
+        if (group > 0) return false;
+#pragma unroll
+        for (int g = 1; g < S::KS; ++g)
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = *(const f32x4*)(mine + g * S::TILE * S::TILE + ((i * S::NT + j) * 4 + q) * 256);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
+                    }
+    }
+    return true;
 }
 
 // Turns the 4 x 4 values of four neighbouring lanes: v[r] of lane t <-> v[t] of lane r.
@@ -394,12 +446,13 @@ int launch(void (*kernel)(Args), dim3 grid, int block, hipStream_t s, const Args
 }
 
 // The shapes in use: (tile, wave rows, wave columns, slabs in LDS).
-typedef Shape<256, 64, 128, 2> Tile256;
+typedef Shape<256, 128, 128, 2> Tile256;
 typedef Shape<192, 96, 96, 3> Tile192;
 typedef Shape<128, 64, 64, 2> Tile128;      // two workgroups on a CU
 typedef Shape<128, 64, 64, 3> Tile128Few;   // at most one workgroup for a CU
-typedef Shape<64, 32, 32, 2> Tile64;
-typedef Shape<64, 32, 32, 4> Tile64Few;
+typedef Shape<64, 32, 32, 2> Tile64;        // four
+typedef Shape<64, 32, 32, 4> Tile64Two;     // two
+typedef Shape<64, 32, 32, 3, 2> Tile64Few;  // at most one: 16 against 21 us with one group (1024 x 1024 x 4096)
 
 // The shape that a product takes, by the tiles it has at each: microseconds a slab
 // as measured (fp16, 256 CUs, tiles of 4096 long rows) times the rounds that the
@@ -409,14 +462,15 @@ typedef Shape<64, 32, 32, 4> Tile64Few;
 template <class F>
 int pick_tile(F tiles) {
     const int64_t t256 = tiles(256), t192 = tiles(192), t128 = tiles(128), t64 = tiles(64);
-    const double cost[6] = {2.05 * (double)ceil_div(t256, 256),
-                            1.20 * (double)ceil_div(t192, 256),
+    const double cost[7] = {1.93 * (double)ceil_div(t256, 256),
+                            1.17 * (double)ceil_div(t192, 256),
                             1.14 * (double)ceil_div(t128, 512),
                             0.61 * (double)ceil_div(t128, 256),
                             0.81 * (double)ceil_div(t64, 1024),
-                            0.31 * (double)ceil_div(t64, 256)};
+                            0.46 * (double)ceil_div(t64, 512),
+                            0.25 * (double)ceil_div(t64, 256)};
     int k = 0;
-    for (int i = 1; i < 6; ++i)
+    for (int i = 1; i < 7; ++i)
         if (cost[i] < cost[k]) k = i;
     return k;
 }
@@ -429,6 +483,7 @@ int with_tile(int pick, F f) {
         case 2: return f(Tile128());
         case 3: return f(Tile128Few());
         case 4: return f(Tile64());
+        case 5: return f(Tile64Two());
         default: return f(Tile64Few());
     }
 }

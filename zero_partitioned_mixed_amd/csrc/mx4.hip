@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(S::THREADS) mx4_matmul_kernel(MatmulArgs g) {
     const Operand A{(const char*)g.a + i0 * ld, ld, rows_a}, B{(const char*)g.b + j0 * ld, ld, rows_b};
     const Operand SA{(const char*)g.sa + i0 * ls, ls, rows_a}, SB{(const char*)g.sb + j0 * ls, ls, rows_b};
     f32x16 acc[S::MT][S::NT];
-    tile_product<S, MmFp4>(A, B, SA, SB, (int)(g.p / 256), g.p % 256 != 0, lds, acc);
+    if (!tile_product<S, MmFp4>(A, B, SA, SB, (int)(g.p / 256), g.p % 256 != 0, lds, acc)) return;
 
     typedef typename Elem<DT>::type T;
-    const Lane L;
+    const Lane L(S::WAVES);
     const int64_t iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
 #pragma unroll
     for (int ii = 0; ii < S::MT; ++ii)

@@ -636,10 +636,11 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     const Operand A{from + (int64_t)i0 * ld * 2, (uint32_t)ld * 2, w.m - i0};
     const Operand B{from + (int64_t)j0 * ld * 2, (uint32_t)ld * 2, w.m - j0};
     f32x16 acc[S::MT][S::NT];
-    tile_product<S, MmF16>(A, B, A, B, ld / 64, false, lds, acc);
+    const bool holds = tile_product<S, MmF16>(A, B, A, B, ld / 64, false, lds, acc);
     __syncthreads();  // LDS is free
+    if (!holds) return;
 
-    const Lane L;
+    const Lane L(S::WAVES);
     const int iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
     const Coeffs& k = a.k;
     float* diag = (float*)(base + (POLY ? w.dm : w.ds));
@@ -735,10 +736,11 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     const Operand A{base + w.m16 + (int64_t)i0 * w.kp * 2, (uint32_t)w.kp * 2, w.m - i0};
     const Operand B{xt + (int64_t)j0 * w.kp * 2, (uint32_t)w.kp * 2, w.n - j0};
     f32x16 acc[S::MT][S::NT];
-    tile_product<S, MmF16>(A, B, A, B, w.kp / 64, false, lds, acc);
+    const bool holds = tile_product<S, MmF16>(A, B, A, B, w.kp / 64, false, lds, acc);
     __syncthreads();  // LDS is free
+    if (!holds) return;
 
-    const Lane L;
+    const Lane L(S::WAVES);
     const int iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
     const float un = 1.0f / a.k.mscale;
     const float* dm = (const float*)(base + w.dm);
