@@ -699,12 +699,35 @@ int zero_mx4_matmul(const void *a_codes_dev, const void *a_scales_dev, const voi
 /* zero_mx4_matmul with A given as values (ZERO_F16, ZERO_BF16 or ZERO_F32, row
  * stride lda) and quantised on the way in, for the few rows of single tokens:
  * equal to zero_mx4_quantize and zero_mx4_matmul.  m is at most
- * ZERO_MX4_ROWS_MAX. */
+ * ZERO_MX4_ROWS_MAX.  No workspace is needed up to m = 32 where m times the padded
+ * k is at most 16384. */
 #define ZERO_MX4_ROWS_MAX 64
 size_t zero_mx4_matmul_rows_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int zero_mx4_matmul_rows(const void *a_dev, int32_t a_dtype, int64_t lda, const void *b_codes_dev,
                          const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,
                          int32_t c_dtype, int64_t ldc, void *ws_dev, size_t ws_bytes,
+                         void *stream);
+
+/* A linear layer whose three products take MXFP4 operands, each quantised along the
+ * dimension that the product sums over:
+ *     y = x w^T,  dx = dy w,  dw = dy^T x
+ * x is tokens x k, w n x k, y and dy tokens x n; all of one dtype (ZERO_F16,
+ * ZERO_BF16 or ZERO_F32), each with its row stride in elements.  The forward
+ * call reads x and w once and also leaves what the gradients need: x_t and w_t,
+ * the operands of x^T and w^T (k x tokens and k x n), each one buffer of
+ * zero_mx4_operand_bytes; either may be NULL.  dx needs w_t and dw x_t; either
+ * gradient may be NULL.  The rounding to 4 bits is passed through.  Sizes are
+ * at least 1.  Errors: EINVAL, EALIGN (matrices to their elements, the rest to
+ * 16 bytes), ERANGE, ESPACE. */
+size_t zero_mx4_operand_bytes(int64_t rows, int64_t cols);
+size_t zero_mx4_linear_workspace_bytes(int64_t tokens, int64_t n, int64_t k);
+int zero_mx4_linear(const void *x_dev, int64_t ldx, const void *w_dev, int64_t ldw, int32_t dtype,
+                    int64_t tokens, int64_t n, int64_t k, void *y_dev, int64_t ldy, void *x_t_dev,
+                    void *w_t_dev, void *ws_dev, size_t ws_bytes, void *stream);
+size_t zero_mx4_linear_grad_workspace_bytes(int64_t tokens, int64_t n);
+int zero_mx4_linear_grad(const void *dy_dev, int64_t lddy, int32_t dtype, int64_t tokens, int64_t n,
+                         int64_t k, const void *x_t_dev, const void *w_t_dev, void *dx_dev,
+                         int64_t lddx, void *dw_dev, int64_t lddw, void *ws_dev, size_t ws_bytes,
                          void *stream);
 
 /* Message for the last nonzero return on the calling thread ("" if none). */

@@ -118,7 +118,7 @@ def test_matmul_refuses(Z, kw, code):
     (dict(adt=0), EINVAL), (dict(a=None), EINVAL), (dict(b=None), EINVAL), (dict(ws=None), EINVAL), (dict(a=P + 1), EALIGN),
     (dict(ws=P + 4), EALIGN), (dict(m=65), ERANGE), (dict(lda=63), ERANGE), (dict(wsb=1), ESPACE)])
 def test_matmul_rows_refuses(Z, kw, code):
-    a = dict(a=P, adt=BF16, lda=64, b=P, sb=P, m=8, n=8, k=64, c=P, cdt=BF16, ldc=8, ws=P, wsb=1 << 40)
+    a = dict(a=P, adt=BF16, lda=4096, b=P, sb=P, m=8, n=8, k=4096, c=P, cdt=BF16, ldc=8, ws=P, wsb=1 << 40)
     a.update(kw)
     assert Z._lib.zero_mx4_matmul_rows(a["a"], a["adt"], a["lda"], a["b"], a["sb"], a["m"], a["n"], a["k"], a["c"], a["cdt"],
                                        a["ldc"], a["ws"], a["wsb"], None) == code
@@ -134,3 +134,41 @@ def test_cpu_tensors_refused(Z):
             call()
     with pytest.raises(ValueError):
         Z.MX4(torch.zeros(4, 31, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 4, 64)
+
+
+def linear(Z, x=P, ldx=64, w=P, ldw=64, dt=BF16, t=8, n=16, k=64, y=P, ldy=16, xt=P, wt=P, ws=P, wsb=1 << 40):
+    return Z._lib.zero_mx4_linear(x, ldx, w, ldw, dt, t, n, k, y, ldy, xt, wt, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=0), EINVAL), (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(y=None), EINVAL), (dict(ws=None), EINVAL),
+    (dict(x=P + 1), EALIGN), (dict(y=P + 1), EALIGN), (dict(xt=P + 8), EALIGN), (dict(ws=P + 8), EALIGN), (dict(ldx=63), ERANGE),
+    (dict(ldw=63), ERANGE), (dict(ldy=15), ERANGE), (dict(t=0), ERANGE), (dict(k=0), ERANGE), (dict(n=-1), ERANGE),
+    (dict(wsb=100), ESPACE)])
+def test_linear_refuses(Z, kw, code):
+    assert linear(Z, **kw) == code
+    assert "zero_mx4_linear" in Z.zero_last_error()
+
+
+def grad(Z, dy=P, ld=16, dt=BF16, t=8, n=16, k=64, xt=P, wt=P, dx=P, ldx=64, dw=P, ldw=64, ws=P, wsb=1 << 40):
+    return Z._lib.zero_mx4_linear_grad(dy, ld, dt, t, n, k, xt, wt, dx, ldx, dw, ldw, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=5), EINVAL), (dict(dy=None), EINVAL), (dict(xt=None), EINVAL), (dict(wt=None), EINVAL), (dict(ws=None), EINVAL),
+    (dict(dy=P + 1), EALIGN), (dict(dw=P + 1), EALIGN), (dict(wt=P + 4), EALIGN), (dict(ld=15), ERANGE), (dict(ldx=63), ERANGE),
+    (dict(ldw=1), ERANGE), (dict(t=0), ERANGE), (dict(wsb=8), ESPACE)])
+def test_linear_grad_refuses(Z, kw, code):
+    assert grad(Z, **kw) == code
+    assert "zero_mx4_linear_grad" in Z.zero_last_error()
+
+
+def test_linear_grad_of_nothing(Z):
+    assert grad(Z, dx=None, dw=None, xt=None, wt=None, ws=None, wsb=0) == 0
+
+
+def test_operand_sizes(Z):
+    assert Z._lib.zero_mx4_operand_bytes(3, 129) == 512 + 256
+    assert Z._lib.zero_mx4_operand_bytes(0, 129) == 0 == Z._lib.zero_mx4_operand_bytes(1, 1 << 25)
+    assert Z._lib.zero_mx4_matmul_rows_workspace_bytes(1, 100, 4096) == 0
+    assert Z._lib.zero_mx4_matmul_rows_workspace_bytes(64, 100, 4096) > 64 * 2048

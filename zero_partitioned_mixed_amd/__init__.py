@@ -193,6 +193,13 @@ _sig = {
     "zero_mx4_matmul_rows_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "zero_mx4_matmul_rows": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i32,
                                             _i64, _vp, ctypes.c_size_t, _vp]),
+    "zero_mx4_operand_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_mx4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "zero_mx4_linear": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64, _vp,
+                                       _vp, _vp, ctypes.c_size_t, _vp]),
+    "zero_mx4_linear_grad_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_mx4_linear_grad": (ctypes.c_int, [_vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i64,
+                                            _vp, _i64, _vp, ctypes.c_size_t, _vp]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 for _name, (_res, _args) in _sig.items():

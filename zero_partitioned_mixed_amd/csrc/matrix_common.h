@@ -178,176 +178,199 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MT][S::NT], const Frag
         for (int j = 0; j < S::NT; ++j) acc[i][j] = MM::template mma<KK>(f.a[i], f.b[j], acc[i][j], sa[i], sb[j]);
 }
 
-// acc = the wave's part of the tile over `slabs` whole slabs, then (4-bit
-// operands) half a slab if `half`.  Element r of acc[i][j] is output row
-// wm * WM + 32 i + 8 (r / 4) + 4 h + r % 4, column wn * WN + 32 j + c.
-// SA and SB: the scales' rows (4-bit operands).  lds: product_lds bytes, free for
-// other use once every wave has returned and met.  True for the waves that hold
-// the result (the first group).
+// The product of one tile after another.  A tile is `slabs` whole slabs and then
+// (4-bit operands) half a slab if `half`.
+//   Product<S, MM> p(lds, slabs, half);
+//   p.tile(A, B, SA, SB);  its operands, SA and SB their scales' rows (4-bit)
+//   p.ahead();             its first loads: LDS has no readers any more
+//   p.run(acc);            acc = the wave's part of the tile
+// Element r of acc[i][j] is output row wm * WM + 32 i + 8 (r / 4) + 4 h + r % 4, column
+// wn * WN + 32 j + c.  run() is true for the waves that hold the result (the first
+// group); LDS (product_lds bytes) is free once all waves have met after it.
 template <class S, class MM>
-__device__ __forceinline__ bool tile_product(const Operand& A, const Operand& B, const Operand& SA, const Operand& SB,
-                                             int slabs, bool half, char* lds, f32x16 (&acc)[S::MT][S::NT]) {
-    const Lane L(S::WAVES);
-    const int group = S::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (S::WAVES * 64));
-    char* const all = lds;
-    const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
-#pragma unroll
-    for (int i = 0; i < S::MT; ++i)
-#pragma unroll
-        for (int j = 0; j < S::NT; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    const int total = slabs + (MM::kScaled && half ? 1 : 0);
-    // this wave's direct loads: groups of 8 rows, all of one operand
-    const int g0 = L.wave * S::LOADS;
-    const bool is_a = g0 < S::TILE / 8;
-    const char* base = is_a ? A.base : B.base;
-    const uint32_t ld = is_a ? A.ld : B.ld;
-    const int last = (is_a ? A.rows : B.rows) - 1;
-    const int row0 = (is_a ? g0 : g0 - S::TILE / 8) * 8 + (L.lane >> 3);
+struct Product {
+    static constexpr int kScaleLoads = MM::kScaled ? S::SCALES : 0;
+    static constexpr int kStage = S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0);
+    const Lane L;
+    const int group, slabs, total;
+    const bool half;
+    char *const all, *const lds;  // the workgroup's LDS, the group's part of it
+    const char* base;             // this wave's operand
     uint32_t off[S::LOADS];
-    bool upper[S::LOADS];  // a piece of the slab's second half
-#pragma unroll
-    for (int i = 0; i < S::LOADS; ++i) {
-        const int row = row0 + i * 8;
-        const uint32_t piece = (L.lane & 7) ^ ((row >> 1) & 7);
-        off[i] = (uint32_t)(row < last ? row : last) * ld + piece * 16;
-        upper[i] = piece >= 4;
-    }
-    // and of scales: dword h * 2 TILE + row of the two operands' rows
-    constexpr int kScaleLoads = MM::kScaled ? S::SCALES : 0;
     const char* scale_base[kScaleLoads + 1];
-    uint32_t scale_off[kScaleLoads + 1], scale_h[kScaleLoads + 1];
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-        const int first = (L.wave * S::SCALES + i) * 64, h = first / (2 * S::TILE), r = first % (2 * S::TILE);
-        const Operand& O = r < S::TILE ? SA : SB;
-        const int row = (r < S::TILE ? r : r - S::TILE) + L.lane;
-        scale_base[i] = O.base;
-        scale_off[i] = (uint32_t)(row < O.rows - 1 ? row : O.rows - 1) * O.ld;
-        scale_h[i] = 4 * h;
+    uint32_t scale_off[kScaleLoads + 1];
+
+    __device__ __forceinline__ Product(char* shared, int slabs_, bool half_)
+        : L(S::WAVES),
+          group(S::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (S::WAVES * 64))),
+          slabs(slabs_),
+          total(slabs_ + (MM::kScaled && half_ ? 1 : 0)),
+          half(half_),
+          all(shared),
+          lds(shared + group * S::STAGES * kStage) {}
+
+    // This wave's direct loads: groups of 8 rows, all of one operand.
+    __device__ __forceinline__ int first_load() const { return L.wave * S::LOADS; }
+    __device__ __forceinline__ int row_of(int i) const {
+        const int g0 = first_load();
+        return (g0 < S::TILE / 8 ? g0 : g0 - S::TILE / 8) * 8 + (L.lane >> 3) + i * 8;
     }
-    constexpr int kStage = S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0);
+    __device__ __forceinline__ uint32_t piece_of(int i) const { return (L.lane & 7) ^ ((row_of(i) >> 1) & 7); }
+    // And of scales: dword h * 2 TILE + row of the two operands' rows.
+    __device__ __forceinline__ int scale_first(int i) const { return (L.wave * S::SCALES + i) * 64; }
+
+    __device__ __forceinline__ void tile(const Operand& A, const Operand& B, const Operand& SA, const Operand& SB) {
+        const Operand& O = first_load() < S::TILE / 8 ? A : B;
+        base = O.base;
+#pragma unroll
+        for (int i = 0; i < S::LOADS; ++i) {
+            const int row = row_of(i);
+            off[i] = (uint32_t)(row < O.rows - 1 ? row : O.rows - 1) * O.ld + piece_of(i) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) {
+            const int r = scale_first(i) % (2 * S::TILE);
+            const Operand& C = r < S::TILE ? SA : SB;
+            const int row = (r < S::TILE ? r : r - S::TILE) + L.lane;
+            scale_base[i] = C.base;
+            scale_off[i] = (uint32_t)(row < C.rows - 1 ? row : C.rows - 1) * C.ld;
+        }
+    }
+
     // quarter q of the loads of a slab (q = 4: all)
-    auto stage = [&](int slab, char* buf, int q) {
+    __device__ __forceinline__ void stage(int slab, char* buf, int q) const {
         const bool cut = MM::kScaled && slab >= slabs;  // past a half slab lies the next row
         const char* from = base + (int64_t)slab * kSlab;
-        char* to = buf + g0 * 1024;
+        char* to = buf + first_load() * 1024;
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i)
             if (q == 4 || i * 4 / S::LOADS == q)
-                load_to_lds16(from + (off[i] - (cut && upper[i] ? 64u : 0u)), to + i * 1024);
+                load_to_lds16(from + (off[i] - (cut && piece_of(i) >= 4 ? 64u : 0u)), to + i * 1024);
         if (q >= 3) {
 #pragma unroll
             for (int i = 0; i < kScaleLoads; ++i)
-                load_to_lds4(scale_base[i] + (int64_t)slab * 8 + (scale_off[i] + (cut ? 0u : scale_h[i])),
+                load_to_lds4(scale_base[i] + (int64_t)slab * 8 +
+                                 (scale_off[i] + (cut ? 0 : scale_first(i) / (2 * S::TILE) * 4)),
                              buf + S::ROWS + (L.wave * S::SCALES + i) * 256);
         }
-    };
-    const int fa = (wm * S::WM + L.c) * kSlab, fb = (S::TILE + wn * S::WN + L.c) * kSlab;
-    const int turn = (L.c >> 1) & 7;
-    auto scales = [&](const char* buf, int shift, uint32_t (&sa)[S::MT], uint32_t (&sb)[S::NT]) {
+    }
+
+    __device__ __forceinline__ int slab_of(int t) const { return t * S::KS + group; }  // round t of this group
+
+    __device__ __forceinline__ void ahead() const {
+#pragma unroll
+        for (int t = 0; t < S::STAGES - 1; ++t)
+            if (slab_of(t) < total) stage(slab_of(t), lds + t * kStage, 4);
+    }
+
+    __device__ __forceinline__ void scales(const char* buf, int shift, uint32_t (&sa)[S::MT], uint32_t (&sb)[S::NT]) const {
         if constexpr (MM::kScaled) {
+            const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
             const uint32_t* at = (const uint32_t*)(buf + S::ROWS) + L.h * 2 * S::TILE + L.c;
 #pragma unroll
             for (int i = 0; i < S::MT; ++i) sa[i] = at[wm * S::WM + 32 * i] >> shift;
 #pragma unroll
             for (int j = 0; j < S::NT; ++j) sb[j] = at[S::TILE + wn * S::WN + 32 * j] >> shift;
         }
-    };
+    }
 
-    lds += group * S::STAGES * kStage;
-    // round t of this group: slab t * KS + group
-    const int rounds = (slabs + S::KS - 1) / S::KS;
-    auto slab_of = [&](int t) { return t * S::KS + group; };
-    for (int t = 0; t < S::STAGES - 1; ++t)
-        if (slab_of(t) < total) stage(slab_of(t), lds + t * kStage, 4);
-    char* const end = lds + S::STAGES * kStage;
-    char *buf = lds, *fill = lds + (S::STAGES - 1) * kStage;
-    auto after = [&](char* b) { return b + kStage == end ? lds : b + kStage; };
-    for (int t = 0; t < rounds; ++t) {
-        // this round's slab has landed in every wave's part, and the buffer used before it is free
-        if (slab_of(t + S::STAGES - 2) < total)
-            wait_and_meet<(S::STAGES - 2) * (S::LOADS + kScaleLoads)>();
-        else
-            wait_and_meet<0>();
-        const int slab = slab_of(t), ahead = slab_of(t + S::STAGES - 1);
-        const bool more = ahead < total;
-        if (S::KS == 1 || slab < slabs) {
-            uint32_t sa[S::MT], sb[S::NT];
-            scales(buf, 0, sa, sb);
-            const char *ra = buf + fa, *rb = buf + fb;
-            const int slot = (4 * L.h) ^ turn;
-            Frags<S> f[2];
-            f[0].load(ra, rb, (slot ^ 0) << 4);
-            if (more) stage(ahead, fill, 0);
-            f[1].load(ra, rb, (slot ^ 1) << 4);
-            multiply<S, MM, 0>(acc, f[0], sa, sb);
-            if (more) stage(ahead, fill, 1);
-            f[0].load(ra, rb, (slot ^ 2) << 4);
-            multiply<S, MM, 1>(acc, f[1], sa, sb);
-            if (more) stage(ahead, fill, 2);
-            f[1].load(ra, rb, (slot ^ 3) << 4);
-            multiply<S, MM, 2>(acc, f[0], sa, sb);
-            if (more) stage(ahead, fill, 3);
-            multiply<S, MM, 3>(acc, f[1], sa, sb);
-        }
-        buf = after(buf);
-        fill = after(fill);
-    }
-    if constexpr (MM::kScaled) {
-        if (half) {
-            wait_and_meet<0>();
-            if (S::KS == 1 || group == slabs % S::KS) {
-                buf = lds + slabs / S::KS % S::STAGES * kStage;
-                uint32_t sa[S::MT], sb[S::NT];
-                scales(buf, 16 * L.h, sa, sb);  // group h takes blocks 2h and 2h + 1 of four
-                const char *ra = buf + fa, *rb = buf + fb;
-                const int slot = (2 * L.h) ^ turn;
-                Frags<S> f[2];
-                f[0].load(ra, rb, (slot ^ 0) << 4);
-                f[1].load(ra, rb, (slot ^ 1) << 4);
-                multiply<S, MM, 0>(acc, f[0], sa, sb);
-                multiply<S, MM, 1>(acc, f[1], sa, sb);
-            }
-        }
-    }
-    if constexpr (S::KS > 1) {
-        static_assert((S::KS - 1) * S::TILE * S::TILE * 4 <= product_lds<S, MM>(), "the groups' sums fit");
-        __syncthreads();
-        float* mine = (float*)all + (group - 1) * S::TILE * S::TILE + L.wave * S::MT * S::NT * 1024 + L.lane * 4;
+    __device__ __forceinline__ bool run(f32x16 (&acc)[S::MT][S::NT]) const {
+        const int wm = L.wave / (S::TILE / S::WN), wn = L.wave % (S::TILE / S::WN);
 #pragma unroll
         for (int i = 0; i < S::MT; ++i)
 #pragma unroll
             for (int j = 0; j < S::NT; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    f32x4 v;
-                    float* at = mine + ((i * S::NT + j) * 4 + q) * 256;
-                    if (group > 0) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r];
-                        *(f32x4*)at = v;
-                    }
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        const int fa = (wm * S::WM + L.c) * kSlab, fb = (S::TILE + wn * S::WN + L.c) * kSlab;
+        const int turn = (L.c >> 1) & 7;
+        const int rounds = (slabs + S::KS - 1) / S::KS;
+        char* const end = lds + S::STAGES * kStage;
+        char *buf = lds, *fill = lds + (S::STAGES - 1) * kStage;
+        auto after = [&](char* b) { return b + kStage == end ? lds : b + kStage; };
+        for (int t = 0; t < rounds; ++t) {
+            // this round's slab has landed in every wave's part, and the buffer used before it is free
+            if (slab_of(t + S::STAGES - 2) < total)
+                wait_and_meet<(S::STAGES - 2) * (S::LOADS + kScaleLoads)>();
+            else
+                wait_and_meet<0>();
+            const int slab = slab_of(t), next = slab_of(t + S::STAGES - 1);
+            const bool more = next < total;
+            if (S::KS == 1 || slab < slabs) {
+                uint32_t sa[S::MT], sb[S::NT];
+                scales(buf, 0, sa, sb);
+                const char *ra = buf + fa, *rb = buf + fb;
+                const int slot = (4 * L.h) ^ turn;
+                Frags<S> f[2];
+                f[0].load(ra, rb, (slot ^ 0) << 4);
+                if (more) stage(next, fill, 0);
+                f[1].load(ra, rb, (slot ^ 1) << 4);
+                multiply<S, MM, 0>(acc, f[0], sa, sb);
+                if (more) stage(next, fill, 1);
+                f[0].load(ra, rb, (slot ^ 2) << 4);
+                multiply<S, MM, 1>(acc, f[1], sa, sb);
+                if (more) stage(next, fill, 2);
+                f[1].load(ra, rb, (slot ^ 3) << 4);
+                multiply<S, MM, 2>(acc, f[0], sa, sb);
+                if (more) stage(next, fill, 3);
+                multiply<S, MM, 3>(acc, f[1], sa, sb);
+            }
+            buf = after(buf);
+            fill = after(fill);
+        }
+        if constexpr (MM::kScaled) {
+            if (half) {
+                wait_and_meet<0>();
+                if (S::KS == 1 || group == slabs % S::KS) {
+                    buf = lds + slabs / S::KS % S::STAGES * kStage;
+                    uint32_t sa[S::MT], sb[S::NT];
+                    scales(buf, 16 * L.h, sa, sb);  // group h takes blocks 2h and 2h + 1 of four
+                    const char *ra = buf + fa, *rb = buf + fb;
+                    const int slot = (2 * L.h) ^ turn;
+                    Frags<S> f[2];
+                    f[0].load(ra, rb, (slot ^ 0) << 4);
+                    f[1].load(ra, rb, (slot ^ 1) << 4);
+                    multiply<S, MM, 0>(acc, f[0], sa, sb);
+                    multiply<S, MM, 1>(acc, f[1], sa, sb);
                 }
-        __syncthreads();
-        if (group > 0) return false;
+            }
+        }
+        if constexpr (S::KS > 1) {
+            static_assert((S::KS - 1) * S::TILE * S::TILE * 4 <= product_lds<S, MM>(), "the groups' sums fit");
+            __syncthreads();
+            float* mine = (float*)all + (group - 1) * S::TILE * S::TILE + L.wave * S::MT * S::NT * 1024 + L.lane * 4;
+            if (group > 0) {
 #pragma unroll
-        for (int g = 1; g < S::KS; ++g)
+                for (int i = 0; i < S::MT; ++i)
 #pragma unroll
-            for (int i = 0; i < S::MT; ++i)
+                    for (int j = 0; j < S::NT; ++j)
 #pragma unroll
-                for (int j = 0; j < S::NT; ++j)
+                        for (int q = 0; q < 4; ++q) {
+                            f32x4 v;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f32x4 v = *(const f32x4*)(mine + g * S::TILE * S::TILE + ((i * S::NT + j) * 4 + q) * 256);
+                            for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r];
+                            *(f32x4*)(mine + ((i * S::NT + j) * 4 + q) * 256) = v;
+                        }
+            }
+            __syncthreads();
+            if (group > 0) return false;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
-                    }
+            for (int g = 1; g < S::KS; ++g)
+#pragma unroll
+                for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f32x4 v =
+                                *(const f32x4*)(mine + g * S::TILE * S::TILE + ((i * S::NT + j) * 4 + q) * 256);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
+                        }
+        }
+        return true;
     }
-    return true;
-}
+};
 
 // Turns the 4 x 4 values of four neighbouring lanes: v[r] of lane t <-> v[t] of lane r.
 template <int CTRL>

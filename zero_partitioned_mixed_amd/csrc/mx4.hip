@@ -59,25 +59,46 @@ __device__ __forceinline__ uint32_t block_top(const float* x) {
 }
 
 // Eight elements of a row from column c on; past the row's end zeros.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const typename Elem<DT>::type* row, int64_t c, int64_t cols, float* x) {
+template <int DT>
+struct Eight {
     typedef typename Elem<DT>::type T;
-    T v[8];
-    if (VEC && c + 8 <= cols) {
+    static constexpr int kVecs = (int)sizeof(T) / 2;
+    u32x4 v[kVecs];
+
+    // Whole vectors at any alignment of the elements: the memory pipeline takes them.
+    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t cols) {
+        if (c + 8 <= cols) {
+            __builtin_memcpy(v, row + c, sizeof(v));
+        } else {
+            T x[8];
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(v) / 16; ++i) ((u32x4*)v)[i] = *((const u32x4*)(row + c) + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : (T)0;
+            for (int i = 0; i < 8; ++i) x[i] = c + i < cols ? row[c + i] : (T)0;
+            __builtin_memcpy(v, x, sizeof(v));
+        }
     }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_float<DT>(v[i]);
-}
+        for (int i = 0; i < kVecs; ++i) v[i] = u32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void values(float* x) const {
+        T t[8];
+        __builtin_memcpy(t, v, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_float<DT>(t[i]);
+    }
+};
 
 struct QuantArgs {
     const void* src;
     int64_t rows, cols, ld;
     uint8_t *codes, *scales, *codes_t, *scales_t;
+};
+
+// One or two matrices in one launch: workgroups from `second` on take the second.
+struct QuantJobs {
+    QuantArgs job[2];
+    uint32_t across[2];  // patches in a row of patches
+    uint32_t second;
 };
 
 // Codes and scale of this lane's eight elements of a row (four lanes a block).
@@ -87,69 +108,69 @@ __device__ __forceinline__ void put_row8(const QuantArgs& a, int64_t r, int64_t 
     if ((threadIdx.x & 3) == 0) a.scales[r * (p / kMxBlock) + c / kMxBlock] = (uint8_t)s;
 }
 
-// Along rows: eight elements per thread.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) mx4_rows_kernel(QuantArgs a) {
-    const int64_t p = padded(a.cols), pieces = p / 8;
-    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t r = t / pieces, c = (t - r * pieces) * 8;
-    if (r >= a.rows) return;  // whole groups of 16 lanes
-    float x[8];
-    load8<DT, VEC>((const typename Elem<DT>::type*)a.src + r * a.ld, c, a.cols, x);
-    put_row8(a, r, c, p, x);
-}
-
-// Along columns, and along rows too where asked, from one read: a 128 x 128
-// patch through LDS.  A thread then takes 32 elements of a column; four
-// neighbouring lanes write 64 contiguous bytes of codes.  Every 32 rows start
-// 16 columns further on, which keeps those four lanes on different banks.
-constexpr int kPatch = 128;
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) mx4_cols_kernel(QuantArgs a) {
+// A patch of ROWS x 128 elements per workgroup, sixteen lanes to a row, all its loads
+// before the first use.  Along rows four lanes hold a block.  Along columns (COLS)
+// the patch goes through LDS and a thread takes 32 elements of a column; four
+// neighbouring lanes then write 64 contiguous bytes of codes.  Every 32 rows start
+// 16 columns further on, which keeps those four lanes on different banks.  Bound
+// by memory: both directions of 8192 x 8192 bf16 read and write 205 MB.
+template <int DT, int ROWS, bool COLS>
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(QuantJobs jobs) {
     typedef typename Elem<DT>::type T;
-    constexpr int kLd = kPatch + 16 / (int)sizeof(T);
-    __shared__ __attribute__((aligned(16))) T patch[kPatch * kLd + 3 * 16];
-    const int64_t r0 = (int64_t)blockIdx.y * kPatch, c0 = (int64_t)blockIdx.x * kPatch;
+    constexpr int kCols = kMxPad, kLd = kCols + 16 / (int)sizeof(T), kLoads = ROWS / 16;
+    __shared__ __attribute__((aligned(16))) T patch[COLS ? ROWS * kLd + (ROWS / 32 - 1) * 16 : 8];
+    const bool other = blockIdx.x >= jobs.second;
+    const QuantArgs& a = jobs.job[other];
+    const uint32_t wg = other ? blockIdx.x - jobs.second : blockIdx.x, across = jobs.across[other];
+    const int64_t r0 = (int64_t)(wg / across) * ROWS, c0 = (int64_t)(wg % across) * kCols;
     const int64_t p = padded(a.cols), pt = padded(a.rows);
-    const int tid = threadIdx.x;
-    auto at = [](int r, int c) { return r * kLd + (r / kMxBlock) * 16 + c; };
+    const int tid = threadIdx.x, r = tid / 16, c = tid % 16 * 8;
+    auto at = [](int row, int col) { return row * kLd + row / kMxBlock * 16 + col; };
+    Eight<DT> e[kLoads];
 #pragma unroll
-    for (int i = 0; i < kPatch; i += kThreads / 16) {
-        const int r = i + tid / 16, c = (tid % 16) * 8;
-        float x[8];
-        if (r0 + r < a.rows) {
-            load8<DT, VEC>((const T*)a.src + (r0 + r) * a.ld, c0 + c, a.cols, x);
-            if (a.codes != nullptr) put_row8(a, r0 + r, c0 + c, p, x);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = 0.0f;
-        }
-        T v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = from_float<DT>(x[k]);
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(v) / 16; ++k) *((u32x4*)(patch + at(r, c)) + k) = ((u32x4*)v)[k];
+    for (int i = 0; i < kLoads; ++i) {
+        const int64_t row = r0 + r + 16 * i;
+        if (row < a.rows)
+            e[i].load((const T*)a.src + row * a.ld, c0 + c, a.cols);
+        else
+            e[i].zero();
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int c = i * 64 + tid / 4, block = tid % 4;
-        if (c0 + c >= a.cols) continue;
-        float x[kMxBlock];
-        uint32_t top = 0;
+    for (int i = 0; i < kLoads; ++i) {
+        const int row = r + 16 * i;
+        if constexpr (COLS) {
 #pragma unroll
-        for (int k = 0; k < kMxBlock; ++k) {
-            x[k] = to_float<DT>(patch[at(block * kMxBlock, c) + k * kLd]);
-            top = umax(top, magnitude(x[k]));
+            for (int k = 0; k < Eight<DT>::kVecs; ++k) *((u32x4*)(patch + at(row, c)) + k) = e[i].v[k];
         }
-        const uint32_t s = scale_byte(top);
-        const float inv = inverse_scale(s);
-        u32x4 q;
+        if ((!COLS || a.codes != nullptr) && r0 + row < a.rows) {
+            float x[8];
+            e[i].values(x);
+            put_row8(a, r0 + row, c0 + c, p, x);
+        }
+    }
+    if constexpr (COLS) {
+        __syncthreads();
+        constexpr int kBlocks = ROWS / kMxBlock;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = s == 255 ? 0u : codes8(x + 8 * k, inv);
-        const int64_t row = c0 + c, blk = r0 / kMxBlock + block;
-        *(u32x4*)(a.codes_t + row * (pt / 2) + blk * (kMxBlock / 2)) = q;
-        a.scales_t[row * (pt / kMxBlock) + blk] = (uint8_t)s;
+        for (int t = tid; t < kCols * kBlocks; t += kThreads) {
+            const int col = t / kBlocks, block = t % kBlocks;
+            if (c0 + col >= a.cols) continue;
+            float x[kMxBlock];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < kMxBlock; ++k) {
+                x[k] = to_float<DT>(patch[at(block * kMxBlock, col) + k * kLd]);
+                top = umax(top, magnitude(x[k]));
+            }
+            const uint32_t s = scale_byte(top);
+            const float inv = inverse_scale(s);
+            u32x4 q;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[k] = s == 255 ? 0u : codes8(x + 8 * k, inv);
+            const int64_t row = c0 + col, blk = r0 / kMxBlock + block;
+            *(u32x4*)(a.codes_t + row * (pt / 2) + blk * (kMxBlock / 2)) = q;
+            a.scales_t[row * (pt / kMxBlock) + blk] = (uint8_t)s;
+        }
     }
 }
 
@@ -170,26 +191,38 @@ __device__ __forceinline__ float scaled(float v, uint32_t s) {
     return s == 255 ? __builtin_nanf("") : ldexpf(v, (int)s - 127);
 }
 
-template <int DT, bool VEC>
+// 64 rows x 128 columns per workgroup, sixteen lanes to a row.
+constexpr int kValueRows = 64;
+template <int DT>
 __global__ void __launch_bounds__(kThreads) mx4_values_kernel(DequantArgs a) {
     typedef typename Elem<DT>::type T;
-    const int64_t p = padded(a.cols), pieces = p / 8;
-    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t r = t / pieces, c = (t - r * pieces) * 8;
-    if (r >= a.rows || c >= a.cols) return;
-    const uint32_t q = *(const uint32_t*)(a.codes + r * (p / 2) + c / 2);
-    const uint32_t s = a.scales[r * (p / kMxBlock) + c / kMxBlock];
-    T v[8];
+    const int64_t p = padded(a.cols);
+    const uint32_t across = (uint32_t)(p / kMxPad);
+    const int64_t r0 = (int64_t)(blockIdx.x / across) * kValueRows + threadIdx.x / 16;
+    const int64_t c = (int64_t)(blockIdx.x % across) * kMxPad + threadIdx.x % 16 * 8;
+    if (c >= a.cols) return;
+    constexpr int kEach = kValueRows / 16;
+    uint32_t q[kEach], s[kEach];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = from_float<DT>(scaled(code_value(q >> (4 * i)), s));
-    T* dst = (T*)a.dst + r * a.ld + c;
-    if (VEC && c + 8 <= a.cols) {
+    for (int i = 0; i < kEach; ++i) {
+        const int64_t r = r0 + 16 * i < a.rows ? r0 + 16 * i : a.rows - 1;
+        q[i] = *(const uint32_t*)(a.codes + r * (p / 2) + c / 2);
+        s[i] = a.scales[r * (p / kMxBlock) + c / kMxBlock];
+    }
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(v) / 16; ++i) ((u32x4*)dst)[i] = ((u32x4*)v)[i];
-    } else {
+    for (int i = 0; i < kEach; ++i) {
+        if (r0 + 16 * i >= a.rows) return;
+        T v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < a.cols) dst[i] = v[i];
+        for (int k = 0; k < 8; ++k) v[k] = from_float<DT>(scaled(code_value(q[i] >> (4 * k)), s[i]));
+        T* dst = (T*)a.dst + (r0 + 16 * i) * a.ld + c;
+        if (c + 8 <= a.cols) {
+            __builtin_memcpy(dst, v, sizeof(v));  // whole vectors at any alignment
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < a.cols) dst[k] = v[k];
+        }
     }
 }
 
@@ -213,51 +246,192 @@ __global__ void __launch_bounds__(S::THREADS) mx4_matmul_kernel(MatmulArgs g) {
     const int64_t left_m = g.m - i0, left_n = g.n - j0;
     const int rows_a = (int)(left_m < S::TILE ? left_m : S::TILE), rows_b = (int)(left_n < S::TILE ? left_n : S::TILE);
     const uint32_t ld = (uint32_t)(g.p / 2), ls = (uint32_t)(g.p / kMxBlock);
-    const Operand A{(const char*)g.a + i0 * ld, ld, rows_a}, B{(const char*)g.b + j0 * ld, ld, rows_b};
-    const Operand SA{(const char*)g.sa + i0 * ls, ls, rows_a}, SB{(const char*)g.sb + j0 * ls, ls, rows_b};
+    Product<S, MmFp4> product(lds, (int)(g.p / 256), g.p % 256 != 0);
+    product.tile(Operand{(const char*)g.a + i0 * ld, ld, rows_a}, Operand{(const char*)g.b + j0 * ld, ld, rows_b},
+                 Operand{(const char*)g.sa + i0 * ls, ls, rows_a}, Operand{(const char*)g.sb + j0 * ls, ls, rows_b});
+    product.ahead();
     f32x16 acc[S::MT][S::NT];
-    if (!tile_product<S, MmFp4>(A, B, SA, SB, (int)(g.p / 256), g.p % 256 != 0, lds, acc)) return;
+    if (!product.run(acc)) return;
 
+    // A lane's place in the tile: 32-bit offsets from the tile's first element.
     typedef typename Elem<DT>::type T;
-    const Lane L(S::WAVES);
-    const int64_t iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    const Lane& L = product.L;
+    const int iw = L.wave / (S::TILE / S::WN) * S::WM + 4 * L.h + (L.c & 3);
+    const int jw = L.wave % (S::TILE / S::WN) * S::WN + (L.c & ~3);
+    T* const out = (T*)g.c + i0 * g.ldc + j0;
+    const bool whole = g.vector && rows_a == S::TILE && rows_b == S::TILE;
 #pragma unroll
     for (int ii = 0; ii < S::MT; ++ii)
 #pragma unroll
-        for (int jj = 0; jj < S::NT; ++jj)
+        for (int q = 0; q < 4; ++q) {
+            const int i = iw + ii * 32 + 8 * q;
+            T* const row = out + i * g.ldc + jw;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int jj = 0; jj < S::NT; ++jj) {
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
                 quad_turn(v);  // four columns of one row
-                const int64_t i = iw + ii * 32 + 8 * q + 4 * L.h + (L.c & 3), j = jw + jj * 32 + (L.c & ~3);
-                if (i >= g.m || j >= g.n) continue;
-                T* out = (T*)g.c + i * g.ldc + j;
-                if (g.vector && j + 4 <= g.n) {
-                    typedef T T4 __attribute__((ext_vector_type(4)));
+                const int j = jw + jj * 32;
+                T* const at = row + jj * 32;
+                if (whole || (g.vector && i < rows_a && j + 4 <= rows_b)) {
                     T4 w;
                     if constexpr (DT == ZERO_F32) {
                         if (g.accumulate) {
-                            w = *(const T4*)out;
+                            w = *(const T4*)at;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) v[e] += w[e];
                         }
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = from_float<DT>(v[e]);
-                    *(T4*)out = w;
-                } else {
+                    *(T4*)at = w;
+                } else if (i < rows_a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (j + e >= g.n) break;
+                        if (j + e >= rows_b) break;
                         if constexpr (DT == ZERO_F32) {
-                            if (g.accumulate) v[e] += out[e];
+                            if (g.accumulate) v[e] += at[e];
                         }
-                        out[e] = from_float<DT>(v[e]);
+                        at[e] = from_float<DT>(v[e]);
                     }
                 }
             }
+        }
+}
+
+// Few rows (m <= 64, as single tokens bring): bound by reading B once.  A workgroup
+// takes 32 of B's rows, its four waves a quarter of k each, straight from memory
+// to registers in runs of 64 bytes per lane; the waves' sums meet in LDS.
+// VALUES (m k up to kFewValues): A comes as values, and every workgroup quantises
+// all of it to LDS first, which saves a launch.
+constexpr int kFewWaves = 4;
+constexpr int kFewValues = 16384;
+constexpr int kFewUnroll = 4;  // slabs of a wave on their way at once
+
+struct FewArgs {
+    MatmulArgs g;
+    int64_t lda, k;  // values of A: row stride, length
+};
+
+template <int MT, int DTA, int DT, bool VALUES>
+__global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
+    const MatmulArgs& g = f.g;
+    constexpr int kCodes = VALUES ? kFewValues / 2 : 16, kScales = kCodes / 16;
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kCodes];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[VALUES ? kScales : 16];
+    __shared__ float sums[kFewWaves][MT * 32][33];
+    const Lane L;
+    const uint32_t p = (uint32_t)g.p, half_row = p / 2, scale_row = p / kMxBlock;
+    const int64_t j = (int64_t)blockIdx.x * 32 + L.c;
+    const int64_t jc = j < g.n ? j : g.n - 1;
+    const uint8_t *b = g.b + jc * half_row + 64 * L.h, *sb = g.sb + jc * scale_row + 4 * L.h;
+    const int slabs = (int)(p / 256);
+
+    i32x4 bw[kFewUnroll][4];
+    uint32_t bs[kFewUnroll];
+    auto fetch = [&](int first) {
+#pragma unroll
+        for (int u = 0; u < kFewUnroll; ++u) {
+            const int s = first + u * kFewWaves < slabs ? first + u * kFewWaves : slabs - 1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) bw[u][q] = *(const i32x4*)(b + (int64_t)s * 128 + 16 * q);
+            bs[u] = *(const uint32_t*)(sb + (int64_t)s * 8);
+        }
+    };
+    if constexpr (VALUES) {
+        typedef typename Elem<DTA>::type T;
+        const int pieces = (int)(g.m * p / 8);
+        auto read = [&](int t, Eight<DTA>& e) {
+            const uint32_t r = (uint32_t)t / (p / 8), c = ((uint32_t)t - r * (p / 8)) * 8;
+            e.load((const T*)g.a + r * f.lda, c, f.k);
+        };
+        auto put = [&](int t, const Eight<DTA>& e) {  // whole groups of four lanes
+            const uint32_t r = (uint32_t)t / (p / 8), c = ((uint32_t)t - r * (p / 8)) * 8;
+            float x[8];
+            e.values(x);
+            const uint32_t s = scale_byte(block_top(x));
+            *(uint32_t*)(codes + r * half_row + c / 2) = s == 255 ? 0u : codes8(x, inverse_scale(s));
+            if ((t & 3) == 0) scales[r * scale_row + c / kMxBlock] = (uint8_t)s;
+        };
+        // loads return in order: the first of A go out before B's, so that A is ready while B is on its way
+        constexpr int kFirst = 2;
+        const int tid = threadIdx.x;
+        Eight<DTA> e[kFirst];
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i)
+            if (tid + i * kFewWaves * 64 < pieces) read(tid + i * kFewWaves * 64, e[i]);
+        if (slabs > 0) fetch(L.wave);
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i)
+            if (tid + i * kFewWaves * 64 < pieces) put(tid + i * kFewWaves * 64, e[i]);
+        for (int t = tid + kFirst * kFewWaves * 64; t < pieces; t += kFewWaves * 64) {
+            read(t, e[0]);
+            put(t, e[0]);
+        }
+        __syncthreads();
+    } else {
+        if (slabs > 0) fetch(L.wave);
+    }
+    const uint8_t *a = VALUES ? codes : g.a, *sa = VALUES ? scales : g.sa;
+    uint32_t row[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) row[i] = (uint32_t)(L.c + 32 * i < g.m ? L.c + 32 * i : g.m - 1);
+    f32x16 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+
+    for (int first = L.wave; first < slabs; first += kFewWaves * kFewUnroll) {
+        if (first != L.wave) fetch(first);
+#pragma unroll
+        for (int u = 0; u < kFewUnroll; ++u) {
+            const int s = first + u * kFewWaves;
+            if (s >= slabs) break;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const uint32_t as = *(const uint32_t*)(sa + row[i] * scale_row + s * 8 + 4 * L.h);
+                const i32x4* aw = (const i32x4*)(a + row[i] * half_row + s * 128 + 64 * L.h);
+                acc[i] = MmFp4::mma<0>(aw[0], bw[u][0], acc[i], as, bs[u]);
+                acc[i] = MmFp4::mma<1>(aw[1], bw[u][1], acc[i], as, bs[u]);
+                acc[i] = MmFp4::mma<2>(aw[2], bw[u][2], acc[i], as, bs[u]);
+                acc[i] = MmFp4::mma<3>(aw[3], bw[u][3], acc[i], as, bs[u]);
+            }
+        }
+    }
+    if (p % 256 != 0 && L.wave == 0) {  // half a slab: group h takes blocks 2h and 2h + 1 of four
+        const int64_t at = (int64_t)slabs * 128 - 32 * L.h, sat = (int64_t)slabs * 8 - 4 * L.h;
+        const uint32_t bsh = *(const uint32_t*)(sb + sat) >> (16 * L.h);
+        const i32x4 b0 = *(const i32x4*)(b + at), b1 = *(const i32x4*)(b + at + 16);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const uint32_t as = *(const uint32_t*)(sa + row[i] * scale_row + slabs * 8) >> (16 * L.h);
+            const i32x4* aw = (const i32x4*)(a + row[i] * half_row + slabs * 128 + 32 * L.h);
+            acc[i] = MmFp4::mma<0>(aw[0], b0, acc[i], as, bsh);
+            acc[i] = MmFp4::mma<1>(aw[1], b1, acc[i], as, bsh);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sums[L.wave][32 * i + 8 * (r / 4) + 4 * L.h + r % 4][L.c] = acc[i][r];
+    __syncthreads();
+    typedef typename Elem<DT>::type T;
+    for (int t = threadIdx.x; t < (int)g.m * 32; t += kFewWaves * 64) {
+        const int i = t / 32, c = t % 32;
+        const int64_t col = (int64_t)blockIdx.x * 32 + c;
+        if (col >= g.n) continue;
+        float v = sums[0][i][c];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += sums[w][i][c];
+        T* out = (T*)g.c + i * g.ldc + col;
+        if constexpr (DT == ZERO_F32) {
+            if (g.accumulate) v += *out;
+        }
+        *out = from_float<DT>(v);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -267,32 +441,37 @@ int check_sides(int64_t rows, int64_t cols, const char* what) {
     return ZERO_OK;
 }
 
-bool vector_rows(const void* p, int64_t ld, int32_t dtype) {
-    return aligned(p, 16) && (ld * (int64_t)elem_bytes(dtype)) % 16 == 0;
-}
-
+// One or two matrices of one type (the second may be absent: rows 0), along rows or,
+// where the first asks for its transpose, along columns too.
 template <int DT>
-int quantize_with(const QuantArgs& a, hipStream_t s, const char* what) {
-    const bool vec = vector_rows(a.src, a.ld, DT);
-    if (a.codes_t == nullptr) {
-        const int64_t wgs = ceil_div(a.rows * (padded(a.cols) / 8), kThreads);
-        if (wgs > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
-        return launch(vec ? mx4_rows_kernel<DT, true> : mx4_rows_kernel<DT, false>, dim3((unsigned)wgs), kThreads, s,
-                      a, what);
+int quantize_with(const QuantArgs* jobs, int count, hipStream_t s, const char* what) {
+    QuantJobs q{};
+    for (int i = 0; i < count; ++i) {
+        q.job[i] = jobs[i];
+        q.across[i] = (uint32_t)(padded(jobs[i].cols) / kMxPad);
     }
-    const int64_t gx = ceil_div(a.cols, kPatch), gy = ceil_div(a.rows, kPatch);
-    if (gy > 65535) return fail(ZERO_ERANGE, "%s: too many rows to quantise along columns", what);
-    return launch(vec ? mx4_cols_kernel<DT, true> : mx4_cols_kernel<DT, false>, dim3((unsigned)gx, (unsigned)gy),
-                  kThreads, s, a, what);
+    const bool cols = jobs[0].codes_t != nullptr;
+    auto patches = [&](int i, int64_t rows) -> int64_t {  // along columns the padding of the rows too
+        return i < count ? ceil_div(cols ? padded(jobs[i].rows) : jobs[i].rows, rows) * q.across[i] : 0;
+    };
+    // Patches of 32 rows where those of 128 would leave CUs without work: 500 x 768 and
+    // 1024 x 768 together, 5 against 7 us; at 8192 x 8192 they write the transposed
+    // codes in runs of 16 bytes, not 64.
+    const int high = !cols ? 64 : patches(0, 128) + patches(1, 128) >= 512 ? 128 : 32;
+    const int64_t first = patches(0, high), all = first + patches(1, high);
+    if (all > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
+    q.second = (uint32_t)first;
+    const dim3 grid((unsigned)all);
+    if (high == 64) return launch(mx4_quantize_kernel<DT, 64, false>, grid, kThreads, s, q, what);
+    if (high == 128) return launch(mx4_quantize_kernel<DT, 128, true>, grid, kThreads, s, q, what);
+    return launch(mx4_quantize_kernel<DT, 32, true>, grid, kThreads, s, q, what);
 }
 
-int quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, void* codes, void* scales,
-             void* codes_t, void* scales_t, hipStream_t s, const char* what) {
-    const QuantArgs a{src, rows, cols, ld, (uint8_t*)codes, (uint8_t*)scales, (uint8_t*)codes_t, (uint8_t*)scales_t};
+int quantize(const QuantArgs* jobs, int count, int32_t dtype, hipStream_t s, const char* what) {
     switch (dtype) {
-        case ZERO_F16: return quantize_with<ZERO_F16>(a, s, what);
-        case ZERO_BF16: return quantize_with<ZERO_BF16>(a, s, what);
-        default: return quantize_with<ZERO_F32>(a, s, what);
+        case ZERO_F16: return quantize_with<ZERO_F16>(jobs, count, s, what);
+        case ZERO_BF16: return quantize_with<ZERO_BF16>(jobs, count, s, what);
+        default: return quantize_with<ZERO_F32>(jobs, count, s, what);
     }
 }
 
@@ -311,7 +490,33 @@ int matmul_with(MatmulArgs g, int32_t c_dtype, hipStream_t s, const char* what) 
     }
 }
 
+template <int MT, int DTA, bool VALUES>
+int few_with(const FewArgs& f, int32_t c_dtype, hipStream_t s, const char* what) {
+    const dim3 grid((unsigned)ceil_div(f.g.n, 32));
+    switch (c_dtype) {
+        case ZERO_F16: return launch(mx4_few_kernel<MT, DTA, ZERO_F16, VALUES>, grid, kFewWaves * 64, s, f, what);
+        case ZERO_BF16: return launch(mx4_few_kernel<MT, DTA, ZERO_BF16, VALUES>, grid, kFewWaves * 64, s, f, what);
+        default: return launch(mx4_few_kernel<MT, DTA, ZERO_F32, VALUES>, grid, kFewWaves * 64, s, f, what);
+    }
+}
+
+// Values of A quantised in the product's own kernel.
+bool few_values(int64_t m, int64_t k) { return m <= 32 && m * padded(k) <= kFewValues; }
+
+int few_of_values(const FewArgs& f, int32_t a_dtype, int32_t c_dtype, hipStream_t s, const char* what) {
+    switch (a_dtype) {
+        case ZERO_F16: return few_with<1, ZERO_F16, true>(f, c_dtype, s, what);
+        case ZERO_BF16: return few_with<1, ZERO_BF16, true>(f, c_dtype, s, what);
+        default: return few_with<1, ZERO_F32, true>(f, c_dtype, s, what);
+    }
+}
+
 int matmul(const MatmulArgs& g, int32_t c_dtype, hipStream_t s, const char* what) {
+    if (g.m <= ZERO_MX4_ROWS_MAX) {
+        const FewArgs f{g, 0, 0};
+        return g.m <= 32 ? few_with<1, ZERO_F32, false>(f, c_dtype, s, what)
+                         : few_with<2, ZERO_F32, false>(f, c_dtype, s, what);
+    }
     const int pick = pick_tile([&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); });
     return with_tile(pick, [&](auto shape) { return matmul_with<decltype(shape)>(g, c_dtype, s, what); });
 }
@@ -333,6 +538,22 @@ int check_matmul(const void* b, const void* sb, int64_t m, int64_t n, int64_t k,
 
 size_t quantized_bytes(int64_t rows, int64_t cols) {
     return (size_t)(round_up(rows * (padded(cols) / 2), 256) + round_up(rows * (padded(cols) / kMxBlock), 256));
+}
+
+// Where an operand's codes and scales are in one buffer of zero_mx4_operand_bytes.
+struct Operand2 {
+    uint8_t *codes, *scales;
+    Operand2(void* at, int64_t rows, int64_t cols)
+        : codes((uint8_t*)at),
+          scales(at == nullptr ? nullptr : (uint8_t*)at + round_up(rows * (padded(cols) / 2), 256)) {}
+};
+
+int check_operands(const void* x_t, const void* w_t, const void* ws, size_t ws_bytes, size_t need, const char* what) {
+    if (!aligned(x_t, 16) || !aligned(w_t, 16)) return fail(ZERO_EALIGN, "%s: operands not 16-byte aligned", what);
+    if (ws == nullptr) return fail(ZERO_EINVAL, "%s: null workspace", what);
+    if (!aligned(ws, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", what);
+    if (ws_bytes < need) return fail(ZERO_ESPACE, "%s: workspace %zu bytes, needs %zu", what, ws_bytes, need);
+    return ZERO_OK;
 }
 
 }  // namespace
@@ -364,7 +585,8 @@ int zero_mx4_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols
     if (rows == 0 || cols == 0) return ok();
     if (src == nullptr) return fail(ZERO_EINVAL, "%s: null source", what);
     if (!aligned(src, elem_bytes(dtype))) return fail(ZERO_EALIGN, "%s: source not aligned to its elements", what);
-    return quantize(src, dtype, rows, cols, ld, codes, scales, codes_t, scales_t, (hipStream_t)stream, what);
+    const QuantArgs job{src, rows, cols, ld, (uint8_t*)codes, (uint8_t*)scales, (uint8_t*)codes_t, (uint8_t*)scales_t};
+    return quantize(&job, 1, dtype, (hipStream_t)stream, what);
 }
 
 int zero_mx4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, void* dst, int32_t dtype,
@@ -379,18 +601,17 @@ int zero_mx4_dequantize(const void* codes, const void* scales, int64_t rows, int
     if (!aligned(codes, 16) || !aligned(scales, 16)) return fail(ZERO_EALIGN, "%s: operand not 16-byte aligned", what);
     if (!aligned(dst, elem_bytes(dtype))) return fail(ZERO_EALIGN, "%s: result not aligned to its elements", what);
     const DequantArgs a{(const uint8_t*)codes, (const uint8_t*)scales, rows, cols, ld, dst};
-    const int64_t wgs = ceil_div(rows * (padded(cols) / 8), kThreads);
+    const int64_t wgs = ceil_div(rows, kValueRows) * (padded(cols) / kMxPad);
     if (wgs > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     const dim3 grid((unsigned)wgs);
     const hipStream_t s = (hipStream_t)stream;
-    const bool vec = vector_rows(dst, ld, dtype);
     switch (dtype) {
         case ZERO_F16:
-            return launch(vec ? mx4_values_kernel<ZERO_F16, true> : mx4_values_kernel<ZERO_F16, false>, grid, kThreads, s, a, what);
+            return launch(mx4_values_kernel<ZERO_F16>, grid, kThreads, s, a, what);
         case ZERO_BF16:
-            return launch(vec ? mx4_values_kernel<ZERO_BF16, true> : mx4_values_kernel<ZERO_BF16, false>, grid, kThreads, s, a, what);
+            return launch(mx4_values_kernel<ZERO_BF16>, grid, kThreads, s, a, what);
         default:
-            return launch(vec ? mx4_values_kernel<ZERO_F32, true> : mx4_values_kernel<ZERO_F32, false>, grid, kThreads, s, a, what);
+            return launch(mx4_values_kernel<ZERO_F32>, grid, kThreads, s, a, what);
     }
 }
 
@@ -413,7 +634,7 @@ int zero_mx4_matmul(const void* a, const void* sa, const void* b, const void* sb
 
 size_t zero_mx4_matmul_rows_workspace_bytes(int64_t m, int64_t n, int64_t k) {
     if (m <= 0 || n <= 0 || k <= 0 || m > ZERO_MX4_ROWS_MAX || n > kMaxSide || k > kMaxSide) return 0;
-    return quantized_bytes(m, k);
+    return few_values(m, k) ? 0 : quantized_bytes(m, k);
 }
 
 int zero_mx4_matmul_rows(const void* a, int32_t a_dtype, int64_t lda, const void* b, const void* sb, int64_t m,
@@ -434,12 +655,87 @@ int zero_mx4_matmul_rows(const void* a, int32_t a_dtype, int64_t lda, const void
         if (!aligned(ws, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", what);
         if (ws_bytes < need) return fail(ZERO_ESPACE, "%s: workspace %zu bytes, needs %zu", what, ws_bytes, need);
     }
-    uint8_t* codes = (uint8_t*)ws;
-    uint8_t* scales = codes + round_up(m * (padded(k) / 2), 256);
-    if (k > 0 && (rc = quantize(a, a_dtype, m, k, lda, codes, scales, nullptr, nullptr, (hipStream_t)stream, what)) != ZERO_OK)
-        return rc;
-    const MatmulArgs g{codes, scales, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, 0, 0};
+    MatmulArgs g{(const uint8_t*)a, nullptr, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, 0, 0};
+    if (few_values(m, k)) return few_of_values(FewArgs{g, lda, k}, a_dtype, c_dtype, (hipStream_t)stream, what);
+    const Operand2 q(ws, m, k);
+    const QuantArgs job{a, m, k, lda, q.codes, q.scales, nullptr, nullptr};
+    if ((rc = quantize(&job, 1, a_dtype, (hipStream_t)stream, what)) != ZERO_OK) return rc;
+    g.a = q.codes;
+    g.sa = q.scales;
     return matmul(g, c_dtype, (hipStream_t)stream, what);
+}
+
+size_t zero_mx4_operand_bytes(int64_t rows, int64_t cols) {
+    return rows <= 0 || cols <= 0 || rows > kMaxSide || cols > kMaxSide ? 0 : quantized_bytes(rows, cols);
+}
+
+size_t zero_mx4_linear_workspace_bytes(int64_t tokens, int64_t n, int64_t k) {
+    return zero_mx4_operand_bytes(tokens, k) + zero_mx4_operand_bytes(n, k);
+}
+
+int zero_mx4_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t dtype, int64_t tokens, int64_t n,
+                    int64_t k, void* y, int64_t ldy, void* x_t, void* w_t, void* ws, size_t ws_bytes, void* stream) {
+    const char* what = "zero_mx4_linear";
+    int rc;
+    if (!valid_dtype(dtype, true)) return fail(ZERO_EINVAL, "%s: unknown dtype", what);
+    if ((rc = check_sides(tokens, n, what)) != ZERO_OK || (rc = check_sides(k, k, what)) != ZERO_OK) return rc;
+    if (tokens == 0 || n == 0 || k == 0) return fail(ZERO_ERANGE, "%s: an empty product", what);
+    if (x == nullptr || w == nullptr || y == nullptr) return fail(ZERO_EINVAL, "%s: null matrix", what);
+    if (!aligned(x, elem_bytes(dtype)) || !aligned(w, elem_bytes(dtype)) || !aligned(y, elem_bytes(dtype)))
+        return fail(ZERO_EALIGN, "%s: matrices not aligned to their elements", what);
+    if (ldx < k || ldw < k || ldy < n) return fail(ZERO_ERANGE, "%s: row stride below the row", what);
+    if ((rc = check_operands(x_t, w_t, ws, ws_bytes, zero_mx4_linear_workspace_bytes(tokens, n, k), what)) != ZERO_OK)
+        return rc;
+    const hipStream_t s = (hipStream_t)stream;
+    const Operand2 xr(ws, tokens, k), wr((char*)ws + quantized_bytes(tokens, k), n, k);
+    const Operand2 xt(x_t, k, tokens), wt(w_t, k, n);
+    const QuantArgs jobs[2] = {{x, tokens, k, ldx, xr.codes, xr.scales, xt.codes, xt.scales},
+                               {w, n, k, ldw, wr.codes, wr.scales, wt.codes, wt.scales}};
+    if ((x_t == nullptr) == (w_t == nullptr))
+        rc = quantize(jobs, 2, dtype, s, what);
+    else if ((rc = quantize(jobs, 1, dtype, s, what)) == ZERO_OK)
+        rc = quantize(jobs + 1, 1, dtype, s, what);
+    if (rc != ZERO_OK) return rc;
+    return matmul(MatmulArgs{xr.codes, xr.scales, wr.codes, wr.scales, tokens, n, padded(k), y, ldy, 0, 0, 0, 0}, dtype, s,
+                  what);
+}
+
+size_t zero_mx4_linear_grad_workspace_bytes(int64_t tokens, int64_t n) {
+    return zero_mx4_operand_bytes(tokens, n) + zero_mx4_operand_bytes(n, tokens);
+}
+
+int zero_mx4_linear_grad(const void* dy, int64_t lddy, int32_t dtype, int64_t tokens, int64_t n, int64_t k,
+                         const void* x_t, const void* w_t, void* dx, int64_t lddx, void* dw, int64_t lddw, void* ws,
+                         size_t ws_bytes, void* stream) {
+    const char* what = "zero_mx4_linear_grad";
+    int rc;
+    if (!valid_dtype(dtype, true)) return fail(ZERO_EINVAL, "%s: unknown dtype", what);
+    if ((rc = check_sides(tokens, n, what)) != ZERO_OK || (rc = check_sides(k, k, what)) != ZERO_OK) return rc;
+    if (tokens == 0 || n == 0 || k == 0) return fail(ZERO_ERANGE, "%s: an empty product", what);
+    if (dx == nullptr && dw == nullptr) return ok();
+    if (dy == nullptr || (dx != nullptr && w_t == nullptr) || (dw != nullptr && x_t == nullptr))
+        return fail(ZERO_EINVAL, "%s: null matrix or operand", what);
+    if (!aligned(dy, elem_bytes(dtype)) || !aligned(dx, elem_bytes(dtype)) || !aligned(dw, elem_bytes(dtype)))
+        return fail(ZERO_EALIGN, "%s: matrices not aligned to their elements", what);
+    if (lddy < n || (dx != nullptr && lddx < k) || (dw != nullptr && lddw < k))
+        return fail(ZERO_ERANGE, "%s: row stride below the row", what);
+    if ((rc = check_operands(x_t, w_t, ws, ws_bytes, zero_mx4_linear_grad_workspace_bytes(tokens, n), what)) != ZERO_OK)
+        return rc;
+    const hipStream_t s = (hipStream_t)stream;
+    const Operand2 r(ws, tokens, n), c((char*)ws + quantized_bytes(tokens, n), n, tokens);
+    const Operand2 xt(const_cast<void*>(x_t), k, tokens), wt(const_cast<void*>(w_t), k, n);
+    QuantArgs job{dy, tokens, n, lddy, r.codes, r.scales, c.codes, c.scales};
+    if (dx == nullptr) job.codes = job.scales = nullptr;
+    if (dw == nullptr) job.codes_t = job.scales_t = nullptr;
+    if ((rc = quantize(&job, 1, dtype, s, what)) != ZERO_OK) return rc;
+    if (dx != nullptr &&
+        (rc = matmul(MatmulArgs{r.codes, r.scales, wt.codes, wt.scales, tokens, k, padded(n), dx, lddx, 0, 0, 0, 0}, dtype,
+                     s, what)) != ZERO_OK)
+        return rc;
+    if (dw != nullptr)
+        return matmul(MatmulArgs{c.codes, c.scales, xt.codes, xt.scales, n, k, padded(tokens), dw, lddw, 0, 0, 0, 0}, dtype,
+                      s, what);
+    return ok();
 }
 
 }  // extern "C"

@@ -636,7 +636,10 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     const Operand A{from + (int64_t)i0 * ld * 2, (uint32_t)ld * 2, w.m - i0};
     const Operand B{from + (int64_t)j0 * ld * 2, (uint32_t)ld * 2, w.m - j0};
     f32x16 acc[S::MT][S::NT];
-    const bool holds = tile_product<S, MmF16>(A, B, A, B, ld / 64, false, lds, acc);
+    Product<S, MmF16> product(lds, ld / 64, false);
+    product.tile(A, B, A, B);
+    product.ahead();
+    const bool holds = product.run(acc);
     __syncthreads();  // LDS is free
     if (!holds) return;
 
@@ -736,7 +739,10 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     const Operand A{base + w.m16 + (int64_t)i0 * w.kp * 2, (uint32_t)w.kp * 2, w.m - i0};
     const Operand B{xt + (int64_t)j0 * w.kp * 2, (uint32_t)w.kp * 2, w.n - j0};
     f32x16 acc[S::MT][S::NT];
-    const bool holds = tile_product<S, MmF16>(A, B, A, B, w.kp / 64, false, lds, acc);
+    Product<S, MmF16> product(lds, w.kp / 64, false);
+    product.tile(A, B, A, B);
+    product.ahead();
+    const bool holds = product.run(acc);
     __syncthreads();  // LDS is free
     if (!holds) return;
 

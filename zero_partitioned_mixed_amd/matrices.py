@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import (BF16, F16, F32, MUON_SCALE_RMS, MUON_SCALE_SHAPE, MX4_ROWS_MAX,  # noqa: F401
-               MuonHparams, NewtonSchulz, _check, _lib, _vp)
+               MuonHparams, NewtonSchulz, _check, _lib)
 
 _DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 COEFFS = (3.4445, -4.7750, 2.0315)  # the usual quintic's
@@ -27,47 +27,39 @@ def _code(dtype, allowed=_DTYPES) -> int:
 
 
 _HALVES = (torch.float16, torch.bfloat16)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without its object
 
 
-def _gpu(*tensors) -> None:
-    dev = tensors[0].device
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("expected a GPU tensor")
-        if t.device != dev:
-            raise ValueError("tensors on different GPUs")
+def _gpu(first, *others) -> int:
+    """The index of the GPU that all the tensors are on."""
+    index = first.get_device()
+    for t in (first, *others):
+        if t.get_device() != index or not t.is_cuda:
+            raise ValueError("expected GPU tensors" if not t.is_cuda else "tensors on different GPUs")
+    return index
 
 
-def _stream(t) -> ctypes.c_void_p:
-    return _vp(torch.cuda.current_stream(t.device).cuda_stream)
-
-
-class _on:
-    """The tensor's device as the current one (launches go to it)."""
-
-    def __init__(self, t):
-        self.dev = t.device
-        self.swap = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.swap = torch.cuda.device(self.dev)
-            self.swap.__enter__()
-
-    def __exit__(self, *exc):
-        if self.swap is not None:
-            self.swap.__exit__(*exc)
+def _call(index: int, name: str, *args) -> None:
+    """The C call on the GPU's current stream."""
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        _check(name, rc)
 
 
 def _space(nbytes: int, ws, like):
     """(pointer, bytes, tensor) of a workspace: ws, or a new tensor."""
     if ws is None:
         if nbytes == 0:
-            return _vp(None), 0, None
+            return None, 0, None
         ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    else:
-        _gpu(like, ws)
-    return _vp(ws.data_ptr()), ws.numel() * ws.element_size(), ws
+        return ws.data_ptr(), nbytes, ws
+    _gpu(like, ws)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 # ----------------------------------------------------------------------------- orthogonalised updates
@@ -114,19 +106,17 @@ def orthogonalize(x, out_dtype=None, *, coeffs=COEFFS, steps: int = 5, eps: floa
     src_code, dst_code = _code(x.dtype), _code(out_dtype, _HALVES)
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    _gpu(x, out)
+    index = _gpu(x, out)
     if out.shape != x.shape or not _laid_out(out):
         raise ValueError("out: another shape, or rows without unit stride")
     if not _laid_out(x):
         x = x.contiguous()
     count, rows, cols, ld, stride = _stack(x)
     _, _, _, out_ld, out_stride = _stack(out)
-    ns = newton_schulz(coeffs, steps, eps)
-    with _on(x):
-        p, n, _keep = _space(_lib.zero_ns_workspace_bytes(count, rows, cols), ws, x)
-        _check("zero_orthogonalize", _lib.zero_orthogonalize(
-            x.data_ptr(), src_code, count, rows, cols, ld, stride, out.data_ptr(), dst_code,
-            out_ld, out_stride, ctypes.byref(ns), p, n, _stream(x)))
+    p, n, _keep = _space(_lib.zero_ns_workspace_bytes(count, rows, cols), ws, x)
+    _call(index, "zero_orthogonalize", x.data_ptr(), src_code, count, rows, cols, ld, stride,
+          out.data_ptr(), dst_code, out_ld, out_stride,
+          ctypes.byref(newton_schulz(coeffs, steps, eps)), p, n)
     return out
 
 
@@ -136,24 +126,20 @@ def muon_step(master, mom, g, hp: MuonHparams, *, slot=None, ctrl=None, ws=None)
     views of a shard's flat buffers).  slot: the fp16 or bf16 parameters laid
     out like master (a view of the gather buffer).  ctrl: the rank's control
     block, whose clip and skip then apply."""
+    matrices = (master, mom, g) if slot is None else (master, mom, g, slot)
+    index = _gpu(*matrices) if ctrl is None else _gpu(*matrices, ctrl)
     for t in (master, mom, g):
         _code(t.dtype, (torch.float32,))
-    tensors = [master, mom, g] + [t for t in (slot, ctrl) if t is not None]
-    _gpu(*tensors)
-    for t in [master, mom, g] + ([slot] if slot is not None else []):
-        if t.shape != master.shape or not _laid_out(t):
-            raise ValueError("master, mom, g and slot take one shape and layout")
-    count, rows, cols, ld, stride = _stack(master)
-    if master.numel() and (ld != cols or any(_stack(t)[3:] != (ld, stride)
-                                             for t in tensors[1:3] + ([slot] if slot is not None else []))):
-        raise ValueError("master, mom, g and slot: contiguous matrices at one stride")
-    with _on(master):
-        p, n, _keep = _space(_lib.zero_ns_workspace_bytes(count, rows, cols), ws, master)
-        _check("zero_muon_step", _lib.zero_muon_step(
-            master.data_ptr(), mom.data_ptr(), g.data_ptr(), count, rows, cols, stride,
-            ctypes.byref(hp), None if ctrl is None else ctrl.data_ptr(),
-            None if slot is None else slot.data_ptr(),
-            F16 if slot is None else _code(slot.dtype, _HALVES), 0, p, n, _stream(master)))
+    slot_code = F16 if slot is None else _code(slot.dtype, _HALVES)
+    place = _stack(master)
+    count, rows, cols, ld, stride = place
+    for t in matrices:
+        if t.shape != master.shape or not _laid_out(t) or (t.numel() and (ld != cols or _stack(t) != place)):
+            raise ValueError("master, mom, g and slot: one shape, contiguous matrices at one stride")
+    p, n, _keep = _space(_lib.zero_ns_workspace_bytes(count, rows, cols), ws, master)
+    _call(index, "zero_muon_step", master.data_ptr(), mom.data_ptr(), g.data_ptr(), count, rows, cols,
+          stride, ctypes.byref(hp), None if ctrl is None else ctrl.data_ptr(),
+          None if slot is None else slot.data_ptr(), slot_code, 0, p, n)
 
 
 # ----------------------------------------------------------------------------- MXFP4
@@ -166,16 +152,20 @@ class MX4:
 
     def __init__(self, codes, scales, rows: int, cols: int):
         p = (cols + 127) // 128 * 128
-        for t, width, what in ((codes, p // 2, "codes"), (scales, p // 32, "scales")):
+        for t, width in ((codes, p // 2), (scales, p // 32)):
             if t.dtype != torch.uint8 or t.numel() != rows * width or not t.is_contiguous():
-                raise ValueError(f"{what}: {rows * width} contiguous bytes for {rows} x {cols}")
+                raise ValueError(f"{rows} x {cols} takes {rows * p // 2} contiguous bytes of codes and "
+                                 f"{rows * p // 32} of scales")
         self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
 
     @staticmethod
     def alloc(rows: int, cols: int, device) -> "MX4":
         p = (cols + 127) // 128 * 128
-        return MX4(torch.empty((rows, p // 2), dtype=torch.uint8, device=device),
-                   torch.empty((rows, p // 32), dtype=torch.uint8, device=device), rows, cols)
+        q = MX4.__new__(MX4)
+        q.codes = torch.empty((rows, p // 2), dtype=torch.uint8, device=device)
+        q.scales = torch.empty((rows, p // 32), dtype=torch.uint8, device=device)
+        q.rows, q.cols = rows, cols
+        return q
 
 
 def _matrix(x):
@@ -194,32 +184,31 @@ def mx4_quantize(x, rows: bool = True, cols: bool = False):
     code = _code(x.dtype)
     if not rows and not cols:
         raise ValueError("neither rows nor columns")
-    _gpu(x)
+    index = _gpu(x)
     x, ld = _matrix(x)
     m, n = x.shape
     r = MX4.alloc(m, n, x.device) if rows else None
     c = MX4.alloc(n, m, x.device) if cols else None
     if x.numel():
-        with _on(x):
-            _check("zero_mx4_quantize", _lib.zero_mx4_quantize(
-                x.data_ptr(), code, m, n, ld, r and r.codes.data_ptr(), r and r.scales.data_ptr(),
-                c and c.codes.data_ptr(), c and c.scales.data_ptr(), _stream(x)))
-    return (r, c) if rows and cols else r or c
+        _call(index, "zero_mx4_quantize", x.data_ptr(), code, m, n, ld,
+              *((r.codes.data_ptr(), r.scales.data_ptr()) if rows else (None, None)),
+              *((c.codes.data_ptr(), c.scales.data_ptr()) if cols else (None, None)))
+    return (r, c) if rows and cols else r if rows else c
 
 
 def mx4_dequantize(q: MX4, dtype=torch.bfloat16, out=None):
     """The matrix that q stands for."""
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    if tuple(out.shape) != (q.rows, q.cols) or not _laid_out(out):
+        ld = q.cols
+    elif tuple(out.shape) != (q.rows, q.cols) or not _laid_out(out):
         raise ValueError("out: another shape, or rows without unit stride")
-    _gpu(q.codes, q.scales, out)
-    code = _code(out.dtype)
+    else:
+        ld = _stack(out)[3]
+    index, code = _gpu(q.codes, q.scales, out), _code(out.dtype)
     if out.numel():
-        with _on(out):
-            _check("zero_mx4_dequantize", _lib.zero_mx4_dequantize(
-                q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, out.data_ptr(), code,
-                _stack(out)[3], _stream(out)))
+        _call(index, "zero_mx4_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
+              out.data_ptr(), code, ld)
     return out
 
 
@@ -229,34 +218,35 @@ def mx4_matmul(a, b: MX4, out_dtype=torch.bfloat16, *, out=None, accumulate: boo
     same columns.  accumulate adds into ``out`` (fp32)."""
     values = not isinstance(a, MX4)
     m, k = a.shape if values else (a.rows, a.cols)
+    n = b.rows
     if k != b.cols:
         raise ValueError(f"a has {k} columns and b {b.cols}")
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate needs an fp32 out")
     if out is None:
-        out = torch.empty((m, b.rows), dtype=out_dtype, device=b.codes.device)
-    elif tuple(out.shape) != (m, b.rows) or not _laid_out(out):
+        out = torch.empty((m, n), dtype=out_dtype, device=b.codes.device)
+        ldc = n
+    elif tuple(out.shape) != (m, n) or not _laid_out(out):
         raise ValueError("out: another shape, or rows without unit stride")
-    c_code, n = _code(out.dtype), b.rows
+    else:
+        ldc = _stack(out)[3]
+    c_code = _code(out.dtype)
     if values and (m > MX4_ROWS_MAX or accumulate):
         a, values = mx4_quantize(a), False
-    _gpu(b.codes, b.scales, out, *((a,) if values else (a.codes, a.scales)))
-    if not out.numel():
-        return out
-    with _on(out):
-        if values:
-            a_code = _code(a.dtype)
-            a, lda = _matrix(a)
+    if values:
+        index = _gpu(b.codes, b.scales, out, a)
+        a_code = _code(a.dtype)
+        a, lda = _matrix(a)
+        if out.numel():
             p, size, _keep = _space(_lib.zero_mx4_matmul_rows_workspace_bytes(m, n, k), ws, out)
-            _check("zero_mx4_matmul_rows", _lib.zero_mx4_matmul_rows(
-                a.data_ptr(), a_code, lda, b.codes.data_ptr(), b.scales.data_ptr(), m, n, k,
-                out.data_ptr(), c_code, _stack(out)[3], p, size, _stream(out)))
-        else:
+            _call(index, "zero_mx4_matmul_rows", a.data_ptr(), a_code, lda, b.codes.data_ptr(),
+                  b.scales.data_ptr(), m, n, k, out.data_ptr(), c_code, ldc, p, size)
+    else:
+        index = _gpu(b.codes, b.scales, out, a.codes, a.scales)
+        if out.numel():
             p, size, _keep = _space(_lib.zero_mx4_matmul_workspace_bytes(m, n, k), ws, out)
-            _check("zero_mx4_matmul", _lib.zero_mx4_matmul(
-                a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-                m, n, k, out.data_ptr(), c_code, _stack(out)[3], int(accumulate), p, size,
-                _stream(out)))
+            _call(index, "zero_mx4_matmul", a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+                  b.scales.data_ptr(), m, n, k, out.data_ptr(), c_code, ldc, int(accumulate), p, size)
     return out
 
 
@@ -267,35 +257,53 @@ class _Mx4Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
         need_x, need_w = ctx.needs_input_grad
-        xr, xc = mx4_quantize(x, cols=True) if need_w else (mx4_quantize(x), None)
-        wr, wc = mx4_quantize(w, cols=True) if need_x else (mx4_quantize(w), None)
-        keep = [t for q in (xc, wc) if q is not None for t in (q.codes, q.scales)]
-        ctx.save_for_backward(*keep)
-        ctx.sizes = (x.shape[0], w.shape[0], w.shape[1], x.dtype, w.dtype)
-        return mx4_matmul(xr, wr, x.dtype)
+        x, ldx = _matrix(x)
+        w, ldw = _matrix(w)
+        tokens, k = x.shape
+        n = w.shape[0]
+        code, index, dev = _DTYPES[x.dtype], x.get_device(), x.device
+        y = torch.empty((tokens, n), dtype=x.dtype, device=dev)
+        size_x = _lib.zero_mx4_operand_bytes(k, tokens) if need_w else 0
+        size_w = _lib.zero_mx4_operand_bytes(k, n) if need_x else 0
+        kept = torch.empty(size_x + size_w, dtype=torch.uint8, device=dev)  # what the gradients need
+        size = _lib.zero_mx4_linear_workspace_bytes(tokens, n, k)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        at = kept.data_ptr()
+        _call(index, "zero_mx4_linear", x.data_ptr(), ldx, w.data_ptr(), ldw, code, tokens, n, k,
+              y.data_ptr(), n, at if need_w else None, at + size_x if need_x else None,
+              ws.data_ptr(), size)
+        ctx.save_for_backward(kept)
+        ctx.sizes = (tokens, n, k, code, size_x)
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        tokens, n, k, x_dtype, w_dtype = ctx.sizes
+        tokens, n, k, code, size_x = ctx.sizes
         need_x, need_w = ctx.needs_input_grad
-        saved = list(ctx.saved_tensors)
-        dx = dw = None
-        dy, _ = _matrix(dy)
-        q = mx4_quantize(dy, rows=need_x, cols=need_w)
-        dr, dc = q if need_x and need_w else (q, q)
-        if need_w:
-            dw = mx4_matmul(dc, MX4(saved[0], saved[1], k, tokens), w_dtype)
-            saved = saved[2:]
-        if need_x:
-            dx = mx4_matmul(dr, MX4(saved[0], saved[1], k, n), x_dtype)
+        kept, = ctx.saved_tensors
+        dy, ld = _matrix(dy)
+        dev = dy.device
+        dx = torch.empty((tokens, k), dtype=dy.dtype, device=dev) if need_x else None
+        dw = torch.empty((n, k), dtype=dy.dtype, device=dev) if need_w else None
+        size = _lib.zero_mx4_linear_grad_workspace_bytes(tokens, n)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        at = kept.data_ptr()
+        _call(dy.get_device(), "zero_mx4_linear_grad", dy.data_ptr(), ld, code, tokens, n, k,
+              at if need_w else None, at + size_x if need_x else None,
+              dx.data_ptr() if need_x else None, k, dw.data_ptr() if need_w else None, k,
+              ws.data_ptr(), size)
         return dx, dw
 
 
 def mx4_linear(x, w):
-    """x w^T for x [tokens, k] and w [n, k] (fp16, bf16 or fp32), both quantised to
-    MXFP4; differentiable: the gradients are the products of quantised operands
-    too (the rounding itself is passed through)."""
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError("expected x [tokens, k] and w [n, k]")
+    """x w^T for x [tokens, k] and w [n, k] of one type (fp16, bf16 or fp32), both
+    quantised to MXFP4; differentiable: the gradients are the products of quantised
+    operands too (the rounding itself is passed through)."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or not x.numel() or not w.numel():
+        raise ValueError("expected x [tokens, k] and w [n, k], not empty")
+    if x.dtype != w.dtype:
+        raise TypeError(f"x is {x.dtype} and w {w.dtype}")
+    _code(x.dtype)
+    _gpu(x, w)
     return _Mx4Linear.apply(x, w)
