@@ -49,7 +49,6 @@ struct Work {
 // The matrices of zero_orthogonalize.
 template <int DTI, int DTO>
 struct PlainIo {
-    static constexpr bool kInPlace = false;
     const typename Elem<DTI>::type* src;
     typename Elem<DTO>::type* dst;
     int64_t src_ld, src_stride, dst_ld, dst_stride;
@@ -57,9 +56,16 @@ struct PlainIo {
 
     __device__ float clip() const { return 1.0f; }
     // first reading of an element, and any later one
-    __device__ float first(int b, int r, int c, float) const { return again(b, r, c, 1.0f); }
-    __device__ float again(int b, int r, int c, float) const {
+    __device__ float first(int b, int r, int64_t c, float) const { return again(b, r, c, 1.0f); }
+    __device__ float again(int b, int r, int64_t c, float) const {
         return to_float<DTI>(src[b * src_stride + r * src_ld + c]);
+    }
+    __device__ bool contiguous() const { return src_ld == cols; }
+    __device__ void first4(int b, int r, int64_t c, float, float* v) const {  // vectors at any alignment
+        typename Elem<DTI>::type x[4];
+        __builtin_memcpy(x, src + b * src_stride + r * src_ld + c, sizeof(x));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = to_float<DTI>(x[e]);
     }
     __device__ void put(int b, int r, int c, float o) const {
         dst[b * dst_stride + r * dst_ld + c] = from_float<DTO>(o);
@@ -69,7 +75,6 @@ struct PlainIo {
 // The matrices of zero_muon_step: the momentum is updated at the first reading.
 template <int DTO>
 struct MuonIo {
-    static constexpr bool kInPlace = true;
     float* master;
     float* mom;
     const float* g;
@@ -82,13 +87,27 @@ struct MuonIo {
 
     __device__ float clip() const { return ctrl != nullptr ? ctrl->clip : 1.0f; }
     __device__ float direction(float gi, float m) const { return nesterov ? one_mu * gi + mu * m : m; }
-    __device__ float first(int b, int r, int c, float clip) const {
+    __device__ float first(int b, int r, int64_t c, float clip) const {
         const int64_t i = b * stride + (int64_t)r * cols + c;
         const float gi = g[i] * clip, m = mu * mom[i] + one_mu * gi;
         mom[i] = m;
         return direction(gi, m);
     }
-    __device__ float again(int b, int r, int c, float clip) const {
+    __device__ bool contiguous() const { return true; }
+    __device__ void first4(int b, int, int64_t c, float clip, float* v) const {
+        const int64_t i = b * stride + c;
+        float gi[4], m[4];
+        __builtin_memcpy(gi, g + i, sizeof(gi));
+        __builtin_memcpy(m, mom + i, sizeof(m));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            gi[e] *= clip;
+            m[e] = mu * m[e] + one_mu * gi[e];
+            v[e] = direction(gi[e], m[e]);
+        }
+        __builtin_memcpy(mom + i, m, sizeof(m));
+    }
+    __device__ float again(int b, int r, int64_t c, float clip) const {
         const int64_t i = b * stride + (int64_t)r * cols + c;
         return direction(g[i] * clip, mom[i]);
     }
@@ -126,25 +145,31 @@ __device__ __forceinline__ double block_sum(double v, double* red, int waves) {
 // operand is kept in two fp16 parts (high and rest; three products in place of one),
 // which makes the iteration as exact as fp32: 1e-5 against 64 bits.
 //
-// A workgroup holds a strip of X in registers, in the layout of the matrix
-// cores' results: blocks of T x T, each by a group of waves with CT tiles of
-// 32 x 32 elements per wave; G groups side by side and NB blocks after each other,
-// so a strip is G * NB * T columns.  Eight waves, so that a wave has 256 registers:
-// sixteen with half of them spilled a hundred and took twice as long.  A matrix of one strip takes one
-// launch for all its steps; a longer one takes, per step, one workgroup that
-// makes M from the strips' parts of S, and one workgroup per strip that
-// applies M and makes its part of the next S.
-template <int T_, int CT_, int G_, int NB_>
+// A workgroup of sixteen waves holds a strip of X in registers, in the layout of the
+// matrix cores' results: blocks of T x T, each by a group of waves with RT x RT tiles
+// of 16 x 16 per wave; G groups side by side and NB blocks after each other, so a
+// strip is G * NB * T columns.  A matrix of one strip takes one launch for all its
+// steps.  A longer one takes a launch a step, a workgroup a strip: it makes M from all
+// the strips' parts of S, applies it to its own columns and writes its part of the
+// next S.  Past kFused strips, reading all the parts in every strip costs more than
+// one workgroup that makes M in a launch of its own.
+//
+// What bounds a step is its chain of barriers and the arithmetic of splitting and
+// storing, not the products: hence many waves with small tiles (eight waves
+// with 32 x 32 tiles took 4.3 us a step at 64 x 64 and 10 at 128 x 128).
+template <int T_, int RT_, int G_, int NB_>
 struct Strip {
-    static constexpr int T = T_, CT = CT_, G = G_, NB = NB_;
-    static constexpr int TILES = T / 32 / CT, GROUP = T / 32 * TILES, WAVES = G * GROUP, THREADS = WAVES * 64;
+    static constexpr int T = T_, RT = RT_, G = G_, NB = NB_;
+    static constexpr int SIDE = T / 16 / RT, GROUP = SIDE * SIDE, WAVES = G * GROUP, THREADS = WAVES * 64;
     static constexpr int COLS = G * NB * T;
     static constexpr int ARRAY = T * T * 2;  // bytes of a T x T fp16 array
+    static constexpr int VALUES = RT * RT * 4;  // of a block, per lane
     static constexpr int SIZE = COLS * T;    // elements of a strip
 };
-typedef Strip<32, 1, 8, 4> Strip32;
-typedef Strip<64, 1, 2, 4> Strip64;
+typedef Strip<32, 1, 4, 8> Strip32;
+typedef Strip<64, 1, 1, 8> Strip64;
 typedef Strip<128, 2, 1, 2> Strip128;
+constexpr int kFused = 32;
 
 struct Pair {  // high part and rest, arrays in LDS
     char *hi, *lo;
@@ -153,79 +178,41 @@ struct Pair {  // high part and rest, arrays in LDS
 template <int T>
 __device__ __forceinline__ int small_at(int row, int col) {  // byte of an element of a swizzled T x T fp16 array
     constexpr int kPieces = T / 8;
-    return row * T * 2 + (((col >> 3) ^ (row & (kPieces - 1))) << 4) + (col & 7) * 2;
+    return row * T * 2 + (((col >> 3) ^ ((row / (128 / T)) & (kPieces - 1))) << 4) + (col & 7) * 2;
 }
 
-template <int T>
-__device__ __forceinline__ f16x8 small_frag(const char* a, int row, int kk, int h) {
-    return *(const f16x8*)(a + small_at<T>(row, kk * 16 + h * 8));
+// Two dwords of four 16-bit values each: those of four neighbouring lanes turned, as
+// quad_turn does.
+__device__ __forceinline__ uint32_t lane_xor1(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t lane_xor2(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+}
+__device__ __forceinline__ u32x2 quad_turn16(u32x2 d) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    // even lanes: the low halves of (own, other); odd lanes: the high halves of (other, own)
+    const uint32_t pick = odd ? 0x07060302u : 0x01000504u;
+    const uint32_t a = __builtin_amdgcn_perm(d[0], lane_xor1(d[0]), pick);
+    const uint32_t b = __builtin_amdgcn_perm(d[1], lane_xor1(d[1]), pick);
+    const uint32_t o = lane_xor2(high ? a : b);
+    return u32x2{high ? o : a, high ? b : o};
 }
 
-// acc += A B^T of two pairs over the first `pieces` 16 columns, the product of the
-// two rests left out: a wave's CT tiles from row i0, columns j0, + 32, ...  The next
-// k step's fragments are read while one multiplies.
-template <int T, int CT>
-struct SmallFrags {
-    f16x8 ah, al, bh[CT], bl[CT];
-    __device__ __forceinline__ void load(const Pair& A, const Pair& B, int i0, int j0, int kk, const Lane& L) {
-        ah = small_frag<T>(A.hi, i0 + L.c, kk, L.h);
-        al = small_frag<T>(A.lo, i0 + L.c, kk, L.h);
+// Four values as two dwords of fp16, and what that leaves.
+__device__ __forceinline__ void split4(const float* x, u32x2& h, u32x2& l) {
+    f16x4 a, b;
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            bh[t] = small_frag<T>(B.hi, j0 + 32 * t + L.c, kk, L.h);
-            bl[t] = small_frag<T>(B.lo, j0 + 32 * t + L.c, kk, L.h);
-        }
+    for (int r = 0; r < 4; ++r) {
+        a[r] = (_Float16)x[r];
+        b[r] = (_Float16)(x[r] - (float)a[r]);
     }
-    __device__ __forceinline__ void multiply(f32x16 (&acc)[CT]) const {
-#pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh[t], acc[t], 0, 0, 0);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl[t], acc[t], 0, 0, 0);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh[t], acc[t], 0, 0, 0);
-    }
-};
-
-template <int T, int CT>
-__device__ __forceinline__ void small_product(const Pair& A, const Pair& B, int i0, int j0, int pieces, const Lane& L,
-                                              f32x16 (&acc)[CT]) {
-    SmallFrags<T, CT> f, g;
-    f.load(A, B, i0, j0, 0, L);
-#pragma unroll 1
-    for (int kk = 0; kk < pieces; kk += 2) {  // an odd one more meets zeros; past the end the first is read again
-        g.load(A, B, i0, j0, kk + 1, L);
-        f.multiply(acc);
-        f.load(A, B, i0, j0, (kk + 2) % (T / 16), L);
-        g.multiply(acc);
-    }
+    h = __builtin_bit_cast(u32x2, a);
+    l = __builtin_bit_cast(u32x2, b);
 }
 
-// A wave's tiles into a pair; TURNED: into its transpose.
-template <int T, int CT, bool TURNED>
-__device__ __forceinline__ void small_store(const Pair& P, int i0, int j0, const Lane& L, const float (&v)[CT][16]) {
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float x[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = v[t][4 * q + r];
-            if constexpr (!TURNED) quad_turn(x);  // four columns of one row
-            f16x4 h, l;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                h[r] = (_Float16)x[r];
-                l[r] = (_Float16)(x[r] - (float)h[r]);
-            }
-            const int i = i0 + 8 * q + 4 * L.h, j = j0 + 32 * t;
-            const int at = TURNED ? small_at<T>(j + L.c, i) : small_at<T>(i + (L.c & 3), j + (L.c & ~3));
-            *(f16x4*)(P.hi + at) = h;
-            *(f16x4*)(P.lo + at) = l;
-        }
-}
-
-// LDS of a strip's workgroup: a pair per group for its current block of X (or the
-// groups' parts of S), one for S and then M, the diagonals.
+// LDS of a strip's workgroup: two pairs per group for its current block of X, row-major
+// and transposed (or the groups' parts of S), one for S and then M, the diagonals.
 template <class P>
 struct StripLds {
     __attribute__((aligned(16))) char block[P::G * 2 * P::ARRAY];
@@ -236,141 +223,191 @@ struct StripLds {
 
 template <class P>
 struct StripWave {
-    static constexpr int T = P::T, CT = P::CT;
-    typedef float Tiles[CT][16];
-    Lane L;
-    int group, i0, j0;  // this wave's group, and its tiles' place in a block
+    static constexpr int T = P::T, RT = P::RT;
+    typedef float Tiles[RT][RT][4];
+    int lane, quarter, c;  // lane / 16, lane % 16
+    int group, i0, j0;     // this wave's group, and its tiles' place in a block
     StripLds<P>& lds;
     Pair mine, square;
+    int side;        // 32-column pieces of the smaller side
+    bool live, both; // whether this wave's rows, and its columns too, meet the smaller side
 
-    int side, live;  // 16-column pieces of the smaller side; whether this wave's rows have any
-
-    __device__ StripWave(StripLds<P>& s, int m) : lds(s) {
-        group = L.wave / P::GROUP;
-        i0 = L.wave % P::GROUP / P::TILES * 32;
-        j0 = L.wave % P::TILES * 32 * CT;
+    __device__ __forceinline__ StripWave(StripLds<P>& s, int m) : lds(s) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        quarter = lane >> 4;
+        c = lane & 15;
+        group = wave / P::GROUP;
+        i0 = wave % P::GROUP / P::SIDE * 16 * RT;
+        j0 = wave % P::SIDE * 16 * RT;
         mine = {s.block + group * 2 * P::ARRAY, s.block + (group * 2 + 1) * P::ARRAY};
         square = {s.square, s.square + P::ARRAY};
-        side = (m + 15) / 16;
+        side = (m + 31) / 32;
         live = i0 < m;
+        both = live && j0 < m;
     }
-    __device__ __forceinline__ int row(int r) const { return i0 + 8 * (r / 4) + 4 * L.h + r % 4; }
-    __device__ __forceinline__ int at(int t) const { return j0 + 32 * t + L.c; }  // column within a block
-    __device__ __forceinline__ int col(int b, int t) const { return (b * P::G + group) * T + at(t); }  // within the strip
+    __device__ __forceinline__ int row(int a, int r) const { return i0 + 16 * a + 4 * quarter + r; }
+    __device__ __forceinline__ int at(int b) const { return j0 + 16 * b + c; }  // column within a block
+    __device__ __forceinline__ int col(int n, int b) const { return (n * P::G + group) * T + at(b); }  // within the strip
 
-    __device__ __forceinline__ void product(const Pair& A, const Pair& B, f32x16 (&acc)[CT]) const {
+    // Forgets what the compiler knows of the lane's place, so that it works addresses
+    // and bounds out again rather than keep them in registers across the steps.
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(c), "+v"(quarter)); }
+
+    __device__ __forceinline__ f16x8 frag(const char* a, int first, int kk) const {
+        return *(const f16x8*)(a + small_at<T>(first + c, kk * 32 + quarter * 8));
+    }
+    // acc += A B^T of two pairs over the first `pieces` 32 columns, the product of the two
+    // rests left out.
+    __device__ __forceinline__ void product(const Pair& A, const Pair& B, int pieces, f32x4 (&acc)[RT][RT]) const {
+#pragma unroll 1
+        for (int kk = 0; kk < pieces; ++kk) {
+            f16x8 ah[RT], al[RT], bh[RT], bl[RT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
+            for (int t = 0; t < RT; ++t) {
+                ah[t] = frag(A.hi, i0 + 16 * t, kk);
+                bh[t] = frag(B.hi, j0 + 16 * t, kk);
+                al[t] = frag(A.lo, i0 + 16 * t, kk);
+                bl[t] = frag(B.lo, j0 + 16 * t, kk);
+            }
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[t][r] = 0.0f;
-        if (live) small_product<T, CT>(A, B, i0, j0, side, L, acc);
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int b = 0; b < RT; ++b)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[a], bh[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int b = 0; b < RT; ++b)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(al[a], bh[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int b = 0; b < RT; ++b)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[a], bl[b], acc[a][b], 0, 0, 0);
+        }
+    }
+    // This wave's tiles into a pair; TURNED: into its transpose.
+    template <bool TURNED>
+    __device__ __forceinline__ void store(const Pair& P_, const Tiles& v) const {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b) {
+                u32x2 h, l;
+                split4(v[a][b], h, l);
+                int to;
+                if constexpr (TURNED) {
+                    to = small_at<T>(at(b), row(a, 0));
+                } else {
+                    h = quad_turn16(h);  // four columns of one row
+                    l = quad_turn16(l);
+                    to = small_at<T>(row(a, c & 3), j0 + 16 * b + (c & ~3));
+                }
+                *(u32x2*)(P_.hi + to) = h;
+                *(u32x2*)(P_.lo + to) = l;
+            }
+    }
+    static __device__ __forceinline__ void zero(f32x4 (&acc)[RT][RT]) {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
+    }
+    // f(a, b, r) for every value of a block
+    template <class F>
+    static __device__ __forceinline__ void values(F f) {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f(a, b, r);
     }
 
     // This wave's tiles of S = X X^T of the strip's first nb blocks of every group.
     // cols: the strip's columns.
     __device__ __forceinline__ void gram(const Tiles (&x)[P::NB], int nb, int cols, Tiles& s) {
-        f32x16 acc[CT];
+        f32x4 acc[RT][RT];
+        zero(acc);
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[t][r] = 0.0f;
-#pragma unroll
-        for (int b = 0; b < P::NB; ++b) {
-            if (b >= nb) break;
+        for (int n = 0; n < P::NB; ++n) {
+            if (n >= nb) break;
             __syncthreads();  // the block's last readers are done
-            small_store<T, CT, false>(mine, i0, j0, L, x[b]);
+            store<false>(mine, x[n]);
             __syncthreads();
-            const int left = cols - (b * P::G + group) * T, k = left < T ? left : T;
-            if (live && k > 0) small_product<T, CT>(mine, mine, i0, j0, (k + 15) / 16, L, acc);
+            const int left = cols - (n * P::G + group) * T, k = left < T ? left : T;
+            if (both && k > 0) product(mine, mine, (k + 31) / 32, acc);
         }
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[t][r] = acc[t][r] * (1.0f / (kXScale * kXScale));
+        values([&](int a, int b, int r) { s[a][b][r] = acc[a][b][r] * (1.0f / (kXScale * kXScale)); });
         if constexpr (P::G > 1) {
             float* parts = (float*)lds.block;
             __syncthreads();
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) parts[group * T * T + row(r) * T + at(t)] = s[t][r];
+            values([&](int a, int b, int r) { parts[group * T * T + row(a, r) * T + at(b)] = s[a][b][r]; });
             __syncthreads();
+            values([&](int a, int b, int r) {
+                float v = 0.0f;
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int g = 0; g < P::G; ++g) v += parts[g * T * T + row(r) * T + at(t)];
-                    s[t][r] = v;
-                }
+                for (int g = 0; g < P::G; ++g) v += parts[g * T * T + row(a, r) * T + at(b)];
+                s[a][b][r] = v;
+            });
         }
     }
 
-    // M from S, which every group holds: m this wave's tiles off the diagonal
-    // (times mscale), lds.dm the diagonal.
-    __device__ __forceinline__ void poly(const Coeffs& k, Tiles& s, Tiles& m) {
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const bool diag = row(r) == at(t);
-                if (diag && group == 0) lds.ds[row(r)] = s[t][r];
-                s[t][r] = diag ? 0.0f : s[t][r];
-                m[t][r] = s[t][r] * kSScale;
-            }
-        if (group == 0) small_store<T, CT, true>(square, i0, j0, L, m);  // symmetric
+    // M from S, which every group holds: into the square pair, the diagonal into lds.dm.
+    // No barrier after the last writes.
+    __device__ __forceinline__ void poly(const Coeffs& k, Tiles& s) {
+        Tiles v;
+        values([&](int a, int b, int r) {
+            const bool diag = row(a, r) == at(b);
+            if (diag && group == 0) lds.ds[row(a, r)] = s[a][b][r];
+            s[a][b][r] = diag ? 0.0f : s[a][b][r];
+            v[a][b][r] = s[a][b][r] * kSScale;
+        });
+        if (group == 0) store<true>(square, v);  // symmetric: its transpose
         __syncthreads();
-        f32x16 acc[CT];
-        product(square, square, acc);
+        f32x4 acc[RT][RT];
+        zero(acc);
+        if (both) product(square, square, side, acc);
+        float dj[RT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int i = row(r), j = at(t);
-                const float di = lds.ds[i];
-                float s2 = acc[t][r] * (1.0f / (kSScale * kSScale)) + s[t][r] * (di + lds.ds[j]);
-                if (i == j) {
-                    s2 += di * di;
-                    if (group == 0) lds.dm[i] = k.a + k.b * di + k.c * s2;
-                }
-                m[t][r] = i == j ? 0.0f : (k.b * s[t][r] + k.c * s2) * k.mscale;
+        for (int b = 0; b < RT; ++b) dj[b] = lds.ds[at(b)];
+        values([&](int a, int b, int r) {
+            const float di = lds.ds[row(a, r)];
+            float s2 = acc[a][b][r] * (1.0f / (kSScale * kSScale)) + s[a][b][r] * (di + dj[b]);
+            v[a][b][r] = (k.b * s[a][b][r] + k.c * s2) * k.mscale;
+            if (row(a, r) == at(b)) {
+                s2 += di * di;
+                if (group == 0) lds.dm[row(a, r)] = k.a + k.b * di + k.c * s2;
+                v[a][b][r] = 0.0f;
             }
+        });
         __syncthreads();  // the readers of S are done
+        if (group == 0) store<true>(square, v);
     }
 
-    // X <- M X; M's pair is written by the caller before, without a barrier.
+    // X <- M X; M's pair and diagonal are written just before, without a barrier.
     __device__ __forceinline__ void apply(const Coeffs& k, int nb, Tiles (&x)[P::NB]) {
         const float un = 1.0f / k.mscale;
 #pragma unroll
-        for (int b = 0; b < P::NB; ++b) {
-            if (b >= nb) break;
-            if (b > 0) __syncthreads();
-            small_store<T, CT, true>(mine, i0, j0, L, x[b]);
+        for (int n = 0; n < P::NB; ++n) {
+            if (n >= nb) break;
+            if (n > 0) __syncthreads();
+            store<true>(mine, x[n]);
             __syncthreads();
-            f32x16 acc[CT];
-            product(square, mine, acc);
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) x[b][t][r] = lds.dm[row(r)] * x[b][t][r] + acc[t][r] * un;
+            f32x4 acc[RT][RT];
+            zero(acc);
+            if (live) product(square, mine, side, acc);
+            values([&](int a, int b, int r) { x[n][a][b][r] = lds.dm[row(a, r)] * x[n][a][b][r] + acc[a][b][r] * un; });
         }
     }
 
-    // Forgets what the compiler knows of the lane's place, so that it works addresses
-    // and bounds out again rather than keep them in registers across the steps (a
-    // hundred spilled registers otherwise).
-    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(L.c), "+v"(L.h)); }
-
-    // every value of a strip: f(block, tile, value's number, row, column in the strip)
+    // every value of a strip: f(value, row, column in the strip)
     template <class F>
-    __device__ __forceinline__ void each(F f) const {
+    __device__ __forceinline__ void each(Tiles (&x)[P::NB], F f) const {
 #pragma unroll
-        for (int b = 0; b < P::NB; ++b)
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) f(b, t, r, row(r), col(b, t));
+        for (int n = 0; n < P::NB; ++n)
+            values([&](int a, int b, int r) { f(x[n][a][b][r], row(a, r), col(n, b)); });
     }
 };
 
@@ -382,11 +419,12 @@ struct StripArgs {
     const int32_t* skip;
     // several strips a matrix:
     char* ws;
-    int64_t stride;     // bytes from one matrix's workspace to the next
-    int64_t parts, mat; // byte offsets of the strips' parts of S and of M; X at 0
+    int64_t stride;             // bytes from one matrix's workspace to the next
+    int64_t parts, next, mat;   // byte offsets of the strips' parts of S, now and next, and of M; X at 0
     int64_t sums;
     int sum_parts, strips;
-    int step;           // 0: normalise; k: apply the k-th M
+    int step;                   // 0: normalise; k: apply the k-th M
+    int fused;                  // M is made in every strip
 };
 
 // The whole iteration of a matrix of one strip.
@@ -401,46 +439,54 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     StripWave<P> w(lds, m);
     const int nb = (n + P::G * P::T - 1) / (P::G * P::T);
     const float clip = io.clip();
-    typename StripWave<P>::Tiles x[P::NB], s, mv;
+    typename StripWave<P>::Tiles x[P::NB], s;
     double ss = 0.0;
-    w.each([&](int bl, int t, int r, int i, int j) {
-        const float v = i < m && j < n ? io.first(b, tall ? j : i, tall ? i : j, clip) : 0.0f;
+    w.each(x, [&](float& v, int i, int j) {
+        v = i < m && j < n ? io.first(b, tall ? j : i, tall ? i : j, clip) : 0.0f;
         ss += (double)v * (double)v;
-        x[bl][t][r] = v;
     });
     const double scale = scale_of(sqrt(block_sum(ss, lds.red, P::WAVES)), a.k.eps);
-    w.each([&](int bl, int t, int r, int, int) { x[bl][t][r] = (float)(x[bl][t][r] * scale); });
+    w.each(x, [&](float& v, int, int) { v = (float)(v * scale); });
     w.forget();
 #pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
         w.gram(x, nb, n, s);
-        w.poly(a.k, s, mv);
-        if (w.group == 0) small_store<P::T, P::CT, true>(w.square, w.i0, w.j0, w.L, mv);
+        w.poly(a.k, s);
         w.apply(a.k, nb, x);
     }
     w.forget();
-    w.each([&](int bl, int t, int r, int i, int j) {
-        if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, x[bl][t][r] * (1.0f / kXScale));
+    w.each(x, [&](float& v, int i, int j) {
+        if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, v * (1.0f / kXScale));
     });
 }
 
-// M of a matrix of several strips: fp32 [T][T] off the diagonal, then the diagonal.
+// S of a matrix of several strips, this wave's tiles: the sum of the strips' parts.
+template <class P, class W, class IO>
+__device__ __forceinline__ void sum_parts_of(const W& w, const StripArgs<IO>& a, const char* ws, typename W::Tiles& s) {
+    const float* parts = (const float*)(ws + a.parts);
+    W::values([&](int i, int j, int r) { s[i][j][r] = 0.0f; });
+#pragma unroll 4
+    for (int p = 0; p < a.strips; ++p)
+        W::values([&](int i, int j, int r) {
+            s[i][j][r] += parts[(int64_t)p * P::T * P::T + w.row(i, r) * P::T + w.at(j)];
+        });
+}
+
+// M of a matrix of many strips: both parts of its pair, then the diagonal.
 template <class P, class IO>
 __global__ void __launch_bounds__(P::GROUP * 64) ns_poly_kernel(StripArgs<IO> a) {
-    typedef Strip<P::T, P::CT, 1, 1> One;
+    typedef Strip<P::T, P::RT, 1, 1> One;
     __shared__ StripLds<One> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
     StripWave<One> w(lds, a.io.rows < a.io.cols ? a.io.rows : a.io.cols);
     char* ws = a.ws + blockIdx.x * a.stride;
-    const float* parts = (const float*)(ws + a.parts);
-    typename StripWave<One>::Tiles s, mv;
-    w.each([&](int, int t, int r, int, int) { s[t][r] = 0.0f; });
-    for (int p = 0; p < a.strips; ++p)
-        w.each([&](int, int t, int r, int i, int j) { s[t][r] += parts[(int64_t)p * P::T * P::T + i * P::T + j]; });
-    w.poly(a.k, s, mv);
-    float* mat = (float*)(ws + a.mat);
-    w.each([&](int, int t, int r, int i, int j) { mat[i * P::T + j] = mv[t][r]; });
-    for (int i = threadIdx.x; i < P::T; i += One::THREADS) mat[P::T * P::T + i] = lds.dm[i];
+    typename StripWave<One>::Tiles s;
+    sum_parts_of<P>(w, a, ws, s);
+    w.poly(a.k, s);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * P::ARRAY / 16; i += One::THREADS)
+        ((u32x4*)(ws + a.mat))[i] = ((const u32x4*)lds.square)[i];
+    for (int i = threadIdx.x; i < P::T; i += One::THREADS) ((float*)(ws + a.mat + 2 * P::ARRAY))[i] = lds.dm[i];
 }
 
 // One strip: step 0 makes X; step k applies the k-th M; the last one writes the
@@ -456,50 +502,48 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     StripWave<P> w(lds, m);
     const int left = n - j0 < P::COLS ? n - j0 : P::COLS, nb = (left + P::G * P::T - 1) / (P::G * P::T);
     char* ws = a.ws + b * a.stride;
-    float* mine = (float*)ws + (int64_t)strip * P::SIZE + w.L.wave * (P::NB * P::CT * 1024) + w.L.lane;
+    float* mine = (float*)ws + (int64_t)strip * P::SIZE + threadIdx.x;
     typename StripWave<P>::Tiles x[P::NB], s;
+    int slot = 0;
     if (a.step == 0) {
         double ss = 0.0;
         for (int p = threadIdx.x; p < a.sum_parts; p += P::THREADS) ss += ((const double*)(ws + a.sums))[p];
         const double scale = scale_of(sqrt(block_sum(ss, lds.red, P::WAVES)), a.k.eps);
         const float clip = io.clip();
-        w.each([&](int bl, int t, int r, int i, int jj) {
+        w.each(x, [&](float& v, int i, int jj) {
             const int j = j0 + jj;
-            x[bl][t][r] = i < m && j < n ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
+            v = i < m && j < n ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
         });
     } else {
-        w.each([&](int bl, int t, int r, int, int) { x[bl][t][r] = mine[((bl * P::CT + t) * 16 + r) * 64]; });
-        const float* mat = (const float*)(ws + a.mat);
-        if (w.group == 0) {
-            w.each([&](int bl, int t, int r, int i, int) {
-                if (bl == 0) s[t][r] = mat[i * P::T + w.at(t)];
-            });
-            small_store<P::T, P::CT, true>(w.square, w.i0, w.j0, w.L, s);
+        w.each(x, [&](float& v, int, int) { v = mine[slot++ * P::THREADS]; });
+        if (a.fused) {
+            sum_parts_of<P>(w, a, ws, s);
+            w.poly(a.k, s);
+        } else {
+            for (int i = threadIdx.x; i < 2 * P::ARRAY / 16; i += P::THREADS)
+                ((u32x4*)lds.square)[i] = ((const u32x4*)(ws + a.mat))[i];
+            for (int i = threadIdx.x; i < P::T; i += P::THREADS) lds.dm[i] = ((const float*)(ws + a.mat + 2 * P::ARRAY))[i];
         }
-        for (int i = threadIdx.x; i < P::T; i += P::THREADS) lds.dm[i] = mat[P::T * P::T + i];
         w.apply(a.k, nb, x);
     }
     if (a.step == a.steps) {
-        w.each([&](int bl, int t, int r, int i, int jj) {
+        w.each(x, [&](float& v, int i, int jj) {
             const int j = j0 + jj;
-            if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, x[bl][t][r] * (1.0f / kXScale));
+            if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, v * (1.0f / kXScale));
         });
         return;
     }
-    w.each([&](int bl, int t, int r, int, int) { mine[((bl * P::CT + t) * 16 + r) * 64] = x[bl][t][r]; });
+    slot = 0;
+    w.each(x, [&](float& v, int, int) { mine[slot++ * P::THREADS] = v; });
     w.gram(x, nb, left, s);
-    float* part = (float*)(ws + a.parts) + (int64_t)strip * P::T * P::T;
-    if (w.group == 0) {
-#pragma unroll
-        for (int t = 0; t < P::CT; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) part[w.row(r) * P::T + w.at(t)] = s[t][r];
-    }
+    float* part = (float*)(ws + a.next) + (int64_t)strip * P::T * P::T;
+    if (w.group == 0)
+        w.values([&](int i, int j, int r) { part[w.row(i, r) * P::T + w.at(j)] = s[i][j][r]; });
 }
 
 // ---------------------------------------------------------------- large matrices
 constexpr int kSumThreads = 256;
-constexpr int64_t kSumElems = 16384;  // elements per partial sum of squares, at least
+constexpr int64_t kSumElems = 8192;  // elements per partial sum of squares, at least
 constexpr int kMaxParts = 1024;
 
 template <class IO>
@@ -509,22 +553,31 @@ struct IoArgs {
     float eps;
 };
 
-// One partial of the squared norm per workgroup (and the momentum update):
-// rows blockIdx.x, + gridDim.x, ...
+// One partial of the squared norm per workgroup (and the momentum update): runs of
+// kSumRun elements, four per thread; contiguous matrices as one long row.
+constexpr int kSumRun = 4 * kSumThreads;
 template <class IO>
 __global__ void __launch_bounds__(kSumThreads) ns_sum_kernel(IoArgs<IO> a) {
     __shared__ double red[kSumThreads / 64];
     if (a.w.skipped()) return;
-    const int b = blockIdx.y, cols = a.io.cols;
-    const int64_t elems = (int64_t)a.io.rows * cols;
+    const int b = blockIdx.y;
+    const bool flat = a.io.contiguous();
+    const int64_t cols = flat ? (int64_t)a.io.rows * a.io.cols : a.io.cols;
+    const uint32_t across = (uint32_t)((cols + kSumRun - 1) / kSumRun), runs = across * (flat ? 1 : a.io.rows);
     const float clip = a.io.clip();
-    const int64_t per = (elems + gridDim.x - 1) / gridDim.x;
-    const int64_t e0 = blockIdx.x * per, e1 = e0 + per < elems ? e0 + per : elems;
     double ss = 0.0;
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += kSumThreads) {
-        const int r = (int)(e / cols), c = (int)(e - (int64_t)r * cols);
-        const float v = a.io.first(b, r, c, clip);
-        ss += (double)v * (double)v;
+    for (uint32_t run = blockIdx.x; run < runs; run += gridDim.x) {
+        const int r = (int)(run / across);
+        const int64_t c = (int64_t)(run % across) * kSumRun + threadIdx.x * 4;
+        if (c >= cols) continue;
+        float v[4] = {0, 0, 0, 0};
+        if (c + 4 <= cols) {
+            a.io.first4(b, r, c, clip, v);
+        } else {
+            for (int e = 0; c + e < cols; ++e) v[e] = a.io.first(b, r, c + e, clip);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ss += (double)v[e] * (double)v[e];
     }
     const double t = block_sum(ss, red, kSumThreads / 64);
     if (threadIdx.x == 0) ((double*)(a.w.of(b) + a.w.sums))[blockIdx.x] = t;
@@ -866,15 +919,16 @@ auto with_strip(int64_t rows, int64_t cols, F f) {
 
 // Workspace of one narrow matrix of several strips: X, the parts of S, M, the sums.
 struct StripWork {
-    int64_t parts, mat, sums, stride;
+    int64_t parts[2], mat, sums, stride;
 };
 
 template <class P>
 StripWork strip_work(int strips, int sum_parts) {
     StripWork w;
-    w.parts = round_up((int64_t)strips * P::SIZE * 4, 256);
-    w.mat = w.parts + round_up((int64_t)strips * P::T * P::T * 4, 256);
-    w.sums = w.mat + round_up((P::T * P::T + P::T) * 4, 256);
+    w.parts[0] = round_up((int64_t)strips * P::SIZE * 4, 256);
+    w.parts[1] = w.parts[0] + round_up((int64_t)strips * P::T * P::T * 4, 256);
+    w.mat = w.parts[1] + round_up((int64_t)strips * P::T * P::T * 4, 256);
+    w.sums = w.mat + round_up(2 * P::ARRAY + P::T * 4, 256);
     w.stride = w.sums + round_up((int64_t)sum_parts * 8, 256);
     return w;
 }
@@ -951,12 +1005,11 @@ int run_strips(const IO& io, int32_t count, const zero_newton_schulz& ns, const 
                void* ws, hipStream_t s, const char* what) {
     return with_strip(io.rows, io.cols, [&](auto shape, int strips) {
         typedef decltype(shape) P;
-        StripArgs<IO> a{io, k, ns.steps, skip, (char*)ws, 0, 0, 0, 0, 0, strips, 0};
+        StripArgs<IO> a{io, k, ns.steps, skip, (char*)ws, 0, 0, 0, 0, 0, 0, strips, 0, strips <= kFused};
         const dim3 each((unsigned)count);
         if (strips == 1) return launch(ns_strip_kernel<P, IO>, each, P::THREADS, s, a, what);
         a.sum_parts = sum_parts(io.rows, io.cols);
         const StripWork w = strip_work<P>(strips, a.sum_parts);
-        a.parts = w.parts;
         a.mat = w.mat;
         a.sums = w.sums;
         a.stride = w.stride;
@@ -968,7 +1021,9 @@ int run_strips(const IO& io, int32_t count, const zero_newton_schulz& ns, const 
         int rc = launch(ns_sum_kernel<IO>, dim3((unsigned)a.sum_parts, (unsigned)count), kSumThreads, s,
                         IoArgs<IO>{io, sum, ns.eps}, what);
         for (a.step = 0; rc == ZERO_OK && a.step <= ns.steps; ++a.step) {
-            if (a.step > 0) rc = launch(ns_poly_kernel<P, IO>, each, P::GROUP * 64, s, a, what);
+            a.parts = w.parts[a.step & 1];  // a strip may still read them when another one writes the next
+            a.next = w.parts[(a.step + 1) & 1];
+            if (a.step > 0 && !a.fused) rc = launch(ns_poly_kernel<P, IO>, each, P::GROUP * 64, s, a, what);
             if (rc == ZERO_OK)
                 rc = launch(ns_strips_kernel<P, IO>, dim3((unsigned)strips, (unsigned)count), P::THREADS, s, a, what);
         }
