@@ -609,8 +609,8 @@ typedef struct zero_newton_schulz {
 } zero_newton_schulz;
 
 /* Bytes of device workspace for zero_orthogonalize and zero_muon_step over
- * such a stack (16-byte aligned; 0 where one workgroup holds a whole matrix:
- * up to 32 x 1024, 64 x 512 or 128 x 256).  0 for sizes the calls refuse. */
+ * such a stack (16-byte aligned; 0 where a workgroup holds a whole matrix, among
+ * them all with both sides up to 128).  0 for sizes the calls refuse. */
 size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
 
 /* dst[b] = orthogonalisation of src[b].  src: src_dtype ZERO_F16, ZERO_BF16

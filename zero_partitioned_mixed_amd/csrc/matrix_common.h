@@ -393,6 +393,24 @@ __device__ __forceinline__ void quad_turn(float (&v)[4]) {
     }
 }
 
+// Two dwords of four 16-bit values each: those of four neighbouring lanes turned, as
+// quad_turn does.
+__device__ __forceinline__ uint32_t lane_xor1(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t lane_xor2(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+}
+__device__ __forceinline__ u32x2 quad_turn16(u32x2 d) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    // even lanes: the low halves of (own, other); odd lanes: the high halves of (other, own)
+    const uint32_t pick = odd ? 0x07060302u : 0x01000504u;
+    const uint32_t a = __builtin_amdgcn_perm(d[0], lane_xor1(d[0]), pick);
+    const uint32_t b = __builtin_amdgcn_perm(d[1], lane_xor1(d[1]), pick);
+    const uint32_t o = lane_xor2(high ? a : b);
+    return u32x2{high ? o : a, high ? b : o};
+}
+
 // A wave's fp16 results on their way to the transposed place: 32 columns by WM rows
 // at a time, through this wave's own part of LDS, so that a column's WM values
 // leave as one run.

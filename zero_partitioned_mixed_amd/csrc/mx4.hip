@@ -269,33 +269,39 @@ __global__ void __launch_bounds__(S::THREADS) mx4_matmul_kernel(MatmulArgs g) {
             T* const row = out + i * g.ldc + jw;
 #pragma unroll
             for (int jj = 0; jj < S::NT; ++jj) {
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
-                quad_turn(v);  // four columns of one row
                 const int j = jw + jj * 32;
                 T* const at = row + jj * 32;
-                if (whole || (g.vector && i < rows_a && j + 4 <= rows_b)) {
-                    T4 w;
-                    if constexpr (DT == ZERO_F32) {
-                        if (g.accumulate) {
+                const bool vector = whole || (g.vector && i < rows_a && j + 4 <= rows_b);
+                T4 w;  // four columns of one row
+                if constexpr (DT == ZERO_F32) {
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
+                    quad_turn(v);
+                    if (g.accumulate) {
+                        if (vector) {
                             w = *(const T4*)at;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) v[e] += w[e];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (i < rows_a && j + e < rows_b) v[e] += at[e];
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = from_float<DT>(v[e]);
+                    for (int e = 0; e < 4; ++e) w[e] = v[e];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) w[r] = from_float<DT>(acc[ii][jj][4 * q + r]);
+                    w = __builtin_bit_cast(T4, quad_turn16(__builtin_bit_cast(u32x2, w)));
+                }
+                if (vector) {
                     *(T4*)at = w;
-                } else if (i < rows_a) {
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (j + e >= rows_b) break;
-                        if constexpr (DT == ZERO_F32) {
-                            if (g.accumulate) v[e] += at[e];
-                        }
-                        at[e] = from_float<DT>(v[e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (i < rows_a && j + e < rows_b) at[e] = w[e];
                 }
             }
         }

@@ -165,6 +165,9 @@ struct Strip {
     static constexpr int ARRAY = T * T * 2;  // bytes of a T x T fp16 array
     static constexpr int VALUES = RT * RT * 4;  // of a block, per lane
     static constexpr int SIZE = COLS * T;    // elements of a strip
+    // S and M by the waves on and below the diagonal only, mirrored: where LDS reads
+    // bound the products (128 x 128: 8 against 10 us a step)
+    static constexpr bool MIRROR = RT == 2;
 };
 typedef Strip<32, 1, 4, 8> Strip32;
 typedef Strip<64, 1, 1, 8> Strip64;
@@ -179,24 +182,6 @@ template <int T>
 __device__ __forceinline__ int small_at(int row, int col) {  // byte of an element of a swizzled T x T fp16 array
     constexpr int kPieces = T / 8;
     return row * T * 2 + (((col >> 3) ^ ((row / (128 / T)) & (kPieces - 1))) << 4) + (col & 7) * 2;
-}
-
-// Two dwords of four 16-bit values each: those of four neighbouring lanes turned, as
-// quad_turn does.
-__device__ __forceinline__ uint32_t lane_xor1(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
-}
-__device__ __forceinline__ uint32_t lane_xor2(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
-}
-__device__ __forceinline__ u32x2 quad_turn16(u32x2 d) {
-    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
-    // even lanes: the low halves of (own, other); odd lanes: the high halves of (other, own)
-    const uint32_t pick = odd ? 0x07060302u : 0x01000504u;
-    const uint32_t a = __builtin_amdgcn_perm(d[0], lane_xor1(d[0]), pick);
-    const uint32_t b = __builtin_amdgcn_perm(d[1], lane_xor1(d[1]), pick);
-    const uint32_t o = lane_xor2(high ? a : b);
-    return u32x2{high ? o : a, high ? b : o};
 }
 
 // Four values as two dwords of fp16, and what that leaves.
@@ -231,6 +216,7 @@ struct StripWave {
     Pair mine, square;
     int side;        // 32-column pieces of the smaller side
     bool live, both; // whether this wave's rows, and its columns too, meet the smaller side
+    bool lower;      // whether it makes its tiles of S and M
 
     __device__ __forceinline__ StripWave(StripLds<P>& s, int m) : lds(s) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -238,13 +224,21 @@ struct StripWave {
         quarter = lane >> 4;
         c = lane & 15;
         group = wave / P::GROUP;
-        i0 = wave % P::GROUP / P::SIDE * 16 * RT;
-        j0 = wave % P::SIDE * 16 * RT;
+        int ti = wave % P::GROUP / P::SIDE, tj = wave % P::SIDE;
+        if constexpr (P::MIRROR) {
+            // the ten tiles on and below the diagonal first, so that they spread over the SIMDs
+            static_assert(P::SIDE == 4, "tables of a 4 x 4 grid");
+            ti = (int)(0x2110003333222110ull >> 4 * wave & 15);
+            tj = (int)(0x3323213210210100ull >> 4 * wave & 15);
+        }
+        i0 = ti * 16 * RT;
+        j0 = tj * 16 * RT;
         mine = {s.block + group * 2 * P::ARRAY, s.block + (group * 2 + 1) * P::ARRAY};
         square = {s.square, s.square + P::ARRAY};
         side = (m + 31) / 32;
         live = i0 < m;
         both = live && j0 < m;
+        lower = !P::MIRROR || i0 >= j0;
     }
     __device__ __forceinline__ int row(int a, int r) const { return i0 + 16 * a + 4 * quarter + r; }
     __device__ __forceinline__ int at(int b) const { return j0 + 16 * b + c; }  // column within a block
@@ -337,7 +331,7 @@ struct StripWave {
             store<false>(mine, x[n]);
             __syncthreads();
             const int left = cols - (n * P::G + group) * T, k = left < T ? left : T;
-            if (both && k > 0) product(mine, mine, (k + 31) / 32, acc);
+            if (both && lower && k > 0) product(mine, mine, (k + 31) / 32, acc);
         }
         values([&](int a, int b, int r) { s[a][b][r] = acc[a][b][r] * (1.0f / (kXScale * kXScale)); });
         if constexpr (P::G > 1) {
@@ -354,21 +348,28 @@ struct StripWave {
         }
     }
 
+    // Symmetric tiles into the square pair.
+    __device__ __forceinline__ void store_square(const Tiles& v) const {
+        if (group != 0 || !lower) return;
+        store<true>(square, v);
+        if (P::MIRROR && i0 != j0) store<false>(square, v);
+    }
+
     // M from S, which every group holds: into the square pair, the diagonal into lds.dm.
     // No barrier after the last writes.
     __device__ __forceinline__ void poly(const Coeffs& k, Tiles& s) {
         Tiles v;
         values([&](int a, int b, int r) {
             const bool diag = row(a, r) == at(b);
-            if (diag && group == 0) lds.ds[row(a, r)] = s[a][b][r];
+            if (diag && group == 0) lds.ds[row(a, r)] = s[a][b][r];  // (such a wave is on the diagonal)
             s[a][b][r] = diag ? 0.0f : s[a][b][r];
             v[a][b][r] = s[a][b][r] * kSScale;
         });
-        if (group == 0) store<true>(square, v);  // symmetric: its transpose
+        store_square(v);
         __syncthreads();
         f32x4 acc[RT][RT];
         zero(acc);
-        if (both) product(square, square, side, acc);
+        if (both && lower) product(square, square, side, acc);
         float dj[RT];
 #pragma unroll
         for (int b = 0; b < RT; ++b) dj[b] = lds.ds[at(b)];
@@ -383,11 +384,11 @@ struct StripWave {
             }
         });
         __syncthreads();  // the readers of S are done
-        if (group == 0) store<true>(square, v);
+        store_square(v);
     }
 
     // X <- M X; M's pair and diagonal are written just before, without a barrier.
-    __device__ __forceinline__ void apply(const Coeffs& k, int nb, Tiles (&x)[P::NB]) {
+    __device__ __forceinline__ void apply(const Coeffs& k, int nb, int cols, Tiles (&x)[P::NB]) {
         const float un = 1.0f / k.mscale;
 #pragma unroll
         for (int n = 0; n < P::NB; ++n) {
@@ -397,7 +398,7 @@ struct StripWave {
             __syncthreads();
             f32x4 acc[RT][RT];
             zero(acc);
-            if (live) product(square, mine, side, acc);
+            if (live && (n * P::G + group) * T + j0 < cols) product(square, mine, side, acc);
             values([&](int a, int b, int r) { x[n][a][b][r] = lds.dm[row(a, r)] * x[n][a][b][r] + acc[a][b][r] * un; });
         }
     }
@@ -423,6 +424,7 @@ struct StripArgs {
     int64_t parts, next, mat;   // byte offsets of the strips' parts of S, now and next, and of M; X at 0
     int64_t sums;
     int sum_parts, strips;
+    int cols;                   // of a strip
     int step;                   // 0: normalise; k: apply the k-th M
     int fused;                  // M is made in every strip
 };
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     for (int step = 0; step < a.steps; ++step) {
         w.gram(x, nb, n, s);
         w.poly(a.k, s);
-        w.apply(a.k, nb, x);
+        w.apply(a.k, nb, n, x);
     }
     w.forget();
     w.each(x, [&](float& v, int i, int j) {
@@ -465,6 +467,7 @@ template <class P, class W, class IO>
 __device__ __forceinline__ void sum_parts_of(const W& w, const StripArgs<IO>& a, const char* ws, typename W::Tiles& s) {
     const float* parts = (const float*)(ws + a.parts);
     W::values([&](int i, int j, int r) { s[i][j][r] = 0.0f; });
+    if (!w.lower) return;
 #pragma unroll 4
     for (int p = 0; p < a.strips; ++p)
         W::values([&](int i, int j, int r) {
@@ -496,11 +499,11 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     __shared__ StripLds<P> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
     const IO& io = a.io;
-    const int b = blockIdx.y, strip = blockIdx.x, j0 = strip * P::COLS;
+    const int b = blockIdx.y, strip = blockIdx.x, j0 = strip * a.cols;
     const bool tall = io.rows > io.cols;
     const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
     StripWave<P> w(lds, m);
-    const int left = n - j0 < P::COLS ? n - j0 : P::COLS, nb = (left + P::G * P::T - 1) / (P::G * P::T);
+    const int left = n - j0 < a.cols ? n - j0 : a.cols, nb = (left + P::G * P::T - 1) / (P::G * P::T);
     char* ws = a.ws + b * a.stride;
     float* mine = (float*)ws + (int64_t)strip * P::SIZE + threadIdx.x;
     typename StripWave<P>::Tiles x[P::NB], s;
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
         const float clip = io.clip();
         w.each(x, [&](float& v, int i, int jj) {
             const int j = j0 + jj;
-            v = i < m && j < n ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
+            v = i < m && jj < left ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
         });
     } else {
         w.each(x, [&](float& v, int, int) { v = mine[slot++ * P::THREADS]; });
@@ -524,12 +527,12 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
                 ((u32x4*)lds.square)[i] = ((const u32x4*)(ws + a.mat))[i];
             for (int i = threadIdx.x; i < P::T; i += P::THREADS) lds.dm[i] = ((const float*)(ws + a.mat + 2 * P::ARRAY))[i];
         }
-        w.apply(a.k, nb, x);
+        w.apply(a.k, nb, left, x);
     }
     if (a.step == a.steps) {
         w.each(x, [&](float& v, int i, int jj) {
             const int j = j0 + jj;
-            if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, v * (1.0f / kXScale));
+            if (i < m && jj < left) io.put(b, tall ? j : i, tall ? i : j, v * (1.0f / kXScale));
         });
         return;
     }
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     w.each(x, [&](float& v, int, int) { mine[slot++ * P::THREADS] = v; });
     w.gram(x, nb, left, s);
     float* part = (float*)(ws + a.next) + (int64_t)strip * P::T * P::T;
-    if (w.group == 0)
+    if (w.group == 0 && w.lower)
         w.values([&](int i, int j, int r) { part[w.row(i, r) * P::T + w.at(j)] = s[i][j][r]; });
 }
 
@@ -764,12 +767,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
                 }
                 if (inside) *(f16x4*)(out + (int64_t)i * ldo + j) = h;
                 if (inside && twice) *(f16x4*)(out + (int64_t)i * ldo + w.mp + j) = h;
-                if (ti != tj) {
-                    quad_turn(v);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = (_Float16)v[r];
-                    turner.put(L, row, h);
-                }
+                if (ti != tj) turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, h))));
             }
         if (ti != tj) {
             turner.flush(L, out, ldo, jw + jj * 32, iw, w.m, w.mp);
@@ -845,14 +843,11 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
                     if (!a.last) *(f16x4*)(x16 + at) = h;
                 }
                 if (!a.last) {
-                    quad_turn(v);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = (_Float16)v[r];
-                    turner.put(L, row, h);
+                    turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, h))));
                     if (two) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) h[r] = (_Float16)(v[r] - (float)h[r]);
-                        rest.put(L, row, h);
+                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(v[e] - (float)h[e]);
+                        rest.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, h))));
                     }
                 }
             }
@@ -908,13 +903,30 @@ Work work_of(int64_t rows, int64_t cols) {
     return w;
 }
 
-// Strips of a narrow matrix: f(Strip32(), count of strips) and so on.
+// The strips of a narrow matrix of a stack: f(Strip32(), count of strips, columns of
+// each) and so on.  One strip where the stack alone fills the CUs or the
+// matrix has up to three rounds of blocks; else strips as short as kFused of them
+// allow, since a strip takes its blocks one after another.
+template <class P>
+int strip_cols(int32_t count, int64_t n) {
+    const int64_t round = P::G * P::T, rounds = ceil_div(n, round);
+    if (rounds <= P::NB && (rounds <= 3 || count >= 128)) return (int)(rounds * round);
+    int64_t per = ceil_div(rounds, kFused);
+    const int64_t fill = ceil_div(rounds * count, 256);  // more strips than CUs gain nothing
+    if (per < fill) per = fill;
+    return (int)((per < P::NB ? per : P::NB) * round);
+}
+
 template <class F>
-auto with_strip(int64_t rows, int64_t cols, F f) {
+auto with_strip(int32_t count, int64_t rows, int64_t cols, F f) {
     const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-    if (m <= 32) return f(Strip32(), (int)ceil_div(n, Strip32::COLS));
-    if (m <= 64) return f(Strip64(), (int)ceil_div(n, Strip64::COLS));
-    return f(Strip128(), (int)ceil_div(n, Strip128::COLS));
+    auto go = [&](auto shape) {
+        const int each = strip_cols<decltype(shape)>(count, n);
+        return f(shape, (int)ceil_div(n, each), each);
+    };
+    if (m <= 32) return go(Strip32());
+    if (m <= 64) return go(Strip64());
+    return go(Strip128());
 }
 
 // Workspace of one narrow matrix of several strips: X, the parts of S, M, the sums.
@@ -1003,9 +1015,9 @@ int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStrea
 template <class IO>
 int run_strips(const IO& io, int32_t count, const zero_newton_schulz& ns, const Coeffs& k, const int32_t* skip,
                void* ws, hipStream_t s, const char* what) {
-    return with_strip(io.rows, io.cols, [&](auto shape, int strips) {
+    return with_strip(count, io.rows, io.cols, [&](auto shape, int strips, int each_cols) {
         typedef decltype(shape) P;
-        StripArgs<IO> a{io, k, ns.steps, skip, (char*)ws, 0, 0, 0, 0, 0, 0, strips, 0, strips <= kFused};
+        StripArgs<IO> a{io, k, ns.steps, skip, (char*)ws, 0, 0, 0, 0, 0, 0, strips, each_cols, 0, strips <= kFused};
         const dim3 each((unsigned)count);
         if (strips == 1) return launch(ns_strip_kernel<P, IO>, each, P::THREADS, s, a, what);
         a.sum_parts = sum_parts(io.rows, io.cols);
@@ -1057,7 +1069,7 @@ extern "C" {
 size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols) {
     if (count <= 0 || count > kMaxCount || rows <= 0 || cols <= 0 || rows > kMaxSide || cols > kMaxSide) return 0;
     if (narrow(rows, cols))
-        return with_strip(rows, cols, [&](auto shape, int strips) -> size_t {
+        return with_strip(count, rows, cols, [&](auto shape, int strips, int) -> size_t {
             if (strips == 1) return 0;
             return (size_t)strip_work<decltype(shape)>(strips, sum_parts(rows, cols)).stride * (size_t)count;
         });
