@@ -174,8 +174,8 @@ typedef Strip<64, 1, 1, 8> Strip64;
 typedef Strip<128, 2, 1, 2> Strip128;
 constexpr int kFused = 32;
 
-struct Pair {  // high part and rest, arrays in LDS
-    char *hi, *lo;
+struct Pair {  // high part, and the rest right behind it: arrays in LDS
+    char* hi;
 };
 
 template <int T>
@@ -233,8 +233,8 @@ struct StripWave {
         }
         i0 = ti * 16 * RT;
         j0 = tj * 16 * RT;
-        mine = {s.block + group * 2 * P::ARRAY, s.block + (group * 2 + 1) * P::ARRAY};
-        square = {s.square, s.square + P::ARRAY};
+        mine = {s.block + group * 2 * P::ARRAY};
+        square = {s.square};
         side = (m + 31) / 32;
         live = i0 < m;
         both = live && j0 < m;
@@ -248,21 +248,21 @@ struct StripWave {
     // and bounds out again rather than keep them in registers across the steps.
     __device__ __forceinline__ void forget() { asm volatile("" : "+v"(c), "+v"(quarter)); }
 
-    __device__ __forceinline__ f16x8 frag(const char* a, int first, int kk) const {
-        return *(const f16x8*)(a + small_at<T>(first + c, kk * 32 + quarter * 8));
-    }
     // acc += A B^T of two pairs over the first `pieces` 32 columns, the product of the two
-    // rests left out.
+    // rests left out.  Sixteen rows on, the swizzle repeats: a fragment's place is one
+    // exclusive or with the k step and a constant.
     __device__ __forceinline__ void product(const Pair& A, const Pair& B, int pieces, f32x4 (&acc)[RT][RT]) const {
+        const int pa = small_at<T>(i0 + c, quarter * 8), pb = small_at<T>(j0 + c, quarter * 8);
 #pragma unroll 1
         for (int kk = 0; kk < pieces; ++kk) {
+            const int xa = pa ^ kk * 64, xb = pb ^ kk * 64;
             f16x8 ah[RT], al[RT], bh[RT], bl[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                ah[t] = frag(A.hi, i0 + 16 * t, kk);
-                bh[t] = frag(B.hi, j0 + 16 * t, kk);
-                al[t] = frag(A.lo, i0 + 16 * t, kk);
-                bl[t] = frag(B.lo, j0 + 16 * t, kk);
+                ah[t] = *(const f16x8*)(A.hi + xa + t * 16 * T * 2);
+                bh[t] = *(const f16x8*)(B.hi + xb + t * 16 * T * 2);
+                al[t] = *(const f16x8*)(A.hi + xa + t * 16 * T * 2 + P::ARRAY);
+                bl[t] = *(const f16x8*)(B.hi + xb + t * 16 * T * 2 + P::ARRAY);
             }
 #pragma unroll
             for (int a = 0; a < RT; ++a)
@@ -299,7 +299,7 @@ struct StripWave {
                     to = small_at<T>(row(a, c & 3), j0 + 16 * b + (c & ~3));
                 }
                 *(u32x2*)(P_.hi + to) = h;
-                *(u32x2*)(P_.lo + to) = l;
+                *(u32x2*)(P_.hi + to + P::ARRAY) = l;
             }
     }
     static __device__ __forceinline__ void zero(f32x4 (&acc)[RT][RT]) {
@@ -319,8 +319,8 @@ struct StripWave {
                 for (int r = 0; r < 4; ++r) f(a, b, r);
     }
 
-    // This wave's tiles of S = X X^T of the strip's first nb blocks of every group.
-    // cols: the strip's columns.
+    // This wave's tiles of S = X X^T (times kSScale) of the strip's first nb blocks of
+    // every group.  cols: the strip's columns.
     __device__ __forceinline__ void gram(const Tiles (&x)[P::NB], int nb, int cols, Tiles& s) {
         f32x4 acc[RT][RT];
         zero(acc);
@@ -333,7 +333,7 @@ struct StripWave {
             const int left = cols - (n * P::G + group) * T, k = left < T ? left : T;
             if (both && lower && k > 0) product(mine, mine, (k + 31) / 32, acc);
         }
-        values([&](int a, int b, int r) { s[a][b][r] = acc[a][b][r] * (1.0f / (kXScale * kXScale)); });
+        values([&](int a, int b, int r) { s[a][b][r] = acc[a][b][r] * (kSScale / (kXScale * kXScale)); });
         if constexpr (P::G > 1) {
             float* parts = (float*)lds.block;
             __syncthreads();
@@ -358,33 +358,43 @@ struct StripWave {
     // M from S, which every group holds: into the square pair, the diagonal into lds.dm.
     // No barrier after the last writes.
     __device__ __forceinline__ void poly(const Coeffs& k, Tiles& s) {
-        Tiles v;
-        values([&](int a, int b, int r) {
-            const bool diag = row(a, r) == at(b);
-            if (diag && group == 0) lds.ds[row(a, r)] = s[a][b][r];  // (such a wave is on the diagonal)
-            s[a][b][r] = diag ? 0.0f : s[a][b][r];
-            v[a][b][r] = s[a][b][r] * kSScale;
-        });
-        store_square(v);
+        const bool diagonal = i0 == j0;  // of the whole wave
+        if (diagonal) {
+            values([&](int a, int b, int r) {
+                if (row(a, r) != at(b)) return;
+                if (group == 0) lds.ds[row(a, r)] = s[a][b][r];
+                s[a][b][r] = 0.0f;
+            });
+        }
+        store_square(s);
         __syncthreads();
-        f32x4 acc[RT][RT];
-        zero(acc);
-        if (both && lower) product(square, square, side, acc);
-        float dj[RT];
+        if (lower) {
+            f32x4 acc[RT][RT];
+            zero(acc);
+            if (both) product(square, square, side, acc);
+            float dj[RT];
 #pragma unroll
-        for (int b = 0; b < RT; ++b) dj[b] = lds.ds[at(b)];
-        values([&](int a, int b, int r) {
-            const float di = lds.ds[row(a, r)];
-            float s2 = acc[a][b][r] * (1.0f / (kSScale * kSScale)) + s[a][b][r] * (di + dj[b]);
-            v[a][b][r] = (k.b * s[a][b][r] + k.c * s2) * k.mscale;
-            if (row(a, r) == at(b)) {
-                s2 += di * di;
-                if (group == 0) lds.dm[row(a, r)] = k.a + k.b * di + k.c * s2;
-                v[a][b][r] = 0.0f;
+            for (int b = 0; b < RT; ++b) dj[b] = lds.ds[at(b)];
+            // all in powers of kSScale: M - diag(M) = b E + c (E E + (d_i + d_j) E)
+            const float kb = k.b * k.mscale * (1.0f / kSScale), kc = k.c * k.mscale * (1.0f / (kSScale * kSScale));
+            if (diagonal && group == 0) {
+                values([&](int a, int b, int r) {
+                    if (row(a, r) != at(b)) return;
+                    const float d = dj[b] * (1.0f / kSScale), s2 = acc[a][b][r] * (1.0f / (kSScale * kSScale)) + d * d;
+                    lds.dm[row(a, r)] = k.a + k.b * d + k.c * s2;
+                });
             }
-        });
+            values([&](int a, int b, int r) {
+                const float di = lds.ds[row(a, r)];
+                s[a][b][r] = __builtin_fmaf(kb, s[a][b][r], kc * __builtin_fmaf(s[a][b][r], di + dj[b], acc[a][b][r]));
+            });
+            if (diagonal)
+                values([&](int a, int b, int r) {
+                    if (row(a, r) == at(b)) s[a][b][r] = 0.0f;
+                });
+        }
         __syncthreads();  // the readers of S are done
-        store_square(v);
+        store_square(s);
     }
 
     // X <- M X; M's pair and diagonal are written just before, without a barrier.
@@ -399,7 +409,7 @@ struct StripWave {
             f32x4 acc[RT][RT];
             zero(acc);
             if (live && (n * P::G + group) * T + j0 < cols) product(square, mine, side, acc);
-            values([&](int a, int b, int r) { x[n][a][b][r] = lds.dm[row(a, r)] * x[n][a][b][r] + acc[a][b][r] * un; });
+            values([&](int a, int b, int r) { x[n][a][b][r] = __builtin_fmaf(lds.dm[row(a, r)], x[n][a][b][r], acc[a][b][r] * un); });
         }
     }
 
