@@ -196,8 +196,8 @@ __device__ __forceinline__ void split4(const float* x, u32x2& h, u32x2& l) {
     l = __builtin_bit_cast(u32x2, b);
 }
 
-// LDS of a strip's workgroup: two pairs per group for its current block of X, row-major
-// and transposed (or the groups' parts of S), one for S and then M, the diagonals.
+// LDS of a strip's workgroup: a pair per group for X^T of its current block (or the
+// groups' parts of S), one for S and then M, the diagonals.
 template <class P>
 struct StripLds {
     __attribute__((aligned(16))) char block[P::G * 2 * P::ARRAY];
@@ -264,22 +264,56 @@ struct StripWave {
                 al[t] = *(const f16x8*)(A.hi + xa + t * 16 * T * 2 + P::ARRAY);
                 bl[t] = *(const f16x8*)(B.hi + xb + t * 16 * T * 2 + P::ARRAY);
             }
-#pragma unroll
-            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                for (int b = 0; b < RT; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[a], bh[b], acc[a][b], 0, 0, 0);
-#pragma unroll
-            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                for (int b = 0; b < RT; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(al[a], bh[b], acc[a][b], 0, 0, 0);
-#pragma unroll
-            for (int a = 0; a < RT; ++a)
-#pragma unroll
-                for (int b = 0; b < RT; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[a], bl[b], acc[a][b], 0, 0, 0);
+            multiply(ah, al, bh, bl, acc);
         }
+    }
+    // Eight values along a column of a pair's array (rows first .. + 7 of this lane's
+    // quarter): LDS reads that turn 4 rows x 16 columns among sixteen lanes.
+    __device__ __forceinline__ f16x8 column8(const char* a, int to) const {
+        typedef int16_t s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* Place;
+        // four rows on, the swizzle differs in one bit
+        const f16x4 lo = __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Place)(a + to)));
+        const f16x4 hi = __builtin_bit_cast(
+            f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Place)(a + ((to ^ (T / 32) * 16) + 4 * T * 2))));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // acc += X X^T over the first `pieces` 32 columns of X, from the pair of X^T.
+    __device__ __forceinline__ void product_t(const Pair& X, int pieces, f32x4 (&acc)[RT][RT]) const {
+        const int r = quarter * 8 + c / 4;
+        const int pa = small_at<T>(r, i0 + 4 * (c & 3)), pb = small_at<T>(r, j0 + 4 * (c & 3));
+#pragma unroll 1
+        for (int kk = 0; kk < pieces; ++kk) {
+            const char* rows = X.hi + kk * 32 * T * 2;
+            f16x8 ah[RT], al[RT], bh[RT], bl[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                ah[t] = column8(rows, pa ^ t * 32);
+                bh[t] = column8(rows, pb ^ t * 32);
+                al[t] = column8(rows + P::ARRAY, pa ^ t * 32);
+                bl[t] = column8(rows + P::ARRAY, pb ^ t * 32);
+            }
+            multiply(ah, al, bh, bl, acc);
+        }
+    }
+    // The three products of two pairs' fragments.
+    static __device__ __forceinline__ void multiply(const f16x8 (&ah)[RT], const f16x8 (&al)[RT], const f16x8 (&bh)[RT],
+                                                    const f16x8 (&bl)[RT], f32x4 (&acc)[RT][RT]) {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[a], bh[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(al[a], bh[b], acc[a][b], 0, 0, 0);
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah[a], bl[b], acc[a][b], 0, 0, 0);
     }
     // This wave's tiles into a pair; TURNED: into its transpose.
     template <bool TURNED>
@@ -328,10 +362,10 @@ struct StripWave {
         for (int n = 0; n < P::NB; ++n) {
             if (n >= nb) break;
             __syncthreads();  // the block's last readers are done
-            store<false>(mine, x[n]);
+            store<true>(mine, x[n]);
             __syncthreads();
             const int left = cols - (n * P::G + group) * T, k = left < T ? left : T;
-            if (both && lower && k > 0) product(mine, mine, (k + 31) / 32, acc);
+            if (both && lower && k > 0) product_t(mine, (k + 31) / 32, acc);
         }
         values([&](int a, int b, int r) { s[a][b][r] = acc[a][b][r] * (kSScale / (kXScale * kXScale)); });
         if constexpr (P::G > 1) {
@@ -398,13 +432,14 @@ struct StripWave {
     }
 
     // X <- M X; M's pair and diagonal are written just before, without a barrier.
-    __device__ __forceinline__ void apply(const Coeffs& k, int nb, int cols, Tiles (&x)[P::NB]) {
+    // there: the one block's X^T is in its pair (from gram).
+    __device__ __forceinline__ void apply(const Coeffs& k, int nb, int cols, bool there, Tiles (&x)[P::NB]) {
         const float un = 1.0f / k.mscale;
 #pragma unroll
         for (int n = 0; n < P::NB; ++n) {
             if (n >= nb) break;
             if (n > 0) __syncthreads();
-            store<true>(mine, x[n]);
+            if (!there) store<true>(mine, x[n]);
             __syncthreads();
             f32x4 acc[RT][RT];
             zero(acc);
@@ -464,7 +499,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     for (int step = 0; step < a.steps; ++step) {
         w.gram(x, nb, n, s);
         w.poly(a.k, s);
-        w.apply(a.k, nb, n, x);
+        w.apply(a.k, nb, n, P::G == 1 && nb == 1, x);
     }
     w.forget();
     w.each(x, [&](float& v, int i, int j) {
@@ -537,7 +572,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
                 ((u32x4*)lds.square)[i] = ((const u32x4*)(ws + a.mat))[i];
             for (int i = threadIdx.x; i < P::T; i += P::THREADS) lds.dm[i] = ((const float*)(ws + a.mat + 2 * P::ARRAY))[i];
         }
-        w.apply(a.k, nb, left, x);
+        w.apply(a.k, nb, left, false, x);
     }
     if (a.step == a.steps) {
         w.each(x, [&](float& v, int i, int jj) {
