@@ -148,6 +148,24 @@ def test_quantize_borders(Z, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_quantize_range(Z, dtype):
+    """Random values over the whole range of the type, its numbers below the normal ones among them: every exponent
+    as a block's largest, spread below it."""
+    info = torch.finfo(dtype)
+    low, high = math.floor(math.log2(info.smallest_normal)) - (10 if dtype == F16 else 7), math.floor(math.log2(info.max))
+    e = torch.arange(low, high, dtype=torch.float64).repeat_interleave(3)
+    g = torch.Generator().manual_seed(4)
+    x = torch.rand(len(e), 64, generator=g, dtype=torch.float64) + 0.5
+    x = x * torch.pow(2.0, e[:, None] - torch.randint(0, 5, x.shape, generator=g)) * torch.sign(torch.randn(x.shape, generator=g))
+    x = x.to(dtype).cuda()
+    q, t = Z.mx4_quantize(x, cols=True)
+    for got, want in ((q, x), (t, x.t()), (Z.mx4_quantize(x.t().contiguous(), rows=False, cols=True), x)):
+        code, s = mx4_reference(want)
+        assert torch.equal(got.scales.cpu(), s)
+        assert torch.equal(unpack(got), code)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
 def test_quantize_strides(Z, dtype):
     """Rows of a wider buffer, at an odd offset too; a transposed view."""
     base = randn(40, 517, dtype=dtype)

@@ -32,13 +32,35 @@ __device__ __forceinline__ float inverse_scale(uint32_t s) {
 }
 
 // Eight values times 1 / scale as 4-bit codes, the first in the low bits:
-// nearest, ties to even, saturating (what the conversion instruction does).
+// nearest, ties to even, saturating (what the conversion instructions do).
 __device__ __forceinline__ uint32_t codes8(const float* x, float inv) {
     uint32_t c = 0;
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0] * inv, x[1] * inv, 1.0f, 0);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2] * inv, x[3] * inv, 1.0f, 1);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4] * inv, x[5] * inv, 1.0f, 2);
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6] * inv, x[7] * inv, 1.0f, 3);
+    return c;
+}
+
+// The same from four dwords of 16-bit values under a scale.  bf16: not for scales near
+// the smallest numbers, where a value below the normal ones is more than half a code.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+constexpr uint32_t kLowScale = 16;
+template <int DT>
+__device__ __forceinline__ uint32_t codes8_16(const uint32_t* v, float scale) {
+    uint32_t c = 0;
+    if constexpr (DT == ZERO_BF16) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v[0]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v[1]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v[2]), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v[3]), scale, 3);
+    } else {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, v[0]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, v[1]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, v[2]), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, v[3]), scale, 3);
+    }
     return c;
 }
 
@@ -49,13 +71,16 @@ __device__ __forceinline__ uint32_t quad(uint32_t v) {  // v of another lane of 
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// Largest magnitude of the 32 values that four neighbouring lanes hold.
-__device__ __forceinline__ uint32_t block_top(const float* x) {
-    uint32_t top = 0;
+// Largest magnitude, as fp32 bits, of 16-bit values in dwords.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <int DT, int N>
+__device__ __forceinline__ uint32_t top16(const uint32_t* v) {
+    u16x2 m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = umax(top, magnitude(x[i]));
-    top = umax(top, quad<0xB1>(top));  // lanes 1 0 3 2
-    return umax(top, quad<0x4E>(top));  // lanes 2 3 0 1
+    for (int i = 0; i < N; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i] & 0x7FFF7FFFu));
+    const uint16_t top = m[0] > m[1] ? m[0] : m[1];
+    return __builtin_bit_cast(uint32_t, to_float<DT>(top));
 }
 
 // Eight elements of a row from column c on; past the row's end zeros.
@@ -86,6 +111,35 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = to_float<DT>(t[i]);
     }
+    // The largest magnitude of the block that four neighbouring lanes hold, as fp32 bits.
+    __device__ __forceinline__ uint32_t block_top() const {
+        uint32_t top = 0;
+        if constexpr (DT == ZERO_F32) {
+            float x[8];
+            values(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = umax(top, magnitude(x[i]));
+        } else {
+            uint32_t d[4];
+            __builtin_memcpy(d, v, sizeof(d));
+            top = top16<DT, 4>(d);
+        }
+        top = umax(top, quad<0xB1>(top));  // lanes 1 0 3 2
+        return umax(top, quad<0x4E>(top));  // lanes 2 3 0 1
+    }
+    __device__ __forceinline__ uint32_t codes(uint32_t s) const {
+        if (s == 255) return 0;
+        if constexpr (DT != ZERO_F32) {
+            if (s >= kLowScale) {
+                uint32_t d[4];
+                __builtin_memcpy(d, v, sizeof(d));
+                return codes8_16<DT>(d, __builtin_bit_cast(float, s << 23));
+            }
+        }
+        float x[8];
+        values(x);
+        return codes8(x, inverse_scale(s));
+    }
 };
 
 struct QuantArgs {
@@ -102,30 +156,31 @@ struct QuantJobs {
 };
 
 // Codes and scale of this lane's eight elements of a row (four lanes a block).
-__device__ __forceinline__ void put_row8(const QuantArgs& a, int64_t r, int64_t c, int64_t p, const float* x) {
-    const uint32_t s = scale_byte(block_top(x));
-    *(uint32_t*)(a.codes + r * (p / 2) + c / 2) = s == 255 ? 0u : codes8(x, inverse_scale(s));
+template <int DT>
+__device__ __forceinline__ void put_row8(const QuantArgs& a, int64_t r, int64_t c, int64_t p, const Eight<DT>& e) {
+    const uint32_t s = scale_byte(e.block_top());
+    *(uint32_t*)(a.codes + r * (p / 2) + c / 2) = e.codes(s);
     if ((threadIdx.x & 3) == 0) a.scales[r * (p / kMxBlock) + c / kMxBlock] = (uint8_t)s;
 }
 
 // A patch of ROWS x 128 elements per workgroup, sixteen lanes to a row, all its loads
 // before the first use.  Along rows four lanes hold a block.  Along columns (COLS)
-// the patch goes through LDS and a thread takes 32 elements of a column; four
-// neighbouring lanes then write 64 contiguous bytes of codes.  Every 32 rows start
-// 16 columns further on, which keeps those four lanes on different banks.  Bound
+// the patch goes through LDS and a thread takes 32 elements of a column.  A row is
+// eight banks further on than the one before and every 32 rows another 32, so
+// the four rows that sixteen lanes read, and their neighbours', differ.  Bound
 // by memory: both directions of 8192 x 8192 bf16 read and write 205 MB.
 template <int DT, int ROWS, bool COLS>
 __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(QuantJobs jobs) {
     typedef typename Elem<DT>::type T;
-    constexpr int kCols = kMxPad, kLd = kCols + 16 / (int)sizeof(T), kLoads = ROWS / 16;
-    __shared__ __attribute__((aligned(16))) T patch[COLS ? ROWS * kLd + (ROWS / 32 - 1) * 16 : 8];
+    constexpr int kCols = kMxPad, kLd = kCols + (DT == ZERO_F32 ? 4 : 16), kSkip = DT == ZERO_F32 ? 16 : 64, kLoads = ROWS / 16;
+    __shared__ __attribute__((aligned(16))) T patch[COLS ? ROWS * kLd + (ROWS / 32 - 1) * kSkip : 8];
     const bool other = blockIdx.x >= jobs.second;
     const QuantArgs& a = jobs.job[other];
     const uint32_t wg = other ? blockIdx.x - jobs.second : blockIdx.x, across = jobs.across[other];
     const int64_t r0 = (int64_t)(wg / across) * ROWS, c0 = (int64_t)(wg % across) * kCols;
     const int64_t p = padded(a.cols), pt = padded(a.rows);
     const int tid = threadIdx.x, r = tid / 16, c = tid % 16 * 8;
-    auto at = [](int row, int col) { return row * kLd + row / kMxBlock * 16 + col; };
+    auto at = [](int row, int col) { return row * kLd + row / kMxBlock * kSkip + col; };
     Eight<DT> e[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -142,34 +197,61 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(QuantJobs jobs) 
 #pragma unroll
             for (int k = 0; k < Eight<DT>::kVecs; ++k) *((u32x4*)(patch + at(row, c)) + k) = e[i].v[k];
         }
-        if ((!COLS || a.codes != nullptr) && r0 + row < a.rows) {
-            float x[8];
-            e[i].values(x);
-            put_row8(a, r0 + row, c0 + c, p, x);
-        }
+        if ((!COLS || a.codes != nullptr) && r0 + row < a.rows) put_row8<DT>(a, r0 + row, c0 + c, p, e[i]);
     }
     if constexpr (COLS) {
         __syncthreads();
-        constexpr int kBlocks = ROWS / kMxBlock;
+        // sixteen lanes a block of 32 rows and sixteen columns, a column each
+        constexpr int kBlocks = ROWS / kMxBlock, kGroups = kThreads / 16;
 #pragma unroll
-        for (int t = tid; t < kCols * kBlocks; t += kThreads) {
-            const int col = t / kBlocks, block = t % kBlocks;
-            if (c0 + col >= a.cols) continue;
-            float x[kMxBlock];
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < kMxBlock; ++k) {
-                x[k] = to_float<DT>(patch[at(block * kMxBlock, col) + k * kLd]);
-                top = umax(top, magnitude(x[k]));
-            }
-            const uint32_t s = scale_byte(top);
-            const float inv = inverse_scale(s);
+        for (int t = tid / 16; t < kCols / 16 * kBlocks; t += kGroups) {
+            const int col0 = t / kBlocks * 16, col = col0 + tid % 16, block = t % kBlocks;
+            uint32_t s;
             u32x4 q;
+            if constexpr (DT == ZERO_F32) {
+                float x[kMxBlock];
+                uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) q[k] = s == 255 ? 0u : codes8(x + 8 * k, inv);
-            const int64_t row = c0 + col, blk = r0 / kMxBlock + block;
-            *(u32x4*)(a.codes_t + row * (pt / 2) + blk * (kMxBlock / 2)) = q;
-            a.scales_t[row * (pt / kMxBlock) + blk] = (uint8_t)s;
+                for (int k = 0; k < kMxBlock; ++k) {
+                    x[k] = patch[at(block * kMxBlock, col) + k * kLd];
+                    top = umax(top, magnitude(x[k]));
+                }
+                s = scale_byte(top);
+                const float inv = inverse_scale(s);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) q[k] = s == 255 ? 0u : codes8(x + 8 * k, inv);
+            } else {
+                // LDS reads that turn 4 rows x 16 columns: four values of the lane's column
+                typedef int16_t s16x4 __attribute__((ext_vector_type(4)));
+                typedef __attribute__((address_space(3))) s16x4* Place;
+                const T* from = patch + at(block * kMxBlock + tid % 16 / 4, col0 + tid % 4 * 4);
+                uint32_t d[kMxBlock / 2];
+#pragma unroll
+                for (int k = 0; k < kMxBlock / 4; ++k) {
+                    const u32x2 w =
+                        __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Place)(from + 4 * k * kLd)));
+                    d[2 * k] = w[0];
+                    d[2 * k + 1] = w[1];
+                }
+                s = scale_byte(top16<DT, kMxBlock / 2>(d));
+                if (s >= kLowScale) {
+                    const float scale = __builtin_bit_cast(float, s << 23);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] = s == 255 ? 0u : codes8_16<DT>(d + 4 * k, scale);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        Eight<DT> e;
+                        __builtin_memcpy(e.v, d + 4 * k, sizeof(e.v));
+                        q[k] = e.codes(s);
+                    }
+                }
+            }
+            if (c0 + col < a.cols) {
+                const int64_t row = c0 + col, blk = r0 / kMxBlock + block;
+                *(u32x4*)(a.codes_t + row * (pt / 2) + blk * (kMxBlock / 2)) = q;
+                a.scales_t[row * (pt / kMxBlock) + blk] = (uint8_t)s;
+            }
         }
     }
 }
@@ -180,15 +262,14 @@ struct DequantArgs {
     void* dst;
 };
 
-__device__ __forceinline__ float code_value(uint32_t c) {  // 0 .5 1 1.5 2 3 4 6
-    const uint32_t m = c & 1, e = (c >> 1) & 3;
-    const float v = e == 0 ? 0.5f * (float)m : __builtin_bit_cast(float, ((e + 126) << 23) | (m << 22));
-    return c & 8 ? -v : v;
-}
-
-// value * 2^(s - 127) with one rounding, in two exact-or-final steps.
-__device__ __forceinline__ float scaled(float v, uint32_t s) {
-    return s == 255 ? __builtin_nanf("") : ldexpf(v, (int)s - 127);
+// Eight codes times 2^(s - 127), the scaling with one rounding for results below the
+// normal numbers.
+__device__ __forceinline__ void values8(uint32_t q, uint32_t s, float* x) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s == 255 ? __builtin_nanf("") : ldexpf(v[i / 2][i % 2], (int)s - 127);
 }
 
 // 64 rows x 128 columns per workgroup, sixteen lanes to a row.
@@ -212,12 +293,20 @@ __global__ void __launch_bounds__(kThreads) mx4_values_kernel(DequantArgs a) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         if (r0 + 16 * i >= a.rows) return;
+        float x[8];
+        values8(q[i], s[i], x);
         T v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = from_float<DT>(scaled(code_value(q[i] >> (4 * k)), s[i]));
+        for (int k = 0; k < 8; ++k) v[k] = from_float<DT>(x[k]);
         T* dst = (T*)a.dst + (r0 + 16 * i) * a.ld + c;
-        if (c + 8 <= a.cols) {
-            __builtin_memcpy(dst, v, sizeof(v));  // whole vectors at any alignment
+        if (c + 8 <= a.cols) {  // whole vectors at any alignment
+            u32x4 w[sizeof(v) / 16];
+            __builtin_memcpy(w, v, sizeof(v));
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(v) / 16; ++k) {
+                asm volatile("" : "+v"(w[k]));  // one store, not the pieces it was made of
+                __builtin_memcpy((char*)dst + 16 * k, &w[k], 16);
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -355,10 +444,8 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
         };
         auto put = [&](int t, const Eight<DTA>& e) {  // whole groups of four lanes
             const uint32_t r = (uint32_t)t / (p / 8), c = ((uint32_t)t - r * (p / 8)) * 8;
-            float x[8];
-            e.values(x);
-            const uint32_t s = scale_byte(block_top(x));
-            *(uint32_t*)(codes + r * half_row + c / 2) = s == 255 ? 0u : codes8(x, inverse_scale(s));
+            const uint32_t s = scale_byte(e.block_top());
+            *(uint32_t*)(codes + r * half_row + c / 2) = e.codes(s);
             if ((t & 3) == 0) scales[r * scale_row + c / kMxBlock] = (uint8_t)s;
         };
         // loads return in order: the first of A go out before B's, so that A is ready while B is on its way
