@@ -478,6 +478,68 @@ def test_muon_step_in_a_shard(Z):
         assert (gather[outside] == 5).all()
 
 
+# ----------------------------------------------------------------------------- together
+def test_shard_step_with_matrices(Z):
+    """MuonShardStep equals its parts: reduce, decision, AdamW between the matrices, the matrix step on them; a step
+    with an overflow leaves everything."""
+    matrices = [(8, 2, 40, 33), (3000, 1, 150, 200)]
+    n, psi, offset = 3, 34000, 24
+    stride = 34048
+    hp, muon = Z.hparams(lr=1e-2, weight_decay=0.01, max_grad_norm=0.5), Z.muon_hparams(lr=1e-2)
+    state = tuple(randn(psi, seed=i) * f for i, f in ((1, 0.02), (2, 1e-3)))
+    state = (*state, (randn(psi, seed=3) * 1e-3).square())
+    other = tuple(t.clone() for t in state)
+    g, g2 = torch.empty(psi, device="cuda"), torch.empty(psi, device="cuda")
+    gather, gather2 = (torch.zeros(psi + offset, dtype=BF16, device="cuda") for _ in range(2))
+    step = Z.MuonShardStep(n, stride, psi, offset, Z.BF16, Z.BF16, hp, muon, matrices, state, g)
+    ctrl = torch.empty(Z.zero_ctrl_bytes(), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(Z.zero_workspace_bytes(psi), dtype=torch.uint8, device="cuda")
+    Z.zero_ctrl_init(ctrl, 1.0)
+    for k in range(3):
+        c = randn(n, stride, seed=10 + k).to(BF16) * 1e-2
+        if k == 1:
+            c[1, 5000] = float("inf")
+            before = [t.clone() for t in (*state, gather)]
+        step.step(c, gather)
+        Z.zero_reduce_grads(c, Z.BF16, n, stride, psi, ctrl, g2, ws)
+        Z.zero_grad_norm_overflow([ws], [psi], [ctrl], hp, False)
+        for a, b in ((0, 8), (8 + 2 * 40 * 33, 3000), (3000 + 150 * 200, psi)):
+            Z.zero_adam_step(tuple(t[a:] for t in other), g2[a:], b - a, hp, ctrl, gather2, Z.BF16, offset + a)
+        for a, count, rows, cols in matrices:
+            b = a + count * rows * cols
+            part = [t[a:b].view(count, rows, cols) for t in (other[0], other[1], g2)]
+            Z.muon_step(*part, muon, slot=gather2[offset + a:offset + b].view(count, rows, cols), ctrl=ctrl)
+        for a, b in zip((*state, gather), (*other, gather2)):
+            assert torch.equal(a, b)
+        assert step.ctrl_dict()["skip"] == (k == 1)
+        if k == 1:
+            assert all(torch.equal(a, b) for a, b in zip((*state, gather), before))
+    assert step.ctrl_dict()["t"] == 2 and step.ctrl_dict()["clip"] < 1
+    for bad in ([(0, 1, 10, 10), (50, 1, 4, 4)], [(0, 1, 300, 300)], [(0, 1, 3, 3)]):
+        with pytest.raises(ValueError):
+            Z.MuonShardStep(n, stride, psi, 0, Z.BF16, Z.BF16, hp, muon, bad, state, g)
+
+
+def test_example_learns(Z):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "muon_mx4.py")
+    spec = importlib.util.spec_from_file_location("muon_mx4", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses, (weights, bias), ctrl = m.train(steps=40, ranks=2, width=128)
+    assert ctrl["t"] == 40
+    assert sum(losses[-5:]) < 0.5 * sum(losses[:5])
+    rows = randn(4, 64)
+    one = m.serve(weights, bias, rows)
+    x = rows.bfloat16()
+    for i, (w, b) in enumerate(zip(weights, bias)):
+        x = Z.mx4_linear(x, w) + b
+        x = torch.nn.functional.gelu(x) if i < len(weights) - 1 else x
+    # the same codes and fp32 sums in another order: a rounding of a layer's bf16 result now and then
+    assert (one.float() - x.detach().float()).norm() <= 0.02 * x.detach().float().norm()
+
+
 # ----------------------------------------------------------------------------- streams, graphs, refusals
 def test_other_stream_and_graph(Z):
     """Work on a side stream and in a replayed graph equals the eager result each time."""

@@ -573,10 +573,12 @@ class ShardStep:
     arrives in consecutive pieces of that many elements, and each piece is
     reduced (two-pass) or fully stepped (fused) by its own calls before the
     decision over the whole shard; bit-identical to one call per step.
+
+    ``two_pass`` takes the two-pass path without clipping too.
     """
 
     def __init__(self, nranks, stride, valid_len, offset, dtype, gather_dtype, hp: Hparams,
-                 state, g=None, loss_scale=1.0, bucket: int = 0):
+                 state, g=None, loss_scale=1.0, bucket: int = 0, two_pass: bool = False):
         import torch
         if bucket < 0 or bucket % TILE:
             raise ValueError(f"bucket must be a multiple of {TILE} elements")
@@ -584,7 +586,7 @@ class ShardStep:
         self.nranks, self.stride, self.valid_len, self.offset = nranks, stride, valid_len, offset
         self.dtype, self.gather_dtype, self.hp = dtype, gather_dtype, hp
         self.state, self.g = state, g
-        self.fused = hp.max_grad_norm <= 0
+        self.fused = hp.max_grad_norm <= 0 and not two_pass
         if not self.fused and g is None:
             raise ValueError("the two-pass path needs a g buffer")
         dev = state[0].device
@@ -845,5 +847,6 @@ class MultiShardStep:
         return graph
 
 
-from .matrices import (MX4, muon_hparams, muon_step, mx4_dequantize, mx4_linear,  # noqa: E402,F401
-                       mx4_matmul, mx4_quantize, newton_schulz, orthogonalize)
+from .matrices import (MX4, MuonShardStep, muon_hparams, muon_step,  # noqa: E402,F401
+                       mx4_dequantize, mx4_linear, mx4_matmul, mx4_quantize, newton_schulz,
+                       orthogonalize)

@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import (BF16, F16, F32, MUON_SCALE_RMS, MUON_SCALE_SHAPE, MX4_ROWS_MAX,  # noqa: F401
-               MuonHparams, NewtonSchulz, _check, _lib)
+               MuonHparams, NewtonSchulz, ShardStep, _check, _lib, zero_adam_step)
 
 _DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 COEFFS = (3.4445, -4.7750, 2.0315)  # the usual quintic's
@@ -140,6 +140,48 @@ def muon_step(master, mom, g, hp: MuonHparams, *, slot=None, ctrl=None, ws=None)
     _call(index, "zero_muon_step", master.data_ptr(), mom.data_ptr(), g.data_ptr(), count, rows, cols,
           stride, ctypes.byref(hp), None if ctrl is None else ctrl.data_ptr(),
           None if slot is None else slot.data_ptr(), slot_code, 0, p, n)
+
+
+class MuonShardStep(ShardStep):
+    """One rank's shard step with whole matrices in it: the two-pass path's reduce and
+    decision over all of the shard, then muon_step for the matrices and zero_adam_step
+    for what lies between them.
+
+    matrices: (first element in the shard, count, rows, cols) of each stack of
+    contiguous matrices, in order and apart; whatever lies between two stacks starts at a
+    multiple of four elements.  The momentum of a matrix is its part of the state's m; its
+    part of v is not used."""
+
+    def __init__(self, nranks, stride, valid_len, offset, dtype, gather_dtype, hp, muon: MuonHparams,
+                 matrices, state, g, loss_scale=1.0, bucket: int = 0):
+        super().__init__(nranks, stride, valid_len, offset, dtype, gather_dtype, hp, state, g, loss_scale,
+                         bucket, two_pass=True)
+        self.muon, self.matrices, self.between = muon, list(matrices), []
+        at = space = 0
+        for start, count, rows, cols in self.matrices + [(valid_len, 0, 0, 0)]:
+            if start < at or start + count * rows * cols > valid_len:
+                raise ValueError("matrices overlap or leave the shard")
+            if start > at:
+                if at % 4:
+                    raise ValueError("what follows a stack of matrices starts at a multiple of 4 elements")
+                self.between.append((at, start - at))
+            at = start + count * rows * cols
+            space = max(space, _lib.zero_ns_workspace_bytes(count, rows, cols))
+        self.matrix_ws = torch.empty(space, dtype=torch.uint8, device=state[0].device) if space else None
+
+    def complete(self, gather, qgather=None) -> None:
+        if qgather is not None:
+            raise ValueError("no INT8 or INT4 payload with matrices: quantise the slot")
+        master, m, v = self.state
+        for start, length in self.between:
+            zero_adam_step(tuple(t[start:] for t in self.state), self.g[start:], length, self.hp, self.ctrl,
+                           gather, self.gather_dtype, self.offset + start)
+        for start, count, rows, cols in self.matrices:
+            end = start + count * rows * cols
+            part = [t[start:end].view(count, rows, cols) for t in (master, m, self.g)]
+            slot = None if gather is None else \
+                gather[self.offset + start:self.offset + end].view(count, rows, cols)
+            muon_step(*part, self.muon, slot=slot, ctrl=self.ctrl, ws=self.matrix_ws)
 
 
 # ----------------------------------------------------------------------------- MXFP4
