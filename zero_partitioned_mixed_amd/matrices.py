@@ -28,25 +28,28 @@ def _code(dtype, allowed=_DTYPES) -> int:
 
 _HALVES = (torch.float16, torch.bfloat16)
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without its object
+_current_device = torch.cuda.current_device
+_empty, _bytes = torch.empty, torch.uint8
 
 
 def _gpu(first, *others) -> int:
     """The index of the GPU that all the tensors are on."""
-    index = first.get_device()
-    for t in (first, *others):
-        if t.get_device() != index or not t.is_cuda:
+    index = first.get_device()  # -1 on the CPU
+    if index < 0:
+        raise ValueError("expected GPU tensors")
+    for t in others:
+        if t.get_device() != index:
             raise ValueError("expected GPU tensors" if not t.is_cuda else "tensors on different GPUs")
     return index
 
 
 def _call(index: int, name: str, *args) -> None:
     """The C call on the GPU's current stream."""
-    fn = getattr(_lib, name)
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _raw_stream(index))
+    if _current_device() == index:
+        rc = getattr(_lib, name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
+            rc = getattr(_lib, name)(*args, _raw_stream(index))
     if rc != 0:
         _check(name, rc)
 
@@ -56,7 +59,7 @@ def _space(nbytes: int, ws, like):
     if ws is None:
         if nbytes == 0:
             return None, 0, None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        ws = _empty(nbytes, dtype=_bytes, device=like.device)
         return ws.data_ptr(), nbytes, ws
     _gpu(like, ws)
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -76,10 +79,15 @@ def muon_hparams(lr=3e-4, momentum=0.95, weight_decay=0.0, nesterov=True, scale=
 
 def _stack(x):
     """(count, rows, cols, row stride, matrix stride) of [rows, cols] or [count, rows, cols]."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) == 2:
+        (rows, cols), count = shape, 1
+    elif len(shape) == 3:
+        count, rows, cols = shape
+    else:
         raise ValueError("expected [rows, cols] or [count, rows, cols]")
-    count = x.shape[0] if x.dim() == 3 else 1
-    rows, cols = x.shape[-2:]
+    if x.is_contiguous():
+        return count, rows, cols, cols, rows * cols
     ld = x.stride(-2) if rows > 1 else max(x.stride(-2), cols)
     stride = x.stride(0) if x.dim() == 3 and count > 1 else rows * ld
     return count, rows, cols, ld, stride
@@ -87,7 +95,7 @@ def _stack(x):
 
 def _laid_out(x) -> bool:
     """Rows of unit stride that do not overlap, matrices that do not overlap."""
-    if x.numel() == 0:
+    if x.is_contiguous() or x.numel() == 0:
         return True
     _, rows, cols, ld, stride = _stack(x)
     return (cols == 1 or x.stride(-1) == 1) and ld >= cols and stride >= (rows - 1) * ld + cols
@@ -105,10 +113,10 @@ def orthogonalize(x, out_dtype=None, *, coeffs=COEFFS, steps: int = 5, eps: floa
         out_dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
     src_code, dst_code = _code(x.dtype), _code(out_dtype, _HALVES)
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    index = _gpu(x, out)
-    if out.shape != x.shape or not _laid_out(out):
+        out = _empty(x.shape, dtype=out_dtype, device=x.device)
+    elif out.shape != x.shape or not _laid_out(out):
         raise ValueError("out: another shape, or rows without unit stride")
+    index = _gpu(x, out)
     if not _laid_out(x):
         x = x.contiguous()
     count, rows, cols, ld, stride = _stack(x)
@@ -167,7 +175,7 @@ class MuonShardStep(ShardStep):
                 self.between.append((at, start - at))
             at = start + count * rows * cols
             space = max(space, _lib.zero_ns_workspace_bytes(count, rows, cols))
-        self.matrix_ws = torch.empty(space, dtype=torch.uint8, device=state[0].device) if space else None
+        self.matrix_ws = _empty(space, dtype=_bytes, device=state[0].device) if space else None
 
     def complete(self, gather, qgather=None) -> None:
         if qgather is not None:
@@ -187,33 +195,62 @@ class MuonShardStep(ShardStep):
 # ----------------------------------------------------------------------------- MXFP4
 class MX4:
     """A rows x cols matrix in MXFP4, blocks of 32 along its rows: codes
-    [rows, P / 2] and scales [rows, P / 32] bytes, P = mx4 padded cols (a multiple of
-    128, the padding zero)."""
+    [rows, P / 2] and scales [rows, P / 32] bytes, P = cols rounded up to a multiple
+    of 128 (the padding zero)."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("rows", "cols", "_codes", "_scales", "_both", "_places")
 
     def __init__(self, codes, scales, rows: int, cols: int):
         p = (cols + 127) // 128 * 128
         for t, width in ((codes, p // 2), (scales, p // 32)):
-            if t.dtype != torch.uint8 or t.numel() != rows * width or not t.is_contiguous():
+            if t.dtype != _bytes or t.numel() != rows * width or not t.is_contiguous():
                 raise ValueError(f"{rows} x {cols} takes {rows * p // 2} contiguous bytes of codes and "
                                  f"{rows * p // 32} of scales")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
+        self._both, self._places = None, (codes.data_ptr(), scales.data_ptr())
 
     @staticmethod
     def alloc(rows: int, cols: int, device) -> "MX4":
-        p = (cols + 127) // 128 * 128
+        """Codes and scales in one new buffer."""
+        blocks = rows * ((cols + 127) // 128)
         q = MX4.__new__(MX4)
-        q.codes = torch.empty((rows, p // 2), dtype=torch.uint8, device=device)
-        q.scales = torch.empty((rows, p // 32), dtype=torch.uint8, device=device)
-        q.rows, q.cols = rows, cols
+        q.rows, q.cols, q._codes = rows, cols, None
+        q._both = both = _empty(68 * blocks, dtype=_bytes, device=device)
+        at = both.data_ptr()
+        q._places = (at, at + 64 * blocks)
         return q
+
+    def _split(self):
+        n = self.rows * ((self.cols + 127) // 128)
+        self._codes = self._both[:64 * n].view(self.rows, -1) if n else self._both.view(self.rows, 0)
+        self._scales = self._both[64 * n:].view(self.rows, -1) if n else self._codes
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._split()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._codes is None:
+            self._split()
+        return self._scales
+
+    @property
+    def device(self):
+        return (self._codes if self._both is None else self._both).device
+
+    def _index(self) -> int:
+        return _gpu(self._codes, self._scales) if self._both is None else _gpu(self._both)
 
 
 def _matrix(x):
     """x as unit-stride rows, and its row stride."""
     if x.dim() != 2:
         raise ValueError("expected a matrix")
+    if x.is_contiguous():
+        return x, x.shape[1]
     if not _laid_out(x):
         x = x.contiguous()
     return x, _stack(x)[3]
@@ -229,28 +266,33 @@ def mx4_quantize(x, rows: bool = True, cols: bool = False):
     index = _gpu(x)
     x, ld = _matrix(x)
     m, n = x.shape
-    r = MX4.alloc(m, n, x.device) if rows else None
-    c = MX4.alloc(n, m, x.device) if cols else None
-    if x.numel():
+    device = x.device
+    r = MX4.alloc(m, n, device) if rows else None
+    c = MX4.alloc(n, m, device) if cols else None
+    if m and n:
         _call(index, "zero_mx4_quantize", x.data_ptr(), code, m, n, ld,
-              *((r.codes.data_ptr(), r.scales.data_ptr()) if rows else (None, None)),
-              *((c.codes.data_ptr(), c.scales.data_ptr()) if cols else (None, None)))
+              *(r._places if rows else _NOWHERE), *(c._places if cols else _NOWHERE))
     return (r, c) if rows and cols else r if rows else c
+
+
+_NOWHERE = (None, None)
 
 
 def mx4_dequantize(q: MX4, dtype=torch.bfloat16, out=None):
     """The matrix that q stands for."""
+    index = q._index()
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+        out = _empty((q.rows, q.cols), dtype=dtype, device=q.device)
         ld = q.cols
     elif tuple(out.shape) != (q.rows, q.cols) or not _laid_out(out):
         raise ValueError("out: another shape, or rows without unit stride")
     else:
         ld = _stack(out)[3]
-    index, code = _gpu(q.codes, q.scales, out), _code(out.dtype)
-    if out.numel():
-        _call(index, "zero_mx4_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols,
-              out.data_ptr(), code, ld)
+    code = _code(out.dtype)
+    if out.get_device() != index:
+        raise ValueError("out is elsewhere")
+    if q.rows and q.cols:
+        _call(index, "zero_mx4_dequantize", *q._places, q.rows, q.cols, out.data_ptr(), code, ld)
     return out
 
 
@@ -265,8 +307,9 @@ def mx4_matmul(a, b: MX4, out_dtype=torch.bfloat16, *, out=None, accumulate: boo
         raise ValueError(f"a has {k} columns and b {b.cols}")
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate needs an fp32 out")
+    index = b._index()
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=b.codes.device)
+        out = _empty((m, n), dtype=out_dtype, device=b.device)
         ldc = n
     elif tuple(out.shape) != (m, n) or not _laid_out(out):
         raise ValueError("out: another shape, or rows without unit stride")
@@ -275,20 +318,20 @@ def mx4_matmul(a, b: MX4, out_dtype=torch.bfloat16, *, out=None, accumulate: boo
     c_code = _code(out.dtype)
     if values and (m > MX4_ROWS_MAX or accumulate):
         a, values = mx4_quantize(a), False
+    if out.get_device() != index or (a.get_device() if values else a._index()) != index:
+        raise ValueError("operands and result on one GPU")
+    if not (m and n):
+        return out
     if values:
-        index = _gpu(b.codes, b.scales, out, a)
         a_code = _code(a.dtype)
         a, lda = _matrix(a)
-        if out.numel():
-            p, size, _keep = _space(_lib.zero_mx4_matmul_rows_workspace_bytes(m, n, k), ws, out)
-            _call(index, "zero_mx4_matmul_rows", a.data_ptr(), a_code, lda, b.codes.data_ptr(),
-                  b.scales.data_ptr(), m, n, k, out.data_ptr(), c_code, ldc, p, size)
+        p, size, _keep = _space(_lib.zero_mx4_matmul_rows_workspace_bytes(m, n, k), ws, out)
+        _call(index, "zero_mx4_matmul_rows", a.data_ptr(), a_code, lda, *b._places, m, n, k,
+              out.data_ptr(), c_code, ldc, p, size)
     else:
-        index = _gpu(b.codes, b.scales, out, a.codes, a.scales)
-        if out.numel():
-            p, size, _keep = _space(_lib.zero_mx4_matmul_workspace_bytes(m, n, k), ws, out)
-            _call(index, "zero_mx4_matmul", a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
-                  b.scales.data_ptr(), m, n, k, out.data_ptr(), c_code, ldc, int(accumulate), p, size)
+        p, size, _keep = _space(_lib.zero_mx4_matmul_workspace_bytes(m, n, k), ws, out)
+        _call(index, "zero_mx4_matmul", *a._places, *b._places, m, n, k, out.data_ptr(), c_code, ldc,
+              int(accumulate), p, size)
     return out
 
 
@@ -304,12 +347,12 @@ class _Mx4Linear(torch.autograd.Function):
         tokens, k = x.shape
         n = w.shape[0]
         code, index, dev = _DTYPES[x.dtype], x.get_device(), x.device
-        y = torch.empty((tokens, n), dtype=x.dtype, device=dev)
+        y = _empty((tokens, n), dtype=x.dtype, device=dev)
         size_x = _lib.zero_mx4_operand_bytes(k, tokens) if need_w else 0
         size_w = _lib.zero_mx4_operand_bytes(k, n) if need_x else 0
-        kept = torch.empty(size_x + size_w, dtype=torch.uint8, device=dev)  # what the gradients need
+        kept = _empty(size_x + size_w, dtype=_bytes, device=dev)  # what the gradients need
         size = _lib.zero_mx4_linear_workspace_bytes(tokens, n, k)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        ws = _empty(size, dtype=_bytes, device=dev)
         at = kept.data_ptr()
         _call(index, "zero_mx4_linear", x.data_ptr(), ldx, w.data_ptr(), ldw, code, tokens, n, k,
               y.data_ptr(), n, at if need_w else None, at + size_x if need_x else None,
@@ -326,10 +369,10 @@ class _Mx4Linear(torch.autograd.Function):
         kept, = ctx.saved_tensors
         dy, ld = _matrix(dy)
         dev = dy.device
-        dx = torch.empty((tokens, k), dtype=dy.dtype, device=dev) if need_x else None
-        dw = torch.empty((n, k), dtype=dy.dtype, device=dev) if need_w else None
+        dx = _empty((tokens, k), dtype=dy.dtype, device=dev) if need_x else None
+        dw = _empty((n, k), dtype=dy.dtype, device=dev) if need_w else None
         size = _lib.zero_mx4_linear_grad_workspace_bytes(tokens, n)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        ws = _empty(size, dtype=_bytes, device=dev)
         at = kept.data_ptr()
         _call(dy.get_device(), "zero_mx4_linear_grad", dy.data_ptr(), ld, code, tokens, n, k,
               at if need_w else None, at + size_x if need_x else None,
