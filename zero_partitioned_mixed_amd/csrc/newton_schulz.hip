@@ -210,7 +210,7 @@ template <class P>
 struct StripWave {
     static constexpr int T = P::T, RT = P::RT;
     typedef float Tiles[RT][RT][4];
-    int lane, quarter, c;  // lane / 16, lane % 16
+    int wave, lane, quarter, c;  // lane / 16, lane % 16
     int group, i0, j0;     // this wave's group, and its tiles' place in a block
     StripLds<P>& lds;
     Pair mine, square;
@@ -219,7 +219,7 @@ struct StripWave {
     bool lower;      // whether it makes its tiles of S and M
 
     __device__ __forceinline__ StripWave(StripLds<P>& s, int m) : lds(s) {
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         lane = threadIdx.x & 63;
         quarter = lane >> 4;
         c = lane & 15;
@@ -448,13 +448,36 @@ struct StripWave {
         }
     }
 
-    // every value of a strip: f(value, row, column in the strip)
+    // every value of a strip's first nb blocks: f(value, row, column in the strip)
     template <class F>
-    __device__ __forceinline__ void each(Tiles (&x)[P::NB], F f) const {
+    __device__ __forceinline__ void each(Tiles (&x)[P::NB], int nb, F f) const {
 #pragma unroll
-        for (int n = 0; n < P::NB; ++n)
+        for (int n = 0; n < P::NB; ++n) {
+            if (n >= nb) break;
             values([&](int a, int b, int r) { f(x[n][a][b][r], row(a, r), col(n, b)); });
+        }
     }
+    // A wave's tiles in memory, a vector of four values a lane at a time: RT * RT * 256 floats.
+    __device__ __forceinline__ void save(float* to, const Tiles& v) const {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b)
+                *(f32x4*)(to + (a * RT + b) * 256 + lane * 4) = f32x4{v[a][b][0], v[a][b][1], v[a][b][2], v[a][b][3]};
+    }
+    __device__ __forceinline__ void load(const float* from, Tiles& v) const {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+#pragma unroll
+            for (int b = 0; b < RT; ++b) {
+                const f32x4 w = *(const f32x4*)(from + (a * RT + b) * 256 + lane * 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[a][b][r] = w[r];
+            }
+    }
+    // Where this wave's tiles of a T x T matrix, or of a strip's block n, are.
+    __device__ __forceinline__ int place() const { return wave % P::GROUP * RT * RT * 256; }
+    __device__ __forceinline__ int place(int n) const { return (n * P::WAVES + wave) * RT * RT * 256; }
 };
 
 template <class IO>
@@ -488,12 +511,12 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     const float clip = io.clip();
     typename StripWave<P>::Tiles x[P::NB], s;
     double ss = 0.0;
-    w.each(x, [&](float& v, int i, int j) {
+    w.each(x, nb, [&](float& v, int i, int j) {
         v = i < m && j < n ? io.first(b, tall ? j : i, tall ? i : j, clip) : 0.0f;
         ss += (double)v * (double)v;
     });
     const double scale = scale_of(sqrt(block_sum(ss, lds.red, P::WAVES)), a.k.eps);
-    w.each(x, [&](float& v, int, int) { v = (float)(v * scale); });
+    w.each(x, nb, [&](float& v, int, int) { v = (float)(v * scale); });
     w.forget();
 #pragma unroll 1
     for (int step = 0; step < a.steps; ++step) {
@@ -502,22 +525,30 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
         w.apply(a.k, nb, n, P::G == 1 && nb == 1, x);
     }
     w.forget();
-    w.each(x, [&](float& v, int i, int j) {
+    w.each(x, nb, [&](float& v, int i, int j) {
         if (i < m && j < n) io.put(b, tall ? j : i, tall ? i : j, v * (1.0f / kXScale));
     });
 }
 
-// S of a matrix of several strips, this wave's tiles: the sum of the strips' parts.
+// S of a matrix of several strips, this wave's tiles: the sum of the strips' parts,
+// several of them on their way at once.
 template <class P, class W, class IO>
 __device__ __forceinline__ void sum_parts_of(const W& w, const StripArgs<IO>& a, const char* ws, typename W::Tiles& s) {
-    const float* parts = (const float*)(ws + a.parts);
+    constexpr int kAtOnce = P::RT == 1 ? 8 : 2;
+    const float* parts = (const float*)(ws + a.parts) + w.place();
     W::values([&](int i, int j, int r) { s[i][j][r] = 0.0f; });
     if (!w.lower) return;
-#pragma unroll 4
-    for (int p = 0; p < a.strips; ++p)
-        W::values([&](int i, int j, int r) {
-            s[i][j][r] += parts[(int64_t)p * P::T * P::T + w.row(i, r) * P::T + w.at(j)];
-        });
+    for (int p = 0; p < a.strips; p += kAtOnce) {
+        typename W::Tiles v[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+            w.load(parts + (int64_t)(p + k < a.strips ? p + k : p) * P::T * P::T, v[k]);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const float keep = p + k < a.strips ? 1.0f : 0.0f;
+            W::values([&](int i, int j, int r) { s[i][j][r] += keep * v[k][i][j][r]; });
+        }
+    }
 }
 
 // M of a matrix of many strips: both parts of its pair, then the diagonal.
@@ -550,20 +581,21 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     StripWave<P> w(lds, m);
     const int left = n - j0 < a.cols ? n - j0 : a.cols, nb = (left + P::G * P::T - 1) / (P::G * P::T);
     char* ws = a.ws + b * a.stride;
-    float* mine = (float*)ws + (int64_t)strip * P::SIZE + threadIdx.x;
+    float* mine = (float*)ws + (int64_t)strip * P::SIZE;
     typename StripWave<P>::Tiles x[P::NB], s;
-    int slot = 0;
     if (a.step == 0) {
         double ss = 0.0;
         for (int p = threadIdx.x; p < a.sum_parts; p += P::THREADS) ss += ((const double*)(ws + a.sums))[p];
         const double scale = scale_of(sqrt(block_sum(ss, lds.red, P::WAVES)), a.k.eps);
         const float clip = io.clip();
-        w.each(x, [&](float& v, int i, int jj) {
+        w.each(x, nb, [&](float& v, int i, int jj) {
             const int j = j0 + jj;
             v = i < m && jj < left ? (float)(io.again(b, tall ? j : i, tall ? i : j, clip) * scale) : 0.0f;
         });
     } else {
-        w.each(x, [&](float& v, int, int) { v = mine[slot++ * P::THREADS]; });
+#pragma unroll
+        for (int k = 0; k < P::NB; ++k)
+            if (k < nb) w.load(mine + w.place(k), x[k]);
         if (a.fused) {
             sum_parts_of<P>(w, a, ws, s);
             w.poly(a.k, s);
@@ -575,18 +607,17 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
         w.apply(a.k, nb, left, false, x);
     }
     if (a.step == a.steps) {
-        w.each(x, [&](float& v, int i, int jj) {
+        w.each(x, nb, [&](float& v, int i, int jj) {
             const int j = j0 + jj;
             if (i < m && jj < left) io.put(b, tall ? j : i, tall ? i : j, v * (1.0f / kXScale));
         });
         return;
     }
-    slot = 0;
-    w.each(x, [&](float& v, int, int) { mine[slot++ * P::THREADS] = v; });
+#pragma unroll
+    for (int k = 0; k < P::NB; ++k)
+        if (k < nb) w.save(mine + w.place(k), x[k]);
     w.gram(x, nb, left, s);
-    float* part = (float*)(ws + a.next) + (int64_t)strip * P::T * P::T;
-    if (w.group == 0 && w.lower)
-        w.values([&](int i, int j, int r) { part[w.row(i, r) * P::T + w.at(j)] = s[i][j][r]; });
+    if (w.group == 0 && w.lower) w.save((float*)(ws + a.next) + (int64_t)strip * P::T * P::T + w.place(), s);
 }
 
 // ---------------------------------------------------------------- large matrices
