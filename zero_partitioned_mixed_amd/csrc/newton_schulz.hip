@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
 // several of them on their way at once.
 template <class P, class W, class IO>
 __device__ __forceinline__ void sum_parts_of(const W& w, const StripArgs<IO>& a, const char* ws, typename W::Tiles& s) {
-    constexpr int kAtOnce = P::RT == 1 ? 8 : 2;
+    constexpr int kAtOnce = P::RT == 1 ? 8 : 4;
     const float* parts = (const float*)(ws + a.parts) + w.place();
     W::values([&](int i, int j, int r) { s[i][j][r] = 0.0f; });
     if (!w.lower) return;
