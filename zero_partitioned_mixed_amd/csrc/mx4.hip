@@ -396,27 +396,30 @@ __global__ void __launch_bounds__(S::THREADS) mx4_matmul_kernel(MatmulArgs g) {
         }
 }
 
-// Few rows (m <= 64, as single tokens bring): bound by reading B once.  A workgroup
-// takes 32 of B's rows, its four waves a quarter of k each, straight from memory
-// to registers in runs of 64 bytes per lane; the waves' sums meet in LDS.
+// Few rows (m <= 32, as single tokens bring): bound by reading B once.  A workgroup
+// takes 32 of B's rows, its eight waves an eighth of k each: a wave brings its own
+// slabs to its own part of LDS (whole lines; 16 bytes per lane straight to
+// registers touch a line per lane), waits for nobody, and the waves' sums meet in LDS.
 // VALUES (m k up to kFewValues): A comes as values, and every workgroup quantises
 // all of it to LDS first, which saves a launch.
-constexpr int kFewWaves = 4;
+constexpr int kFewWaves = 8;
 constexpr int kFewValues = 16384;
-constexpr int kFewUnroll = 4;  // slabs of a wave on their way at once
+constexpr int kFewSlabs = 2;   // slabs of a wave on their way at once
 
 struct FewArgs {
     MatmulArgs g;
     int64_t lda, k;  // values of A: row stride, length
 };
 
-template <int MT, int DTA, int DT, bool VALUES>
+template <int DTA, int DT, bool VALUES>
 __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
     const MatmulArgs& g = f.g;
     constexpr int kCodes = VALUES ? kFewValues / 2 : 16, kScales = kCodes / 16;
     __shared__ __attribute__((aligned(16))) uint8_t codes[kCodes];
     __shared__ __attribute__((aligned(16))) uint8_t scales[VALUES ? kScales : 16];
-    __shared__ float sums[kFewWaves][MT * 32][33];
+    constexpr int kRing = kFewWaves * kFewSlabs * 32 * kSlab, kSums = kFewWaves * 32 * 33 * 4;
+    __shared__ __attribute__((aligned(16))) char lds[kRing > kSums ? kRing : kSums];
+    float(*sums)[32][33] = (float(*)[32][33])lds;  // after the products
     const Lane L;
     const uint32_t p = (uint32_t)g.p, half_row = p / 2, scale_row = p / kMxBlock;
     const int64_t j = (int64_t)blockIdx.x * 32 + L.c;
@@ -424,14 +427,20 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
     const uint8_t *b = g.b + jc * half_row + 64 * L.h, *sb = g.sb + jc * scale_row + 4 * L.h;
     const int slabs = (int)(p / 256);
 
-    i32x4 bw[kFewUnroll][4];
-    uint32_t bs[kFewUnroll];
+    char* const ring = lds + L.wave * kFewSlabs * 32 * kSlab;
+    uint32_t bs[kFewSlabs];
     auto fetch = [&](int first) {
 #pragma unroll
-        for (int u = 0; u < kFewUnroll; ++u) {
+        for (int u = 0; u < kFewSlabs; ++u) {
             const int s = first + u * kFewWaves < slabs ? first + u * kFewWaves : slabs - 1;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) bw[u][q] = *(const i32x4*)(b + (int64_t)s * 128 + 16 * q);
+            for (int q = 0; q < 4; ++q) {  // eight rows each
+                const int r = 8 * q + (L.lane >> 3);
+                const int64_t row = (int64_t)blockIdx.x * 32 + r;
+                const uint32_t piece = (L.lane & 7) ^ ((r >> 1) & 7);
+                load_to_lds16((const char*)g.b + (row < g.n ? row : g.n - 1) * half_row + (int64_t)s * kSlab + piece * 16,
+                              ring + u * 32 * kSlab + q * 1024);
+            }
             bs[u] = *(const uint32_t*)(sb + (int64_t)s * 8);
         }
     };
@@ -468,48 +477,43 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
         if (slabs > 0) fetch(L.wave);
     }
     const uint8_t *a = VALUES ? codes : g.a, *sa = VALUES ? scales : g.sa;
-    uint32_t row[MT];
+    const uint32_t row = (uint32_t)(L.c < g.m ? L.c : g.m - 1);
+    f32x16 acc;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) row[i] = (uint32_t)(L.c + 32 * i < g.m ? L.c + 32 * i : g.m - 1);
-    f32x16 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
+    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
 
-    for (int first = L.wave; first < slabs; first += kFewWaves * kFewUnroll) {
+    for (int first = L.wave; first < slabs; first += kFewWaves * kFewSlabs) {
         if (first != L.wave) fetch(first);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's slabs are in its part of LDS
 #pragma unroll
-        for (int u = 0; u < kFewUnroll; ++u) {
+        for (int u = 0; u < kFewSlabs; ++u) {
             const int s = first + u * kFewWaves;
             if (s >= slabs) break;
+            const char* from = ring + u * 32 * kSlab + L.c * kSlab;
+            i32x4 bw[4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const uint32_t as = *(const uint32_t*)(sa + row[i] * scale_row + s * 8 + 4 * L.h);
-                const i32x4* aw = (const i32x4*)(a + row[i] * half_row + s * 128 + 64 * L.h);
-                acc[i] = MmFp4::mma<0>(aw[0], bw[u][0], acc[i], as, bs[u]);
-                acc[i] = MmFp4::mma<1>(aw[1], bw[u][1], acc[i], as, bs[u]);
-                acc[i] = MmFp4::mma<2>(aw[2], bw[u][2], acc[i], as, bs[u]);
-                acc[i] = MmFp4::mma<3>(aw[3], bw[u][3], acc[i], as, bs[u]);
-            }
+            for (int q = 0; q < 4; ++q) bw[q] = *(const i32x4*)(from + (((4 * L.h + q) ^ ((L.c >> 1) & 7)) << 4));
+            const uint32_t as = *(const uint32_t*)(sa + row * scale_row + s * 8 + 4 * L.h);
+            const i32x4* aw = (const i32x4*)(a + row * half_row + s * 128 + 64 * L.h);
+            acc = MmFp4::mma<0>(aw[0], bw[0], acc, as, bs[u]);
+            acc = MmFp4::mma<1>(aw[1], bw[1], acc, as, bs[u]);
+            acc = MmFp4::mma<2>(aw[2], bw[2], acc, as, bs[u]);
+            acc = MmFp4::mma<3>(aw[3], bw[3], acc, as, bs[u]);
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next slabs come
     }
     if (p % 256 != 0 && L.wave == 0) {  // half a slab: group h takes blocks 2h and 2h + 1 of four
         const int64_t at = (int64_t)slabs * 128 - 32 * L.h, sat = (int64_t)slabs * 8 - 4 * L.h;
         const uint32_t bsh = *(const uint32_t*)(sb + sat) >> (16 * L.h);
         const i32x4 b0 = *(const i32x4*)(b + at), b1 = *(const i32x4*)(b + at + 16);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const uint32_t as = *(const uint32_t*)(sa + row[i] * scale_row + slabs * 8) >> (16 * L.h);
-            const i32x4* aw = (const i32x4*)(a + row[i] * half_row + slabs * 128 + 32 * L.h);
-            acc[i] = MmFp4::mma<0>(aw[0], b0, acc[i], as, bsh);
-            acc[i] = MmFp4::mma<1>(aw[1], b1, acc[i], as, bsh);
-        }
+        const uint32_t as = *(const uint32_t*)(sa + row * scale_row + slabs * 8) >> (16 * L.h);
+        const i32x4* aw = (const i32x4*)(a + row * half_row + slabs * 128 + 32 * L.h);
+        acc = MmFp4::mma<0>(aw[0], b0, acc, as, bsh);
+        acc = MmFp4::mma<1>(aw[1], b1, acc, as, bsh);
     }
+    __syncthreads();  // the slabs have no readers any more
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sums[L.wave][32 * i + 8 * (r / 4) + 4 * L.h + r % 4][L.c] = acc[i][r];
+    for (int r = 0; r < 16; ++r) sums[L.wave][8 * (r / 4) + 4 * L.h + r % 4][L.c] = acc[r];
     __syncthreads();
     typedef typename Elem<DT>::type T;
     for (int t = threadIdx.x; t < (int)g.m * 32; t += kFewWaves * 64) {
@@ -583,13 +587,13 @@ int matmul_with(MatmulArgs g, int32_t c_dtype, hipStream_t s, const char* what) 
     }
 }
 
-template <int MT, int DTA, bool VALUES>
+template <int DTA, bool VALUES>
 int few_with(const FewArgs& f, int32_t c_dtype, hipStream_t s, const char* what) {
     const dim3 grid((unsigned)ceil_div(f.g.n, 32));
     switch (c_dtype) {
-        case ZERO_F16: return launch(mx4_few_kernel<MT, DTA, ZERO_F16, VALUES>, grid, kFewWaves * 64, s, f, what);
-        case ZERO_BF16: return launch(mx4_few_kernel<MT, DTA, ZERO_BF16, VALUES>, grid, kFewWaves * 64, s, f, what);
-        default: return launch(mx4_few_kernel<MT, DTA, ZERO_F32, VALUES>, grid, kFewWaves * 64, s, f, what);
+        case ZERO_F16: return launch(mx4_few_kernel<DTA, ZERO_F16, VALUES>, grid, kFewWaves * 64, s, f, what);
+        case ZERO_BF16: return launch(mx4_few_kernel<DTA, ZERO_BF16, VALUES>, grid, kFewWaves * 64, s, f, what);
+        default: return launch(mx4_few_kernel<DTA, ZERO_F32, VALUES>, grid, kFewWaves * 64, s, f, what);
     }
 }
 
@@ -598,18 +602,16 @@ bool few_values(int64_t m, int64_t k) { return m <= 32 && m * padded(k) <= kFewV
 
 int few_of_values(const FewArgs& f, int32_t a_dtype, int32_t c_dtype, hipStream_t s, const char* what) {
     switch (a_dtype) {
-        case ZERO_F16: return few_with<1, ZERO_F16, true>(f, c_dtype, s, what);
-        case ZERO_BF16: return few_with<1, ZERO_BF16, true>(f, c_dtype, s, what);
-        default: return few_with<1, ZERO_F32, true>(f, c_dtype, s, what);
+        case ZERO_F16: return few_with<ZERO_F16, true>(f, c_dtype, s, what);
+        case ZERO_BF16: return few_with<ZERO_BF16, true>(f, c_dtype, s, what);
+        default: return few_with<ZERO_F32, true>(f, c_dtype, s, what);
     }
 }
 
 int matmul(const MatmulArgs& g, int32_t c_dtype, hipStream_t s, const char* what) {
-    if (g.m <= ZERO_MX4_ROWS_MAX) {
-        const FewArgs f{g, 0, 0};
-        return g.m <= 32 ? few_with<1, ZERO_F32, false>(f, c_dtype, s, what)
-                         : few_with<2, ZERO_F32, false>(f, c_dtype, s, what);
-    }
+    // Few rows against tiles of 64, us: 1 x 11008 x 4096 8.4 and 9.2, 16 rows 9.8 and 9.1; where the tiles
+    // leave half of the CUs out, 4096 x 11008, 1 row 9.8 and 14.9, 32 rows 13.4 and 15.4, 48 rows 17.2 and 16.9.
+    if (g.m <= 8 || (g.m <= 32 && g.n <= 64 * 128)) return few_with<ZERO_F32, false>(FewArgs{g, 0, 0}, c_dtype, s, what);
     const int pick = pick_tile([&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); });
     return with_tile(pick, [&](auto shape) { return matmul_with<decltype(shape)>(g, c_dtype, s, what); });
 }
