@@ -53,6 +53,19 @@ def ns64(x, steps=5, eps=1e-7, coeffs=COEFFS):
     return x.mT if tall else x
 
 
+def ns64_gpu(x):
+    """ns64 of one matrix in 64 bits on the GPU, for sizes that take the CPU long."""
+    a, b, c = COEFFS
+    x = x.double()
+    tall = x.shape[0] > x.shape[1]
+    x = (x.t() if tall else x).contiguous()
+    x = x / (x.square().sum().sqrt() + 1e-7)
+    for _ in range(5):
+        s = torch.mm(x, x.t())
+        x = a * x + torch.mm(b * s + c * torch.mm(s, s), x)
+    return (x.t() if tall else x).cpu()
+
+
 GRID = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
 
 
@@ -118,6 +131,19 @@ def test_quantize_exact(Z, rows, cols, dtype):
         code, s = mx4_reference(want)
         assert torch.equal(unpack(q), code)
         assert torch.equal(q.scales.cpu(), s)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_quantize_large(Z, dtype):
+    """A matrix of many patches, in both directions; a sample of rows and columns."""
+    rows, cols = 2900, 3001
+    x = (randn(rows, cols, seed=8) * torch.exp(randn(rows, 1, seed=9))).to(dtype)
+    r, c = Z.mx4_quantize(x, cols=True)
+    for q, want, n in ((r, x, rows), (c, x.t(), cols)):
+        pick = torch.cat([torch.arange(0, n, 97), torch.arange(n - 3, n)])
+        code, s = mx4_reference(want[pick.cuda()])
+        part = Z.MX4(q.codes[pick.cuda()], q.scales[pick.cuda()], len(pick), q.cols)
+        assert torch.equal(unpack(part), code) and torch.equal(part.scales.cpu(), s)
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
@@ -236,7 +262,8 @@ def test_product(Z, m, n, k):
     check_product(out, a64, b64, k, extra=before)
 
 
-@pytest.mark.parametrize("m,n,k", [(4096, 4096, 512), (2048, 5000, 640), (1000, 1100, 384), (8192, 130, 256)])
+@pytest.mark.parametrize("m,n,k", [(4096, 4096, 512), (2048, 5000, 640), (1000, 1100, 384), (8192, 130, 256), (1286, 5928, 384),
+                                   (657, 5969, 256), (657, 5395, 320)])
 def test_product_large_tiles(Z, m, n, k):
     """Sizes that take the larger tiles; a sample of rows in 64 bits."""
     qa, qb = Z.mx4_quantize(randn(m, k, seed=1)), Z.mx4_quantize(randn(n, k, seed=2))
@@ -254,7 +281,7 @@ def test_product_of_values(Z, m, dtype):
         x = (randn(m, k, seed=m) * torch.exp(randn(m, k, seed=5))).to(dtype)
         qb = Z.mx4_quantize(randn(n, k, seed=6))
         a64 = values64(Z.mx4_quantize(x))
-        for out in (F32, BF16):
+        for out in (F32, BF16, F16):
             check_product(Z.mx4_matmul(x, qb, out), a64, values64(qb), k)
     wide = randn(m, 700, seed=9).to(dtype)
     qb = Z.mx4_quantize(randn(50, 129, seed=6))
@@ -340,6 +367,21 @@ def test_orthogonalize(Z, count, rows, cols):
             assert rel(out[i], ns64(x[i])) <= ns_tol(rows, cols) + half_step(dst)
 
 
+# one size for every tile shape of the symmetric products, then of the product with X, and strips past the
+# count that makes M in each of them
+NS_SHAPES = [(16, 1160, 1160), (16, 900, 900), (16, 650, 650), (16, 450, 450), (8, 900, 900), (16, 330, 330),
+             (16, 390, 1560), (16, 330, 1320), (16, 1040, 260), (16, 170, 680), (8, 330, 1320), (16, 430, 130),
+             (1, 20, 33000), (1, 40, 17000), (2, 8500, 100), (130, 60, 500), (130, 1000, 20)]
+
+
+@pytest.mark.parametrize("count,rows,cols", NS_SHAPES)
+def test_orthogonalize_every_tile_shape(Z, count, rows, cols):
+    x = randn(count, rows, cols, seed=rows)
+    out = Z.orthogonalize(x, F16)
+    for i in {0, count // 2, count - 1}:
+        assert rel(out[i], ns64_gpu(x[i])) <= ns_tol(rows, cols) + half_step(F16)
+
+
 @pytest.mark.parametrize("rows,cols", [(5, 200), (64, 64), (96, 65), (128, 100), (130, 200), (700, 256)])
 def test_orthogonalize_spectra(Z, rows, cols):
     m = min(rows, cols)
@@ -418,7 +460,8 @@ def muon64(p, m, g, clip, lr, mu, wd, nesterov, scale, rows, cols):
     return p - lr * wd * p - lr * s * o, m, lr * s * o
 
 
-@pytest.mark.parametrize("count,rows,cols", [(1, 1, 1), (3, 40, 33), (2, 128, 128), (2, 200, 130), (1, 130, 300), (1, 700, 257)])
+@pytest.mark.parametrize("count,rows,cols", [(1, 1, 1), (3, 40, 33), (2, 128, 128), (2, 200, 130), (1, 130, 300), (1, 700, 257),
+                                             (1, 20, 2000), (2, 1000, 60), (1, 128, 700)])
 @pytest.mark.parametrize("nesterov,scale,wd", [(True, 1, 0.01), (False, 0, 0.0)])
 def test_muon_step(Z, count, rows, cols, nesterov, scale, wd):
     lr, mu = 1e-2, 0.95

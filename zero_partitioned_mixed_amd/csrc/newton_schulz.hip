@@ -480,11 +480,9 @@ struct StripWave {
     __device__ __forceinline__ int place(int n) const { return (n * P::WAVES + wave) * RT * RT * 256; }
 };
 
-template <class IO>
-struct StripArgs {
-    IO io;
+struct StripPlan {
     Coeffs k;
-    int steps;
+    int m, steps;
     const int32_t* skip;
     // several strips a matrix:
     char* ws;
@@ -497,6 +495,11 @@ struct StripArgs {
     int fused;                  // M is made in every strip
 };
 
+template <class IO>
+struct StripArgs : StripPlan {
+    IO io;
+};
+
 // The whole iteration of a matrix of one strip.
 template <class P, class IO>
 __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
     const IO& io = a.io;
     const int b = blockIdx.x;
     const bool tall = io.rows > io.cols;
-    const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
+    const int m = a.m, n = tall ? io.rows : io.cols;
     StripWave<P> w(lds, m);
     const int nb = (n + P::G * P::T - 1) / (P::G * P::T);
     const float clip = io.clip();
@@ -532,8 +535,8 @@ __global__ void __launch_bounds__(P::THREADS) ns_strip_kernel(StripArgs<IO> a) {
 
 // S of a matrix of several strips, this wave's tiles: the sum of the strips' parts,
 // several of them on their way at once.
-template <class P, class W, class IO>
-__device__ __forceinline__ void sum_parts_of(const W& w, const StripArgs<IO>& a, const char* ws, typename W::Tiles& s) {
+template <class P, class W>
+__device__ __forceinline__ void sum_parts_of(const W& w, const StripPlan& a, const char* ws, typename W::Tiles& s) {
     constexpr int kAtOnce = P::RT == 1 ? 8 : 4;
     const float* parts = (const float*)(ws + a.parts) + w.place();
     W::values([&](int i, int j, int r) { s[i][j][r] = 0.0f; });
@@ -552,12 +555,12 @@ __device__ __forceinline__ void sum_parts_of(const W& w, const StripArgs<IO>& a,
 }
 
 // M of a matrix of many strips: both parts of its pair, then the diagonal.
-template <class P, class IO>
-__global__ void __launch_bounds__(P::GROUP * 64) ns_poly_kernel(StripArgs<IO> a) {
+template <class P>
+__global__ void __launch_bounds__(P::GROUP * 64) ns_poly_kernel(StripPlan a) {
     typedef Strip<P::T, P::RT, 1, 1> One;
     __shared__ StripLds<One> lds;
     if (a.skip != nullptr && *a.skip != 0) return;
-    StripWave<One> w(lds, a.io.rows < a.io.cols ? a.io.rows : a.io.cols);
+    StripWave<One> w(lds, a.m);
     char* ws = a.ws + blockIdx.x * a.stride;
     typename StripWave<One>::Tiles s;
     sum_parts_of<P>(w, a, ws, s);
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(P::THREADS) ns_strips_kernel(StripArgs<IO> a) 
     const IO& io = a.io;
     const int b = blockIdx.y, strip = blockIdx.x, j0 = strip * a.cols;
     const bool tall = io.rows > io.cols;
-    const int m = tall ? io.cols : io.rows, n = tall ? io.rows : io.cols;
+    const int m = a.m, n = tall ? io.rows : io.cols;
     StripWave<P> w(lds, m);
     const int left = n - j0 < a.cols ? n - j0 : a.cols, nb = (left + P::G * P::T - 1) / (P::G * P::T);
     char* ws = a.ws + b * a.stride;
@@ -1093,7 +1096,8 @@ int run_strips(const IO& io, int32_t count, const zero_newton_schulz& ns, const 
                void* ws, hipStream_t s, const char* what) {
     return with_strip(count, io.rows, io.cols, [&](auto shape, int strips, int each_cols) {
         typedef decltype(shape) P;
-        StripArgs<IO> a{io, k, ns.steps, skip, (char*)ws, 0, 0, 0, 0, 0, 0, strips, each_cols, 0, strips <= kFused};
+        const int m = io.rows < io.cols ? io.rows : io.cols;
+        StripArgs<IO> a{{k, m, ns.steps, skip, (char*)ws, 0, 0, 0, 0, 0, 0, strips, each_cols, 0, strips <= kFused}, io};
         const dim3 each((unsigned)count);
         if (strips == 1) return launch(ns_strip_kernel<P, IO>, each, P::THREADS, s, a, what);
         a.sum_parts = sum_parts(io.rows, io.cols);
@@ -1111,7 +1115,7 @@ int run_strips(const IO& io, int32_t count, const zero_newton_schulz& ns, const 
         for (a.step = 0; rc == ZERO_OK && a.step <= ns.steps; ++a.step) {
             a.parts = w.parts[a.step & 1];  // a strip may still read them when another one writes the next
             a.next = w.parts[(a.step + 1) & 1];
-            if (a.step > 0 && !a.fused) rc = launch(ns_poly_kernel<P, IO>, each, P::GROUP * 64, s, a, what);
+            if (a.step > 0 && !a.fused) rc = launch(ns_poly_kernel<P>, each, P::GROUP * 64, s, (const StripPlan&)a, what);
             if (rc == ZERO_OK)
                 rc = launch(ns_strips_kernel<P, IO>, dim3((unsigned)strips, (unsigned)count), P::THREADS, s, a, what);
         }
