@@ -595,10 +595,10 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
  * which drives every singular value of X towards 1 and keeps the singular
  * vectors.  A zero matrix gives zeros; a matrix holding inf or NaN gives NaN.
  * Between steps X is fp32; the products take fp16 operands (power-of-two
- * scaled, fp32 sums) whose diagonals are kept apart in fp32.  The result is
- * within about 1e-3 (relative, Frobenius norm; 1e-5 where the smaller side is at
- * most 128) of the iteration in 64 bits,
- * so it is returned in 16 bits.  The scales are chosen for coefficients that
+ * scaled, fp32 sums) whose diagonals are kept apart in fp32.  Before its own
+ * rounding to 16 bits the result is within about 1e-3 of the iteration in 64 bits
+ * (relative, Frobenius norm), 1e-5 where the smaller side is at most 128, and up
+ * to 4e-3 for larger matrices whose elements all round alike (constant ones).  The scales are chosen for coefficients that
  * keep the singular values below about 1.3, as the usual ones do. */
 #define ZERO_F32 3 /* a dtype of the matrix calls below, where they say so */
 

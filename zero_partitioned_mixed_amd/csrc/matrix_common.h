@@ -9,7 +9,7 @@
 // fragments are read while the one before multiplies, and a quarter of the next
 // loads goes out with each k step: issued together they hold up their wave for as
 // long as the memory pipeline takes them (4096^3, fp16: 900 TFLOP/s with neither,
-// 1050 with both; the library's product 1220 at 8192^3).  A fragment of
+// 1050 with both, 1110 with the shapes below; the library's product 1220 at 8192^3).  A fragment of
 // the 32x32 matrix instructions is 16 bytes per lane, so fp16 (k = 16) and
 // 4-bit (k = 64) operands move alike and share this code; which 16-byte
 // pieces of a slab meet in one instruction does not matter as long as both

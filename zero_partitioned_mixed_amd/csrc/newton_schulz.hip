@@ -8,8 +8,9 @@
 // their weight, are kept in fp32 outside the fp16 operands:
 //   S = D + E,  S^2 = E E + (d_i + d_j) e_ij + D^2,  X <- diag(M) X + (M - diag(M)) X.
 // Only the off-diagonal parts and the product's copy of X are rounded to 11
-// bits: 3e-4 to 9e-4 against 64 bits for spectra from flat to 1/k, up to 4e-3
-// where every element rounds alike (constant matrices).
+// bits: against 64 bits 3e-4 to 9e-4 for spectra from flat to 1/k (a quarter of the
+// rank: up to 1.3e-3), and up to 2.4e-3 for identities and 3.9e-3 for constant
+// matrices, whose elements all round alike.
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
 // keeps |a| + 1.5 |b| + 2.25 |c| below 2^15; entries down to 1 / (65536 * 256)
 // stay normal or lose less than X's own rounding.
@@ -156,7 +157,7 @@ __device__ __forceinline__ double block_sum(double v, double* red, int waves) {
 //
 // What bounds a step is its chain of barriers and the arithmetic of splitting and
 // storing, not the products: hence many waves with small tiles (eight waves
-// with 32 x 32 tiles took 4.3 us a step at 64 x 64 and 10 at 128 x 128).
+// with 32 x 32 tiles took 4.3 us a step at 64 x 64 and 10 at 128 x 128; these 1.7 and 7).
 template <int T_, int RT_, int G_, int NB_>
 struct Strip {
     static constexpr int T = T_, RT = RT_, G = G_, NB = NB_;
@@ -166,7 +167,7 @@ struct Strip {
     static constexpr int VALUES = RT * RT * 4;  // of a block, per lane
     static constexpr int SIZE = COLS * T;    // elements of a strip
     // S and M by the waves on and below the diagonal only, mirrored: where LDS reads
-    // bound the products (128 x 128: 8 against 10 us a step)
+    // bound the products (128 x 128: 8 against 10 us a step when it was taken, 7 now)
     static constexpr bool MIRROR = RT == 2;
 };
 typedef Strip<32, 1, 4, 8> Strip32;
