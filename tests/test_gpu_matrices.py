@@ -616,6 +616,38 @@ def test_other_stream_and_graph(Z):
         assert all(torch.equal(a, b) for a, b in zip([*held, out], eager))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_linear_and_gradients_in_graph(Z, dtype):
+    """Forward and backward replayed with new values equal the eager ones each time.
+
+    The leaves are the capture's own, so that no eager graph holds them."""
+    tokens, n, k = 70, 90, 200
+    x, w, dy = randn(tokens, k, dtype=dtype), randn(n, k, seed=1, dtype=dtype), randn(tokens, n, seed=2, dtype=dtype)
+
+    def work(x, w):
+        y = Z.mx4_linear(x, w)
+        return (y.detach(), *torch.autograd.grad(y, (x, w), dy))
+
+    work(x.clone().requires_grad_(), w.clone().requires_grad_())  # loads the kernels
+    xs, ws = x.clone().requires_grad_(), w.clone().requires_grad_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work(xs, ws)
+    for i in range(4):
+        with torch.no_grad():
+            xs.copy_(randn(tokens, k, seed=10 + i, dtype=dtype))
+            ws.copy_(randn(n, k, seed=20 + i, dtype=dtype))
+            dy.copy_(randn(tokens, n, seed=30 + i, dtype=dtype))
+            for t in held:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        eager = work(xs.detach().clone().requires_grad_(), ws.detach().clone().requires_grad_())
+        assert all(torch.equal(a, b) for a, b in zip(got, eager))
+
+
 def test_refusals_of_tensors(Z):
     x = randn(8, 64)
     with pytest.raises(TypeError):

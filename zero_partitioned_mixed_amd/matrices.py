@@ -384,7 +384,11 @@ class _Mx4Linear(torch.autograd.Function):
 def mx4_linear(x, w):
     """x w^T for x [tokens, k] and w [n, k] of one type (fp16, bf16 or fp32), both
     quantised to MXFP4; differentiable: the gradients are the products of quantised
-    operands too (the rounding itself is passed through)."""
+    operands too (the rounding itself is passed through).
+
+    Forward and backward can be captured into a HIP graph.  As with every autograd
+    function, no eager result of the same leaves may be alive then: torch would
+    accumulate their gradients on that result's stream, inside the capture."""
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or not x.numel() or not w.numel():
         raise ValueError("expected x [tokens, k] and w [n, k], not empty")
     if x.dtype != w.dtype:
