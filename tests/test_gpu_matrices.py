@@ -671,3 +671,16 @@ def test_refusals_of_tensors(Z):
     with pytest.raises(Z.ZeroError) as e:
         Z.orthogonalize(randn(200, 200), F16, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.code == -4
+
+
+# ----------------------------------------------------------------------------- rows whose elements round alike
+# One element a row: S is diagonal then, and its diagonal is fp32, so nothing is rounded to 11 bits but the result.
+# The tolerance is the narrow matrices' share for fp32, and half a step of the result, whose elements all round alike.
+@pytest.mark.parametrize("rows,cols", [(412, 412), (482, 482), (493, 700), (900, 482), (520, 520), (1100, 1040)])
+def test_orthogonalize_one_element_a_row(Z, rows, cols):
+    m = min(rows, cols)
+    torch.manual_seed(rows)
+    spread = torch.zeros(rows, cols)
+    spread[torch.randperm(rows)[:m], torch.randperm(cols)[:m]] = 1.0
+    for x in (torch.eye(rows, cols), spread):
+        assert rel(Z.orthogonalize(x.cuda(), F16), ns64(x)) <= 500 * 2.0 ** -24 + half_step(F16)

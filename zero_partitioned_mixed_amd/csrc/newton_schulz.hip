@@ -7,10 +7,12 @@
 // stays in fp32 between steps, and the diagonals of S and M, which hold most of
 // their weight, are kept in fp32 outside the fp16 operands:
 //   S = D + E,  S^2 = E E + (d_i + d_j) e_ij + D^2,  X <- diag(M) X + (M - diag(M)) X.
+// D is the rows' squared norms of the fp32 X, summed where X is made: from the rounded
+// X, rows whose elements round alike came out up to 6e-3 off (an identity of 482).
 // Only the off-diagonal parts and the product's copy of X are rounded to 11
-// bits: against 64 bits 3e-4 to 9e-4 for spectra from flat to 1/k (a quarter of the
-// rank: up to 1.3e-3), and up to 2.4e-3 for identities and 3.9e-3 for constant
-// matrices, whose elements all round alike.
+// bits: against 64 bits 3e-4 to 1.1e-3 for spectra from flat to 1/k (a quarter of the
+// rank: up to 1.5e-3), and up to 1.2e-2 for constant matrices, whose elements all
+// round alike (55 sizes from 130 x 200 to 4096 x 4096, fp16 results).
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
 // keeps |a| + 1.5 |b| + 2.25 |c| below 2^15; entries down to 1 / (65536 * 256)
 // stay normal or lose less than X's own rounding.
@@ -40,6 +42,7 @@ struct Work {
     int64_t stride;  // bytes from one matrix's block to the next
     char* base;
     int64_t x16, xt0, xt1, s16, m16, ds, dm, sums;  // byte offsets; X in fp32 at 0
+    int64_t rows;  // parts of X's squared row norms: a run of mp floats for every group of columns
     int parts;                                      // partial sums of squares per matrix
     const int32_t* skip;                            // != NULL and set: leave everything as it is
     __device__ char* of(int b) const { return base + (int64_t)b * stride; }
@@ -696,6 +699,18 @@ __global__ void __launch_bounds__(256) ns_begin_kernel(IoArgs<IO> a) {
     _Float16 *x16 = (_Float16*)(base + w.x16), *xt = (_Float16*)(base + w.xt0);
     // wide orientation: row i of the patch's rows (or columns, when tall)
     const int i0 = tall ? c0 : r0, j0 = tall ? r0 : c0;
+    {  // the patch's part of the squared row norms, four lanes a row
+        const int i = tid >> 2, from = (tid & 3) * (kPatch / 4);
+        float t = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kPatch / 4; ++e) {
+            const float v = tall ? patch[from + e][i] : patch[i][from + e];
+            t += v * v;
+        }
+        t += __shfl_xor(t, 1);
+        t += __shfl_xor(t, 2);
+        if ((tid & 3) == 0 && i0 + i < w.m) ((float*)(base + w.rows))[(int64_t)(j0 / kPatch) * w.mp + i0 + i] = t;
+    }
     for (int i = y; i < kPatch; i += 4) {
         const float v = tall ? patch[x][i] : patch[i][x];   // element (i0 + i, j0 + x) of X
         const float vt = tall ? patch[i][x] : patch[x][i];  // element (i0 + x, j0 + i) of X
@@ -735,9 +750,11 @@ __global__ void __launch_bounds__(256) ns_end_kernel(IoArgs<IO> a) {
 struct StepArgs {
     Work w;
     Coeffs k;
-    int tiles_m, tiles_n;  // tile grid of the product
+    int tiles_m, tiles_n;  // tile grid of the product with M
+    int tiles;             // tiles on and above the diagonal of S or M
     int odd;               // which copy of X^T is current
     int last;              // the last step: only the fp32 X is wanted
+    int row_parts;         // parts of each squared row norm of X
 };
 
 // Upper triangle tile t -> (i <= j).
@@ -757,15 +774,40 @@ constexpr int ns_lds() {
     return a > b ? a : b;
 }
 
-// S (POLY false) or M (POLY true): tiles on and above the diagonal, mirrored.
+// The diagonal of S for 64 rows, a lane each: the parts of the rows' squared norms,
+// summed by the waves in turn and then over the waves (`sums`: 64 floats per wave).
+constexpr int kNormRows = 64;
+template <int WAVES>
+__device__ __forceinline__ void row_norms(const Work& w, char* base, int row_parts, int first, float* sums) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = first + lane;
+    const float* parts = (const float*)(base + w.rows) + (i < w.m ? i : w.m - 1);
+    float t = 0.0f;
+#pragma unroll 8
+    for (int p = wave; p < row_parts; p += WAVES) t += parts[(int64_t)p * w.mp];
+    sums[wave * 64 + lane] = t;
+    __syncthreads();
+    if (wave > 0 || i >= w.m) return;
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) t += sums[v * 64 + lane];
+    ((float*)(base + w.ds))[i] = t * (1.0f / (kXScale * kXScale));
+}
+
+// S (POLY false) or M (POLY true): tiles on and above the diagonal, mirrored.  S: the
+// workgroups after the tiles' make its diagonal, 64 rows each.
 template <class S, bool POLY>
 __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     __shared__ __attribute__((aligned(16))) char lds[ns_lds<S>()];
     const Work& w = a.w;
     if (w.skipped()) return;
     char* base = w.of(blockIdx.y);
+    if constexpr (!POLY) {
+        if ((int)blockIdx.x >= a.tiles) {
+            row_norms<S::THREADS / 64>(w, base, a.row_parts, ((int)blockIdx.x - a.tiles) * kNormRows, (float*)lds);
+            return;
+        }
+    }
     int ti, tj;
-    triangle_tile(xcd_tile(blockIdx.x, gridDim.x), ti, tj);
+    triangle_tile(xcd_tile(blockIdx.x, a.tiles), ti, tj);
     const int ld = POLY ? w.mp : w.np;  // elements
     const char* from = base + (POLY ? w.s16 : w.x16);
     const int i0 = ti * S::TILE, j0 = tj * S::TILE;
@@ -782,7 +824,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     const Lane L(S::WAVES);
     const int iw = i0 + L.wave / (S::TILE / S::WN) * S::WM, jw = j0 + L.wave % (S::TILE / S::WN) * S::WN;
     const Coeffs& k = a.k;
-    float* diag = (float*)(base + (POLY ? w.dm : w.ds));
+    float* dm = (float*)(base + w.dm);
     const float* ds = (const float*)(base + w.ds);
     const _Float16* s16 = (const _Float16*)(base + w.s16);
     _Float16* out = (_Float16*)(base + (POLY ? w.m16 : w.s16));
@@ -825,19 +867,15 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
                         float s2 = v[e] * (1.0f / (kSScale * kSScale)) + x * (di + dj[e]);
                         if (i == j + e) {
                             s2 += di * di;
-                            if (i < w.m) diag[i] = k.a + k.b * di + k.c * s2;
+                            if (i < w.m) dm[i] = k.a + k.b * di + k.c * s2;
                         }
                         v[e] = i == j + e ? 0.0f : (k.b * x + k.c * s2) * k.mscale;
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        v[e] *= 1.0f / (kXScale * kXScale);
-                        if (i == j + e) {
-                            if (i < w.m) diag[i] = v[e];
-                            v[e] = 0.0f;
-                        }
-                        v[e] *= kSScale;
+                        v[e] *= kSScale / (kXScale * kXScale);
+                        if (i == j + e) v[e] = 0.0f;
                     }
                 }
 #pragma unroll
@@ -885,6 +923,9 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     _Float16 *x16 = (_Float16*)(base + w.x16), *next = (_Float16*)(base + (a.odd ? w.xt0 : w.xt1));
     const bool two = w.kp > w.mp;
     Turner<S> turner(lds, L), rest(lds + S::WAVES * Turner<S>::kBytes, L);
+    float norms[S::MT * 4];  // of this lane's rows, its columns' part
+#pragma unroll
+    for (int t = 0; t < S::MT * 4; ++t) norms[t] = 0.0f;
 #pragma unroll
     for (int jj = 0; jj < S::NT; ++jj) {
         const int j = jw + jj * 32 + (L.c & ~3);
@@ -917,6 +958,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
                     v[e] = inside && j + e < w.n ? d * x[e] + v[e] * un : 0.0f;
                     x[e] = v[e];
                     h[e] = (_Float16)v[e];
+                    norms[ii * 4 + q] += v[e] * v[e];
                 }
                 if (inside) {
                     *(f32x4*)(x32 + at) = x;
@@ -934,6 +976,19 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
         if (!a.last) {
             turner.flush(L, next, w.kp, jw + jj * 32, iw, w.n, w.mp);
             if (two) rest.flush(L, next + w.mp, w.kp, jw + jj * 32, iw, w.n, w.mp);
+        }
+    }
+    if (!a.last) {  // the eight lanes that share a row: a part of its squared norm for every wave's columns
+        constexpr int kAcross = S::TILE / S::WN;
+        float* part = (float*)(base + w.rows) + (int64_t)(tj * kAcross + L.wave % kAcross) * w.mp;
+#pragma unroll
+        for (int t = 0; t < S::MT * 4; ++t) {
+            float v = norms[t];
+            v += quad_swap<0x124>(v);  // of the lane four on among sixteen, then eight
+            v += quad_swap<0x128>(v);
+            v += __shfl_xor(v, 16);
+            const int i = iw + t / 4 * 32 + 8 * (t % 4) + 4 * L.h + (L.c & 3);
+            if (L.c < 4 && i < w.m) part[i] = v;
         }
     }
 }
@@ -979,6 +1034,7 @@ Work work_of(int64_t rows, int64_t cols) {
     w.ds = take((int64_t)w.m * 4);
     w.dm = take((int64_t)w.m * 4);
     w.sums = take((int64_t)w.parts * 8);
+    w.rows = take((int64_t)(w.np / 64) * 2 * w.mp * 4);  // tiles of 64 have the most: two waves each
     w.stride = at;
     return w;
 }
@@ -1067,11 +1123,13 @@ int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStrea
     auto square_tiles = [&](int64_t t) { return count * (ceil_div(w.m, t) * (ceil_div(w.m, t) + 1) / 2); };
     auto whole_tiles = [&](int64_t t) { return count * ceil_div(w.m, t) * ceil_div(w.np, t); };
     const int square = pick_tile(square_tiles), whole = pick_tile(whole_tiles);
-    StepArgs a{w, k, 0, 0, 0, 0};
+    StepArgs a{w, k, 0, 0, 0, 0, 0, w.np / kPatch};  // ns_begin's parts of the row norms
     auto squares = [&](auto poly) {
         return with_tile(square, [&](auto shape) {
             typedef decltype(shape) S;
-            const dim3 grid((unsigned)(square_tiles(S::TILE) / count), (unsigned)count);
+            a.tiles = (int)(square_tiles(S::TILE) / count);
+            const int64_t norms = decltype(poly)::value ? 0 : ceil_div(w.m, kNormRows);
+            const dim3 grid((unsigned)(a.tiles + norms), (unsigned)count);
             return launch(ns_square_kernel<S, decltype(poly)::value>, grid, S::THREADS, s, a, what);
         });
     };
@@ -1084,8 +1142,10 @@ int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStrea
             typedef decltype(shape) S;
             a.tiles_m = (int)ceil_div(w.m, S::TILE);
             a.tiles_n = (int)ceil_div(w.np, S::TILE);
-            return launch(ns_apply_kernel<S>, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)count), S::THREADS, s, a,
-                          what);
+            const int launched = launch(ns_apply_kernel<S>, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)count),
+                                        S::THREADS, s, a, what);
+            a.row_parts = a.tiles_n * (S::TILE / S::WN);
+            return launched;
         });
         if (rc != ZERO_OK) return rc;
     }
