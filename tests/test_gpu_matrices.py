@@ -684,3 +684,14 @@ def test_orthogonalize_one_element_a_row(Z, rows, cols):
     spread[torch.randperm(rows)[:m], torch.randperm(cols)[:m]] = 1.0
     for x in (torch.eye(rows, cols), spread):
         assert rel(Z.orthogonalize(x.cuda(), F16), ns64(x)) <= 500 * 2.0 ** -24 + half_step(F16)
+
+
+# Elements of one or two values would round alike; independent roundings of rows make the tolerance of other matrices
+# hold for them.
+@pytest.mark.parametrize("rows,cols", [(177, 790), (372, 2000), (817, 1200), (1190, 1500), (6328, 1939), (1393, 21020)])
+def test_orthogonalize_equal_elements(Z, rows, cols):
+    torch.manual_seed(rows)
+    two = 1.0 + (torch.randn(1, cols) > 0).float().expand(rows, cols)
+    for x in (torch.ones(rows, cols), two, two.flip(1) * (1.0 + (torch.randn(rows, 1) > 0).float())):
+        x = x.cuda()
+        assert rel(Z.orthogonalize(x, F16), ns64_gpu(x)) <= NS_TOL + half_step(F16)

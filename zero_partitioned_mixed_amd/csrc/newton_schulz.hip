@@ -10,8 +10,8 @@
 // D is the rows' squared norms of the fp32 X, summed where X is made: from the rounded
 // X, rows whose elements round alike came out up to 6e-3 off (an identity of 482).
 // Only the off-diagonal parts and the product's copy of X are rounded to 11
-// bits: against 64 bits 3e-4 to 1.1e-3 for spectra from flat to 1/k (a quarter of the
-// rank: up to 1.5e-3), and up to 1.2e-2 for constant matrices, whose elements all
+// bits: against 64 bits 3e-4 to 1.1e-3 for spectra from flat to 1/k, up to 1.5e-3 for a
+// quarter of the rank and 1.7e-3 for matrices of one or two values, whose elements all
 // round alike (55 sizes from 130 x 200 to 4096 x 4096, fp16 results).
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
 // keeps |a| + 1.5 |b| + 2.25 |c| below 2^15; entries down to 1 / (65536 * 256)
@@ -28,6 +28,17 @@
 namespace {
 
 constexpr float kXScale = 256.0f, kSScale = 4096.0f;
+
+// Row i of an fp16 operand of the large matrices is stored times spread(i), a number in
+// [1, 2) that differs from row to row, and a product's results are divided by their row's
+// and column's.  Elements that are equal then round differently in different rows, so that
+// the roundings average out as those of other matrices do: with plain powers of two,
+// constant matrices came out up to 1.2e-2 off (1393 x 21020; now at most 1.7e-3 at 55 sizes).
+__device__ __forceinline__ float spread(int i) {
+    return __builtin_bit_cast(float, 0x3F800000u | ((uint32_t)i * 0x9E3779B1u) >> 9);
+}
+// a b + c in fp16, one instruction.
+__device__ __forceinline__ _Float16 half_fma(float a, float b, float c = 0.0f) { return (_Float16)__builtin_fmaf(a, b, c); }
 
 struct Coeffs {
     float a, b, c, eps;
@@ -716,12 +727,13 @@ __global__ void __launch_bounds__(256) ns_begin_kernel(IoArgs<IO> a) {
         const float vt = tall ? patch[i][x] : patch[x][i];  // element (i0 + x, j0 + i) of X
         if (i0 + i < w.m && j0 + x < w.np) {
             x32[(int64_t)(i0 + i) * w.np + j0 + x] = v;
-            x16[(int64_t)(i0 + i) * w.np + j0 + x] = (_Float16)v;
+            x16[(int64_t)(i0 + i) * w.np + j0 + x] = half_fma(v, spread(i0 + i));
         }
         if (j0 + i < w.n && i0 + x < w.mp) {
             const int64_t at = (int64_t)(j0 + i) * w.kp + i0 + x;
-            xt[at] = (_Float16)vt;
-            if (w.kp > w.mp) xt[at + w.mp] = (_Float16)(vt - (float)(_Float16)vt);
+            const _Float16 high = half_fma(vt, spread(j0 + i));
+            xt[at] = high;
+            if (w.kp > w.mp) xt[at + w.mp] = half_fma(vt, spread(j0 + i), -(float)high);
         }
     }
 }
@@ -834,6 +846,16 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
 #pragma unroll
     for (int jj = 0; jj < S::NT; ++jj) {
         const int j = jw + jj * 32 + (L.c & ~3);  // and the three after it
+        // worked out again for every column block: kept across them, the rows' addresses and
+        // factors take registers that the tile of 256 has not left
+        int mine = iw + 4 * L.h + (L.c & 3);
+        asm volatile("" : "+v"(mine));
+        float tj4[4], uj4[4];  // the columns' factors: their rows' of the mirrored tile
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            tj4[e] = spread(j + e);
+            uj4[e] = __builtin_amdgcn_rcpf(tj4[e]);
+        }
         // what the tile needs from memory, all of a column block before its first use
         float dj[4], di4[S::MT * 4];
         f16x4 old[S::MT * 4];
@@ -842,7 +864,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
             for (int e = 0; e < 4; ++e) dj[e] = ds[j + e < w.m ? j + e : w.m - 1];
 #pragma unroll
             for (int t = 0; t < S::MT * 4; ++t) {
-                const int i = iw + t / 4 * 32 + 8 * (t % 4) + 4 * L.h + (L.c & 3), ic = i < w.m ? i : w.m - 1;
+                const int i = mine + 8 * t, ic = i < w.m ? i : w.m - 1;
                 old[t] = *(const f16x4*)(s16 + (int64_t)ic * w.mp + (j < w.mp ? j : w.mp - 4));
                 di4[t] = ds[ic];
             }
@@ -851,20 +873,21 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
         for (int ii = 0; ii < S::MT; ++ii)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int row = ii * 32 + 8 * q + 4 * L.h, i = iw + row + (L.c & 3);
+                const int row = ii * 32 + 8 * q + 4 * L.h, i = mine + ii * 32 + 8 * q;
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
                 quad_turn(v);
                 const bool inside = i < w.m && j < w.mp;
-                f16x4 h;
+                const float ti1 = spread(i), ui1 = __builtin_amdgcn_rcpf(ti1);
+                f16x4 h, mirrored;  // the value times its row's factor, and times its column's
                 if constexpr (POLY) {
                     const float di = di4[ii * 4 + q];
                     const f16x4 e16 = old[ii * 4 + q];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = (float)e16[e] * (1.0f / kSScale);
-                        float s2 = v[e] * (1.0f / (kSScale * kSScale)) + x * (di + dj[e]);
+                        const float x = (float)e16[e] * (1.0f / kSScale) * ui1;
+                        float s2 = v[e] * (1.0f / (kSScale * kSScale)) * (ui1 * uj4[e]) + x * (di + dj[e]);
                         if (i == j + e) {
                             s2 += di * di;
                             if (i < w.m) dm[i] = k.a + k.b * di + k.c * s2;
@@ -874,18 +897,20 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        v[e] *= kSScale / (kXScale * kXScale);
                         if (i == j + e) v[e] = 0.0f;
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (i >= w.m || j + e >= w.m) v[e] = 0.0f;  // rows repeated past the end
-                    h[e] = (_Float16)v[e];
+                    // S: one of the two factors that the product carries is wanted
+                    constexpr float kOne = kSScale / (kXScale * kXScale);
+                    h[e] = half_fma(v[e], POLY ? ti1 : uj4[e] * kOne);
+                    mirrored[e] = half_fma(v[e], POLY ? tj4[e] : ui1 * kOne);
                 }
                 if (inside) *(f16x4*)(out + (int64_t)i * ldo + j) = h;
                 if (inside && twice) *(f16x4*)(out + (int64_t)i * ldo + w.mp + j) = h;
-                if (ti != tj) turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, h))));
+                if (ti != tj) turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, mirrored))));
             }
         if (ti != tj) {
             turner.flush(L, out, ldo, jw + jj * 32, iw, w.m, w.mp);
@@ -929,12 +954,21 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
 #pragma unroll
     for (int jj = 0; jj < S::NT; ++jj) {
         const int j = jw + jj * 32 + (L.c & ~3);
+        // worked out again, as in ns_square_kernel (47 registers spilled without)
+        int mine = iw + 4 * L.h + (L.c & 3);
+        asm volatile("" : "+v"(mine));
+        float tj4[4], uj4[4];  // the columns' factors
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            tj4[e] = spread(j + e);
+            uj4[e] = __builtin_amdgcn_rcpf(tj4[e]) * un;
+        }
         // X of the column block, all of it before its first use
         f32x4 old[S::MT * 4];
         float dm4[S::MT * 4];
 #pragma unroll
         for (int t = 0; t < S::MT * 4; ++t) {
-            const int i = iw + t / 4 * 32 + 8 * (t % 4) + 4 * L.h + (L.c & 3), ic = i < w.m ? i : w.m - 1;
+            const int i = mine + 8 * t, ic = i < w.m ? i : w.m - 1;
             old[t] = *(const f32x4*)(x32 + (int64_t)ic * w.np + (j < w.np ? j : w.np - 4));
             dm4[t] = dm[ic];
         }
@@ -942,7 +976,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
         for (int ii = 0; ii < S::MT; ++ii)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int row = ii * 32 + 8 * q + 4 * L.h, i = iw + row + (L.c & 3);
+                const int row = ii * 32 + 8 * q + 4 * L.h, i = mine + ii * 32 + 8 * q;
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = acc[ii][jj][4 * q + r];
@@ -950,26 +984,27 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
                 const bool inside = i < w.m && j < w.np;
                 const int64_t at = (int64_t)i * w.np + j;
                 f32x4 x = old[ii * 4 + q];
-                const float d = dm4[ii * 4 + q];
-                f16x4 h;
+                const float d = dm4[ii * 4 + q], ti1 = spread(i), ui1 = __builtin_amdgcn_rcpf(ti1);
+                f16x4 h, turned;  // for X and for X^T, whose rows are the columns here
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     // past the ends of both sides: rows repeated
-                    v[e] = inside && j + e < w.n ? d * x[e] + v[e] * un : 0.0f;
+                    v[e] = inside && j + e < w.n ? __builtin_fmaf(d, x[e], v[e] * (ui1 * uj4[e])) : 0.0f;
                     x[e] = v[e];
-                    h[e] = (_Float16)v[e];
-                    norms[ii * 4 + q] += v[e] * v[e];
+                    norms[ii * 4 + q] = __builtin_fmaf(v[e], v[e], norms[ii * 4 + q]);
+                    h[e] = half_fma(v[e], ti1);
+                    turned[e] = half_fma(v[e], tj4[e]);
                 }
                 if (inside) {
                     *(f32x4*)(x32 + at) = x;
                     if (!a.last) *(f16x4*)(x16 + at) = h;
                 }
                 if (!a.last) {
-                    turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, h))));
+                    turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, turned))));
                     if (two) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = (_Float16)(v[e] - (float)h[e]);
-                        rest.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, h))));
+                        for (int e = 0; e < 4; ++e) turned[e] = half_fma(v[e], tj4[e], -(float)turned[e]);
+                        rest.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, turned))));
                     }
                 }
             }
