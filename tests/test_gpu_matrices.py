@@ -695,3 +695,17 @@ def test_orthogonalize_equal_elements(Z, rows, cols):
     for x in (torch.ones(rows, cols), two, two.flip(1) * (1.0 + (torch.randn(rows, 1) > 0).float())):
         x = x.cuda()
         assert rel(Z.orthogonalize(x, F16), ns64_gpu(x)) <= NS_TOL + half_step(F16)
+
+
+# ----------------------------------------------------------------------------- few rows, few slabs
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("k", [100, 256, 300, 640, 1024, 1700, 1920, 2047])
+def test_product_of_few_rows_and_slabs(Z, k, dtype):
+    """Up to seven slabs of 256: some of the eight waves have none.  Rows as values and as operands take the same sums."""
+    for m, n in ((1, 4096), (5, 1000), (8, 33)):
+        x = randn(m, k, seed=k).to(dtype)
+        qx, qb = Z.mx4_quantize(x), Z.mx4_quantize(randn(n, k, seed=6))
+        want = Z.mx4_matmul(qx, qb, F32)
+        check_product(want, values64(qx), values64(qb), k)
+        for _ in range(20):
+            assert torch.equal(Z.mx4_matmul(x, qb, F32), want)

@@ -427,7 +427,9 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
     const uint8_t *b = g.b + jc * half_row + 64 * L.h, *sb = g.sb + jc * scale_row + 4 * L.h;
     const int slabs = (int)(p / 256);
 
+    // A wave fetches only slabs that it then waits for: the waves' sums overwrite the ring.
     char* const ring = lds + L.wave * kFewSlabs * 32 * kSlab;
+    const bool any = L.wave < slabs;
     uint32_t bs[kFewSlabs];
     auto fetch = [&](int first) {
 #pragma unroll
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
 #pragma unroll
         for (int i = 0; i < kFirst; ++i)
             if (tid + i * kFewWaves * 64 < pieces) read(tid + i * kFewWaves * 64, e[i]);
-        if (slabs > 0) fetch(L.wave);
+        if (any) fetch(L.wave);
 #pragma unroll
         for (int i = 0; i < kFirst; ++i)
             if (tid + i * kFewWaves * 64 < pieces) put(tid + i * kFewWaves * 64, e[i]);
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
         }
         __syncthreads();
     } else {
-        if (slabs > 0) fetch(L.wave);
+        if (any) fetch(L.wave);
     }
     const uint8_t *a = VALUES ? codes : g.a, *sa = VALUES ? scales : g.sa;
     const uint32_t row = (uint32_t)(L.c < g.m ? L.c : g.m - 1);
@@ -511,7 +513,8 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx4_few_kernel(FewArgs f) {
         acc = MmFp4::mma<0>(aw[0], b0, acc, as, bsh);
         acc = MmFp4::mma<1>(aw[1], b1, acc, as, bsh);
     }
-    __syncthreads();  // the slabs have no readers any more
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no slab is on its way
+    __syncthreads();                                  // nor has one a reader any more
 #pragma unroll
     for (int r = 0; r < 16; ++r) sums[L.wave][8 * (r / 4) + 4 * L.h + r % 4][L.c] = acc[r];
     __syncthreads();
