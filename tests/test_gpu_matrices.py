@@ -709,3 +709,40 @@ def test_product_of_few_rows_and_slabs(Z, k, dtype):
         check_product(want, values64(qx), values64(qb), k)
         for _ in range(20):
             assert torch.equal(Z.mx4_matmul(x, qb, F32), want)
+
+
+# ----------------------------------------------------------------------------- several ranks with matrices
+def test_several_ranks_with_matrices(Z):
+    """Two ranks on one decision equal their own calls around the same decision, eager and from a replayed graph."""
+    n, psi, stride = 2, 4000, 4032
+    matrices = [(0, 2, 20, 33), (1400, 1, 40, 60)]
+    hp, muon = Z.hparams(lr=1e-2, max_grad_norm=0.5), Z.muon_hparams(lr=1e-2)
+
+    def ranks():
+        out = []
+        for r in range(2):
+            state = (randn(psi, seed=r) * 0.02, randn(psi, seed=r + 5) * 1e-3, (randn(psi, seed=r + 9) * 1e-3).square())
+            out.append(Z.MuonShardStep(n, stride, psi, r * psi, Z.BF16, Z.BF16, hp, muon, matrices, state,
+                                       torch.empty(psi, device="cuda")))
+        return out
+
+    contribs = [torch.zeros(n, stride, dtype=BF16, device="cuda") for _ in range(2)]
+    gathers = [torch.zeros(2 * psi, dtype=BF16, device="cuda") for _ in range(3)]
+    a, b, c = ranks(), ranks(), ranks()
+    multi, graphed = Z.MultiShardStep(a), Z.MultiShardStep(c)
+    graph = graphed.capture(contribs, gathers[2])
+    for k in range(3):
+        for r in range(2):
+            contribs[r].copy_(randn(n, stride, seed=20 + 2 * k + r) * 1e-2)
+        multi.step(contribs, gathers[0])
+        for s, t in zip(b, contribs):
+            s.run_pieces(t, gathers[1])
+        Z.zero_grad_norm_overflow([s.ws for s in b], [psi] * 2, [s.ctrl for s in b], hp, False)
+        for s in b:
+            s.complete(gathers[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, gathers[0]) for g in gathers[1:])
+        for other in (b, c):
+            for s, t in zip(a, other):
+                assert all(torch.equal(x, y) for x, y in zip(s.state, t.state))

@@ -172,3 +172,50 @@ def test_operand_sizes(Z):
     assert Z._lib.zero_mx4_operand_bytes(0, 129) == 0 == Z._lib.zero_mx4_operand_bytes(1, 1 << 25)
     assert Z._lib.zero_mx4_matmul_rows_workspace_bytes(1, 100, 4096) == 0
     assert Z._lib.zero_mx4_matmul_rows_workspace_bytes(64, 100, 4096) > 64 * 2048
+
+
+# ----------------------------------------------------------------------------- several ranks with matrices
+class Rows:
+    """Stands in for a contribution tensor, and for any buffer that is only sliced."""
+
+    def data_ptr(self):
+        return id(self)
+
+    def __getitem__(self, _):
+        return self
+
+    def view(self, *_):
+        return self
+
+
+def fake_rank(Z, cls, two_pass=True):
+    st = object.__new__(cls)
+    st.bucket, st.nranks, st.stride, st.valid_len, st.offset = 0, 2, 4096, 4096, 0
+    st.dtype = st.gather_dtype = Z.F16
+    st.hp, st.fused = Z.hparams(), not two_pass
+    st.state, st.g, st.ctrl, st.ws, st.pair = (Rows(), Rows(), Rows()), Rows(), "ctrl", "ws", None
+    st.muon, st.matrices, st.between, st.matrix_ws = "muon", [(0, 2, 8, 16)], [(256, 3840)], None
+    return st
+
+
+def test_several_ranks_with_matrices(Z, monkeypatch):
+    """The batched calls know nothing of matrices: ranks that hold some take their own calls, the matrix step among
+    them, also beside ranks that hold none."""
+    from zero_partitioned_mixed_amd import matrices
+    calls = []
+    names = ("zero_reduce_grads", "zero_reduce_grads_shards", "zero_adam_step", "zero_adam_step_shards",
+             "zero_grad_norm_overflow")
+    for name in names:
+        monkeypatch.setattr(Z, name, lambda *a, _n=name, **k: calls.append(_n))
+    monkeypatch.setattr(Z, "shard_table", lambda shards: list(shards))
+    for name in ("zero_adam_step", "muon_step"):
+        monkeypatch.setattr(matrices, name, lambda *a, _n=name, **k: calls.append(_n))
+    for other, last in ((Z.MuonShardStep, ["zero_adam_step", "muon_step"]), (Z.ShardStep, ["zero_adam_step"])):
+        calls.clear()
+        multi = Z.MultiShardStep([fake_rank(Z, Z.MuonShardStep), fake_rank(Z, other)])
+        rows = [Rows(), Rows()]
+        assert not multi.takes_batched(rows, Rows())
+        multi.step(rows, Rows())
+        assert calls == ["zero_reduce_grads"] * 2 + ["zero_grad_norm_overflow", "zero_adam_step", "muon_step"] + last
+    with pytest.raises(ValueError):  # the fused path's decision is not the two-pass path's
+        Z.MultiShardStep([fake_rank(Z, Z.MuonShardStep), fake_rank(Z, Z.ShardStep, two_pass=False)])

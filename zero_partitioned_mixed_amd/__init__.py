@@ -725,7 +725,8 @@ class MultiShardStep:
     pass: zero_fused_step_shards, the decision, zero_fused_restore_shards on
     the fused path (which also needs the 16-bit slot); zero_reduce_grads_shards,
     the decision, zero_adam_step_shards on the two-pass path.  Bit-identical to
-    every rank's own calls."""
+    every rank's own calls.  Ranks that complete a step in a way of their own
+    (MuonShardStep) take their own calls."""
 
     def __init__(self, steps: list, batched: bool = True):
         if not 1 <= len(steps) <= MAX_RANKS:
@@ -733,6 +734,8 @@ class MultiShardStep:
         first = bytes(steps[0].hp)
         if any(bytes(s.hp) != first for s in steps):
             raise ValueError("the ranks of one decision share their hyperparameters")
+        if any(s.fused != steps[0].fused for s in steps):
+            raise ValueError("the ranks of one decision share their path")
         self.steps = steps
         self.fused = steps[0].fused
         self.batched = batched
@@ -744,6 +747,8 @@ class MultiShardStep:
         if not self.batched or any(q is not None for q in qgathers):
             return None
         if self.fused and gather is None:
+            return None
+        if any(type(s).complete is not ShardStep.complete for s in ss):
             return None
         cap = launch_tiles(s0.nranks) * TILE
         if any(s.bucket or s.valid_len > cap or s.nranks != s0.nranks or s.dtype != s0.dtype
