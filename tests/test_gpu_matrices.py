@@ -746,3 +746,15 @@ def test_several_ranks_with_matrices(Z):
         for other in (b, c):
             for s, t in zip(a, other):
                 assert all(torch.equal(x, y) for x, y in zip(s.state, t.state))
+
+
+@pytest.mark.parametrize("m", [1, 32, 33, 64, 65])
+def test_product_of_empty_rows(Z, m):
+    """k = 0, as values and as operands: zeros, or what was there."""
+    b = Z.MX4.alloc(70, 0, "cuda")
+    for dtype in (F32, BF16):
+        for a in (torch.empty(m, 0, dtype=dtype, device="cuda"), Z.MX4.alloc(m, 0, "cuda")):
+            out = torch.full((m, 70), 3.0, device="cuda")
+            assert (Z.mx4_matmul(a, b, out=out) == 0).all()
+            out.fill_(3.0)
+            assert (Z.mx4_matmul(a, b, out=out, accumulate=True) == 3).all()

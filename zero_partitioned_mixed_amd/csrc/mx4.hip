@@ -755,6 +755,7 @@ int zero_mx4_matmul_rows(const void* a, int32_t a_dtype, int64_t lda, const void
     }
     MatmulArgs g{(const uint8_t*)a, nullptr, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, 0, 0};
     if (few_values(m, k)) return few_of_values(FewArgs{g, lda, k}, a_dtype, c_dtype, (hipStream_t)stream, what);
+    if (k == 0) return matmul(g, c_dtype, (hipStream_t)stream, what);  // nothing to quantise
     const Operand2 q(ws, m, k);
     const QuantArgs job{a, m, k, lda, q.codes, q.scales, nullptr, nullptr};
     if ((rc = quantize(&job, 1, a_dtype, (hipStream_t)stream, what)) != ZERO_OK) return rc;
