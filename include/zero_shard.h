@@ -585,7 +585,9 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
 
 /* ---- Matrices: orthogonalised updates ---------------------------------------
  * For parameters that are whole matrices inside a shard.  A stack is `count`
- * row-major matrices of rows x cols elements.
+ * row-major matrices of rows x cols elements.  In this part and the next one no
+ * output may share memory with what its call still reads (EINVAL), except
+ * where it says so; outputs and workspaces of one call lie apart.
  *
  * The orthogonalisation of G is k steps of an odd quintic iteration on the
  * normalised matrix, on whichever side is smaller:
@@ -616,7 +618,7 @@ size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
 /* dst[b] = orthogonalisation of src[b].  src: src_dtype ZERO_F16, ZERO_BF16
  * or ZERO_F32; row r of matrix b starts at element b * src_stride + r * src_ld.
  * dst: dst_dtype ZERO_F16 or ZERO_BF16, laid out likewise; it may be src when
- * type and layout agree.  count, rows or cols of 0: nothing is enqueued.
+ * the elements' size and the layout agree.  count, rows or cols of 0: nothing is enqueued.
  * Errors: EINVAL (null pointer, dtype, coefficients, steps, eps), EALIGN (a
  * pointer not aligned to its elements, workspace not to 16 bytes), ERANGE
  * (rows or cols above 65536, negative sizes, count above 65535, ld below

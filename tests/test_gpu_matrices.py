@@ -758,3 +758,28 @@ def test_product_of_empty_rows(Z, m):
             assert (Z.mx4_matmul(a, b, out=out) == 0).all()
             out.fill_(3.0)
             assert (Z.mx4_matmul(a, b, out=out, accumulate=True) == 3).all()
+
+
+def test_results_beside_what_is_read(Z):
+    """A result may take columns or rows of the operand's own buffer, not its elements."""
+    base = randn(40, 200, dtype=BF16)
+    x, q = base[:, :64], Z.mx4_quantize(randn(64, 64, seed=1))
+    for rows in (1, 16, 40):
+        want = Z.mx4_matmul(x[:rows].clone(), q)
+        Z.mx4_matmul(x[:rows], q, out=base[:rows, 64:128])
+        assert torch.equal(base[:rows, 64:128], want)
+        for over in (x[:rows], base[:rows, 63:127]):
+            with pytest.raises(Z.ZeroError):
+                Z.mx4_matmul(x[:rows], q, out=over)
+    h = randn(4, 70, 90, dtype=BF16)
+    want = Z.orthogonalize(h[::2, :, :40].clone())
+    for out in (h[1::2, :, :40], h[::2, :, 41:81], h[::2, :, :40]):  # the last one in place
+        Z.orthogonalize(h[::2, :, :40], out=out)
+        assert torch.equal(out, want)
+    with pytest.raises(Z.ZeroError):
+        Z.orthogonalize(h[::2, :, :40], out=h[::2, :, 1:41])
+    space = torch.zeros(4, 256, dtype=BF16, device="cuda")
+    held = Z.MX4(space.view(torch.uint8)[0, :256].view(4, 64), torch.zeros(4, 4, dtype=torch.uint8, device="cuda"), 4, 128)
+    with pytest.raises(Z.ZeroError):
+        Z.mx4_dequantize(held, out=space[:, :128])
+    Z.mx4_dequantize(held, out=space[:, 128:])

@@ -1,6 +1,9 @@
 """The matrix calls' sizes and refusals, on the host: every argument error is
 returned before anything is enqueued, so no GPU is needed."""
 import ctypes
+import os
+import random
+import subprocess
 
 import pytest
 
@@ -219,3 +222,76 @@ def test_several_ranks_with_matrices(Z, monkeypatch):
         assert calls == ["zero_reduce_grads"] * 2 + ["zero_grad_norm_overflow", "zero_adam_step", "muon_step"] + last
     with pytest.raises(ValueError):  # the fused path's decision is not the two-pass path's
         Z.MultiShardStep([fake_rank(Z, Z.MuonShardStep), fake_rank(Z, Z.ShardStep, two_pass=False)])
+
+
+# ----------------------------------------------------------------------------- results over what is read
+@pytest.fixture(scope="module")
+def overlap(tmp_path_factory):
+    """The library's own predicate of two places, built for the host alone."""
+    folder = tmp_path_factory.mktemp("overlap")
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "zero_partitioned_mixed_amd", "csrc")
+    (folder / "o.cpp").write_text("""#include "zero_internal.h"
+        extern "C" int meet(const int64_t* p) {
+            auto place = [](const int64_t* q) { return Place((const void*)q[0], q[1], q[2], q[3], q[4], q[5]); };
+            return overlap(place(p), place(p + 6)); }""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", csrc, "-o", "o.so", "o.cpp"],
+                   cwd=folder, check=True)
+    meet = ctypes.CDLL(str(folder / "o.so")).meet
+    return lambda *p: bool(meet((ctypes.c_int64 * 12)(*p)))
+
+
+def test_overlap_by_comparing_bytes(overlap):
+    """Random stacks of strided runs against their bytes: runs that lie between each other are apart."""
+    rng = random.Random(3)
+    seen = [0, 0]
+
+    def place(like):
+        rows, width, count = rng.choice([1, 2, 5]), rng.randint(1, 9), rng.choice([1, 1, 3])
+        ld = like[3] if like and rng.random() < 0.6 and like[3] >= width else rng.randint(width, width + 12)
+        span = (rows - 1) * ld + width
+        stride = like[5] if like and rng.random() < 0.6 and like[5] >= span else span + rng.randint(0, 20)
+        return [1000 + rng.randint(-150, 150), rows, width, ld, count, stride]
+
+    def taken(p):
+        at, rows, width, ld, count, stride = p
+        return {at + c * stride + r * ld + b for c in range(count) for r in range(rows) for b in range(width)}
+
+    for _ in range(20000):
+        p = place(None)
+        q = place(p)
+        meet = not taken(p).isdisjoint(taken(q))
+        assert overlap(*p, *q) == meet == overlap(*q, *p), (p, q)
+        seen[meet] += 1
+    assert min(seen) > 3000
+    assert not overlap(0, 1, 8, 8, 1, 8, 0, 1, 8, 8, 1, 8)  # null
+    assert not overlap(1000, 0, 8, 8, 1, 8, 1000, 1, 8, 8, 1, 8)
+    far = 1 << 40  # large matrices, far apart and not, at once
+    assert not overlap(far, 1 << 24, 100, 400, 1, 0, far + 100, 1 << 24, 300, 400, 1, 0)
+    assert not overlap(far, 1 << 20, 1, 64, 1, 0, far + 32, 1 << 20, 1, 128, 1, 0)
+    assert overlap(far, 1 << 20, 1, 64, 1, 0, far + 32, 1 << 20, 33, 128, 1, 0)
+    for at, meet in ((65535 << 34, False), ((65535 << 34) - 1, True), (0, True), (-1, False)):
+        assert overlap(far, 65536, 1 << 18, 1 << 18, 65535, 1 << 34, far + at, 1, 1, 1, 1, 1) == meet
+
+
+def test_overlaps_refused(Z):
+    big = 1 << 30
+    over = dict(ws=8 * big, ws_bytes=1 << 40)
+    for kw in (dict(sdt=F32), dict(sdt=BF16, dld=301), dict(sdt=BF16, dst=P + 600), dict(sdt=BF16, dst=P - 2)):
+        assert ortho(Z, src=P, **{"dst": P, **kw}, **over) == EINVAL
+    for kw in (dict(mom=P), dict(g=P + 4 * 59999), dict(gather=P + 4), dict(g=big + 16)):
+        kw = {**dict(master=P, mom=big, g=2 * big, gather=None, gdt=BF16), **kw}
+        assert muon(Z, **kw, **over) == EINVAL
+    # matrices of one buffer, into the others' of it
+    assert muon(Z, count=3, stride=180000, master=big, mom=big + 4 * 60000, g=big + 4 * 119999, gather=None, **over) == EINVAL
+    assert quant(Z, src=P, c=P, s=big, ct=None, st=None) == EINVAL
+    assert quant(Z, src=P, c=big, s=2 * big, ct=3 * big, st=P + 512 - 16) == EINVAL
+    assert Z._lib.zero_mx4_dequantize(P, big, 4, 64, P + 16, F16, 64, None) == EINVAL
+    assert Z._lib.zero_mx4_matmul(P, big, 2 * big, 3 * big, 8, 8, 64, P + 48, F16, 8, 0, None, 0, None) == EINVAL
+    assert Z._lib.zero_mx4_matmul(P, big, 2 * big, 3 * big, 8, 8, 64, 3 * big, F16, 8, 0, None, 0, None) == EINVAL
+    for m, k in ((1, 64), (32, 64), (33, 64), (8, 5000)):
+        rows = lambda c, ldc=64: Z._lib.zero_mx4_matmul_rows(P, BF16, k, big, 2 * big, m, 64, k, c, BF16, ldc, 3 * big,  # noqa: E731
+                                                             1 << 40, None)
+        assert rows(P) == rows(P + 2 * m * k - 2) == rows(P - 2, 6400) == rows(big) == rows(2 * big) == EINVAL
+    assert grad(Z, dy=P, xt=big, wt=2 * big, dx=big, dw=3 * big, ws=4 * big) == EINVAL
+    assert linear(Z, x=P, w=big, y=2 * big, xt=P, wt=3 * big, ws=4 * big) == EINVAL
+    assert "overlap" in Z.zero_last_error()

@@ -567,7 +567,23 @@ int quantize_with(const QuantArgs* jobs, int count, hipStream_t s, const char* w
     return launch(mx4_quantize_kernel<DT, 32, true>, grid, kThreads, s, q, what);
 }
 
+// Places of values (rows x cols, row stride ld) and of an operand's codes and scales.
+Place values_at(const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+    const int64_t size = (int64_t)elem_bytes(dtype);
+    return Place(p, rows, cols * size, ld * size);
+}
+Place codes_at(const void* p, int64_t rows, int64_t cols) { return Place(p, rows * (padded(cols) / 2)); }
+Place scales_at(const void* p, int64_t rows, int64_t cols) { return Place(p, rows * (padded(cols) / kMxBlock)); }
+
 int quantize(const QuantArgs* jobs, int count, int32_t dtype, hipStream_t s, const char* what) {
+    for (int i = 0; i < count; ++i)
+        for (int j = 0; j < count; ++j) {
+            const Place from = values_at(jobs[i].src, dtype, jobs[i].rows, jobs[i].cols, jobs[i].ld);
+            const int64_t rows = jobs[j].rows, cols = jobs[j].cols;
+            if (overlap(from, codes_at(jobs[j].codes, rows, cols)) || overlap(from, scales_at(jobs[j].scales, rows, cols)) ||
+                overlap(from, codes_at(jobs[j].codes_t, cols, rows)) || overlap(from, scales_at(jobs[j].scales_t, cols, rows)))
+                return fail(ZERO_EINVAL, "%s: codes or scales overlap the values", what);
+        }
     switch (dtype) {
         case ZERO_F16: return quantize_with<ZERO_F16>(jobs, count, s, what);
         case ZERO_BF16: return quantize_with<ZERO_BF16>(jobs, count, s, what);
@@ -612,6 +628,10 @@ int few_of_values(const FewArgs& f, int32_t a_dtype, int32_t c_dtype, hipStream_
 }
 
 int matmul(const MatmulArgs& g, int32_t c_dtype, hipStream_t s, const char* what) {
+    const Place c = values_at(g.c, c_dtype, g.m, g.n, g.ldc);
+    if (overlap(c, codes_at(g.a, g.m, g.p)) || overlap(c, scales_at(g.sa, g.m, g.p)) || overlap(c, codes_at(g.b, g.n, g.p)) ||
+        overlap(c, scales_at(g.sb, g.n, g.p)))
+        return fail(ZERO_EINVAL, "%s: the result overlaps an operand", what);
     // Few rows against tiles of 64, us: 1 x 11008 x 4096 8.4 and 9.2, 16 rows 9.8 and 9.1; where the tiles
     // leave half of the CUs out, 4096 x 11008, 1 row 9.8 and 14.9, 32 rows 13.4 and 15.4, 48 rows 17.2 and 16.9.
     if (g.m <= 8 || (g.m <= 32 && g.n <= 64 * 128)) return few_with<ZERO_F32, false>(FewArgs{g, 0, 0}, c_dtype, s, what);
@@ -698,6 +718,9 @@ int zero_mx4_dequantize(const void* codes, const void* scales, int64_t rows, int
     if (codes == nullptr || scales == nullptr || dst == nullptr) return fail(ZERO_EINVAL, "%s: null buffer", what);
     if (!aligned(codes, 16) || !aligned(scales, 16)) return fail(ZERO_EALIGN, "%s: operand not 16-byte aligned", what);
     if (!aligned(dst, elem_bytes(dtype))) return fail(ZERO_EALIGN, "%s: result not aligned to its elements", what);
+    const Place to = values_at(dst, dtype, rows, cols, ld);
+    if (overlap(to, codes_at(codes, rows, cols)) || overlap(to, scales_at(scales, rows, cols)))
+        return fail(ZERO_EINVAL, "%s: the result overlaps the operand", what);
     const DequantArgs a{(const uint8_t*)codes, (const uint8_t*)scales, rows, cols, ld, dst};
     const int64_t wgs = ceil_div(rows, kValueRows) * (padded(cols) / kMxPad);
     if (wgs > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
@@ -753,6 +776,9 @@ int zero_mx4_matmul_rows(const void* a, int32_t a_dtype, int64_t lda, const void
         if (!aligned(ws, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", what);
         if (ws_bytes < need) return fail(ZERO_ESPACE, "%s: workspace %zu bytes, needs %zu", what, ws_bytes, need);
     }
+    const Place to = values_at(c, c_dtype, m, n, ldc);
+    if (overlap(to, values_at(a, a_dtype, m, k, lda)) || overlap(to, codes_at(b, n, k)) || overlap(to, scales_at(sb, n, k)))
+        return fail(ZERO_EINVAL, "%s: the result overlaps an operand", what);
     MatmulArgs g{(const uint8_t*)a, nullptr, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, 0, 0};
     if (few_values(m, k)) return few_of_values(FewArgs{g, lda, k}, a_dtype, c_dtype, (hipStream_t)stream, what);
     if (k == 0) return matmul(g, c_dtype, (hipStream_t)stream, what);  // nothing to quantise
@@ -820,6 +846,9 @@ int zero_mx4_linear_grad(const void* dy, int64_t lddy, int32_t dtype, int64_t to
         return fail(ZERO_ERANGE, "%s: row stride below the row", what);
     if ((rc = check_operands(x_t, w_t, ws, ws_bytes, zero_mx4_linear_grad_workspace_bytes(tokens, n), what)) != ZERO_OK)
         return rc;
+    // dx is written before dw's product reads x_t
+    if (dw != nullptr && overlap(values_at(dx, dtype, tokens, k, lddx), Place(x_t, (int64_t)quantized_bytes(k, tokens))))
+        return fail(ZERO_EINVAL, "%s: dx overlaps x_t", what);
     const hipStream_t s = (hipStream_t)stream;
     const Operand2 r(ws, tokens, n), c((char*)ws + quantized_bytes(tokens, n), n, tokens);
     const Operand2 xt(const_cast<void*>(x_t), k, tokens), wt(const_cast<void*>(w_t), k, n);

@@ -1269,6 +1269,11 @@ int zero_orthogonalize(const void* src, int32_t src_dtype, int32_t count, int64_
     if (count > 1 && (src_stride < (rows - 1) * src_ld + cols || dst_stride < (rows - 1) * dst_ld + cols))
         return fail(ZERO_ERANGE, "%s: matrices overlap", what);
     if ((rc = check_space(ws, ws_bytes, count, rows, cols, what)) != ZERO_OK) return rc;
+    const int64_t from = (int64_t)elem_bytes(src_dtype);
+    const bool same = src == dst && from == 2 && src_ld == dst_ld && (count == 1 || src_stride == dst_stride);
+    if (!same && overlap(Place(src, rows, cols * from, src_ld * from, count, src_stride * from),
+                         Place(dst, rows, cols * 2, dst_ld * 2, count, dst_stride * 2)))
+        return fail(ZERO_EINVAL, "%s: the result overlaps the source, in another layout", what);
     auto with = [&](auto si, auto so) {
         constexpr int DTI = decltype(si)::value, DTO = decltype(so)::value;
         PlainIo<DTI, DTO> io{(const typename Elem<DTI>::type*)src, (typename Elem<DTO>::type*)dst,
@@ -1307,6 +1312,13 @@ int zero_muon_step(float* master, float* mom, const float* g, int32_t count, int
     if (offset < 0) return fail(ZERO_ERANGE, "%s: negative offset", what);
     if (count > 1 && stride < rows * cols) return fail(ZERO_ERANGE, "%s: matrices overlap", what);
     if ((rc = check_space(ws, ws_bytes, count, rows, cols, what)) != ZERO_OK) return rc;
+    const int64_t size = rows * cols * 4, apart = stride * 4;
+    const Place place[4] = {Place(master, 1, size, size, count, apart), Place(mom, 1, size, size, count, apart),
+                            Place(g, 1, size, size, count, apart),
+                            Place(gather == nullptr ? nullptr : (uint16_t*)gather + offset, 1, size / 2, size / 2, count, apart / 2)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(place[i], place[j])) return fail(ZERO_EINVAL, "%s: master, mom, g or slot overlap", what);
     const double wide = (double)(rows > cols ? rows : cols);
     const double s = hp->scale == ZERO_MUON_SCALE_RMS ? 0.2 * std::sqrt(wide)
                                                       : std::sqrt(rows > cols ? (double)rows / (double)cols : 1.0);
