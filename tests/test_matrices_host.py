@@ -295,3 +295,16 @@ def test_overlaps_refused(Z):
     assert grad(Z, dy=P, xt=big, wt=2 * big, dx=big, dw=3 * big, ws=4 * big) == EINVAL
     assert linear(Z, x=P, w=big, y=2 * big, xt=P, wt=3 * big, ws=4 * big) == EINVAL
     assert "overlap" in Z.zero_last_error()
+
+
+def test_workspace_of_scattered_bytes_refused(Z, monkeypatch):
+    """A strided tensor holds fewer bytes from its address on than it has elements."""
+    import torch
+    from zero_partitioned_mixed_amd import matrices
+    monkeypatch.setattr(matrices, "_gpu", lambda *t: 0)
+    space = torch.zeros(64, dtype=torch.float32)
+    pointer, size, _ = matrices._space(100, space[8:40], space)
+    assert (pointer, size) == (space.data_ptr() + 32, 128)
+    for ws in (space[::2], space.view(8, 8).t(), space.view(8, 8)[:, :4]):
+        with pytest.raises(ValueError, match="contiguous"):
+            matrices._space(16, ws, space)

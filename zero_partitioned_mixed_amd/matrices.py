@@ -62,6 +62,8 @@ def _space(nbytes: int, ws, like):
         ws = _empty(nbytes, dtype=_bytes, device=like.device)
         return ws.data_ptr(), nbytes, ws
     _gpu(like, ws)
+    if not ws.is_contiguous():
+        raise ValueError("ws: its bytes are not contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
