@@ -783,3 +783,20 @@ def test_results_beside_what_is_read(Z):
     with pytest.raises(Z.ZeroError):
         Z.mx4_dequantize(held, out=space[:, :128])
     Z.mx4_dequantize(held, out=space[:, 128:])
+
+
+def test_linear_without_gradients(Z):
+    """The same values where torch does not record; a checkpointed block's gradients are those of a recorded one."""
+    from torch.utils.checkpoint import checkpoint
+    x, w, dy = randn(70, 200, dtype=BF16), randn(90, 200, seed=1, dtype=BF16), randn(70, 90, seed=2, dtype=BF16)
+    xs, ws = x.clone().requires_grad_(), w.clone().requires_grad_()
+    y = Z.mx4_linear(xs, ws)
+    grads = torch.autograd.grad(y, (xs, ws), dy)
+    for mode in (torch.no_grad(), torch.inference_mode()):
+        with mode:
+            assert torch.equal(Z.mx4_linear(xs, ws), y)
+    for reentrant in (False, True):
+        xs, ws = x.clone().requires_grad_(), w.clone().requires_grad_()
+        again = checkpoint(Z.mx4_linear, xs, ws, use_reentrant=reentrant)
+        again.backward(dy)
+        assert torch.equal(again, y) and torch.equal(xs.grad, grads[0]) and torch.equal(ws.grad, grads[1])

@@ -308,3 +308,33 @@ def test_workspace_of_scattered_bytes_refused(Z, monkeypatch):
     for ws in (space[::2], space.view(8, 8).t(), space.view(8, 8)[:, :4]):
         with pytest.raises(ValueError, match="contiguous"):
             matrices._space(16, ws, space)
+
+
+def test_linear_without_gradients_keeps_nothing(Z, monkeypatch):
+    """Where torch does not record, the forward call is asked for no operands of the gradients, whatever its inputs
+    require; where it does, for those of the gradients that are wanted."""
+    import torch
+    from zero_partitioned_mixed_amd import matrices
+    calls, kept = [], []
+    monkeypatch.setattr(matrices, "_gpu", lambda *t: 0)
+    monkeypatch.setattr(matrices, "_call", lambda index, name, *a: calls.append((name, a[10], a[11])))
+    monkeypatch.setattr(matrices, "_empty", lambda *a, **k: kept.append(torch.empty(*a, **k)) or kept[-1])
+    x, w = torch.randn(8, 64, requires_grad=True), torch.randn(16, 64, requires_grad=True)
+
+    def wanted(x, w):
+        calls.clear(), kept.clear()
+        Z.mx4_linear(x, w)
+        (name, x_t, w_t), = calls
+        assert name == "zero_mx4_linear"
+        size = Z._lib.zero_mx4_operand_bytes(64, 8) * (x_t is not None) + Z._lib.zero_mx4_operand_bytes(64, 16) * (w_t is not None)
+        # the result and the call's workspace, and what is kept for the gradients
+        assert [t.numel() for t in kept] == [8 * 16] + [size] * (size > 0) + [Z._lib.zero_mx4_linear_workspace_bytes(8, 16, 64)]
+        return x_t is not None, w_t is not None
+
+    assert wanted(x, w) == (True, True)
+    assert wanted(x, w.detach()) == (False, True) and wanted(x.detach(), w) == (True, False)
+    assert wanted(x.detach(), w.detach()) == (False, False)
+    for mode in (torch.no_grad(), torch.inference_mode()):
+        with mode:
+            assert wanted(x, w) == (False, False)
+            assert wanted(x.detach(), w) == (False, False)

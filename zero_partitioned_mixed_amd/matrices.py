@@ -342,8 +342,9 @@ class _Mx4Linear(torch.autograd.Function):
     operands whose blocks lie along the dimension that it sums over."""
 
     @staticmethod
-    def forward(ctx, x, w):
-        need_x, need_w = ctx.needs_input_grad
+    def forward(ctx, x, w, grad):
+        # grad: whether torch records (here it never does); needs_input_grad is set all the same
+        need_x, need_w = (grad and need for need in ctx.needs_input_grad[:2])
         x, ldx = _matrix(x)
         w, ldw = _matrix(w)
         tokens, k = x.shape
@@ -352,22 +353,24 @@ class _Mx4Linear(torch.autograd.Function):
         y = _empty((tokens, n), dtype=x.dtype, device=dev)
         size_x = _lib.zero_mx4_operand_bytes(k, tokens) if need_w else 0
         size_w = _lib.zero_mx4_operand_bytes(k, n) if need_x else 0
-        kept = _empty(size_x + size_w, dtype=_bytes, device=dev)  # what the gradients need
+        # what the gradients need
+        kept = _empty(size_x + size_w, dtype=_bytes, device=dev) if need_x or need_w else None
         size = _lib.zero_mx4_linear_workspace_bytes(tokens, n, k)
         ws = _empty(size, dtype=_bytes, device=dev)
-        at = kept.data_ptr()
+        at = kept.data_ptr() if need_x or need_w else None
         _call(index, "zero_mx4_linear", x.data_ptr(), ldx, w.data_ptr(), ldw, code, tokens, n, k,
               y.data_ptr(), n, at if need_w else None, at + size_x if need_x else None,
               ws.data_ptr(), size)
-        ctx.save_for_backward(kept)
-        ctx.sizes = (tokens, n, k, code, size_x)
+        if kept is not None:
+            ctx.save_for_backward(kept)
+            ctx.sizes = (tokens, n, k, code, size_x)
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         tokens, n, k, code, size_x = ctx.sizes
-        need_x, need_w = ctx.needs_input_grad
+        need_x, need_w, _ = ctx.needs_input_grad
         kept, = ctx.saved_tensors
         dy, ld = _matrix(dy)
         dev = dy.device
@@ -380,13 +383,14 @@ class _Mx4Linear(torch.autograd.Function):
               at if need_w else None, at + size_x if need_x else None,
               dx.data_ptr() if need_x else None, k, dw.data_ptr() if need_w else None, k,
               ws.data_ptr(), size)
-        return dx, dw
+        return dx, dw, None
 
 
 def mx4_linear(x, w):
     """x w^T for x [tokens, k] and w [n, k] of one type (fp16, bf16 or fp32), both
     quantised to MXFP4; differentiable: the gradients are the products of quantised
-    operands too (the rounding itself is passed through).
+    operands too (the rounding itself is passed through).  Where torch does not record,
+    nothing is made or kept for them.
 
     Forward and backward can be captured into a HIP graph.  As with every autograd
     function, no eager result of the same leaves may be alive then: torch would
@@ -397,4 +401,4 @@ def mx4_linear(x, w):
         raise TypeError(f"x is {x.dtype} and w {w.dtype}")
     _code(x.dtype)
     _gpu(x, w)
-    return _Mx4Linear.apply(x, w)
+    return _Mx4Linear.apply(x, w, torch.is_grad_enabled())
