@@ -599,13 +599,18 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
  * Between steps X is fp32; the products take fp16 operands (power-of-two
  * scaled, fp32 sums) whose diagonals are kept apart in fp32.  Before its own
  * rounding to 16 bits the result is within about 1e-3 of the iteration in 64 bits
- * (relative, Frobenius norm), 1e-5 where the smaller side is at most 128, and up
- * to 4e-3 for larger matrices whose elements all round alike (constant ones).  The scales are chosen for coefficients that
- * keep the singular values below about 1.3, as the usual ones do. */
+ * (relative, Frobenius norm; up to 1.7e-3 where the rank is low or the elements are
+ * equal), 1e-5 where the smaller side is at most 128. */
 #define ZERO_F32 3 /* a dtype of the matrix calls below, where they say so */
 
+#define ZERO_NS_REACH 3.5 /* singular values between steps, at most: the fp16 operands' range */
+
 typedef struct zero_newton_schulz {
-    float a, b, c; /* the polynomial's coefficients, finite */
+    /* The polynomial's coefficients, finite.  Singular values of X start in [0, 1]; a
+     * step takes those up to r to at most the largest |a s + b s^3 + c s^5|, s in [0, r].
+     * That bound, from step to step, may not exceed ZERO_NS_REACH before the last step
+     * (EINVAL).  The usual coefficients stay below 1.3. */
+    float a, b, c;
     float eps;     /* added to the Frobenius norm, >= 0 */
     int32_t steps; /* k, 0..64 */
 } zero_newton_schulz;

@@ -800,3 +800,14 @@ def test_linear_without_gradients(Z):
         again = checkpoint(Z.mx4_linear, xs, ws, use_reentrant=reentrant)
         again.backward(dy)
         assert torch.equal(again, y) and torch.equal(xs.grad, grads[0]) and torch.equal(ws.grad, grads[1])
+
+
+@pytest.mark.parametrize("rows,cols", [(60, 40), (20, 3000), (150, 200), (600, 530)])
+def test_orthogonalize_coefficients_up_to_the_range(Z, rows, cols):
+    """Singular values that reach 3 between two steps, S 9 and M 90: the products' operands stay in fp16's range.  The
+    second step magnifies the first one's relative error by s f'(s) / f(s) = 4.8 there, and adds its own."""
+    x = torch.randn(rows, 1, generator=torch.Generator().manual_seed(rows)) * torch.ones(1, cols)
+    tol = NS_TOL if min(rows, cols) > 128 else ns_tol(rows, cols)
+    for coeffs in ((1.0, 1.0, 1.0), (-1.0, -1.0, -1.0), (0.0, 3.0, 0.0)):
+        got = Z.orthogonalize(x.cuda(), BF16, coeffs=coeffs, steps=2)
+        assert rel(got, ns64(x, 2, coeffs=coeffs)) <= 5.8 * tol + half_step(BF16)

@@ -338,3 +338,34 @@ def test_linear_without_gradients_keeps_nothing(Z, monkeypatch):
         with mode:
             assert wanted(x, w) == (False, False)
             assert wanted(x.detach(), w) == (False, False)
+
+
+def test_coefficients_that_leave_the_range_refused(Z):
+    """Against the largest value on a fine grid, step by step; too small a workspace ends what is taken."""
+    import numpy as np
+
+    def reach(a, b, c, steps):
+        r = top = 1.0
+        for _ in range(steps - 1):
+            s = np.linspace(0.0, r, 2001)
+            r = float(np.abs(a * s + b * s ** 3 + c * s ** 5).max())
+            top = max(top, r)
+            if top > 100:
+                break
+        return top
+
+    rng = random.Random(6)
+    seen = [0, 0]
+    for _ in range(1000):
+        coeffs = rng.uniform(-4, 4), rng.choice([0.0, rng.uniform(-6, 6)]), rng.choice([0.0, rng.uniform(-4, 4)])
+        steps = rng.randint(0, 6)
+        top = reach(*coeffs, steps)
+        if abs(top - 3.5) < 0.01:
+            continue
+        taken = top < 3.5
+        assert ortho(Z, s=ns(Z, coeffs=coeffs, steps=steps), ws_bytes=0) == (ESPACE if taken else EINVAL), (coeffs, steps, top)
+        assert muon(Z, coeffs=coeffs, steps=steps, ws_bytes=0) == (ESPACE if taken else EINVAL)
+        seen[taken] += 1
+    assert min(seen) > 200
+    for usual in ((3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0), (2.0, -1.5, 0.5), (1.875, -1.25, 0.375)):
+        assert ortho(Z, s=ns(Z, coeffs=usual, steps=64), ws_bytes=0) == ESPACE

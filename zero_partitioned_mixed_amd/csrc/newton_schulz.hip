@@ -14,7 +14,7 @@
 // quarter of the rank and 1.7e-3 for matrices of one or two values, whose elements all
 // round alike (55 sizes from 130 x 200 to 4096 x 4096, fp16 results).
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
-// keeps |a| + 1.5 |b| + 2.25 |c| below 2^15; entries down to 1 / (65536 * 256)
+// the coefficients choose (coeffs_of); entries down to 1 / (65536 * 256)
 // stay normal or lose less than X's own rounding.
 //
 // Memory.  X and its transpose are both kept row-major along k, so every
@@ -42,7 +42,7 @@ __device__ __forceinline__ _Float16 half_fma(float a, float b, float c = 0.0f) {
 
 struct Coeffs {
     float a, b, c, eps;
-    float mscale;  // power of two of the fp16 M
+    float mscale;  // power of two of the fp16 M: (|a| + |b| S + |c| S^2) * mscale is below 2^15
 };
 
 // A stack in the workspace, on the wide side: m <= n, mp and np the row lengths
@@ -1116,12 +1116,41 @@ StripWork strip_work(int strips, int sum_parts) {
     return w;
 }
 
+// The largest singular value that an iterate which enters a product (all but the last)
+// can have: those of the first are up to 1.
+double reach(const zero_newton_schulz& ns) {
+    const double a = ns.a, b = ns.b, c = ns.c;
+    double top = 1.0, r = 1.0;
+    for (int step = 1; step < ns.steps && top <= ZERO_NS_REACH; ++step) {
+        auto at = [&](double t) { return std::fabs(std::sqrt(t) * (a + t * (b + t * c))); };  // t = s^2
+        double next = at(r * r);
+        auto turn = [&](double t) {
+            if (t > 0.0 && t < r * r) next = std::fmax(next, at(t));
+        };
+        // a + 3 b t + 5 c t^2 = 0
+        if (c == 0.0) {
+            if (b != 0.0) turn(-a / (3.0 * b));
+        } else {
+            const double half = -3.0 * b / (10.0 * c), under = half * half - a / (5.0 * c);
+            if (under >= 0.0) {
+                turn(half - std::sqrt(under));
+                turn(half + std::sqrt(under));
+            }
+        }
+        r = next;
+        top = std::fmax(top, r);
+    }
+    return top;
+}
+
 int check_ns(const zero_newton_schulz* ns, const char* what) {
     if (ns == nullptr) return fail(ZERO_EINVAL, "%s: null settings", what);
     if (!std::isfinite(ns->a) || !std::isfinite(ns->b) || !std::isfinite(ns->c))
         return fail(ZERO_EINVAL, "%s: coefficients must be finite", what);
     if (!std::isfinite(ns->eps) || ns->eps < 0.0f) return fail(ZERO_EINVAL, "%s: eps must be >= 0", what);
     if (ns->steps < 0 || ns->steps > 64) return fail(ZERO_EINVAL, "%s: steps must be 0..64", what);
+    if (!(reach(*ns) <= ZERO_NS_REACH))
+        return fail(ZERO_EINVAL, "%s: the coefficients let singular values between steps grow above %g", what, ZERO_NS_REACH);
     return ZERO_OK;
 }
 
@@ -1145,7 +1174,10 @@ int check_space(const void* ws, size_t ws_bytes, int32_t count, int64_t rows, in
 
 Coeffs coeffs_of(const zero_newton_schulz& ns) {
     Coeffs k{ns.a, ns.b, ns.c, ns.eps, 0.0f};
-    const double top = std::fabs((double)ns.a) + 1.5 * std::fabs((double)ns.b) + 2.25 * std::fabs((double)ns.c);
+    // M for S up to 1.5, which the usual coefficients keep to, or up to what these let it reach; S times
+    // kSScale stays in fp16's range for a reach of ZERO_NS_REACH, its elements off the diagonal at most half of it
+    const double far = reach(ns), s = far * far > 1.5 ? far * far : 1.5;
+    const double top = std::fabs((double)ns.a) + s * std::fabs((double)ns.b) + s * s * std::fabs((double)ns.c);
     int e = 0;
     std::frexp(top, &e);  // top < 2^e
     e = 15 - e;

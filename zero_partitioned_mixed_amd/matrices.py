@@ -69,6 +69,8 @@ def _space(nbytes: int, ws, like):
 
 # ----------------------------------------------------------------------------- orthogonalised updates
 def newton_schulz(coeffs=COEFFS, steps: int = 5, eps: float = 1e-7) -> NewtonSchulz:
+    """The settings of an orthogonalisation.  The coefficients may not let singular values,
+    which start in [0, 1], grow above 3.5 between the steps (the calls refuse them)."""
     a, b, c = coeffs
     return NewtonSchulz(a, b, c, eps, steps)
 
@@ -108,7 +110,8 @@ def orthogonalize(x, out_dtype=None, *, coeffs=COEFFS, steps: int = 5, eps: floa
     """The Newton-Schulz orthogonalisation of every matrix of x ([rows, cols] or
     [count, rows, cols]; fp16, bf16 or fp32, any strides: other layouts than
     unit-stride rows are copied).  Returns fp16 or bf16 (out_dtype; by default x's
-    type, bf16 for fp32), in ``out`` when given (it may be x).  Not differentiable."""
+    type, bf16 for fp32), in ``out`` when given (it may be x).  coeffs: as
+    newton_schulz takes them.  Not differentiable."""
     if out is not None:
         out_dtype = out.dtype
     elif out_dtype is None:
