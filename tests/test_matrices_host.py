@@ -4,6 +4,7 @@ import ctypes
 import os
 import random
 import subprocess
+import sys
 
 import pytest
 
@@ -369,3 +370,17 @@ def test_coefficients_that_leave_the_range_refused(Z):
     assert min(seen) > 200
     for usual in ((3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0), (2.0, -1.5, 0.5), (1.875, -1.25, 0.375)):
         assert ortho(Z, s=ns(Z, coeffs=usual, steps=64), ws_bytes=0) == ESPACE
+
+
+def test_import_without_torch_internals():
+    """The package needs no private name of torch."""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import zero_partitioned_mixed_amd as Z\n"
+            "class Stream: cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda index=None: Stream\n"
+            "from zero_partitioned_mixed_amd import matrices\n"
+            "assert matrices._raw_stream(0) == 77")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -27,7 +27,9 @@ def _code(dtype, allowed=_DTYPES) -> int:
 
 
 _HALVES = (torch.float16, torch.bfloat16)
-_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream without its object
+# torch.cuda.current_stream(index).cuda_stream, without the object where this torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = torch.cuda.current_device
 _empty, _bytes = torch.empty, torch.uint8
 
