@@ -696,7 +696,8 @@ int zero_mx4_dequantize(const void *codes_dev, const void *scales_dev, int64_t r
 /* c[i][j] = sum over k of A[i][k] B[j][k] (+ c[i][j] when accumulate is 1 and
  * c is ZERO_F32), A m x k and B n x k quantised along k, sums in fp32; c is
  * m x n, row stride ldc, ZERO_F16, ZERO_BF16 or ZERO_F32.  k = 0 gives zeros
- * (or c unchanged).  ws: zero_mx4_matmul_workspace_bytes, 16-byte aligned. */
+ * (or c unchanged).  No product needs a workspace: zero_mx4_matmul_workspace_bytes
+ * is 0 for all sizes, and ws is not looked at. */
 size_t zero_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int zero_mx4_matmul(const void *a_codes_dev, const void *a_scales_dev, const void *b_codes_dev,
                     const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,
@@ -704,8 +705,9 @@ int zero_mx4_matmul(const void *a_codes_dev, const void *a_scales_dev, const voi
                     size_t ws_bytes, void *stream);
 
 /* zero_mx4_matmul with A given as values (ZERO_F16, ZERO_BF16 or ZERO_F32, row
- * stride lda) and quantised on the way in, for the few rows of single tokens:
- * equal to zero_mx4_quantize and zero_mx4_matmul.  m is at most
+ * stride lda) and quantised on the way in, for the few rows of single tokens: the codes
+ * and scales of zero_mx4_quantize and the product of zero_mx4_matmul, whose fp32
+ * sums may be added in another order (9 to 32 rows with n above 8192).  m is at most
  * ZERO_MX4_ROWS_MAX.  No workspace is needed up to m = 32 where m times the padded
  * k is at most 16384. */
 #define ZERO_MX4_ROWS_MAX 64

@@ -811,3 +811,12 @@ def test_orthogonalize_coefficients_up_to_the_range(Z, rows, cols):
     for coeffs in ((1.0, 1.0, 1.0), (-1.0, -1.0, -1.0), (0.0, 3.0, 0.0)):
         got = Z.orthogonalize(x.cuda(), BF16, coeffs=coeffs, steps=2)
         assert rel(got, ns64(x, 2, coeffs=coeffs)) <= 5.8 * tol + half_step(BF16)
+
+
+@pytest.mark.parametrize("m,n,k", [(16, 9000, 1024), (9, 8200, 1792), (32, 8193, 500)])
+def test_product_of_values_and_of_operands(Z, m, n, k):
+    """Where the two forms add their sums in different orders, both keep to the same bound."""
+    x = randn(m, k, seed=1) * torch.exp(4 * randn(m, k, seed=2))
+    qx, qb = Z.mx4_quantize(x), Z.mx4_quantize(randn(n, k, seed=3) * torch.exp(4 * randn(n, k, seed=4)))
+    for a in (x, qx):
+        check_product(Z.mx4_matmul(a, qb, F32), values64(qx), values64(qb), k)
