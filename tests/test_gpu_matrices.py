@@ -820,3 +820,79 @@ def test_product_of_values_and_of_operands(Z, m, n, k):
     qx, qb = Z.mx4_quantize(x), Z.mx4_quantize(randn(n, k, seed=3) * torch.exp(4 * randn(n, k, seed=4)))
     for a in (x, qx):
         check_product(Z.mx4_matmul(a, qb, F32), values64(qx), values64(qb), k)
+
+
+# ----------------------------------------------------------------------------- large matrices and strips, all that is special
+# Above a smaller side of 512 X^T has one fp16 part.  Tolerances: NS_TOL, twice it where the rank is low, as for
+# rank-one matrices above: the roundings then put noise into directions that X lacks.
+@pytest.mark.parametrize("rows,cols", [(513, 513), (520, 1030), (2304, 768), (1041, 1166)])
+def test_orthogonalize_spectra_large(Z, rows, cols):
+    m = min(rows, cols)
+    torch.manual_seed(rows)
+    r = lambda *shape: torch.randn(*shape, dtype=torch.float64)  # noqa: E731
+    u, v = torch.linalg.qr(r(rows, m))[0], torch.linalg.qr(r(cols, m))[0]
+    k = torch.arange(1, m + 1, dtype=torch.float64)
+    hot = torch.zeros(rows, cols, dtype=torch.float64)
+    hot[torch.arange(rows), torch.randint(0, cols, (rows,))] = 1.0
+    for name, x, tol in (("1/k", (u / k) @ v.t(), 1), ("1/sqrt k", (u / k.sqrt()) @ v.t(), 1), ("flat", u @ v.t(), 1),
+                         ("rank one", r(rows, 1) @ r(1, cols), 2), ("quarter rank", r(rows, m // 4) @ r(m // 4, cols), 2),
+                         ("one-hot rows", hot, 1), ("signs", torch.sign(r(rows, cols)), 1), ("constant", torch.ones(rows, cols), 1),
+                         ("scaled", r(rows, cols) * torch.exp(r(1, cols)) * torch.exp(r(rows, 1)), 1)):
+        x = x.float().cuda()
+        assert rel(Z.orthogonalize(x, F16), ns64_gpu(x)) <= tol * NS_TOL + half_step(F16), name
+
+
+STRIPS = [(2, 20, 3000), (2, 20, 33000), (2, 3000, 60), (2, 17000, 40), (2, 100, 700), (2, 8500, 100)]
+
+
+@pytest.mark.parametrize("count,rows,cols", STRIPS)
+def test_strips_zero_and_not_finite(Z, count, rows, cols):
+    x = randn(count, rows, cols)
+    x[0] = 0
+    for eps in (1e-7, 0.0):
+        o = Z.orthogonalize(x, BF16, eps=eps)
+        assert (o[0] == 0).all() and torch.isfinite(o[1].float()).all()
+    for bad in (float("inf"), float("nan")):
+        y = x.clone()
+        y[0, rows - 1, cols - 1] = bad
+        o = Z.orthogonalize(y, BF16)
+        assert torch.isnan(o[0].float()).all() and torch.isfinite(o[1].float()).all()
+
+
+@pytest.mark.parametrize("count,rows,cols", [*STRIPS, (2, 30, 20), (2, 130, 200)])
+def test_muon_step_skipped_and_clipped(Z, count, rows, cols):
+    """A skipped step leaves master, momentum and slot as they are, whatever the gradient holds; a clipped one is the
+    step of the clipped gradient."""
+    ctrl = torch.empty(Z.zero_ctrl_bytes(), dtype=torch.uint8, device="cuda")
+    Z.zero_ctrl_init(ctrl, 1.0)
+    skip, clip = Z.Ctrl.skip.offset, Z.Ctrl.clip.offset
+    p, m, g = (randn(count, rows, cols, seed=i) * f for i, f in ((1, 0.02), (2, 1e-3), (3, 1e-3)))
+    slot = torch.full((count, rows, cols), 5.0, dtype=BF16, device="cuda")
+    hp = Z.muon_hparams(lr=1e-2, weight_decay=0.01)
+    before = [t.clone() for t in (p, m)]
+    bad = g.clone()
+    bad[0, 0, 0] = float("inf")
+    ctrl[skip:skip + 4] = torch.tensor([1], dtype=torch.int32).view(torch.uint8).cuda()
+    Z.muon_step(p, m, bad, hp, slot=slot, ctrl=ctrl)
+    assert torch.equal(p, before[0]) and torch.equal(m, before[1]) and (slot == 5).all()
+    ctrl[skip:skip + 4] = 0
+    ctrl[clip:clip + 4] = torch.tensor([0.25]).view(torch.uint8).cuda()
+    Z.muon_step(p, m, g, hp, slot=slot, ctrl=ctrl)
+    q, n = before[0].clone(), before[1].clone()
+    Z.muon_step(q, n, g * 0.25, hp)  # a power of two: the same numbers
+    assert torch.equal(p, q) and torch.equal(m, n) and torch.equal(slot, p.to(BF16))
+    for i in range(count):
+        step = before[0][i].double() * (1 - 1e-4) - p[i].double()
+        u = 0.95 * (0.95 * before[1][i].double() + 0.05 * 0.25 * g[i].double()) + 0.05 * 0.25 * g[i].double()
+        want = 1e-2 * 0.2 * math.sqrt(max(rows, cols)) * ns64_gpu(u)
+        err = float((step.cpu() - want).norm())
+        # NS, and what fp32 leaves of the momentum and of master
+        assert err <= ns_tol(rows, cols) * float(want.norm()) + 4 * 2.0 ** -24 * float(before[0][i].double().norm())
+
+
+def test_orthogonalize_large_is_reproducible(Z):
+    for shape in ((1500, 4099), (700, 2304)):
+        x = randn(*shape, dtype=F16)
+        first = Z.orthogonalize(x, F16)
+        for _ in range(3):
+            assert torch.equal(Z.orthogonalize(x, F16), first)
