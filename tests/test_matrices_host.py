@@ -384,3 +384,16 @@ def test_import_without_torch_internals():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_payload_with_matrices_refused_before_the_step(Z, monkeypatch):
+    """Nothing is enqueued: a decision made before the refusal would have counted the step."""
+    calls = []
+    for name in ("zero_reduce_grads", "zero_grad_norm_overflow"):
+        monkeypatch.setattr(Z, name, lambda *a, _n=name, **k: calls.append(_n))
+    payload = Z.QGather(1 << 24, 1 << 25, 8, 4096)
+    with pytest.raises(ValueError, match="payload"):
+        fake_rank(Z, Z.MuonShardStep).step(Rows(), Rows(), payload)
+    with pytest.raises(ValueError, match="payload"):
+        Z.MultiShardStep([fake_rank(Z, Z.MuonShardStep)]).step([Rows()], Rows(), [payload])
+    assert calls == []

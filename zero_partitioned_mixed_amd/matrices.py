@@ -184,9 +184,17 @@ class MuonShardStep(ShardStep):
             space = max(space, _lib.zero_ns_workspace_bytes(count, rows, cols))
         self.matrix_ws = _empty(space, dtype=_bytes, device=state[0].device) if space else None
 
-    def complete(self, gather, qgather=None) -> None:
+    @staticmethod
+    def _no_payload(qgather) -> None:
         if qgather is not None:
             raise ValueError("no INT8 or INT4 payload with matrices: quantise the slot")
+
+    def run_pieces(self, contrib, gather, qgather=None) -> None:
+        self._no_payload(qgather)  # before the step has begun
+        super().run_pieces(contrib, gather)
+
+    def complete(self, gather, qgather=None) -> None:
+        self._no_payload(qgather)
         master, m, v = self.state
         for start, length in self.between:
             zero_adam_step(tuple(t[start:] for t in self.state), self.g[start:], length, self.hp, self.ctrl,
