@@ -896,3 +896,18 @@ def test_orthogonalize_large_is_reproducible(Z):
         first = Z.orthogonalize(x, F16)
         for _ in range(3):
             assert torch.equal(Z.orthogonalize(x, F16), first)
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 700, 900), (2, 1100, 600), (1, 1200, 2500)])
+def test_muon_step_large(Z, count, rows, cols):
+    lr, wd = 1e-2, 0.01
+    p, m, g = (randn(count, rows, cols, seed=i) * f for i, f in ((1, 0.02), (2, 1e-3), (3, 1e-3)))
+    slot, before = torch.empty_like(p, dtype=BF16), [t.double() for t in (p, m)]
+    Z.muon_step(p, m, g, Z.muon_hparams(lr=lr, weight_decay=wd), slot=slot)
+    for i in range(count):
+        mom = 0.95 * before[1][i] + 0.05 * g[i].double()
+        assert ((m[i].double() - mom).abs() <= 5 * 2.0 ** -24 * (mom.abs() + g[i].double().abs() + before[1][i].abs())).all()
+        step = (before[0][i] * (1 - lr * wd) - p[i].double()).cpu()
+        want = lr * 0.2 * math.sqrt(max(rows, cols)) * ns64_gpu(0.05 * g[i].double() + 0.95 * mom)
+        assert float((step - want).norm()) <= NS_TOL * float(want.norm()) + 4 * 2.0 ** -24 * float(before[0][i].norm())
+    assert torch.equal(slot, p.to(BF16))
