@@ -596,11 +596,15 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
  *     X <- X (a I + b S + c S^2),  S = X^T X      (rows >  cols)
  * which drives every singular value of X towards 1 and keeps the singular
  * vectors.  A zero matrix gives zeros; a matrix holding inf or NaN gives NaN.
- * Between steps X is fp32; the products take fp16 operands (power-of-two
- * scaled, fp32 sums) whose diagonals are kept apart in fp32.  Before its own
- * rounding to 16 bits the result is within about 1e-3 of the iteration in 64 bits
- * (relative, Frobenius norm; up to 1.7e-3 where the rank is low or the elements are
- * equal), 1e-5 where the smaller side is at most 128. */
+ * Between steps X is fp32; the products take fp16 operands (scaled, fp32 sums)
+ * whose diagonals are kept apart in fp32.  Results in fp16, and all of matrices
+ * whose smaller side is at most 128, take every operand in two fp16 parts: before
+ * their own rounding they are within 1e-5 of the iteration in 64 bits (relative,
+ * Frobenius norm).  Results in bf16 and the optimizer's update take one part
+ * above 128: within about 1e-3, up to 1.8e-3 where the rank is low or the
+ * elements are equal, beside bf16's own 1.7e-3, in 0.4 of the time.  Sums of equal
+ * terms round alike, so that constant matrices may be off by 5e-7 times their
+ * smaller side more. */
 #define ZERO_F32 3 /* a dtype of the matrix calls below, where they say so */
 
 #define ZERO_NS_REACH 3.5 /* singular values between steps, at most: the fp16 operands' range */
@@ -617,8 +621,11 @@ typedef struct zero_newton_schulz {
 
 /* Bytes of device workspace for zero_orthogonalize and zero_muon_step over
  * such a stack (16-byte aligned; 0 where a workgroup holds a whole matrix, among
- * them all with both sides up to 128).  0 for sizes the calls refuse. */
+ * them all with both sides up to 128).  0 for sizes the calls refuse.
+ * zero_muon_step, and zero_orthogonalize with a result in bf16, need only
+ * zero_muon_workspace_bytes, which is never more. */
 size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
+size_t zero_muon_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
 
 /* dst[b] = orthogonalisation of src[b].  src: src_dtype ZERO_F16, ZERO_BF16
  * or ZERO_F32; row r of matrix b starts at element b * src_stride + r * src_ld.

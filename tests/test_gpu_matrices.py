@@ -911,3 +911,85 @@ def test_muon_step_large(Z, count, rows, cols):
         want = lr * 0.2 * math.sqrt(max(rows, cols)) * ns64_gpu(0.05 * g[i].double() + 0.95 * mom)
         assert float((step - want).norm()) <= NS_TOL * float(want.norm()) + 4 * 2.0 ** -24 * float(before[0][i].norm())
     assert torch.equal(slot, p.to(BF16))
+
+
+# ----------------------------------------------------------------------------- operands of two parts, and of one
+# An fp16 result leaves nothing but its own rounding: the operands have 22 bits, a thousandth of NS_TOL and what fp32
+# adds, as for narrow matrices.  Sums over m equal terms (the products with M and M's own, of matrices of rank one) round
+# alike at each of their m / 4 steps, 2^-24 of the sum, and the first cancels to a quarter: 10 m 2^-24 over five steps.
+def spectra(rows, cols):
+    m = min(rows, cols)
+    torch.manual_seed(rows)
+    r = lambda *shape: torch.randn(*shape, dtype=torch.float64)  # noqa: E731
+    u, v = torch.linalg.qr(r(rows, m))[0], torch.linalg.qr(r(cols, m))[0]
+    k = torch.arange(1, m + 1, dtype=torch.float64)
+    hot = torch.zeros(rows, cols, dtype=torch.float64)
+    hot[torch.arange(rows), torch.randint(0, cols, (rows,))] = 1.0
+    return {"normal": r(rows, cols), "1/k": (u / k) @ v.t(), "1/sqrt k": (u / k.sqrt()) @ v.t(), "flat": u @ v.t(),
+            "quarter rank": r(rows, m // 4) @ r(m // 4, cols), "one-hot rows": hot, "signs": torch.sign(r(rows, cols)),
+            "scaled": r(rows, cols) * torch.exp(r(1, cols)) * torch.exp(r(rows, 1)), "rank one": r(rows, 1) @ r(1, cols),
+            "constant": torch.ones(rows, cols, dtype=torch.float64)}
+
+
+@pytest.mark.parametrize("rows,cols", [(130, 200), (300, 700), (513, 513), (1100, 1600), (2304, 768)])
+def test_orthogonalize_fp16_leaves_its_rounding(Z, rows, cols):
+    for name, x in spectra(rows, cols).items():
+        x = x.float().cuda()
+        want = ns64_gpu(x)
+        if name in ("rank one", "constant", "one-hot rows"):  # equal elements round to the next one alike
+            tol = half_step(F16) + 10 * min(rows, cols) * 2.0 ** -24
+        else:
+            tol = 1.02 * rel(want.half(), want) + NS_TOL / 1000 + 500 * 2.0 ** -24
+        assert rel(Z.orthogonalize(x, F16), want) <= tol, name
+
+
+def update(Z, x):
+    """The optimizer's update of one matrix in fp32: no 16-bit rounding hides what its products leave."""
+    hp = Z.muon_hparams(lr=1.0, momentum=0.0, nesterov=False, scale=Z.MUON_SCALE_SHAPE)
+    p, m = torch.zeros_like(x), torch.zeros_like(x)
+    Z.muon_step(p, m, x, hp)
+    return -p.double() / math.sqrt(max(1.0, x.shape[0] / x.shape[1]))
+
+
+@pytest.mark.parametrize("rows,cols", [(130, 200), (300, 700), (513, 513), (1100, 1600), (2304, 768)])
+def test_update_of_spectra(Z, rows, cols):
+    for name, x in spectra(rows, cols).items():
+        x = x.float().cuda()
+        tol = 2 * NS_TOL if name in ("quarter rank", "rank one") else NS_TOL
+        assert rel(update(Z, x), ns64_gpu(x)) <= tol, name
+
+
+@pytest.mark.parametrize("rows,cols", [(412, 412), (482, 482), (900, 482), (520, 520), (1100, 1040)])
+def test_update_of_one_element_a_row(Z, rows, cols):
+    x = torch.eye(rows, cols, device="cuda")
+    assert rel(update(Z, x), ns64_gpu(x)) <= 500 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows,cols", [(177, 790), (817, 1200), (6328, 1939), (1393, 21020)])
+def test_update_of_equal_elements(Z, rows, cols):
+    x = torch.ones(rows, cols, device="cuda")
+    assert rel(update(Z, x), ns64_gpu(x)) <= NS_TOL
+
+
+def test_workspaces_of_results(Z):
+    """A bf16 result and the optimizer step take the smaller workspace to the byte, an fp16 result the larger."""
+    x = randn(200, 300)
+    large, small = (f(1, 200, 300) for f in (Z._lib.zero_ns_workspace_bytes, Z._lib.zero_muon_workspace_bytes))
+    space = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    assert torch.equal(Z.orthogonalize(x, BF16, ws=space(small)), Z.orthogonalize(x, BF16))
+    assert torch.equal(Z.orthogonalize(x, F16, ws=space(large)), Z.orthogonalize(x, F16))
+    Z.muon_step(x.clone(), x.clone(), x.clone(), Z.muon_hparams(), ws=space(small))
+    for dtype, n in ((BF16, small - 1), (F16, large - 1), (F16, small)):
+        with pytest.raises(Z.ZeroError) as e:
+            Z.orthogonalize(x, dtype, ws=space(n))
+        assert e.value.code == -4
+
+
+@pytest.mark.parametrize("count,rows,cols", [shape for shape in NS_SHAPES if min(shape[1:]) > 128])
+def test_update_every_tile_shape(Z, count, rows, cols):
+    x = randn(count, rows, cols, seed=rows)
+    hp = Z.muon_hparams(lr=1.0, momentum=0.0, nesterov=False, scale=Z.MUON_SCALE_SHAPE)
+    p, m = torch.zeros_like(x), torch.zeros_like(x)
+    Z.muon_step(p, m, x, hp)
+    for i in {0, count // 2, count - 1}:
+        assert rel(-p[i].double() / math.sqrt(max(1.0, rows / cols)), ns64_gpu(x[i])) <= NS_TOL

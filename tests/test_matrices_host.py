@@ -397,3 +397,17 @@ def test_payload_with_matrices_refused_before_the_step(Z, monkeypatch):
     with pytest.raises(ValueError, match="payload"):
         Z.MultiShardStep([fake_rank(Z, Z.MuonShardStep)]).step([Rows()], Rows(), [payload])
     assert calls == []
+
+
+def test_workspace_of_the_step(Z):
+    """Never more than an orthogonalisation's, and the same where every operand has two parts anyway."""
+    ns_bytes, muon_bytes = Z._lib.zero_ns_workspace_bytes, Z._lib.zero_muon_workspace_bytes
+    for size in ((1, 129, 400), (3, 700, 300), (2, 5000, 5000)):
+        assert 0 < muon_bytes(*size) < ns_bytes(*size)
+    for size in ((5, 128, 128), (1, 20, 33000), (2, 3000, 60)):
+        assert muon_bytes(*size) == ns_bytes(*size)
+    for size in ((0, 500, 500), (1, 0, 9), (1, 70000, 9), (-1, 5, 5), (65536, 5, 5)):
+        assert muon_bytes(*size) == 0
+    size = muon_bytes(1, 200, 300)
+    assert muon(Z, ws_bytes=size - 1) == ESPACE
+    assert ortho(Z, dst=1 << 40, ddt=BF16, ws_bytes=size - 1) == ESPACE == ortho(Z, dst=1 << 40, ddt=F16, ws_bytes=size)

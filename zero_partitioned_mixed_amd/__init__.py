@@ -176,6 +176,7 @@ _sig = {
                                              _vp, _i32, _vp]),
     "zero_launch_tiles": (ctypes.c_int64, [_i32]),
     "zero_ns_workspace_bytes": (ctypes.c_size_t, [_i32, _i64, _i64]),
+    "zero_muon_workspace_bytes": (ctypes.c_size_t, [_i32, _i64, _i64]),
     "zero_orthogonalize": (ctypes.c_int, [_vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _i64,
                                           _i64, ctypes.POINTER(NewtonSchulz), _vp,
                                           ctypes.c_size_t, _vp]),

@@ -179,7 +179,10 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MT][S::NT], const Frag
 }
 
 // The product of one tile after another.  A tile is `slabs` whole slabs and then
-// (4-bit operands) half a slab if `half`.
+// (4-bit operands) half a slab if `half`.  PARTS = 2: rows hold `slabs` slabs of rests
+// and right behind them the high parts that left them; the product is rest x high +
+// high x rest + high x high, three times the slabs, the small terms first: a matrix
+// instruction cuts each term to the sum's last bits.
 //   Product<S, MM> p(lds, slabs, half);
 //   p.tile(A, B, SA, SB);  its operands, SA and SB their scales' rows (4-bit)
 //   p.ahead();             its first loads: LDS has no readers any more
@@ -187,12 +190,14 @@ __device__ __forceinline__ void multiply(f32x16 (&acc)[S::MT][S::NT], const Frag
 // Element r of acc[i][j] is output row wm * WM + 32 i + 8 (r / 4) + 4 h + r % 4, column
 // wn * WN + 32 j + c.  run() is true for the waves that hold the result (the first
 // group); LDS (product_lds bytes) is free once all waves have met after it.
-template <class S, class MM>
+template <class S, class MM, int PARTS = 1>
 struct Product {
+    static_assert(PARTS == 1 || (PARTS == 2 && !MM::kScaled), "two parts of fp16 operands");
     static constexpr int kScaleLoads = MM::kScaled ? S::SCALES : 0;
     static constexpr int kStage = S::ROWS + (MM::kScaled ? 4 * S::TILE * 4 : 0);
     const Lane L;
     const int group, slabs, total;
+    const int part, first_part, edge;  // PARTS = 2: slabs of a part; where this wave's operand starts, up to which slab
     const bool half;
     char *const all, *const lds;  // the workgroup's LDS, the group's part of it
     const char* base;             // this wave's operand
@@ -203,8 +208,11 @@ struct Product {
     __device__ __forceinline__ Product(char* shared, int slabs_, bool half_)
         : L(S::WAVES),
           group(S::KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (S::WAVES * 64))),
-          slabs(slabs_),
-          total(slabs_ + (MM::kScaled && half_ ? 1 : 0)),
+          slabs(PARTS == 2 ? 3 * slabs_ : slabs_),
+          total(slabs + (MM::kScaled && half_ ? 1 : 0)),
+          part(slabs_),
+          first_part(first_load() < S::TILE / 8 ? 0 : slabs_),
+          edge(2 * slabs_ - first_part),
           half(half_),
           all(shared),
           lds(shared + group * S::STAGES * kStage) {}
@@ -240,7 +248,8 @@ struct Product {
     // quarter q of the loads of a slab (q = 4: all)
     __device__ __forceinline__ void stage(int slab, char* buf, int q) const {
         const bool cut = MM::kScaled && slab >= slabs;  // past a half slab lies the next row
-        const char* from = base + (int64_t)slab * kSlab;
+        // A's parts in the order rest, high, high; B's high, rest, high
+        const char* from = base + (int64_t)(PARTS == 1 ? slab : slab < edge ? slab + first_part : slab - part) * kSlab;
         char* to = buf + first_load() * 1024;
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i)
@@ -409,6 +418,9 @@ __device__ __forceinline__ u32x2 quad_turn16(u32x2 d) {
     const uint32_t b = __builtin_amdgcn_perm(d[1], lane_xor1(d[1]), pick);
     const uint32_t o = lane_xor2(high ? a : b);
     return u32x2{high ? o : a, high ? b : o};
+}
+__device__ __forceinline__ f16x4 quad_turn16(f16x4 v) {
+    return __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, v)));
 }
 
 // A wave's fp16 results on their way to the transposed place: 32 columns by WM rows

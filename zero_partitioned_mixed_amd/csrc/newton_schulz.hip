@@ -9,10 +9,17 @@
 //   S = D + E,  S^2 = E E + (d_i + d_j) e_ij + D^2,  X <- diag(M) X + (M - diag(M)) X.
 // D is the rows' squared norms of the fp32 X, summed where X is made: from the rounded
 // X, rows whose elements round alike came out up to 6e-3 off (an identity of 482).
-// Only the off-diagonal parts and the product's copy of X are rounded to 11
-// bits: against 64 bits 3e-4 to 1.1e-3 for spectra from flat to 1/k, up to 1.5e-3 for a
-// quarter of the rank and 1.7e-3 for matrices of one or two values, whose elements all
-// round alike (55 sizes from 130 x 200 to 4096 x 4096, fp16 results).
+// Only the off-diagonal parts and the product's copy of X are rounded.
+//
+// How far.  A result in fp16 shows what 11-bit operands leave (3e-4 to 1e-3 beside its own
+// 2e-4), so there each of them has two parts, high and rest, of 22 bits together, and
+// each product three products: nothing but the result's rounding is left.  A result in bf16
+// rounds by 1.7e-3, and an update meets the weights times lr: their operands have one
+// part, in 0.4 of the time (11008 x 4096: 3.8 against 9.6 ms, 1500 x 4099 0.42 against 0.99).
+// In one part, against 64 bits: 2e-4 to 1e-3 for spectra from flat to 1/k, up to 1.5e-3
+// for a quarter of the rank and 1.8e-3 for matrices of one or two values (55 sizes from
+// 130 x 200 to 4096 x 4096).  In both forms sums over equal terms round alike: constant
+// matrices are off by 5e-7 times the smaller side more (8192 x 8192: 4e-3).
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
 // the coefficients choose (coeffs_of); entries down to 1 / (65536 * 256)
 // stay normal or lose less than X's own rounding.
@@ -33,7 +40,7 @@ constexpr float kXScale = 256.0f, kSScale = 4096.0f;
 // [1, 2) that differs from row to row, and a product's results are divided by their row's
 // and column's.  Elements that are equal then round differently in different rows, so that
 // the roundings average out as those of other matrices do: with plain powers of two,
-// constant matrices came out up to 1.2e-2 off (1393 x 21020; now at most 1.7e-3 at 55 sizes).
+// constant matrices came out up to 1.2e-2 off in one part (1393 x 21020; now at most 1.8e-3 at 55 sizes).
 __device__ __forceinline__ float spread(int i) {
     return __builtin_bit_cast(float, 0x3F800000u | ((uint32_t)i * 0x9E3779B1u) >> 9);
 }
@@ -49,7 +56,9 @@ struct Coeffs {
 // (multiples of 64, the padding zero).
 struct Work {
     int m, n, mp, np;
-    int kp;                  // row length of M and X^T: mp, or 2 mp where X^T is kept in two parts
+    // Row lengths of M and X^T (mp, or 2 mp where X^T has two parts), of X and of S (np and
+    // mp, or twice that where all operands have two).  Of two parts the rests come first.
+    int kp, nx, ms;
     int64_t stride;  // bytes from one matrix's block to the next
     char* base;
     int64_t x16, xt0, xt1, s16, m16, ds, dm, sums;  // byte offsets; X in fp32 at 0
@@ -64,6 +73,7 @@ struct Work {
 // The matrices of zero_orthogonalize.
 template <int DTI, int DTO>
 struct PlainIo {
+    static constexpr bool kExact = DTO == ZERO_F16;  // a result of 11 bits: the operands have 22
     const typename Elem<DTI>::type* src;
     typename Elem<DTO>::type* dst;
     int64_t src_ld, src_stride, dst_ld, dst_stride;
@@ -90,6 +100,7 @@ struct PlainIo {
 // The matrices of zero_muon_step: the momentum is updated at the first reading.
 template <int DTO>
 struct MuonIo {
+    static constexpr bool kExact = false;  // an update: lr times it meets the weights
     float* master;
     float* mom;
     const float* g;
@@ -727,13 +738,16 @@ __global__ void __launch_bounds__(256) ns_begin_kernel(IoArgs<IO> a) {
         const float vt = tall ? patch[i][x] : patch[x][i];  // element (i0 + x, j0 + i) of X
         if (i0 + i < w.m && j0 + x < w.np) {
             x32[(int64_t)(i0 + i) * w.np + j0 + x] = v;
-            x16[(int64_t)(i0 + i) * w.np + j0 + x] = half_fma(v, spread(i0 + i));
+            const int64_t at = (int64_t)(i0 + i) * w.nx + j0 + x;
+            const _Float16 high = half_fma(v, spread(i0 + i));
+            x16[at + (w.nx - w.np)] = high;
+            if (w.nx > w.np) x16[at] = half_fma(v, spread(i0 + i), -(float)high);
         }
         if (j0 + i < w.n && i0 + x < w.mp) {
             const int64_t at = (int64_t)(j0 + i) * w.kp + i0 + x;
             const _Float16 high = half_fma(vt, spread(j0 + i));
-            xt[at] = high;
-            if (w.kp > w.mp) xt[at + w.mp] = half_fma(vt, spread(j0 + i), -(float)high);
+            xt[at + (w.kp - w.mp)] = high;
+            if (w.kp > w.mp) xt[at] = half_fma(vt, spread(j0 + i), -(float)high);
         }
     }
 }
@@ -805,8 +819,8 @@ __device__ __forceinline__ void row_norms(const Work& w, char* base, int row_par
 }
 
 // S (POLY false) or M (POLY true): tiles on and above the diagonal, mirrored.  S: the
-// workgroups after the tiles' make its diagonal, 64 rows each.
-template <class S, bool POLY>
+// workgroups after the tiles' make its diagonal, 64 rows each.  EXACT: operands of two parts.
+template <class S, bool POLY, bool EXACT>
 __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     __shared__ __attribute__((aligned(16))) char lds[ns_lds<S>()];
     const Work& w = a.w;
@@ -820,13 +834,13 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     }
     int ti, tj;
     triangle_tile(xcd_tile(blockIdx.x, a.tiles), ti, tj);
-    const int ld = POLY ? w.mp : w.np;  // elements
+    const int ld = POLY ? w.ms : w.nx;  // elements
     const char* from = base + (POLY ? w.s16 : w.x16);
     const int i0 = ti * S::TILE, j0 = tj * S::TILE;
     const Operand A{from + (int64_t)i0 * ld * 2, (uint32_t)ld * 2, w.m - i0};
     const Operand B{from + (int64_t)j0 * ld * 2, (uint32_t)ld * 2, w.m - j0};
     f32x16 acc[S::MT][S::NT];
-    Product<S, MmF16> product(lds, ld / 64, false);
+    Product<S, MmF16, EXACT ? 2 : 1> product(lds, (POLY ? w.mp : w.np) / 64, false);
     product.tile(A, B, A, B);
     product.ahead();
     const bool holds = product.run(acc);
@@ -840,9 +854,9 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
     const float* ds = (const float*)(base + w.ds);
     const _Float16* s16 = (const _Float16*)(base + w.s16);
     _Float16* out = (_Float16*)(base + (POLY ? w.m16 : w.s16));
-    const int ldo = POLY ? w.kp : w.mp;
-    const bool twice = POLY && w.kp > w.mp;  // M meets both parts of X^T
-    Turner<S> turner(lds, L);
+    const int ldo = POLY ? w.kp : w.ms;
+    const bool twice = POLY && !EXACT && w.kp > w.mp;  // M meets both parts of X^T
+    Turner<S> turner(lds, L), rest(lds + S::WAVES * Turner<S>::kBytes, L);
 #pragma unroll
     for (int jj = 0; jj < S::NT; ++jj) {
         const int j = jw + jj * 32 + (L.c & ~3);  // and the three after it
@@ -858,14 +872,16 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
         }
         // what the tile needs from memory, all of a column block before its first use
         float dj[4], di4[S::MT * 4];
-        f16x4 old[S::MT * 4];
+        f16x4 old[S::MT * 4], old_rest[EXACT ? S::MT * 4 : 1];
         if constexpr (POLY) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) dj[e] = ds[j + e < w.m ? j + e : w.m - 1];
 #pragma unroll
             for (int t = 0; t < S::MT * 4; ++t) {
                 const int i = mine + 8 * t, ic = i < w.m ? i : w.m - 1;
-                old[t] = *(const f16x4*)(s16 + (int64_t)ic * w.mp + (j < w.mp ? j : w.mp - 4));
+                const _Float16* at = s16 + (int64_t)ic * w.ms + (j < w.mp ? j : w.mp - 4);
+                old[t] = *(const f16x4*)(EXACT ? at + w.mp : at);
+                if constexpr (EXACT) old_rest[t] = *(const f16x4*)at;
                 di4[t] = ds[ic];
             }
         }
@@ -880,13 +896,15 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
                 quad_turn(v);
                 const bool inside = i < w.m && j < w.mp;
                 const float ti1 = spread(i), ui1 = __builtin_amdgcn_rcpf(ti1);
-                f16x4 h, mirrored;  // the value times its row's factor, and times its column's
+                // the value times its row's factor, and times its column's; what their rounding leaves
+                f16x4 h, mirrored, h_rest, mirrored_rest;
                 if constexpr (POLY) {
                     const float di = di4[ii * 4 + q];
-                    const f16x4 e16 = old[ii * 4 + q];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = (float)e16[e] * (1.0f / kSScale) * ui1;
+                        float x = (float)old[ii * 4 + q][e];
+                        if constexpr (EXACT) x += (float)old_rest[ii * 4 + q][e];
+                        x *= (1.0f / kSScale) * ui1;
                         float s2 = v[e] * (1.0f / (kSScale * kSScale)) * (ui1 * uj4[e]) + x * (di + dj[e]);
                         if (i == j + e) {
                             s2 += di * di;
@@ -905,22 +923,31 @@ __global__ void __launch_bounds__(S::THREADS) ns_square_kernel(StepArgs a) {
                     if (i >= w.m || j + e >= w.m) v[e] = 0.0f;  // rows repeated past the end
                     // S: one of the two factors that the product carries is wanted
                     constexpr float kOne = kSScale / (kXScale * kXScale);
-                    h[e] = half_fma(v[e], POLY ? ti1 : uj4[e] * kOne);
-                    mirrored[e] = half_fma(v[e], POLY ? tj4[e] : ui1 * kOne);
+                    const float fi = POLY ? ti1 : uj4[e] * kOne, fj = POLY ? tj4[e] : ui1 * kOne;
+                    h[e] = half_fma(v[e], fi);
+                    mirrored[e] = half_fma(v[e], fj);
+                    if constexpr (EXACT) {
+                        h_rest[e] = half_fma(v[e], fi, -(float)h[e]);
+                        mirrored_rest[e] = half_fma(v[e], fj, -(float)mirrored[e]);
+                    }
                 }
-                if (inside) *(f16x4*)(out + (int64_t)i * ldo + j) = h;
-                if (inside && twice) *(f16x4*)(out + (int64_t)i * ldo + w.mp + j) = h;
-                if (ti != tj) turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, mirrored))));
+                if (inside) *(f16x4*)(out + (int64_t)i * ldo + j) = EXACT ? h_rest : h;
+                if (inside && (EXACT || twice)) *(f16x4*)(out + (int64_t)i * ldo + w.mp + j) = h;
+                if (ti != tj) {
+                    turner.put(L, row, quad_turn16(mirrored));
+                    if constexpr (EXACT) rest.put(L, row, quad_turn16(mirrored_rest));
+                }
             }
         if (ti != tj) {
-            turner.flush(L, out, ldo, jw + jj * 32, iw, w.m, w.mp);
+            turner.flush(L, EXACT ? out + w.mp : out, ldo, jw + jj * 32, iw, w.m, w.mp);
+            if constexpr (EXACT) rest.flush(L, out, ldo, jw + jj * 32, iw, w.m, w.mp);
             if (twice) turner.flush(L, out + w.mp, ldo, jw + jj * 32, iw, w.m, w.mp);
         }
     }
 }
 
 // X <- diag(M) X + (M - diag(M)) X, with its fp16 copies for the next step.
-template <class S>
+template <class S, bool EXACT>
 __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     __shared__ __attribute__((aligned(16))) char lds[ns_lds<S>()];
     const Work& w = a.w;
@@ -933,7 +960,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     const Operand A{base + w.m16 + (int64_t)i0 * w.kp * 2, (uint32_t)w.kp * 2, w.m - i0};
     const Operand B{xt + (int64_t)j0 * w.kp * 2, (uint32_t)w.kp * 2, w.n - j0};
     f32x16 acc[S::MT][S::NT];
-    Product<S, MmF16> product(lds, w.kp / 64, false);
+    Product<S, MmF16, EXACT ? 2 : 1> product(lds, (EXACT ? w.mp : w.kp) / 64, false);
     product.tile(A, B, A, B);
     product.ahead();
     const bool holds = product.run(acc);
@@ -946,7 +973,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
     const float* dm = (const float*)(base + w.dm);
     float* x32 = (float*)base;
     _Float16 *x16 = (_Float16*)(base + w.x16), *next = (_Float16*)(base + (a.odd ? w.xt0 : w.xt1));
-    const bool two = w.kp > w.mp;
+    const bool two = EXACT || w.kp > w.mp;
     Turner<S> turner(lds, L), rest(lds + S::WAVES * Turner<S>::kBytes, L);
     float norms[S::MT * 4];  // of this lane's rows, its columns' part
 #pragma unroll
@@ -985,7 +1012,7 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
                 const int64_t at = (int64_t)i * w.np + j;
                 f32x4 x = old[ii * 4 + q];
                 const float d = dm4[ii * 4 + q], ti1 = spread(i), ui1 = __builtin_amdgcn_rcpf(ti1);
-                f16x4 h, turned;  // for X and for X^T, whose rows are the columns here
+                f16x4 h, turned, h_rest;  // for X and for X^T, whose rows are the columns here
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     // past the ends of both sides: rows repeated
@@ -993,24 +1020,29 @@ __global__ void __launch_bounds__(S::THREADS) ns_apply_kernel(StepArgs a) {
                     x[e] = v[e];
                     norms[ii * 4 + q] = __builtin_fmaf(v[e], v[e], norms[ii * 4 + q]);
                     h[e] = half_fma(v[e], ti1);
+                    if constexpr (EXACT) h_rest[e] = half_fma(v[e], ti1, -(float)h[e]);
                     turned[e] = half_fma(v[e], tj4[e]);
                 }
                 if (inside) {
                     *(f32x4*)(x32 + at) = x;
-                    if (!a.last) *(f16x4*)(x16 + at) = h;
+                    if (!a.last) {
+                        _Float16* const to = x16 + (int64_t)i * w.nx + j;
+                        *(f16x4*)(EXACT ? to + w.np : to) = h;
+                        if constexpr (EXACT) *(f16x4*)to = h_rest;
+                    }
                 }
                 if (!a.last) {
-                    turner.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, turned))));
+                    turner.put(L, row, quad_turn16(turned));
                     if (two) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) turned[e] = half_fma(v[e], tj4[e], -(float)turned[e]);
-                        rest.put(L, row, __builtin_bit_cast(f16x4, quad_turn16(__builtin_bit_cast(u32x2, turned))));
+                        rest.put(L, row, quad_turn16(turned));
                     }
                 }
             }
         if (!a.last) {
-            turner.flush(L, next, w.kp, jw + jj * 32, iw, w.n, w.mp);
-            if (two) rest.flush(L, next + w.mp, w.kp, jw + jj * 32, iw, w.n, w.mp);
+            turner.flush(L, next + (w.kp - w.mp), w.kp, jw + jj * 32, iw, w.n, w.mp);
+            if (two) rest.flush(L, next, w.kp, jw + jj * 32, iw, w.n, w.mp);
         }
     }
     if (!a.last) {  // the eight lanes that share a row: a part of its squared norm for every wave's columns
@@ -1045,14 +1077,16 @@ int sum_parts(int64_t rows, int64_t cols) {
     return (int)(p < kMaxParts ? p : kMaxParts);
 }
 
-// The workspace block of one matrix.
-Work work_of(int64_t rows, int64_t cols) {
+// The workspace block of one matrix; exact: all operands in two parts.
+Work work_of(int64_t rows, int64_t cols, bool exact) {
     Work w{};
     w.m = (int)(rows < cols ? rows : cols);
     w.n = (int)(rows < cols ? cols : rows);
     w.mp = (int)round_up(w.m, 64);
     w.np = (int)round_up(w.n, 64);
-    w.kp = w.m <= kTwoParts ? 2 * w.mp : w.mp;
+    w.kp = exact || w.m <= kTwoParts ? 2 * w.mp : w.mp;
+    w.nx = exact ? 2 * w.np : w.np;
+    w.ms = exact ? 2 * w.mp : w.mp;
     w.parts = sum_parts(rows, cols);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -1061,10 +1095,10 @@ Work work_of(int64_t rows, int64_t cols) {
         return here;
     };
     take((int64_t)w.m * w.np * 4);
-    w.x16 = take((int64_t)w.m * w.np * 2);
+    w.x16 = take((int64_t)w.m * w.nx * 2);
     w.xt0 = take((int64_t)w.n * w.kp * 2);
     w.xt1 = take((int64_t)w.n * w.kp * 2);
-    w.s16 = take((int64_t)w.m * w.mp * 2);
+    w.s16 = take((int64_t)w.m * w.ms * 2);
     w.m16 = take((int64_t)w.m * w.kp * 2);
     w.ds = take((int64_t)w.m * 4);
     w.dm = take((int64_t)w.m * 4);
@@ -1162,8 +1196,7 @@ int check_stack(int32_t count, int64_t rows, int64_t cols, const char* what) {
     return ZERO_OK;
 }
 
-int check_space(const void* ws, size_t ws_bytes, int32_t count, int64_t rows, int64_t cols, const char* what) {
-    const size_t need = zero_ns_workspace_bytes(count, rows, cols);
+int check_space(const void* ws, size_t ws_bytes, size_t need, const char* what) {
     if (need == 0) return ZERO_OK;
     if (ws == nullptr) return fail(ZERO_EINVAL, "%s: null workspace", what);
     if (!aligned(ws, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", what);
@@ -1186,6 +1219,7 @@ Coeffs coeffs_of(const zero_newton_schulz& ns) {
 }
 
 // The steps of a large stack: three launches each.
+template <bool EXACT>
 int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStream_t s, const char* what) {
     auto square_tiles = [&](int64_t t) { return count * (ceil_div(w.m, t) * (ceil_div(w.m, t) + 1) / 2); };
     auto whole_tiles = [&](int64_t t) { return count * ceil_div(w.m, t) * ceil_div(w.np, t); };
@@ -1197,7 +1231,7 @@ int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStrea
             a.tiles = (int)(square_tiles(S::TILE) / count);
             const int64_t norms = decltype(poly)::value ? 0 : ceil_div(w.m, kNormRows);
             const dim3 grid((unsigned)(a.tiles + norms), (unsigned)count);
-            return launch(ns_square_kernel<S, decltype(poly)::value>, grid, S::THREADS, s, a, what);
+            return launch(ns_square_kernel<S, decltype(poly)::value, EXACT>, grid, S::THREADS, s, a, what);
         });
     };
     for (int i = 0; i < steps; ++i) {
@@ -1209,7 +1243,7 @@ int run_steps(const Work& w, const Coeffs& k, int32_t count, int steps, hipStrea
             typedef decltype(shape) S;
             a.tiles_m = (int)ceil_div(w.m, S::TILE);
             a.tiles_n = (int)ceil_div(w.np, S::TILE);
-            const int launched = launch(ns_apply_kernel<S>, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)count),
+            const int launched = launch(ns_apply_kernel<S, EXACT>, dim3((unsigned)(a.tiles_m * a.tiles_n), (unsigned)count),
                                         S::THREADS, s, a, what);
             a.row_parts = a.tiles_n * (S::TILE / S::WN);
             return launched;
@@ -1257,7 +1291,7 @@ int run_stack(const IO& io, int32_t count, const zero_newton_schulz& ns, const i
     int rc = ZERO_OK;
     const Coeffs k = coeffs_of(ns);
     if (narrow(io.rows, io.cols)) return run_strips(io, count, ns, k, skip, ws, s, what);
-    Work w = work_of(io.rows, io.cols);
+    Work w = work_of(io.rows, io.cols, IO::kExact);
     w.base = (char*)ws;
     w.skip = skip;
     const IoArgs<IO> a{io, w, ns.eps};
@@ -1266,7 +1300,7 @@ int run_stack(const IO& io, int32_t count, const zero_newton_schulz& ns, const i
     // patches cover the padding of both orientations
     const dim3 patches((unsigned)ceil_div(io.cols, kPatch), (unsigned)ceil_div(io.rows, kPatch), (unsigned)count);
     if ((rc = launch(ns_begin_kernel<IO>, patches, 256, s, a, what)) != ZERO_OK) return rc;
-    if ((rc = run_steps(w, k, count, ns.steps, s, what)) != ZERO_OK) return rc;
+    if ((rc = run_steps<IO::kExact>(w, k, count, ns.steps, s, what)) != ZERO_OK) return rc;
     return launch(ns_end_kernel<IO>, patches, 256, s, a, what);
 }
 
@@ -1274,14 +1308,22 @@ int run_stack(const IO& io, int32_t count, const zero_newton_schulz& ns, const i
 
 extern "C" {
 
-size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols) {
+static size_t workspace_bytes(int32_t count, int64_t rows, int64_t cols, bool exact) {
     if (count <= 0 || count > kMaxCount || rows <= 0 || cols <= 0 || rows > kMaxSide || cols > kMaxSide) return 0;
     if (narrow(rows, cols))
         return with_strip(count, rows, cols, [&](auto shape, int strips, int) -> size_t {
             if (strips == 1) return 0;
             return (size_t)strip_work<decltype(shape)>(strips, sum_parts(rows, cols)).stride * (size_t)count;
         });
-    return (size_t)work_of(rows, cols).stride * (size_t)count;
+    return (size_t)work_of(rows, cols, exact).stride * (size_t)count;
+}
+
+size_t zero_ns_workspace_bytes(int32_t count, int64_t rows, int64_t cols) {
+    return workspace_bytes(count, rows, cols, true);
+}
+
+size_t zero_muon_workspace_bytes(int32_t count, int64_t rows, int64_t cols) {
+    return workspace_bytes(count, rows, cols, false);
 }
 
 int zero_orthogonalize(const void* src, int32_t src_dtype, int32_t count, int64_t rows, int64_t cols,
@@ -1300,7 +1342,8 @@ int zero_orthogonalize(const void* src, int32_t src_dtype, int32_t count, int64_
     if (src_ld < cols || dst_ld < cols) return fail(ZERO_ERANGE, "%s: row stride below cols", what);
     if (count > 1 && (src_stride < (rows - 1) * src_ld + cols || dst_stride < (rows - 1) * dst_ld + cols))
         return fail(ZERO_ERANGE, "%s: matrices overlap", what);
-    if ((rc = check_space(ws, ws_bytes, count, rows, cols, what)) != ZERO_OK) return rc;
+    const size_t need = workspace_bytes(count, rows, cols, dst_dtype == ZERO_F16);
+    if ((rc = check_space(ws, ws_bytes, need, what)) != ZERO_OK) return rc;
     const int64_t from = (int64_t)elem_bytes(src_dtype);
     const bool same = src == dst && from == 2 && src_ld == dst_ld && (count == 1 || src_stride == dst_stride);
     if (!same && overlap(Place(src, rows, cols * from, src_ld * from, count, src_stride * from),
@@ -1343,7 +1386,7 @@ int zero_muon_step(float* master, float* mom, const float* g, int32_t count, int
         return fail(ZERO_EALIGN, "%s: buffers not aligned to their elements", what);
     if (offset < 0) return fail(ZERO_ERANGE, "%s: negative offset", what);
     if (count > 1 && stride < rows * cols) return fail(ZERO_ERANGE, "%s: matrices overlap", what);
-    if ((rc = check_space(ws, ws_bytes, count, rows, cols, what)) != ZERO_OK) return rc;
+    if ((rc = check_space(ws, ws_bytes, zero_muon_workspace_bytes(count, rows, cols), what)) != ZERO_OK) return rc;
     const int64_t size = rows * cols * 4, apart = stride * 4;
     const Place place[4] = {Place(master, 1, size, size, count, apart), Place(mom, 1, size, size, count, apart),
                             Place(g, 1, size, size, count, apart),
