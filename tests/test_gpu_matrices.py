@@ -993,3 +993,27 @@ def test_update_every_tile_shape(Z, count, rows, cols):
     Z.muon_step(p, m, x, hp)
     for i in {0, count // 2, count - 1}:
         assert rel(-p[i].double() / math.sqrt(max(1.0, rows / cols)), ns64_gpu(x[i])) <= NS_TOL
+
+
+@pytest.mark.parametrize("count,rows,cols", [(2, 60, 40), (1, 20, 3000), (2, 130, 200), (1, 1100, 600), (2, 513, 700)])
+def test_exact_update(Z, count, rows, cols):
+    """In fp32, with nothing but fp32's own roundings; in a shard step too."""
+    x = randn(count, rows, cols, seed=rows)
+    hp = Z.muon_hparams(lr=1.0, momentum=0.0, nesterov=False, scale=Z.MUON_SCALE_SHAPE)
+    p, m = torch.zeros_like(x), torch.zeros_like(x)
+    slot = torch.empty_like(x, dtype=F16)
+    ws = torch.empty(Z._lib.zero_ns_workspace_bytes(count, rows, cols), dtype=torch.uint8, device="cuda")
+    Z.muon_step(p, m, x, hp, slot=slot, ws=ws, exact=True)
+    for i in range(count):
+        got = -p[i].double() / math.sqrt(max(1.0, rows / cols))
+        assert rel(got, ns64_gpu(x[i])) <= NS_TOL / 1000 + 500 * 2.0 ** -24
+    assert torch.equal(slot, p.to(F16))
+    size = count * rows * cols
+    state = [torch.zeros(size, device="cuda") for _ in range(3)]
+    contrib, gather = x.view(1, -1).to(BF16), torch.empty(size, dtype=BF16, device="cuda")
+    step = Z.MuonShardStep(1, size, size, 0, Z.BF16, Z.BF16, Z.hparams(max_grad_norm=1e9), hp, [(0, count, rows, cols)], state,
+                           torch.empty(size, device="cuda"), exact=True)
+    step.step(contrib, gather)
+    want, mom = torch.zeros_like(x), torch.zeros_like(x)
+    Z.muon_step(want, mom, contrib.float().view_as(x), hp, exact=True)
+    assert torch.equal(state[0].view_as(x), want) and torch.equal(gather.view_as(x), want.to(BF16))

@@ -199,6 +199,7 @@ def fake_rank(Z, cls, two_pass=True):
     st.hp, st.fused = Z.hparams(), not two_pass
     st.state, st.g, st.ctrl, st.ws, st.pair = (Rows(), Rows(), Rows()), Rows(), "ctrl", "ws", None
     st.muon, st.matrices, st.between, st.matrix_ws = "muon", [(0, 2, 8, 16)], [(256, 3840)], None
+    st.exact = False
     return st
 
 
@@ -410,4 +411,7 @@ def test_workspace_of_the_step(Z):
         assert muon_bytes(*size) == 0
     size = muon_bytes(1, 200, 300)
     assert muon(Z, ws_bytes=size - 1) == ESPACE
+    hp = Z.muon_hparams()
+    assert Z._lib.zero_muon_step_exact(P, P, P, 1, 200, 300, 60000, ctypes.byref(hp), None, P, F16, 0, P, size, None) == ESPACE
+    assert "zero_muon_step_exact" in Z.zero_last_error()
     assert ortho(Z, dst=1 << 40, ddt=BF16, ws_bytes=size - 1) == ESPACE == ortho(Z, dst=1 << 40, ddt=F16, ws_bytes=size)

@@ -183,6 +183,9 @@ _sig = {
     "zero_muon_step": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64,
                                       ctypes.POINTER(MuonHparams), _vp, _vp, _i32, _i64, _vp,
                                       ctypes.c_size_t, _vp]),
+    "zero_muon_step_exact": (ctypes.c_int, [_vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                                            ctypes.POINTER(MuonHparams), _vp, _vp, _i32, _i64, _vp,
+                                            ctypes.c_size_t, _vp]),
     "zero_mx4_padded": (_i64, [_i64]),
     "zero_mx4_code_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "zero_mx4_scale_bytes": (ctypes.c_size_t, [_i64, _i64]),

@@ -98,9 +98,9 @@ struct PlainIo {
 };
 
 // The matrices of zero_muon_step: the momentum is updated at the first reading.
-template <int DTO>
+template <int DTO, bool EXACT>
 struct MuonIo {
-    static constexpr bool kExact = false;  // an update: lr times it meets the weights
+    static constexpr bool kExact = EXACT;
     float* master;
     float* mom;
     const float* g;
@@ -180,9 +180,10 @@ __device__ __forceinline__ double block_sum(double v, double* red, int waves) {
 // next S.  Past kFused strips, reading all the parts in every strip costs more than
 // one workgroup that makes M in a launch of its own.
 //
-// What bounds a step is its chain of barriers and the arithmetic of splitting and
-// storing, not the products: hence many waves with small tiles (eight waves
-// with 32 x 32 tiles took 4.3 us a step at 64 x 64 and 10 at 128 x 128; these 1.7 and 7).
+// What bounds a step is its chain of barriers: of the waves' cycles (32 of 128 x 128) 58%
+// wait, 23% for their turn to issue, 7% for LDS, and the matrix cores are busy for 7%.
+// Hence many waves with small tiles (eight waves with 32 x 32 tiles took 4.3 us a step at
+// 64 x 64 and 10 at 128 x 128; these 1.7 and 7).  Strip<128> spills 7 registers.
 template <int T_, int RT_, int G_, int NB_>
 struct Strip {
     static constexpr int T = T_, RT = RT_, G = G_, NB = NB_;
@@ -1366,10 +1367,10 @@ int zero_orthogonalize(const void* src, int32_t src_dtype, int32_t count, int64_
     }
 }
 
-int zero_muon_step(float* master, float* mom, const float* g, int32_t count, int64_t rows, int64_t cols,
-                   int64_t stride, const zero_muon_hparams* hp, const zero_ctrl* ctrl, void* gather,
-                   int32_t gather_dtype, int64_t offset, void* ws, size_t ws_bytes, void* stream) {
-    const char* what = "zero_muon_step";
+static int muon_step(float* master, float* mom, const float* g, int32_t count, int64_t rows, int64_t cols,
+                     int64_t stride, const zero_muon_hparams* hp, const zero_ctrl* ctrl, void* gather,
+                     int32_t gather_dtype, int64_t offset, void* ws, size_t ws_bytes, void* stream, bool exact,
+                     const char* what) {
     int rc;
     if (hp == nullptr) return fail(ZERO_EINVAL, "%s: null hyperparameters", what);
     if ((rc = check_ns(&hp->ns, what)) != ZERO_OK) return rc;
@@ -1386,7 +1387,7 @@ int zero_muon_step(float* master, float* mom, const float* g, int32_t count, int
         return fail(ZERO_EALIGN, "%s: buffers not aligned to their elements", what);
     if (offset < 0) return fail(ZERO_ERANGE, "%s: negative offset", what);
     if (count > 1 && stride < rows * cols) return fail(ZERO_ERANGE, "%s: matrices overlap", what);
-    if ((rc = check_space(ws, ws_bytes, zero_muon_workspace_bytes(count, rows, cols), what)) != ZERO_OK) return rc;
+    if ((rc = check_space(ws, ws_bytes, workspace_bytes(count, rows, cols, exact), what)) != ZERO_OK) return rc;
     const int64_t size = rows * cols * 4, apart = stride * 4;
     const Place place[4] = {Place(master, 1, size, size, count, apart), Place(mom, 1, size, size, count, apart),
                             Place(g, 1, size, size, count, apart),
@@ -1397,16 +1398,31 @@ int zero_muon_step(float* master, float* mom, const float* g, int32_t count, int
     const double wide = (double)(rows > cols ? rows : cols);
     const double s = hp->scale == ZERO_MUON_SCALE_RMS ? 0.2 * std::sqrt(wide)
                                                       : std::sqrt(rows > cols ? (double)rows / (double)cols : 1.0);
-    auto with = [&](auto so) {
+    auto with = [&](auto so, auto two) {
         constexpr int DTO = decltype(so)::value;
-        MuonIo<DTO> io{master, mom, g, ctrl, gather == nullptr ? nullptr : (uint16_t*)gather + offset, stride,
+        MuonIo<DTO, decltype(two)::value> io{master, mom, g, ctrl, gather == nullptr ? nullptr : (uint16_t*)gather + offset, stride,
                        (int)rows, (int)cols, hp->momentum, 1.0f - hp->momentum,
                        (float)((double)hp->lr * (double)hp->weight_decay), (float)((double)hp->lr * s),
                        hp->nesterov != 0};
         return run_stack(io, count, hp->ns, ctrl == nullptr ? nullptr : &ctrl->skip, ws, (hipStream_t)stream, what);
     };
-    return gather_dtype == ZERO_F16 ? with(std::integral_constant<int, ZERO_F16>())
-                                    : with(std::integral_constant<int, ZERO_BF16>());
+    auto to = [&](auto so) { return exact ? with(so, std::true_type()) : with(so, std::false_type()); };
+    return gather_dtype == ZERO_F16 ? to(std::integral_constant<int, ZERO_F16>())
+                                    : to(std::integral_constant<int, ZERO_BF16>());
+}
+
+int zero_muon_step(float* master, float* mom, const float* g, int32_t count, int64_t rows, int64_t cols,
+                   int64_t stride, const zero_muon_hparams* hp, const zero_ctrl* ctrl, void* gather,
+                   int32_t gather_dtype, int64_t offset, void* ws, size_t ws_bytes, void* stream) {
+    return muon_step(master, mom, g, count, rows, cols, stride, hp, ctrl, gather, gather_dtype, offset, ws, ws_bytes,
+                     stream, false, "zero_muon_step");
+}
+
+int zero_muon_step_exact(float* master, float* mom, const float* g, int32_t count, int64_t rows, int64_t cols,
+                         int64_t stride, const zero_muon_hparams* hp, const zero_ctrl* ctrl, void* gather,
+                         int32_t gather_dtype, int64_t offset, void* ws, size_t ws_bytes, void* stream) {
+    return muon_step(master, mom, g, count, rows, cols, stride, hp, ctrl, gather, gather_dtype, offset, ws, ws_bytes,
+                     stream, true, "zero_muon_step_exact");
 }
 
 }  // extern "C"
