@@ -400,6 +400,8 @@ __global__ void __launch_bounds__(S::THREADS) mx4_matmul_kernel(MatmulArgs g) {
 // takes 32 of B's rows, its eight waves an eighth of k each: a wave brings its own
 // slabs to its own part of LDS (whole lines; 16 bytes per lane straight to
 // registers touch a line per lane), waits for nobody, and the waves' sums meet in LDS.
+// One token, 11008 x 4096: 5.9 us, where reading B takes 5; the waves wait for 57% of their
+// cycles, 3% for LDS.
 // VALUES (m k up to kFewValues): A comes as values, and every workgroup quantises
 // all of it to LDS first, which saves a launch.
 constexpr int kFewWaves = 8;
@@ -632,8 +634,9 @@ int matmul(const MatmulArgs& g, int32_t c_dtype, hipStream_t s, const char* what
     if (overlap(c, codes_at(g.a, g.m, g.p)) || overlap(c, scales_at(g.sa, g.m, g.p)) || overlap(c, codes_at(g.b, g.n, g.p)) ||
         overlap(c, scales_at(g.sb, g.n, g.p)))
         return fail(ZERO_EINVAL, "%s: the result overlaps an operand", what);
-    // Few rows against tiles of 64, us: 1 x 11008 x 4096 8.4 and 9.2, 16 rows 9.8 and 9.1; where the tiles
-    // leave half of the CUs out, 4096 x 11008, 1 row 9.8 and 14.9, 32 rows 13.4 and 15.4, 48 rows 17.2 and 16.9.
+    // Few rows against tiles of 64, us of operands in a replayed graph: 11008 x 4096, 8 rows 6.7, 9 to 32 rows by
+    // tiles 7.5; where the tiles leave half of the CUs out, 4096 x 11008, 1 row 7.2, 32 rows 10.6, 33 to 64 rows by
+    // tiles 13.6.  Where both fill the CUs tiles win from 9 rows on (11008 x 4096, 16 rows: 9.8 and 9.1, whole calls).
     if (g.m <= 8 || (g.m <= 32 && g.n <= 64 * 128)) return few_with<ZERO_F32, false>(FewArgs{g, 0, 0}, c_dtype, s, what);
     const int pick = pick_tile([&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); });
     return with_tile(pick, [&](auto shape) { return matmul_with<decltype(shape)>(g, c_dtype, s, what); });
