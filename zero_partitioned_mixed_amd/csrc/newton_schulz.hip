@@ -74,6 +74,7 @@ struct Work {
 template <int DTI, int DTO>
 struct PlainIo {
     static constexpr bool kExact = DTO == ZERO_F16;  // a result of 11 bits: the operands have 22
+    static constexpr bool kNarrow = true;            // narrow matrices come with this type too
     const typename Elem<DTI>::type* src;
     typename Elem<DTO>::type* dst;
     int64_t src_ld, src_stride, dst_ld, dst_stride;
@@ -101,6 +102,7 @@ struct PlainIo {
 template <int DTO, bool EXACT>
 struct MuonIo {
     static constexpr bool kExact = EXACT;
+    static constexpr bool kNarrow = !EXACT;  // their operands have two parts anyway
     float* master;
     float* mom;
     const float* g;
@@ -1291,7 +1293,9 @@ int run_stack(const IO& io, int32_t count, const zero_newton_schulz& ns, const i
               hipStream_t s, const char* what) {
     int rc = ZERO_OK;
     const Coeffs k = coeffs_of(ns);
-    if (narrow(io.rows, io.cols)) return run_strips(io, count, ns, k, skip, ws, s, what);
+    if constexpr (IO::kNarrow) {
+        if (narrow(io.rows, io.cols)) return run_strips(io, count, ns, k, skip, ws, s, what);
+    }
     Work w = work_of(io.rows, io.cols, IO::kExact);
     w.base = (char*)ws;
     w.skip = skip;
@@ -1398,15 +1402,16 @@ static int muon_step(float* master, float* mom, const float* g, int32_t count, i
     const double wide = (double)(rows > cols ? rows : cols);
     const double s = hp->scale == ZERO_MUON_SCALE_RMS ? 0.2 * std::sqrt(wide)
                                                       : std::sqrt(rows > cols ? (double)rows / (double)cols : 1.0);
-    auto with = [&](auto so, auto two) {
+    auto with = [&](auto so, auto parts) {
         constexpr int DTO = decltype(so)::value;
-        MuonIo<DTO, decltype(two)::value> io{master, mom, g, ctrl, gather == nullptr ? nullptr : (uint16_t*)gather + offset, stride,
+        MuonIo<DTO, decltype(parts)::value> io{master, mom, g, ctrl, gather == nullptr ? nullptr : (uint16_t*)gather + offset, stride,
                        (int)rows, (int)cols, hp->momentum, 1.0f - hp->momentum,
                        (float)((double)hp->lr * (double)hp->weight_decay), (float)((double)hp->lr * s),
                        hp->nesterov != 0};
         return run_stack(io, count, hp->ns, ctrl == nullptr ? nullptr : &ctrl->skip, ws, (hipStream_t)stream, what);
     };
-    auto to = [&](auto so) { return exact ? with(so, std::true_type()) : with(so, std::false_type()); };
+    const bool two = exact && !narrow(rows, cols);
+    auto to = [&](auto so) { return two ? with(so, std::true_type()) : with(so, std::false_type()); };
     return gather_dtype == ZERO_F16 ? to(std::integral_constant<int, ZERO_F16>())
                                     : to(std::integral_constant<int, ZERO_BF16>());
 }
