@@ -415,3 +415,18 @@ def test_workspace_of_the_step(Z):
     assert Z._lib.zero_muon_step_exact(P, P, P, 1, 200, 300, 60000, ctypes.byref(hp), None, P, F16, 0, P, size, None) == ESPACE
     assert "zero_muon_step_exact" in Z.zero_last_error()
     assert ortho(Z, dst=1 << 40, ddt=BF16, ws_bytes=size - 1) == ESPACE == ortho(Z, dst=1 << 40, ddt=F16, ws_bytes=size)
+
+
+def test_ranks_of_another_pass_take_their_own_calls(Z, monkeypatch):
+    """A class that replaces either part of the step is not what the batched calls stand for."""
+    monkeypatch.setattr(Z, "shard_table", lambda shards: list(shards))
+
+    class Pass(Z.ShardStep):
+        def run_pieces(self, *a, **k):
+            pass
+
+    class Named(Z.ShardStep):
+        name = "a rank"
+
+    for cls, batched in ((Pass, False), (Named, True), (Z.ShardStep, True)):
+        assert Z.MultiShardStep([fake_rank(Z, cls), fake_rank(Z, Z.ShardStep)]).takes_batched([Rows(), Rows()], Rows()) == batched

@@ -729,8 +729,8 @@ class MultiShardStep:
     pass: zero_fused_step_shards, the decision, zero_fused_restore_shards on
     the fused path (which also needs the 16-bit slot); zero_reduce_grads_shards,
     the decision, zero_adam_step_shards on the two-pass path.  Bit-identical to
-    every rank's own calls.  Ranks that complete a step in a way of their own
-    (MuonShardStep) take their own calls."""
+    every rank's own calls.  Ranks that pass over or complete a step in a way of
+    their own (MuonShardStep) take their own calls."""
 
     def __init__(self, steps: list, batched: bool = True):
         if not 1 <= len(steps) <= MAX_RANKS:
@@ -752,7 +752,8 @@ class MultiShardStep:
             return None
         if self.fused and gather is None:
             return None
-        if any(type(s).complete is not ShardStep.complete for s in ss):
+        own = ("run_pieces", "complete")  # what the batched calls stand for
+        if any(getattr(type(s), f) is not getattr(ShardStep, f) for s in ss for f in own):
             return None
         cap = launch_tiles(s0.nranks) * TILE
         if any(s.bucket or s.valid_len > cap or s.nranks != s0.nranks or s.dtype != s0.dtype

@@ -112,9 +112,10 @@ def orthogonalize(x, out_dtype=None, *, coeffs=COEFFS, steps: int = 5, eps: floa
     """The Newton-Schulz orthogonalisation of every matrix of x ([rows, cols] or
     [count, rows, cols]; fp16, bf16 or fp32, any strides: other layouts than
     unit-stride rows are copied).  Returns fp16 or bf16 (out_dtype; by default x's
-    type, bf16 for fp32), in ``out`` when given (it may be x).  A result in fp16 is exact
-    but for its own rounding (1e-5); one in bf16, for a smaller side above 128, to 1.8e-3
-    in 0.4 of the time.  coeffs: as newton_schulz takes them.  Not differentiable."""
+    type, bf16 for fp32), in ``out`` when given (it may be x, or share no element with
+    it).  A result in fp16 is exact but for its own rounding (1e-5); one in bf16, for a
+    smaller side above 128, to 1.8e-3 in 0.4 of the time.  coeffs: as newton_schulz
+    takes them.  Not differentiable."""
     if out is not None:
         out_dtype = out.dtype
     elif out_dtype is None:
@@ -324,7 +325,7 @@ def mx4_dequantize(q: MX4, dtype=torch.bfloat16, out=None):
 def mx4_matmul(a, b: MX4, out_dtype=torch.bfloat16, *, out=None, accumulate: bool = False, ws=None):
     """a b^T: a an MX4, or a matrix of values that is quantised along its rows (in
     the product's own call for up to MX4_ROWS_MAX rows); b an MX4 over the
-    same columns.  accumulate adds into ``out`` (fp32)."""
+    same columns.  accumulate adds into ``out`` (fp32).  out shares no element with a or b."""
     values = not isinstance(a, MX4)
     m, k = a.shape if values else (a.rows, a.cols)
     n = b.rows
