@@ -600,11 +600,11 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
  * whose diagonals are kept apart in fp32.  Results in fp16, and all of matrices
  * whose smaller side is at most 128, take every operand in two fp16 parts: before
  * their own rounding they are within 1e-5 of the iteration in 64 bits (relative,
- * Frobenius norm).  Results in bf16 and the optimizer's update take one part
+ * Frobenius norm; below for rank one).  Results in bf16 and the optimizer's update take one part
  * above 128: within about 1e-3, up to 1.8e-3 where the rank is low or the
  * elements are equal, beside bf16's own 1.7e-3, in 0.4 of the time.  Sums of equal
- * terms round alike, so that constant matrices may be off by 5e-7 times their
- * smaller side more. */
+ * terms round alike, so that matrices of rank one may be off by up to 5e-7 times
+ * their smaller side more (constant ones; with normal factors 4e-5 to 3e-4). */
 #define ZERO_F32 3 /* a dtype of the matrix calls below, where they say so */
 
 #define ZERO_NS_REACH 3.5 /* singular values between steps, at most: the fp16 operands' range */
@@ -672,7 +672,7 @@ int zero_muon_step(float *master_dev, float *mom_dev, const float *g_dev, int32_
                    int64_t offset, void *ws_dev, size_t ws_bytes, void *stream);
 
 /* The same with every operand in two fp16 parts, as for results in fp16: the update is
- * within 1e-5 above a smaller side of 128 too, in 2.4 times the time (the same
+ * as exact as those above a smaller side of 128 too, in 2.4 times the time (the same
  * call up to 128).  ws: zero_ns_workspace_bytes. */
 int zero_muon_step_exact(float *master_dev, float *mom_dev, const float *g_dev, int32_t count,
                          int64_t rows, int64_t cols, int64_t stride, const zero_muon_hparams *hp,

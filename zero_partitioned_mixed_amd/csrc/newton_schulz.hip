@@ -18,8 +18,9 @@
 // part, in 0.4 of the time (11008 x 4096: 3.8 against 9.6 ms, 1500 x 4099 0.42 against 0.99).
 // In one part, against 64 bits: 2e-4 to 1e-3 for spectra from flat to 1/k, up to 1.5e-3
 // for a quarter of the rank and 1.8e-3 for matrices of one or two values (55 sizes from
-// 130 x 200 to 4096 x 4096).  In both forms sums over equal terms round alike: constant
-// matrices are off by 5e-7 times the smaller side more (8192 x 8192: 4e-3).
+// 130 x 200 to 4096 x 4096).  In two parts: 1e-6, a quarter of the rank 5e-6.  In both
+// forms sums over equal terms round alike: constant matrices are off by 5e-7 times the
+// smaller side more (8192 x 8192: 4e-3), other matrices of rank one by 4e-5 to 3e-4.
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
 // the coefficients choose (coeffs_of); entries down to 1 / (65536 * 256)
 // stay normal or lose less than X's own rounding.
