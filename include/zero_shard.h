@@ -600,10 +600,10 @@ int zero_fused_step_noalloc(const void *contrib_dev, int32_t contrib_dtype, int3
  * whose diagonals are kept apart in fp32.  Results in fp16, and all of matrices
  * whose smaller side is at most 128, take every operand in two fp16 parts: before
  * their own rounding they are within 1e-5 of the iteration in 64 bits (relative,
- * Frobenius norm; below for rank one).  Results in bf16 and the optimizer's update take one part
- * above 128: within about 1e-3, up to 1.8e-3 where the rank is low or the
- * elements are equal, beside bf16's own 1.7e-3, in 0.4 of the time.  Sums of equal
- * terms round alike, so that matrices of rank one may be off by up to 5e-7 times
+ * Frobenius norm; for rank one see below).  Results in bf16 and the optimizer's
+ * update take one part above 128: within about 1e-3, up to 1.8e-3 where the rank
+ * is low or the elements are equal, beside bf16's own 1.7e-3, in 0.4 of the time.
+ * Sums of equal terms round alike, so that matrices of rank one may be off by up to 5e-7 times
  * their smaller side more (constant ones; with normal factors 4e-5 to 3e-4). */
 #define ZERO_F32 3 /* a dtype of the matrix calls below, where they say so */
 

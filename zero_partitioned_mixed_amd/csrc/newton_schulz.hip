@@ -21,6 +21,7 @@
 // 130 x 200 to 4096 x 4096).  In two parts: 1e-6, a quarter of the rank 5e-6.  In both
 // forms sums over equal terms round alike: constant matrices are off by 5e-7 times the
 // smaller side more (8192 x 8192: 4e-3), other matrices of rank one by 4e-5 to 3e-4.
+//
 // fp16 holds powers of two times the values: X * 2^8, E * 2^12, M * a power that
 // the coefficients choose (coeffs_of); entries down to 1 / (65536 * 256)
 // stay normal or lose less than X's own rounding.
