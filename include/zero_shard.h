@@ -754,6 +754,127 @@ int zero_mx4_linear_grad(const void *dy_dev, int64_t lddy, int32_t dtype, int64_
                          int64_t lddx, void *dw_dev, int64_t lddw, void *ws_dev, size_t ws_bytes,
                          void *stream);
 
+/* ---- Rows of tokens -----------------------------------------------------------
+ * What a training step or a served token does between the linear layers.  Rows
+ * are given by their first element and a row stride in elements; dtypes are
+ * ZERO_F16, ZERO_BF16 or ZERO_F32; rows and columns go up to 2^24 unless a call
+ * says otherwise.  Sums are fp32, in an order that depends on sizes alone.
+ *
+ * MXFP8 rows: blocks of 32 along a row as in the part above, with 8-bit codes
+ * (E4M3, largest 448).  A block's scale 2^(s - 127) is the smallest power of two
+ * (s >= 0) that leaves its largest magnitude at 448 or below, so that nothing
+ * saturates; each element is rounded to the nearest code, ties to even.  A block
+ * holding inf or NaN has s = 255 (NaN) and codes 0.  codes: [rows][P] bytes, P as
+ * above; scales: [rows][P / 32] (zero_mx4_scale_bytes); both 16-byte aligned.
+ * Errors of all calls: EINVAL, EALIGN (rows to their elements, codes, scales and
+ * workspaces to 16 bytes), ERANGE, ESPACE. */
+size_t zero_mx8_code_bytes(int64_t rows, int64_t cols);
+int zero_mx8_quantize(const void *src_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                      void *codes_dev, void *scales_dev, void *stream);
+int zero_mx8_dequantize(const void *codes_dev, const void *scales_dev, int64_t rows, int64_t cols,
+                        void *dst_dev, int32_t dtype, int64_t ld, void *stream);
+
+/* c[i][j] = sum over k of A[i][k] B[j][k] (+ c[i][j] when accumulate is 1 and c is
+ * ZERO_F32): A m x k in MXFP8, B n x k in MXFP4, both along k.  The _rows form takes
+ * A as values (a_dtype, row stride lda) and quantises them on the way in; up to m = 32
+ * with m times the padded k up to 16384 in the product's own kernel, without a
+ * workspace.  k = 0 gives zeros (or c unchanged). */
+int zero_mx8_matmul(const void *a_codes_dev, const void *a_scales_dev, const void *b_codes_dev,
+                    const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,
+                    int32_t c_dtype, int64_t ldc, int32_t accumulate, void *stream);
+size_t zero_mx8_matmul_rows_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int zero_mx8_matmul_rows(const void *a_dev, int32_t a_dtype, int64_t lda, const void *b_codes_dev,
+                         const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,
+                         int32_t c_dtype, int64_t ldc, int32_t accumulate, void *ws_dev,
+                         size_t ws_bytes, void *stream);
+
+/* Root-mean-square norm of every row, with the residual's addition:
+ *     h = x + residual, rounded to the residual's type (h = x without one)
+ *     y = h / sqrt(mean(h^2) + eps) * w
+ * x, w and y are of one dtype; the residual and h of the same or ZERO_F32.
+ * residual and h come together or are both NULL.  h may be the residual's place and
+ * y x's (same row stride).  Squares that leave fp32's range are summed scaled.  The _mx8
+ * form leaves y as MXFP8 rows.  eps >= 0. */
+int zero_rms_norm(const void *x_dev, int32_t dtype, int64_t ldx, const void *residual_dev,
+                  int32_t residual_dtype, int64_t ldr, const void *w_dev, int64_t tokens,
+                  int64_t cols, float eps, void *y_dev, int64_t ldy, void *h_dev, int64_t ldh,
+                  void *stream);
+int zero_rms_norm_mx8(const void *x_dev, int32_t dtype, int64_t ldx, const void *residual_dev,
+                      int32_t residual_dtype, int64_t ldr, const void *w_dev, int64_t tokens,
+                      int64_t cols, float eps, void *codes_dev, void *scales_dev, void *h_dev,
+                      int64_t ldh, void *stream);
+
+/* Its gradients, from dy (dtype), h (h_dtype: dtype or ZERO_F32) and, where h went on
+ * too, its gradient dh (h_dtype; may be NULL).  With u = h / sqrt(mean(h^2) + eps), g = dy w:
+ *     dr = (g - u mean(g u)) / sqrt(mean(h^2) + eps) + dh    the residual's, h_dtype
+ *     dx = dr rounded to dtype;   dw = sum over tokens of dy u, dtype
+ * Each of dx, dr and dw may be NULL; the workspace is for dw. */
+size_t zero_rms_norm_grad_workspace_bytes(int64_t tokens, int64_t cols);
+int zero_rms_norm_grad(const void *dy_dev, int64_t lddy, const void *h_dev, int32_t h_dtype,
+                       int64_t ldh, const void *w_dev, int32_t dtype, const void *dh_dev,
+                       int64_t lddh, int64_t tokens, int64_t cols, float eps, void *dx_dev,
+                       int64_t lddx, void *dr_dev, int64_t lddr, void *dw_dev, void *ws_dev,
+                       size_t ws_bytes, void *stream);
+
+/* y = x 65536 / (65536 - T) where element (r, c) stays, else 0; plus the residual
+ * where there is one.  T = p 65536 rounded to a whole number (p in [0, 1]).  An element stays when its 16 bits are T or
+ * more: word c % 8 / 2 (low half for even c) of Philox4x32-10 under the key seed (low
+ * word first) at the counter {c / 8, r, low and high word of the offset}.  The offset is `offset` plus,
+ * where offset_dev is not NULL, the number there when the kernel runs: a captured
+ * graph draws anew when the program moves it between replays.  The mask depends on
+ * r, c, seed and offset alone and is stored nowhere; the gradient is the same call
+ * on dy without a residual.  y may be x's or the residual's place (same row stride).
+ * rows up to 2^32, cols up to 2^34, rows times cols up to 2^40. */
+int zero_dropout(const void *x_dev, int32_t dtype, int64_t ldx, const void *residual_dev,
+                 int64_t ldr, int64_t rows, int64_t cols, double p, uint64_t seed,
+                 uint64_t offset, const uint64_t *offset_dev, void *y_dev, int64_t ldy,
+                 void *stream);
+
+/* out[t] = table[ids[t]] * scale, rounded once; ids: `tokens` contiguous numbers of
+ * id_bytes 4 or 8 (signed).  An id outside [0, vocab) gives zeros and takes no part in
+ * the gradient (padding; the other ranks' part of a table that is split by rows).  The
+ * gradient writes every row of the table's: scale times the sum of dy over the
+ * row's tokens, in their order, in fp32, rounded once. */
+int zero_embedding(const void *ids_dev, int32_t id_bytes, int64_t tokens, const void *table_dev,
+                   int32_t dtype, int64_t ldt, int64_t vocab, int64_t cols, float scale,
+                   void *out_dev, int64_t ldo, void *stream);
+size_t zero_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols);
+int zero_embedding_grad(const void *ids_dev, int32_t id_bytes, int64_t tokens, const void *dy_dev,
+                        int32_t dtype, int64_t lddy, int64_t vocab, int64_t cols, float scale,
+                        void *dtable_dev, int64_t ldo, void *ws_dev, size_t ws_bytes,
+                        void *stream);
+
+/* Tokens by expert.  Slot t * k + j is token t's j-th assignment, ids its expert.
+ * zero_expert_sort: order[i] = the slot at place i when the slots are sorted by expert
+ * (equal ones in the order of slots; those outside [0, experts) last), place its
+ * inverse, offsets[e] = the first place of expert e, offsets[experts] = the number of
+ * slots that have one.  slots = tokens k up to 2^24. */
+size_t zero_expert_sort_workspace_bytes(int64_t slots, int64_t experts);
+int zero_expert_sort(const void *ids_dev, int32_t id_bytes, int64_t slots, int64_t experts,
+                     int32_t *order_dev, int32_t *place_dev, int32_t *offsets_dev, void *ws_dev,
+                     size_t ws_bytes, void *stream);
+
+/* rows[place[slot]] = x[slot / k]; zeros at places from *used_dev on (used_dev =
+ * offsets + experts).  rows: tokens k of them. */
+int zero_expert_rows(const void *x_dev, int32_t dtype, int64_t ldx, const int32_t *place_dev,
+                     const int32_t *used_dev, int64_t tokens, int64_t k, int64_t cols,
+                     void *rows_dev, int64_t ldr, void *stream);
+
+/* y[t] = sum over j of weights[t][j] rows[place[t k + j]], slots without an expert left
+ * out; in fp32, rounded once.  weights: [tokens][k], dtype or ZERO_F32; NULL: ones, which
+ * is the gradient of zero_expert_rows.  The gradients: drows[place] = weight * dy[t], zeros
+ * from *used_dev on; dweights[t][j] = rows[place] . dy[t], 0 without an expert.  Either
+ * may be NULL (without dweights rows may be too). */
+int zero_expert_combine(const void *rows_dev, int32_t dtype, int64_t ldr, const int32_t *place_dev,
+                        const int32_t *used_dev, const void *weights_dev, int32_t weights_dtype,
+                        int64_t tokens, int64_t k, int64_t cols, void *y_dev, int64_t ldy,
+                        void *stream);
+int zero_expert_combine_grad(const void *dy_dev, int64_t lddy, const void *rows_dev, int32_t dtype,
+                             int64_t ldr, const int32_t *place_dev, const int32_t *used_dev,
+                             const void *weights_dev, int32_t weights_dtype, int64_t tokens,
+                             int64_t k, int64_t cols, void *drows_dev, int64_t lddr,
+                             void *dweights_dev, void *stream);
+
 /* Message for the last nonzero return on the calling thread ("" if none). */
 const char *zero_last_error(void);
 

@@ -204,6 +204,38 @@ _sig = {
     "zero_mx4_linear_grad_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "zero_mx4_linear_grad": (ctypes.c_int, [_vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _i64,
                                             _vp, _i64, _vp, ctypes.c_size_t, _vp]),
+    "zero_mx8_code_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_mx8_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "zero_mx8_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "zero_mx8_matmul": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _i64, _i32,
+                                       _vp]),
+    "zero_mx8_matmul_rows_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "zero_mx8_matmul_rows": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i32,
+                                            _i64, _i32, _vp, ctypes.c_size_t, _vp]),
+    "zero_rms_norm": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _i64,
+                                     ctypes.c_float, _vp, _i64, _vp, _i64, _vp]),
+    "zero_rms_norm_mx8": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _i64,
+                                         ctypes.c_float, _vp, _vp, _vp, _i64, _vp]),
+    "zero_rms_norm_grad_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_rms_norm_grad": (ctypes.c_int, [_vp, _i64, _vp, _i32, _i64, _vp, _i32, _vp, _i64, _i64,
+                                          _i64, ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp,
+                                          ctypes.c_size_t, _vp]),
+    "zero_dropout": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i64, _i64, _i64, ctypes.c_double,
+                                    ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _i64, _vp]),
+    "zero_embedding": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64, ctypes.c_float,
+                                      _vp, _i64, _vp]),
+    "zero_embedding_grad_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "zero_embedding_grad": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i64, _i64, _i64,
+                                           ctypes.c_float, _vp, _i64, _vp, ctypes.c_size_t, _vp]),
+    "zero_expert_sort_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "zero_expert_sort": (ctypes.c_int, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                        _vp]),
+    "zero_expert_rows": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64,
+                                        _vp]),
+    "zero_expert_combine": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                                           _vp, _i64, _vp]),
+    "zero_expert_combine_grad": (ctypes.c_int, [_vp, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32,
+                                                _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
     "zero_last_error": (ctypes.c_char_p, []),
 }
 for _name, (_res, _args) in _sig.items():
@@ -860,3 +892,6 @@ class MultiShardStep:
 from .matrices import (MX4, MuonShardStep, muon_hparams, muon_step,  # noqa: E402,F401
                        mx4_dequantize, mx4_linear, mx4_matmul, mx4_quantize, newton_schulz,
                        orthogonalize)
+from .tokens import (MX8, ExpertPlan, dropout, embedding, expert_combine,  # noqa: E402,F401
+                     expert_rows, expert_sort, mx8_dequantize, mx8_matmul, mx8_quantize, rms_norm,
+                     rms_norm_mx8)

@@ -19,7 +19,8 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("zero_shard.hip", "newton_schulz.hip", "mx4.hip")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("zero_shard.hip", "newton_schulz.hip", "mx4.hip", "mx8.hip",
+                                                  "rows.hip", "tokens.hip")]
 LIB = os.path.join(HERE, "libzero_shard.so")
 ISA_JSON = os.path.join(HERE, "libzero_shard.isa.json")
 INCLUDE = os.path.join(ROOT, "include")

@@ -484,7 +484,7 @@ bool valid_dtype(int32_t dt, bool f32) { return dt == ZERO_F16 || dt == ZERO_BF1
 size_t elem_bytes(int32_t dt) { return dt == ZERO_F32 ? 4 : 2; }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 template <class Args>
 int launch(void (*kernel)(Args), dim3 grid, int block, hipStream_t s, const Args& args, const char* what) {

@@ -1,0 +1,683 @@
+// Operators on rows of tokens: the root-mean-square norm with the residual's addition (its
+// result in the inputs' type or as MXFP8) and its gradients, and dropout.
+#include "mx_common.h"
+
+namespace {
+
+// ---------------------------------------------------------------- root-mean-square norm
+//   h = x + residual, rounded to the residual's type;  y = h / sqrt(mean(h^2) + eps) * w
+// A row's elements stay in registers between the sum of squares and their use: `T` lanes
+// hold a row, V vectors of eight each, so that x and the residual are read and h and y written
+// once.  Bound by memory.
+
+// 1 / sqrt(mean + eps) = r * pre: squares that leave fp32's range, or that its smallest numbers
+// would swallow, are summed again of elements times pre.
+constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p64f;
+__device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-80f ? kPreUp : 1.0f; }
+
+// The sum over the T lanes of a row, T = 64 or a whole workgroup, the same bits in every lane.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* meet) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    if constexpr (T > 64) {
+        __syncthreads();  // the one before has been read
+        if ((threadIdx.x & 63) == 0) meet[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = meet[0];
+#pragma unroll
+        for (int w = 1; w < T / 64; ++w) v += meet[w];
+    }
+    return v;
+}
+
+struct NormArgs {
+    const void *x, *residual, *w;
+    int64_t ldx, ldr;
+    int64_t tokens, cols;
+    float eps;
+    void *y, *h;
+    int64_t ldy, ldh;
+    uint8_t *codes, *scales;  // MX8
+};
+
+template <int DT>
+__device__ __forceinline__ float rounded(float v) {
+    return to_float<DT>(from_float<DT>(v));
+}
+
+// h of eight elements: from x, or from x and the residual, then also stored.
+template <int DX, int DR>
+__device__ __forceinline__ void sum8(const NormArgs& a, int64_t row, int64_t c, const Eight<DX>& ex, const Eight<DR>& er, float* h) {
+    ex.values(h);
+    if (a.residual != nullptr) {
+        float r[8];
+        er.values(r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = rounded<DR>(h[i] + r[i]);
+        put8<DR>((typename Elem<DR>::type*)a.h + row * a.ldh, c, a.cols, h);
+    }
+}
+
+template <int DX, bool MX>
+__device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int64_t c, const float* y) {
+    if constexpr (MX) {
+        const int64_t p = padded(a.cols);
+        const uint32_t s = scale_byte8(block_top8(y));
+        *(u32x2*)(a.codes + row * p + c) = codes8_e4m3(y, s);
+        if ((threadIdx.x & 3) == 0) a.scales[row * (p / kMxBlock) + c / kMxBlock] = (uint8_t)s;
+    } else {
+        put8<DX>((typename Elem<DX>::type*)a.y + row * a.ldy, c, a.cols, y);
+    }
+}
+
+template <int DX, int DR, int T, int V, bool MX>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
+    typedef typename Elem<DX>::type X;
+    typedef typename Elem<DR>::type R;
+    constexpr int kRows = T < 256 ? 256 / T : 1;
+    __shared__ float meet[T > 64 ? T / 64 : 1];
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+    if (row >= a.tokens) return;  // whole waves; with T > 64 none
+    const int t = threadIdx.x % T;
+    const int64_t end = MX ? padded(a.cols) : a.cols;
+    Eight<DX> ex[V], ew[V];
+    Eight<DR> er[V];
+    float h[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        if (c < a.cols) {
+            ex[v].load((const X*)a.x + row * a.ldx, c, a.cols);
+            if (a.residual != nullptr) er[v].load((const R*)a.residual + row * a.ldr, c, a.cols);
+            ew[v].load((const X*)a.w, c, a.cols);
+        }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        if (c < a.cols) {
+            sum8<DX, DR>(a, row, c, ex[v], er[v], h[v]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[v][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += h[v][i] * h[v][i];
+    }
+    const float n = (float)a.cols;
+    float q = row_sum<T>(ss, meet) / n + a.eps;
+    const float pre = pre_of(q);
+    if (pre != 1.0f) {
+        ss = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[v][i] *= pre;
+                ss += h[v][i] * h[v][i];
+            }
+        q = row_sum<T>(ss, meet) / n + a.eps * pre * pre;
+    }
+    const float r = 1.0f / sqrtf(q);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        if (c >= end) break;
+        float w[8];
+        if (MX && c >= a.cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+        } else {
+            ew[v].values(w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[v][i] = h[v][i] * r * w[i];
+            if (MX && c + i >= a.cols) h[v][i] = 0.0f;  // also where r is not finite
+        }
+        norm_out8<DX, MX>(a, row, c, h[v]);
+    }
+}
+
+// Rows that registers do not hold: a workgroup reads each twice.
+constexpr int kWide = 1024;
+template <int DX, int DR, bool MX>
+__global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
+    typedef typename Elem<DX>::type X;
+    typedef typename Elem<DR>::type R;
+    __shared__ float meet[kWide / 64];
+    const int64_t row = blockIdx.x, end = MX ? padded(a.cols) : a.cols;
+    const int64_t c0 = (int64_t)threadIdx.x * 8;
+    const X* const x = (const X*)a.x + row * a.ldx;
+    const R* const hr = (const R*)a.h + row * a.ldh;  // what this lane wrote
+    auto sum_of = [&](float pre, bool first) {
+        float ss = 0.0f;
+        for (int64_t c = c0; c < a.cols; c += kWide * 8) {
+            float h[8];
+            if (first || a.residual == nullptr) {
+                Eight<DX> ex;
+                Eight<DR> er;
+                ex.load(x, c, a.cols);
+                if (a.residual != nullptr) er.load((const R*)a.residual + row * a.ldr, c, a.cols);
+                sum8<DX, DR>(a, row, c, ex, er, h);
+            } else {
+                Eight<DR> eh;
+                eh.load(hr, c, a.cols);
+                eh.values(h);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] *= pre;
+                ss += h[i] * h[i];
+            }
+        }
+        return row_sum<kWide>(ss, meet);
+    };
+    const float n = (float)a.cols;
+    float q = sum_of(1.0f, true) / n + a.eps;
+    const float pre = pre_of(q);
+    if (pre != 1.0f) q = sum_of(pre, false) / n + a.eps * pre * pre;
+    const float r = 1.0f / sqrtf(q);
+    for (int64_t c = c0; c < end; c += kWide * 8) {
+        float h[8], w[8];
+        if (c < a.cols) {
+            if (a.residual == nullptr) {
+                Eight<DX> ex;
+                ex.load(x, c, a.cols);
+                ex.values(h);
+            } else {
+                Eight<DR> eh;
+                eh.load(hr, c, a.cols);
+                eh.values(h);
+            }
+            Eight<DX> ew;
+            ew.load((const X*)a.w, c, a.cols);
+            ew.values(w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? h[i] * pre * r * w[i] : 0.0f;
+        norm_out8<DX, MX>(a, row, c, h);
+    }
+}
+
+// The gradients.  With u = h / root, root = sqrt(mean(h^2) + eps), and g = dy w:
+//   dh' = (g - u mean(g u)) / root + dh,  dw = sum over tokens of dy u
+// dh' goes to the residual's gradient and, rounded to x's type, to x's.  root is computed again
+// from h, which has to be read anyway: nothing but h is kept for the backward pass.
+// A workgroup takes rows kGroups apart and holds its columns' part of dw in registers; the
+// parts are summed in order by a second launch.  Bound by memory.
+struct NormGradArgs {
+    const void *dy, *h, *w, *dh;
+    int64_t lddy, ldh, lddh;
+    int64_t tokens, cols;
+    float eps;
+    void *dx, *dr;
+    int64_t lddx, lddr;
+    float* parts;  // [groups][cols]
+    void* dw;
+    int groups;
+};
+
+constexpr int kGradGroups = 512;
+
+template <int DX, int DR, int T, int V>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_grad_kernel(NormGradArgs a) {
+    typedef typename Elem<DX>::type X;
+    typedef typename Elem<DR>::type R;
+    constexpr int kRows = T < 256 ? 256 / T : 1;
+    __shared__ float meet[T > 64 ? T / 64 : 1];
+    const int t = threadIdx.x % T;
+    const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+    const float n = (float)a.cols;
+    Eight<DX> ew[V];
+    float dw[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        if (c < a.cols) ew[v].load((const X*)a.w, c, a.cols);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
+    }
+    for (int64_t row = group; row < a.tokens; row += a.groups) {
+        Eight<DX> ey[V];
+        Eight<DR> eh[V], ed[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = (int64_t)(v * T + t) * 8;
+            if (c < a.cols) {
+                eh[v].load((const R*)a.h + row * a.ldh, c, a.cols);
+                ey[v].load((const X*)a.dy + row * a.lddy, c, a.cols);
+                if (a.dh != nullptr) ed[v].load((const R*)a.dh + row * a.lddh, c, a.cols);
+            }
+        }
+        auto sums = [&](float pre, float& ss, float& sg) {
+            ss = sg = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if ((int64_t)(v * T + t) * 8 >= a.cols) break;
+                float h[8], y[8], w[8];
+                eh[v].values(h);
+                ey[v].values(y);
+                ew[v].values(w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] *= pre;
+                    ss += h[i] * h[i];
+                    sg += y[i] * w[i] * h[i];
+                }
+            }
+            ss = row_sum<T>(ss, meet);
+            sg = row_sum<T>(sg, meet);
+        };
+        float ss, sg;
+        sums(1.0f, ss, sg);
+        float q = ss / n + a.eps;
+        const float pre = pre_of(q);
+        if (pre != 1.0f) {
+            sums(pre, ss, sg);
+            q = ss / n + a.eps * pre * pre;
+        }
+        const float r = 1.0f / sqrtf(q), m = sg * r / n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t c = (int64_t)(v * T + t) * 8;
+            if (c >= a.cols) break;
+            float h[8], y[8], w[8], d[8];
+            eh[v].values(h);
+            ey[v].values(y);
+            ew[v].values(w);
+            if (a.dh != nullptr) {
+                ed[v].values(d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = h[i] * pre * r;
+                dw[v][i] += y[i] * u;
+                d[i] = (y[i] * w[i] - u * m) * r * pre + d[i];
+            }
+            if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
+            if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
+        }
+    }
+    if (a.parts == nullptr || group >= a.groups) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        if (c < a.cols) put8<ZERO_F32>(a.parts + group * a.cols, c, a.cols, dw[v]);
+    }
+}
+
+// Rows that registers do not hold: each read twice, the parts of dw kept in memory.
+template <int DX, int DR>
+__global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
+    typedef typename Elem<DX>::type X;
+    typedef typename Elem<DR>::type R;
+    __shared__ float meet[kWide / 64];
+    const int64_t c0 = (int64_t)threadIdx.x * 8;
+    const float n = (float)a.cols;
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < a.tokens; row += a.groups) {
+        const X* const dy = (const X*)a.dy + row * a.lddy;
+        const R* const hr = (const R*)a.h + row * a.ldh;
+        auto sums = [&](float pre, float& ss, float& sg) {
+            ss = sg = 0.0f;
+            for (int64_t c = c0; c < a.cols; c += kWide * 8) {
+                Eight<DX> ey, ew;
+                Eight<DR> eh;
+                eh.load(hr, c, a.cols);
+                ey.load(dy, c, a.cols);
+                ew.load((const X*)a.w, c, a.cols);
+                float h[8], y[8], w[8];
+                eh.values(h);
+                ey.values(y);
+                ew.values(w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] *= pre;
+                    ss += h[i] * h[i];
+                    sg += y[i] * w[i] * h[i];
+                }
+            }
+            ss = row_sum<kWide>(ss, meet);
+            sg = row_sum<kWide>(sg, meet);
+        };
+        float ss, sg;
+        sums(1.0f, ss, sg);
+        float q = ss / n + a.eps;
+        const float pre = pre_of(q);
+        if (pre != 1.0f) {
+            sums(pre, ss, sg);
+            q = ss / n + a.eps * pre * pre;
+        }
+        const float r = 1.0f / sqrtf(q), m = sg * r / n;
+        for (int64_t c = c0; c < a.cols; c += kWide * 8) {
+            Eight<DX> ey, ew;
+            Eight<DR> eh, ed;
+            eh.load(hr, c, a.cols);
+            ey.load(dy, c, a.cols);
+            ew.load((const X*)a.w, c, a.cols);
+            if (a.dh != nullptr)
+                ed.load((const R*)a.dh + row * a.lddh, c, a.cols);
+            else
+                ed.zero();
+            float h[8], y[8], w[8], d[8], p[8];
+            eh.values(h);
+            ey.values(y);
+            ew.values(w);
+            ed.values(d);
+            float* const part = a.parts == nullptr ? nullptr : a.parts + (int64_t)blockIdx.x * a.cols;
+            if (part != nullptr) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = first || c + i >= a.cols ? 0.0f : part[c + i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = h[i] * pre * r;
+                p[i] += y[i] * u;
+                d[i] = (y[i] * w[i] - u * m) * r * pre + d[i];
+            }
+            if (part != nullptr) put8<ZERO_F32>(part, c, a.cols, p);
+            if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
+            if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
+        }
+        first = false;
+    }
+}
+
+// dw: the groups' parts added in order, 64 columns a workgroup, sixteen runs of groups.
+template <int DX>
+__global__ void __launch_bounds__(256) norm_dw_kernel(NormGradArgs a) {
+    __shared__ float sums[16][64];
+    const int lane = threadIdx.x % 16, run = threadIdx.x / 16;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane * 4;
+    const int each = (a.groups + 15) / 16, to = (run + 1) * each < a.groups ? (run + 1) * each : a.groups;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = run * each; g < to; ++g) {
+        const float* from = a.parts + g * a.cols + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < a.cols) s[i] += from[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[run][lane * 4 + i] = s[i];
+    __syncthreads();
+    const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < a.cols) {
+        float v = sums[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) v += sums[k][threadIdx.x];
+        ((typename Elem<DX>::type*)a.dw)[col] = from_float<DX>(v);
+    }
+}
+
+// ---------------------------------------------------------------- dropout
+// y = x / (1 - p) or 0 (+ residual).  Which elements stay is computed, not stored: element c of
+// row r takes sixteen bits of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", 2011) at the counter (c / 8, r, offset), whose four words serve
+// eight elements; it is dropped where they are below p 2^16.  The gradient is the same pass over dy.
+struct DropArgs {
+    const void *x, *residual;
+    int64_t ldx, ldr, ldy;
+    int64_t rows, cols;
+    void* y;
+    uint32_t key[2];
+    uint64_t offset;
+    const uint64_t* offset_dev;  // added to offset
+    uint32_t limit;              // p 2^16
+    float scale;
+    uint32_t groups;             // of eight in a row
+};
+
+__device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p = (uint64_t)c[0] * 0xD2511F53u, q = (uint64_t)c[2] * 0xCD9E8D57u;
+        c[0] = (uint32_t)(q >> 32) ^ c[1] ^ k0;
+        c[1] = (uint32_t)q;
+        c[2] = (uint32_t)(p >> 32) ^ c[3] ^ k1;
+        c[3] = (uint32_t)p;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) dropout_kernel(DropArgs a) {
+    typedef typename Elem<DT>::type T;
+    const uint64_t offset = a.offset + (a.offset_dev != nullptr ? *a.offset_dev : 0);
+    const uint64_t all = (uint64_t)a.rows * a.groups, step = (uint64_t)gridDim.x * 256;
+    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += step) {
+        const uint64_t row = at >> 32 ? at / a.groups : (uint32_t)at / a.groups;
+        const uint32_t group = (uint32_t)(at - row * a.groups);
+        const int64_t c = (int64_t)group * 8;
+        Eight<DT> ex, er;
+        ex.load((const T*)a.x + row * a.ldx, c, a.cols);
+        if (a.residual != nullptr) er.load((const T*)a.residual + row * a.ldr, c, a.cols);
+        uint32_t w[4] = {group, (uint32_t)row, (uint32_t)offset, (uint32_t)(offset >> 32)};
+        philox(w, a.key[0], a.key[1]);
+        float x[8], r[8];
+        ex.values(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t bits = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFF;
+            x[i] = bits >= a.limit ? x[i] * a.scale : 0.0f;
+        }
+        if (a.residual != nullptr) {
+            er.values(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] += r[i];
+        }
+        put8<DT>((T*)a.y + row * a.ldy, c, a.cols, x);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// f(x's type, residual's type) for the pairs in use.
+template <class F>
+int with_types(int32_t dx, int32_t dr, F f) {
+    typedef std::integral_constant<int, ZERO_F16> H;
+    typedef std::integral_constant<int, ZERO_BF16> B;
+    typedef std::integral_constant<int, ZERO_F32> S;
+    if (dx == ZERO_F16) return dr == ZERO_F32 ? f(H(), S()) : f(H(), H());
+    if (dx == ZERO_BF16) return dr == ZERO_F32 ? f(B(), S()) : f(B(), B());
+    return f(S(), S());
+}
+
+template <class F>
+int with_type(int32_t dt, F f) {
+    return with_types(dt, dt, [&](auto x, auto) { return f(x); });
+}
+
+template <int DX, int DR, bool MX>
+int norm_with(const NormArgs& a, hipStream_t s, const char* what) {
+    const int64_t n = MX ? padded(a.cols) : a.cols;
+    const unsigned one = (unsigned)a.tokens;
+    if (n <= 1024) return launch(norm_kernel<DX, DR, 64, 2, MX>, dim3((unsigned)ceil_div(a.tokens, 4)), 256, s, a, what);
+    if (n <= 4096) return launch(norm_kernel<DX, DR, 256, 2, MX>, dim3(one), 256, s, a, what);
+    if (n <= 8192) return launch(norm_kernel<DX, DR, 256, 4, MX>, dim3(one), 256, s, a, what);
+    if (n <= 32768) return launch(norm_kernel<DX, DR, 1024, 4, MX>, dim3(one), 1024, s, a, what);
+    return launch(norm_wide_kernel<DX, DR, MX>, dim3(one), kWide, s, a, what);
+}
+
+// The checks shared by the norm's two forms.
+int check_norm(const NormArgs& a, int32_t dx, int32_t dr, const char* what) {
+    int rc;
+    if (!valid_dtype(dx, true)) return fail(ZERO_EINVAL, "%s: unknown dtype", what);
+    if (a.residual != nullptr && dr != dx && dr != ZERO_F32)
+        return fail(ZERO_EINVAL, "%s: the residual has x's type or is fp32", what);
+    if (!(a.eps >= 0.0f && a.eps <= 3.4028235e38f)) return fail(ZERO_EINVAL, "%s: eps is finite and not negative", what);
+    if ((rc = check_sides(a.tokens, a.cols, what)) != ZERO_OK) return rc;
+    if (a.ldx < a.cols || (a.residual != nullptr && (a.ldr < a.cols || a.ldh < a.cols)))
+        return fail(ZERO_ERANGE, "%s: row stride below cols", what);
+    if (a.tokens == 0 || a.cols == 0) return ZERO_OK;
+    if (a.x == nullptr || a.w == nullptr) return fail(ZERO_EINVAL, "%s: null input", what);
+    if ((a.residual == nullptr) != (a.h == nullptr)) return fail(ZERO_EINVAL, "%s: a residual and its sum come together", what);
+    if (!aligned(a.x, elem_bytes(dx)) || !aligned(a.w, elem_bytes(dx)) || !aligned(a.residual, elem_bytes(dr)) ||
+        !aligned(a.h, elem_bytes(dr)))
+        return fail(ZERO_EALIGN, "%s: rows not aligned to their elements", what);
+    if (a.residual != nullptr) {
+        const Place h = values_at(a.h, dr, a.tokens, a.cols, a.ldh);
+        const bool same = a.h == a.residual && a.ldh == a.ldr;  // the sum in the residual's place
+        if (overlap(h, values_at(a.x, dx, a.tokens, a.cols, a.ldx)) || overlap(h, values_at(a.w, dx, 1, a.cols, a.cols)) ||
+            (!same && overlap(h, values_at(a.residual, dr, a.tokens, a.cols, a.ldr))))
+            return fail(ZERO_EINVAL, "%s: the sum overlaps an input", what);
+    }
+    return ZERO_OK;
+}
+
+// Groups of rows that a gradient call sums dw over: workgroups, or waves where a wave takes a row.
+int64_t grad_groups(int64_t tokens, int64_t cols) {
+    const int64_t most = cols <= 1024 ? 4 * kGradGroups : kGradGroups;
+    return tokens < most ? tokens : most;
+}
+
+template <int DX, int DR>
+int norm_grad_with(const NormGradArgs& a, hipStream_t s, const char* what) {
+    const unsigned one = (unsigned)a.groups;
+    if (a.cols <= 1024)
+        return launch(norm_grad_kernel<DX, DR, 64, 2>, dim3((unsigned)ceil_div(a.groups, 4)), 256, s, a, what);
+    if (a.cols <= 4096) return launch(norm_grad_kernel<DX, DR, 256, 2>, dim3(one), 256, s, a, what);
+    if (a.cols <= 8192) return launch(norm_grad_kernel<DX, DR, 256, 4>, dim3(one), 256, s, a, what);
+    if (a.cols <= 32768) return launch(norm_grad_kernel<DX, DR, 1024, 4>, dim3(one), 1024, s, a, what);
+    return launch(norm_grad_wide_kernel<DX, DR>, dim3(one), kWide, s, a, what);
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_rms_norm(const void* x, int32_t dtype, int64_t ldx, const void* residual, int32_t residual_dtype, int64_t ldr,
+                  const void* w, int64_t tokens, int64_t cols, float eps, void* y, int64_t ldy, void* h, int64_t ldh,
+                  void* stream) {
+    const char* what = "zero_rms_norm";
+    const int32_t dr = residual == nullptr ? dtype : residual_dtype;
+    const NormArgs a{x, residual, w, ldx, ldr, tokens, cols, eps, y, h, ldy, ldh, nullptr, nullptr};
+    int rc;
+    if ((rc = check_norm(a, dtype, dr, what)) != ZERO_OK) return rc;
+    if (ldy < cols) return fail(ZERO_ERANGE, "%s: row stride below cols", what);
+    if (tokens == 0 || cols == 0) return ok();
+    if (y == nullptr) return fail(ZERO_EINVAL, "%s: null result", what);
+    if (!aligned(y, elem_bytes(dtype))) return fail(ZERO_EALIGN, "%s: rows not aligned to their elements", what);
+    const Place to = values_at(y, dtype, tokens, cols, ldy);
+    const bool same = y == x && ldy == ldx;  // the result in x's place
+    if ((!same && overlap(to, values_at(x, dtype, tokens, cols, ldx))) || overlap(to, values_at(w, dtype, 1, cols, cols)) ||
+        (residual != nullptr && overlap(to, values_at(residual, dr, tokens, cols, ldr))) ||
+        (h != nullptr && overlap(to, values_at(h, dr, tokens, cols, ldh))))
+        return fail(ZERO_EINVAL, "%s: the result overlaps an input or the sum", what);
+    return with_types(dtype, dr, [&](auto dx, auto dr_) {
+        return norm_with<decltype(dx)::value, decltype(dr_)::value, false>(a, (hipStream_t)stream, what);
+    });
+}
+
+int zero_rms_norm_mx8(const void* x, int32_t dtype, int64_t ldx, const void* residual, int32_t residual_dtype, int64_t ldr,
+                      const void* w, int64_t tokens, int64_t cols, float eps, void* codes, void* scales, void* h,
+                      int64_t ldh, void* stream) {
+    const char* what = "zero_rms_norm_mx8";
+    const int32_t dr = residual == nullptr ? dtype : residual_dtype;
+    const NormArgs a{x, residual, w, ldx, ldr, tokens, cols, eps, nullptr, h, 0, ldh, (uint8_t*)codes, (uint8_t*)scales};
+    int rc;
+    if ((rc = check_norm(a, dtype, dr, what)) != ZERO_OK) return rc;
+    if (tokens == 0 || cols == 0) return ok();
+    if (codes == nullptr || scales == nullptr) return fail(ZERO_EINVAL, "%s: null result", what);
+    if (!aligned(codes, 16) || !aligned(scales, 16)) return fail(ZERO_EALIGN, "%s: codes or scales not 16-byte aligned", what);
+    const Place to[2] = {codes8_at(codes, tokens, cols), scales_at(scales, tokens, cols)};
+    for (const Place& p : to)
+        if (overlap(p, values_at(x, dtype, tokens, cols, ldx)) || overlap(p, values_at(w, dtype, 1, cols, cols)) ||
+            (residual != nullptr && (overlap(p, values_at(residual, dr, tokens, cols, ldr)) ||
+                                     overlap(p, values_at(h, dr, tokens, cols, ldh)))))
+            return fail(ZERO_EINVAL, "%s: codes or scales overlap an input or the sum", what);
+    return with_types(dtype, dr, [&](auto dx, auto dr_) {
+        return norm_with<decltype(dx)::value, decltype(dr_)::value, true>(a, (hipStream_t)stream, what);
+    });
+}
+
+size_t zero_rms_norm_grad_workspace_bytes(int64_t tokens, int64_t cols) {
+    if (tokens <= 0 || cols <= 0 || tokens > kMaxSide || cols > kMaxSide) return 0;
+    return (size_t)(grad_groups(tokens, cols) * cols * 4);
+}
+
+int zero_rms_norm_grad(const void* dy, int64_t lddy, const void* h, int32_t h_dtype, int64_t ldh, const void* w,
+                       int32_t dtype, const void* dh, int64_t lddh, int64_t tokens, int64_t cols, float eps, void* dx,
+                       int64_t lddx, void* dr, int64_t lddr, void* dw, void* ws, size_t ws_bytes, void* stream) {
+    const char* what = "zero_rms_norm_grad";
+    int rc;
+    if (!valid_dtype(dtype, true)) return fail(ZERO_EINVAL, "%s: unknown dtype", what);
+    if (h_dtype != dtype && h_dtype != ZERO_F32) return fail(ZERO_EINVAL, "%s: the sum has x's type or is fp32", what);
+    if (!(eps >= 0.0f && eps <= 3.4028235e38f)) return fail(ZERO_EINVAL, "%s: eps is finite and not negative", what);
+    if ((rc = check_sides(tokens, cols, what)) != ZERO_OK) return rc;
+    if (lddy < cols || ldh < cols || (dh != nullptr && lddh < cols) || (dx != nullptr && lddx < cols) ||
+        (dr != nullptr && lddr < cols))
+        return fail(ZERO_ERANGE, "%s: row stride below cols", what);
+    if (cols == 0 || (dx == nullptr && dr == nullptr && dw == nullptr)) return ok();
+    if (tokens > 0 && (dy == nullptr || h == nullptr || w == nullptr)) return fail(ZERO_EINVAL, "%s: null input", what);
+    const size_t size = elem_bytes(dtype), size_h = elem_bytes(h_dtype);
+    if (!aligned(dy, size) || !aligned(h, size_h) || !aligned(w, size) || !aligned(dh, size_h) || !aligned(dx, size) ||
+        !aligned(dr, size_h) || !aligned(dw, size))
+        return fail(ZERO_EALIGN, "%s: rows not aligned to their elements", what);
+    const Place from[4] = {values_at(dy, dtype, tokens, cols, lddy), values_at(h, h_dtype, tokens, cols, ldh),
+                           values_at(dh, h_dtype, tokens, cols, lddh), values_at(w, dtype, 1, cols, cols)};
+    const Place to[3] = {values_at(dx, dtype, tokens, cols, lddx), values_at(dr, h_dtype, tokens, cols, lddr),
+                         values_at(dw, dtype, 1, cols, cols)};
+    for (const Place& p : to)
+        for (const Place& f : from)
+            if (overlap(p, f)) return fail(ZERO_EINVAL, "%s: a gradient overlaps an input", what);
+    NormGradArgs a{dy, h, w, dh, lddy, ldh, lddh, tokens, cols, eps, dx, dr, lddx, lddr, (float*)ws, dw,
+                   (int)grad_groups(tokens, cols)};
+    const hipStream_t s = (hipStream_t)stream;
+    if (dw != nullptr) {
+        const size_t need = zero_rms_norm_grad_workspace_bytes(tokens, cols);
+        if (need > 0 && ws == nullptr) return fail(ZERO_EINVAL, "%s: null workspace", what);
+        if (!aligned(ws, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", what);
+        if (ws_bytes < need) return fail(ZERO_ESPACE, "%s: workspace %zu bytes, needs %zu", what, ws_bytes, need);
+    } else {
+        a.parts = nullptr;
+    }
+    if (tokens > 0) {
+        rc = with_types(dtype, h_dtype, [&](auto x, auto r) {
+            return norm_grad_with<decltype(x)::value, decltype(r)::value>(a, s, what);
+        });
+        if (rc != ZERO_OK) return rc;
+    }
+    if (dw == nullptr) return ok();
+    return with_type(dtype, [&](auto x) {
+        return launch(norm_dw_kernel<decltype(x)::value>, dim3((unsigned)ceil_div(cols, 64)), 256, s, a, what);
+    });
+}
+
+int zero_dropout(const void* x, int32_t dtype, int64_t ldx, const void* residual, int64_t ldr, int64_t rows, int64_t cols,
+                 double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, void* y, int64_t ldy, void* stream) {
+    const char* what = "zero_dropout";
+    if (!valid_dtype(dtype, true)) return fail(ZERO_EINVAL, "%s: unknown dtype", what);
+    if (!(p >= 0.0 && p <= 1.0)) return fail(ZERO_EINVAL, "%s: p is not in [0, 1]", what);
+    // a counter has 32 bits for a row and 32 for a group of eight in it
+    if (rows < 0 || cols < 0 || rows > (int64_t(1) << 32) || cols > (int64_t(1) << 34) ||
+        (cols > 0 && rows > (int64_t(1) << 40) / cols))
+        return fail(ZERO_ERANGE, "%s: %lld x %lld out of range", what, (long long)rows, (long long)cols);
+    if (ldx < cols || ldy < cols || (residual != nullptr && ldr < cols))
+        return fail(ZERO_ERANGE, "%s: row stride below cols", what);
+    if (rows == 0 || cols == 0) return ok();
+    if (x == nullptr || y == nullptr) return fail(ZERO_EINVAL, "%s: null rows", what);
+    if (!aligned(x, elem_bytes(dtype)) || !aligned(y, elem_bytes(dtype)) || !aligned(residual, elem_bytes(dtype)) ||
+        !aligned(offset_dev, 8))
+        return fail(ZERO_EALIGN, "%s: rows not aligned to their elements, or the offset not to 8 bytes", what);
+    const Place to = values_at(y, dtype, rows, cols, ldy);
+    if ((!(y == x && ldy == ldx) && overlap(to, values_at(x, dtype, rows, cols, ldx))) ||
+        (residual != nullptr && !(y == residual && ldy == ldr) && overlap(to, values_at(residual, dtype, rows, cols, ldr))) ||
+        overlap(to, Place(offset_dev, 8)))
+        return fail(ZERO_EINVAL, "%s: the result overlaps an input", what);
+    const uint32_t limit = (uint32_t)__builtin_rint(p * 65536.0);
+    const DropArgs a{x, residual, ldx, ldr, ldy, rows, cols, y, {(uint32_t)seed, (uint32_t)(seed >> 32)}, offset, offset_dev,
+                     limit, limit < 65536 ? (float)(65536.0 / (65536.0 - limit)) : 0.0f, (uint32_t)ceil_div(cols, 8)};
+    const int64_t wgs = ceil_div(rows * ceil_div(cols, 8), 256);
+    const dim3 grid((unsigned)(wgs < 65536 ? wgs : 65536));
+    return with_type(dtype, [&](auto t) {
+        return launch(dropout_kernel<decltype(t)::value>, grid, 256, (hipStream_t)stream, a, what);
+    });
+}
+
+}  // extern "C"

@@ -219,37 +219,39 @@ class MuonShardStep(ShardStep):
 
 
 # ----------------------------------------------------------------------------- MXFP4
-class MX4:
-    """A rows x cols matrix in MXFP4, blocks of 32 along its rows: codes
-    [rows, P / 2] and scales [rows, P / 32] bytes, P = cols rounded up to a multiple
-    of 128 (the padding zero)."""
+class _Blocks:
+    """Microscaled rows: codes [rows, P CODE / 128] and scales [rows, P / 32] bytes, P = cols rounded
+    up to a multiple of 128, CODE the bytes of 128 codes."""
 
     __slots__ = ("rows", "cols", "_codes", "_scales", "_both", "_places")
+    CODE = 0
 
     def __init__(self, codes, scales, rows: int, cols: int):
         p = (cols + 127) // 128 * 128
-        for t, width in ((codes, p // 2), (scales, p // 32)):
+        wide = p * self.CODE // 128
+        for t, width in ((codes, wide), (scales, p // 32)):
             if t.dtype != _bytes or t.numel() != rows * width or not t.is_contiguous():
-                raise ValueError(f"{rows} x {cols} takes {rows * p // 2} contiguous bytes of codes and "
+                raise ValueError(f"{rows} x {cols} takes {rows * wide} contiguous bytes of codes and "
                                  f"{rows * p // 32} of scales")
         self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
         self._both, self._places = None, (codes.data_ptr(), scales.data_ptr())
 
-    @staticmethod
-    def alloc(rows: int, cols: int, device) -> "MX4":
+    @classmethod
+    def alloc(cls, rows: int, cols: int, device):
         """Codes and scales in one new buffer."""
         blocks = rows * ((cols + 127) // 128)
-        q = MX4.__new__(MX4)
+        q = cls.__new__(cls)
         q.rows, q.cols, q._codes = rows, cols, None
-        q._both = both = _empty(68 * blocks, dtype=_bytes, device=device)
+        q._both = both = _empty((cls.CODE + 4) * blocks, dtype=_bytes, device=device)
         at = both.data_ptr()
-        q._places = (at, at + 64 * blocks)
+        q._places = (at, at + cls.CODE * blocks)
         return q
 
     def _split(self):
         n = self.rows * ((self.cols + 127) // 128)
-        self._codes = self._both[:64 * n].view(self.rows, -1) if n else self._both.view(self.rows, 0)
-        self._scales = self._both[64 * n:].view(self.rows, -1) if n else self._codes
+        at = self.CODE * n
+        self._codes = self._both[:at].view(self.rows, -1) if n else self._both.view(self.rows, 0)
+        self._scales = self._both[at:].view(self.rows, -1) if n else self._codes
 
     @property
     def codes(self):
@@ -269,6 +271,15 @@ class MX4:
 
     def _index(self) -> int:
         return _gpu(self._codes, self._scales) if self._both is None else _gpu(self._both)
+
+
+class MX4(_Blocks):
+    """A rows x cols matrix in MXFP4, blocks of 32 along its rows: codes
+    [rows, P / 2] and scales [rows, P / 32] bytes, P = cols rounded up to a multiple
+    of 128 (the padding zero)."""
+
+    __slots__ = ()
+    CODE = 64
 
 
 def _matrix(x):
