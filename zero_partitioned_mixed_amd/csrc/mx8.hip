@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads) mx8_quantize_kernel(Quant8Args a) {
     Eight<DT> e[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-        if (r0 + 16 * i < a.rows) e[i].load((const T*)a.src + (r0 + 16 * i) * a.ld, c, a.cols);
+        if (r0 + 16 * i < a.rows) e[i].fetch((const T*)a.src + (r0 + 16 * i) * a.ld, c, a.cols);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int64_t r = r0 + 16 * i;
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
         const int pieces = (int)(g.m * p / 8);
         auto read = [&](int t, Eight<DTA>& e) {
             const uint32_t r = (uint32_t)t / (p / 8), c = ((uint32_t)t - r * (p / 8)) * 8;
-            e.load((const T*)f.values + r * f.lda, c, f.k);
+            e.fetch((const T*)f.values + r * f.lda, c, f.k);
         };
         auto put = [&](int t, const Eight<DTA>& e) {  // whole groups of four lanes
             const uint32_t r = (uint32_t)t / (p / 8), c = ((uint32_t)t - r * (p / 8)) * 8;

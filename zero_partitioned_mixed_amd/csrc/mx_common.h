@@ -98,6 +98,48 @@ struct Eight {
             __builtin_memcpy(v, x, sizeof(v));
         }
     }
+    // The same with a row's last elements taken from its last whole vector, moved down: one load instead of
+    // eight, whose registers every kernel that holds several such vectors would pay for.
+    __device__ __forceinline__ void fetch(const T* row, int64_t c, int64_t cols) {
+        if (c + 8 <= cols) {
+            __builtin_memcpy(v, row + c, sizeof(v));
+        } else if (c >= cols) {
+            zero();
+        } else if (cols >= 8) {
+            __builtin_memcpy(v, row + cols - 8, sizeof(v));
+            down((int)(c + 8 - cols));
+        } else {  // rows of fewer than eight
+            zero();
+#pragma unroll 1
+            for (int64_t i = cols - 1; i >= c; --i) up(row[i]);
+        }
+    }
+    // The elements `by` (1 to 7) places lower, zeros behind them.
+    __device__ __forceinline__ void down(int by) {
+        if constexpr (kVecs == 1) {
+            unsigned __int128 w;
+            __builtin_memcpy(&w, v, sizeof(w));
+            w >>= 16 * by;
+            __builtin_memcpy(v, &w, sizeof(w));
+        } else {
+            uint32_t d[8];
+            __builtin_memcpy(d, v, sizeof(d));
+#pragma unroll
+            for (int step = 1; step <= 4; step *= 2)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = by & step ? (i + step < 8 ? d[i + step] : 0u) : d[i];
+            __builtin_memcpy(v, d, sizeof(d));
+        }
+    }
+    // x first, the elements one place higher.
+    __device__ __forceinline__ void up(T x) {
+        T d[8];
+        __builtin_memcpy(d, v, sizeof(d));
+#pragma unroll
+        for (int i = 7; i > 0; --i) d[i] = d[i - 1];
+        d[0] = x;
+        __builtin_memcpy(v, d, sizeof(d));
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = u32x4{0, 0, 0, 0};

@@ -15,21 +15,53 @@ namespace {
 constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p64f;
 __device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-80f ? kPreUp : 1.0f; }
 
-// The sum over the T lanes of a row, T = 64 or a whole workgroup, the same bits in every lane.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* meet) {
+// The sums of N values over the T lanes of a row, T = 64 or a whole workgroup, the same bits in every lane.
+// One barrier each: consecutive calls take turns with the places in LDS.
+template <int T, int N>
+struct RowSums {
+    static constexpr int kWaves = T / 64;
+    float at[2][N][kWaves];
+};
+template <int T, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], RowSums<T, N>& meet, int turn) {
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    for (int d = 1; d < 64; d *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
     if constexpr (T > 64) {
-        __syncthreads();  // the one before has been read
-        if ((threadIdx.x & 63) == 0) meet[threadIdx.x / 64] = v;
-        __syncthreads();
-        v = meet[0];
+        if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-        for (int w = 1; w < T / 64; ++w) v += meet[w];
+            for (int i = 0; i < N; ++i) meet.at[turn & 1][i][threadIdx.x / 64] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = meet.at[turn & 1][i][0];
+#pragma unroll
+            for (int w = 1; w < T / 64; ++w) v[i] += meet.at[turn & 1][i][w];
+        }
     }
-    return v;
 }
+
+// The sum of eight squares of h times pre, in pairs.
+__device__ __forceinline__ float squares8(const float* h) {
+    return ((h[0] * h[0] + h[1] * h[1]) + (h[2] * h[2] + h[3] * h[3])) +
+           ((h[4] * h[4] + h[5] * h[5]) + (h[6] * h[6] + h[7] * h[7]));
+}
+
+// 1 / sqrt(q) as the sum of two fp32 numbers: results rounded to 8 bits next to a border, and the
+// last bits of fp32 ones, show the rounding of one.
+struct Root {
+    float r, rest;
+    __device__ __forceinline__ explicit Root(float q) {
+        r = 1.0f / sqrtf(q);
+        // one Newton step: r (1 - q r^2) / 2, q r^2 - 1 with its rounding undone by fused products
+        const float p = q * r, e = fmaf(q, r, -p);
+        const float one = fmaf(p, r, -1.0f) + e * r;
+        rest = q > 0.0f && q < 3.0e38f ? -0.5f * r * one : 0.0f;
+    }
+    __device__ __forceinline__ float times(float x) const { return fmaf(x, r, x * rest); }
+};
 
 struct NormArgs {
     const void *x, *residual, *w;
@@ -76,7 +108,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
     constexpr int kRows = T < 256 ? 256 / T : 1;
-    __shared__ float meet[T > 64 ? T / 64 : 1];
+    __shared__ RowSums<T, 1> meet;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
     if (row >= a.tokens) return;  // whole waves; with T > 64 none
     const int t = threadIdx.x % T;
@@ -88,12 +120,12 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
         if (c < a.cols) {
-            ex[v].load((const X*)a.x + row * a.ldx, c, a.cols);
-            if (a.residual != nullptr) er[v].load((const R*)a.residual + row * a.ldr, c, a.cols);
-            ew[v].load((const X*)a.w, c, a.cols);
+            ex[v].fetch((const X*)a.x + row * a.ldx, c, a.cols);
+            if (a.residual != nullptr) er[v].fetch((const R*)a.residual + row * a.ldr, c, a.cols);
+            ew[v].fetch((const X*)a.w, c, a.cols);
         }
     }
-    float ss = 0.0f;
+    float ss[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
@@ -103,24 +135,24 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[v][i] = 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss += h[v][i] * h[v][i];
+        ss[0] += squares8(h[v]);
     }
     const float n = (float)a.cols;
-    float q = row_sum<T>(ss, meet) / n + a.eps;
+    row_sums<T, 1>(ss, meet, 0);
+    float q = ss[0] / n + a.eps;
     const float pre = pre_of(q);
     if (pre != 1.0f) {
-        ss = 0.0f;
+        ss[0] = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[v][i] *= pre;
-                ss += h[v][i] * h[v][i];
-            }
-        q = row_sum<T>(ss, meet) / n + a.eps * pre * pre;
+            for (int i = 0; i < 8; ++i) h[v][i] *= pre;
+            ss[0] += squares8(h[v]);
+        }
+        row_sums<T, 1>(ss, meet, 1);
+        q = ss[0] / n + a.eps * pre * pre;
     }
-    const float r = 1.0f / sqrtf(q);
+    const Root root(q);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
@@ -134,7 +166,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            h[v][i] = h[v][i] * r * w[i];
+            h[v][i] = root.times(h[v][i] * w[i]);
             if (MX && c + i >= a.cols) h[v][i] = 0.0f;  // also where r is not finite
         }
         norm_out8<DX, MX>(a, row, c, h[v]);
@@ -147,57 +179,56 @@ template <int DX, int DR, bool MX>
 __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    __shared__ float meet[kWide / 64];
+    __shared__ RowSums<kWide, 1> meet;
     const int64_t row = blockIdx.x, end = MX ? padded(a.cols) : a.cols;
     const int64_t c0 = (int64_t)threadIdx.x * 8;
     const X* const x = (const X*)a.x + row * a.ldx;
     const R* const hr = (const R*)a.h + row * a.ldh;  // what this lane wrote
     auto sum_of = [&](float pre, bool first) {
-        float ss = 0.0f;
+        float ss[1] = {0.0f};
         for (int64_t c = c0; c < a.cols; c += kWide * 8) {
             float h[8];
             if (first || a.residual == nullptr) {
                 Eight<DX> ex;
                 Eight<DR> er;
-                ex.load(x, c, a.cols);
-                if (a.residual != nullptr) er.load((const R*)a.residual + row * a.ldr, c, a.cols);
+                ex.fetch(x, c, a.cols);
+                if (a.residual != nullptr) er.fetch((const R*)a.residual + row * a.ldr, c, a.cols);
                 sum8<DX, DR>(a, row, c, ex, er, h);
             } else {
                 Eight<DR> eh;
-                eh.load(hr, c, a.cols);
+                eh.fetch(hr, c, a.cols);
                 eh.values(h);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[i] *= pre;
-                ss += h[i] * h[i];
-            }
+            for (int i = 0; i < 8; ++i) h[i] *= pre;
+            ss[0] += squares8(h);
         }
-        return row_sum<kWide>(ss, meet);
+        row_sums<kWide, 1>(ss, meet, first);
+        return ss[0];
     };
     const float n = (float)a.cols;
     float q = sum_of(1.0f, true) / n + a.eps;
     const float pre = pre_of(q);
     if (pre != 1.0f) q = sum_of(pre, false) / n + a.eps * pre * pre;
-    const float r = 1.0f / sqrtf(q);
+    const Root root(q);
     for (int64_t c = c0; c < end; c += kWide * 8) {
         float h[8], w[8];
         if (c < a.cols) {
             if (a.residual == nullptr) {
                 Eight<DX> ex;
-                ex.load(x, c, a.cols);
+                ex.fetch(x, c, a.cols);
                 ex.values(h);
             } else {
                 Eight<DR> eh;
-                eh.load(hr, c, a.cols);
+                eh.fetch(hr, c, a.cols);
                 eh.values(h);
             }
             Eight<DX> ew;
-            ew.load((const X*)a.w, c, a.cols);
+            ew.fetch((const X*)a.w, c, a.cols);
             ew.values(w);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? h[i] * pre * r * w[i] : 0.0f;
+        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * pre * w[i]) : 0.0f;
         norm_out8<DX, MX>(a, row, c, h);
     }
 }
@@ -222,84 +253,100 @@ struct NormGradArgs {
 
 constexpr int kGradGroups = 512;
 
+// dh' and u of eight elements.
+__device__ __forceinline__ void norm_grad8(const float* h, const float* y, const float* w, float pre, float r, float m, float* u,
+                                           float* d) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        u[i] = h[i] * pre * r;
+        d[i] = (y[i] * w[i] - u[i] * m) * r * pre + d[i];
+    }
+}
+
+// The sums of squares and of g h over eight elements times pre.
+__device__ __forceinline__ void norm_sums8(const float* h, const float* y, const float* w, float pre, float (&s)[2]) {
+    float p[8], g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i] = h[i] * pre;
+        g[i] = y[i] * w[i] * p[i];
+    }
+    s[0] += squares8(p);
+    s[1] += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
+}
+
 template <int DX, int DR, int T, int V>
 __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_grad_kernel(NormGradArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
     constexpr int kRows = T < 256 ? 256 / T : 1;
-    __shared__ float meet[T > 64 ? T / 64 : 1];
+    __shared__ RowSums<T, 2> meet;
     const int t = threadIdx.x % T;
     const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
     const float n = (float)a.cols;
+    struct Row {
+        Eight<DX> y[V];
+        Eight<DR> h[V], d[V];
+        __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int t) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int64_t c = (int64_t)(v * T + t) * 8;
+                if (c >= a.cols) break;
+                h[v].fetch((const R*)a.h + row * a.ldh, c, a.cols);
+                y[v].fetch((const X*)a.dy + row * a.lddy, c, a.cols);
+                if (a.dh != nullptr) d[v].fetch((const R*)a.dh + row * a.lddh, c, a.cols);
+            }
+        }
+    };
     Eight<DX> ew[V];
     float dw[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
-        if (c < a.cols) ew[v].load((const X*)a.w, c, a.cols);
+        if (c < a.cols) ew[v].fetch((const X*)a.w, c, a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
     }
+    Row next;
+    if (group < a.tokens) next.load(a, group, t);
+    int turn = 0;
     for (int64_t row = group; row < a.tokens; row += a.groups) {
-        Eight<DX> ey[V];
-        Eight<DR> eh[V], ed[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * T + t) * 8;
-            if (c < a.cols) {
-                eh[v].load((const R*)a.h + row * a.ldh, c, a.cols);
-                ey[v].load((const X*)a.dy + row * a.lddy, c, a.cols);
-                if (a.dh != nullptr) ed[v].load((const R*)a.dh + row * a.lddh, c, a.cols);
-            }
-        }
-        auto sums = [&](float pre, float& ss, float& sg) {
-            ss = sg = 0.0f;
+        const Row e = next;  // the next row is on its way while this one's sums meet
+        if (row + a.groups < a.tokens) next.load(a, row + a.groups, t);
+        auto sums = [&](float pre, float (&s)[2]) {
+            s[0] = s[1] = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if ((int64_t)(v * T + t) * 8 >= a.cols) break;
                 float h[8], y[8], w[8];
-                eh[v].values(h);
-                ey[v].values(y);
+                e.h[v].values(h);
+                e.y[v].values(y);
                 ew[v].values(w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    h[i] *= pre;
-                    ss += h[i] * h[i];
-                    sg += y[i] * w[i] * h[i];
-                }
+                norm_sums8(h, y, w, pre, s);
             }
-            ss = row_sum<T>(ss, meet);
-            sg = row_sum<T>(sg, meet);
+            row_sums<T, 2>(s, meet, turn++);
         };
-        float ss, sg;
-        sums(1.0f, ss, sg);
-        float q = ss / n + a.eps;
+        float s[2];
+        sums(1.0f, s);
+        float q = s[0] / n + a.eps;
         const float pre = pre_of(q);
         if (pre != 1.0f) {
-            sums(pre, ss, sg);
-            q = ss / n + a.eps * pre * pre;
+            sums(pre, s);
+            q = s[0] / n + a.eps * pre * pre;
         }
-        const float r = 1.0f / sqrtf(q), m = sg * r / n;
+        const float r = 1.0f / sqrtf(q), m = s[1] * r / n;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int64_t c = (int64_t)(v * T + t) * 8;
             if (c >= a.cols) break;
-            float h[8], y[8], w[8], d[8];
-            eh[v].values(h);
-            ey[v].values(y);
+            float h[8], y[8], w[8], u[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            e.h[v].values(h);
+            e.y[v].values(y);
             ew[v].values(w);
-            if (a.dh != nullptr) {
-                ed[v].values(d);
-            } else {
+            if (a.dh != nullptr) e.d[v].values(d);
+            norm_grad8(h, y, w, pre, r, m, u, d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = h[i] * pre * r;
-                dw[v][i] += y[i] * u;
-                d[i] = (y[i] * w[i] - u * m) * r * pre + d[i];
-            }
+            for (int i = 0; i < 8; ++i) dw[v][i] += y[i] * u[i];
             if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
             if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
         }
@@ -317,55 +364,50 @@ template <int DX, int DR>
 __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    __shared__ float meet[kWide / 64];
+    __shared__ RowSums<kWide, 2> meet;
     const int64_t c0 = (int64_t)threadIdx.x * 8;
     const float n = (float)a.cols;
     bool first = true;
+    int turn = 0;
     for (int64_t row = blockIdx.x; row < a.tokens; row += a.groups) {
         const X* const dy = (const X*)a.dy + row * a.lddy;
         const R* const hr = (const R*)a.h + row * a.ldh;
-        auto sums = [&](float pre, float& ss, float& sg) {
-            ss = sg = 0.0f;
+        auto sums = [&](float pre, float (&s)[2]) {
+            s[0] = s[1] = 0.0f;
             for (int64_t c = c0; c < a.cols; c += kWide * 8) {
                 Eight<DX> ey, ew;
                 Eight<DR> eh;
-                eh.load(hr, c, a.cols);
-                ey.load(dy, c, a.cols);
-                ew.load((const X*)a.w, c, a.cols);
+                eh.fetch(hr, c, a.cols);
+                ey.fetch(dy, c, a.cols);
+                ew.fetch((const X*)a.w, c, a.cols);
                 float h[8], y[8], w[8];
                 eh.values(h);
                 ey.values(y);
                 ew.values(w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    h[i] *= pre;
-                    ss += h[i] * h[i];
-                    sg += y[i] * w[i] * h[i];
-                }
+                norm_sums8(h, y, w, pre, s);
             }
-            ss = row_sum<kWide>(ss, meet);
-            sg = row_sum<kWide>(sg, meet);
+            row_sums<kWide, 2>(s, meet, turn++);
         };
-        float ss, sg;
-        sums(1.0f, ss, sg);
-        float q = ss / n + a.eps;
+        float s[2];
+        sums(1.0f, s);
+        float q = s[0] / n + a.eps;
         const float pre = pre_of(q);
         if (pre != 1.0f) {
-            sums(pre, ss, sg);
-            q = ss / n + a.eps * pre * pre;
+            sums(pre, s);
+            q = s[0] / n + a.eps * pre * pre;
         }
-        const float r = 1.0f / sqrtf(q), m = sg * r / n;
+        const float r = 1.0f / sqrtf(q), m = s[1] * r / n;
         for (int64_t c = c0; c < a.cols; c += kWide * 8) {
             Eight<DX> ey, ew;
             Eight<DR> eh, ed;
-            eh.load(hr, c, a.cols);
-            ey.load(dy, c, a.cols);
-            ew.load((const X*)a.w, c, a.cols);
+            eh.fetch(hr, c, a.cols);
+            ey.fetch(dy, c, a.cols);
+            ew.fetch((const X*)a.w, c, a.cols);
             if (a.dh != nullptr)
-                ed.load((const R*)a.dh + row * a.lddh, c, a.cols);
+                ed.fetch((const R*)a.dh + row * a.lddh, c, a.cols);
             else
                 ed.zero();
-            float h[8], y[8], w[8], d[8], p[8];
+            float h[8], y[8], w[8], u[8], d[8], p[8];
             eh.values(h);
             ey.values(y);
             ew.values(w);
@@ -375,12 +417,9 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[i] = first || c + i >= a.cols ? 0.0f : part[c + i];
             }
+            norm_grad8(h, y, w, pre, r, m, u, d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = h[i] * pre * r;
-                p[i] += y[i] * u;
-                d[i] = (y[i] * w[i] - u * m) * r * pre + d[i];
-            }
+            for (int i = 0; i < 8; ++i) p[i] += y[i] * u[i];
             if (part != nullptr) put8<ZERO_F32>(part, c, a.cols, p);
             if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
             if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
@@ -389,28 +428,37 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
     }
 }
 
-// dw: the groups' parts added in order, 64 columns a workgroup, sixteen runs of groups.
+// dw: the groups' parts added in order, 16 columns a workgroup, 64 runs of groups.
 template <int DX>
 __global__ void __launch_bounds__(256) norm_dw_kernel(NormGradArgs a) {
-    __shared__ float sums[16][64];
-    const int lane = threadIdx.x % 16, run = threadIdx.x / 16;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane * 4;
-    const int each = (a.groups + 15) / 16, to = (run + 1) * each < a.groups ? (run + 1) * each : a.groups;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    __shared__ float sums[64][17];
+    const int lane = threadIdx.x % 4, run = threadIdx.x / 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + lane * 4;
+    const int each = (a.groups + 63) / 64, to = (run + 1) * each < a.groups ? (run + 1) * each : a.groups;
+    const bool whole = c + 4 <= a.cols && a.cols % 4 == 0;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
     for (int g = run * each; g < to; ++g) {
         const float* from = a.parts + g * a.cols + c;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (whole) {
+            v = *(const f32x4*)from;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < a.cols) s[i] += from[i];
+            for (int i = 0; i < 4; ++i)
+                if (c + i < a.cols) v[i] = from[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += v[i];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[run][lane * 4 + i] = s[i];
     __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && col < a.cols) {
+    const int64_t col = (int64_t)blockIdx.x * 16 + threadIdx.x;
+    if (threadIdx.x < 16 && col < a.cols) {
         float v = sums[0][threadIdx.x];
 #pragma unroll
-        for (int k = 1; k < 16; ++k) v += sums[k][threadIdx.x];
+        for (int k = 1; k < 64; ++k) v += sums[k][threadIdx.x];
         ((typename Elem<DX>::type*)a.dw)[col] = from_float<DX>(v);
     }
 }
@@ -456,8 +504,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(DropArgs a) {
         const uint32_t group = (uint32_t)(at - row * a.groups);
         const int64_t c = (int64_t)group * 8;
         Eight<DT> ex, er;
-        ex.load((const T*)a.x + row * a.ldx, c, a.cols);
-        if (a.residual != nullptr) er.load((const T*)a.residual + row * a.ldr, c, a.cols);
+        ex.fetch((const T*)a.x + row * a.ldx, c, a.cols);
+        if (a.residual != nullptr) er.fetch((const T*)a.residual + row * a.ldr, c, a.cols);
         uint32_t w[4] = {group, (uint32_t)row, (uint32_t)offset, (uint32_t)(offset >> 32)};
         philox(w, a.key[0], a.key[1]);
         float x[8], r[8];
@@ -499,8 +547,8 @@ int norm_with(const NormArgs& a, hipStream_t s, const char* what) {
     const unsigned one = (unsigned)a.tokens;
     if (n <= 1024) return launch(norm_kernel<DX, DR, 64, 2, MX>, dim3((unsigned)ceil_div(a.tokens, 4)), 256, s, a, what);
     if (n <= 4096) return launch(norm_kernel<DX, DR, 256, 2, MX>, dim3(one), 256, s, a, what);
-    if (n <= 8192) return launch(norm_kernel<DX, DR, 256, 4, MX>, dim3(one), 256, s, a, what);
-    if (n <= 32768) return launch(norm_kernel<DX, DR, 1024, 4, MX>, dim3(one), 1024, s, a, what);
+    if (n <= 8192) return launch(norm_kernel<DX, DR, 512, 2, MX>, dim3(one), 512, s, a, what);
+    if (n <= 16384) return launch(norm_kernel<DX, DR, 1024, 2, MX>, dim3(one), 1024, s, a, what);
     return launch(norm_wide_kernel<DX, DR, MX>, dim3(one), kWide, s, a, what);
 }
 
@@ -541,9 +589,9 @@ int norm_grad_with(const NormGradArgs& a, hipStream_t s, const char* what) {
     const unsigned one = (unsigned)a.groups;
     if (a.cols <= 1024)
         return launch(norm_grad_kernel<DX, DR, 64, 2>, dim3((unsigned)ceil_div(a.groups, 4)), 256, s, a, what);
-    if (a.cols <= 4096) return launch(norm_grad_kernel<DX, DR, 256, 2>, dim3(one), 256, s, a, what);
-    if (a.cols <= 8192) return launch(norm_grad_kernel<DX, DR, 256, 4>, dim3(one), 256, s, a, what);
-    if (a.cols <= 32768) return launch(norm_grad_kernel<DX, DR, 1024, 4>, dim3(one), 1024, s, a, what);
+    if (a.cols <= 4096) return launch(norm_grad_kernel<DX, DR, 512, 1>, dim3(one), 512, s, a, what);
+    if (a.cols <= 8192) return launch(norm_grad_kernel<DX, DR, 1024, 1>, dim3(one), 1024, s, a, what);
+    if (a.cols <= 16384) return launch(norm_grad_kernel<DX, DR, 1024, 2>, dim3(one), 1024, s, a, what);
     return launch(norm_grad_wide_kernel<DX, DR>, dim3(one), kWide, s, a, what);
 }
 
@@ -645,7 +693,7 @@ int zero_rms_norm_grad(const void* dy, int64_t lddy, const void* h, int32_t h_dt
     }
     if (dw == nullptr) return ok();
     return with_type(dtype, [&](auto x) {
-        return launch(norm_dw_kernel<decltype(x)::value>, dim3((unsigned)ceil_div(cols, 64)), 256, s, a, what);
+        return launch(norm_dw_kernel<decltype(x)::value>, dim3((unsigned)ceil_div(cols, 16)), 256, s, a, what);
     });
 }
 

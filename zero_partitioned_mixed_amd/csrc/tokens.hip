@@ -25,7 +25,7 @@ struct Ids {
 // integers using multiplication", 1994).
 struct Divider {
     uint32_t d, m, s1, s2;
-    explicit Divider(uint32_t by = 1) : d(by) {
+    Divider(uint32_t by = 1) : d(by) {
         uint32_t l = 0;
         while (l < 32 && (uint64_t(1) << l) < by) ++l;
         m = (uint32_t)(((((uint64_t)1 << l) - by) << 32) / by + 1);
@@ -72,7 +72,7 @@ __device__ __forceinline__ void places8(const Vectors& v, Place8 (&p)[kEach]) {
 // wave its first place for every digit, and within 64 keys the lanes with the same digit find
 // each other by one ballot per bit.  Integer counts alone are added atomically, in LDS.
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits, kSortWaves = 8, kSortThreads = 64 * kSortWaves;
-constexpr int64_t kMinTile = 2048, kMostTiles = 256;
+constexpr int64_t kMinTile = 2048, kMostTiles = 256;  // three passes at most: 24 bits of key
 
 struct SortArgs {
     Ids ids;                  // first pass
@@ -99,28 +99,49 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
     a.counts[blockIdx.x * kBins + threadIdx.x] = bins[threadIdx.x];
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
+// A batch of a wave's part: kAtOnce keys a lane, 64 apart, loaded together.
+constexpr int kAtOnce = 4, kBatch = 64 * kAtOnce;
+struct Batch {
+    uint32_t key[kAtOnce], from[kAtOnce];
+    __device__ __forceinline__ void load(const SortArgs& a, uint32_t i0, uint32_t end, bool origins) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const uint32_t i = i0 + u * 64 + (threadIdx.x & 63);
+            key[u] = i < end ? sort_key(a, i) : 0;
+            from[u] = origins && a.from != nullptr && i < end ? a.from[i] : i;
+        }
+    }
+};
+
+__device__ __forceinline__ void sort_pass(const SortArgs& a, uint32_t (&next)[kSortWaves][kBins], uint32_t (&meet)[kSortWaves]) {
     static_assert(kBins == kSortThreads, "a thread a digit");
-    __shared__ uint32_t next[kSortWaves][kBins];  // of a wave and digit: how many, then the next one's place
-    __shared__ uint32_t meet[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t mask = (1u << a.bits) - 1, part = a.tile / kSortWaves;
     const uint64_t start = (uint64_t)blockIdx.x * a.tile + (uint64_t)wave * part;
     const uint32_t first = start < a.n ? (uint32_t)start : a.n, end = a.n - first < part ? a.n : first + part;
+    const bool once = part <= kBatch;  // the keys stay in registers
+    Batch k;
+    if (once) k.load(a, first, end, true);
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) next[w][tid] = 0;
     __syncthreads();
-    for (uint32_t i = first + lane; i < end; i += 64) atomicAdd(&next[wave][sort_key(a, i) >> a.shift & mask], 1u);
+    for (uint32_t i0 = first; i0 < end; i0 += kBatch) {
+        if (!once) k.load(a, i0, end, false);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+            if (i0 + u * 64 + lane < end) atomicAdd(&next[wave][k.key[u] >> a.shift & mask], 1u);
+    }
     __syncthreads();
     uint32_t all = 0, before = 0;  // this thread's digit: everywhere, in tiles before this one
     if (a.tiles == 1) {
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) all += next[w][tid];
     } else {
+#pragma unroll 8
         for (uint32_t t = 0; t < a.tiles; ++t) {
             const uint32_t c = a.counts[t * kBins + tid];
             all += c;
-            if (t < blockIdx.x) before += c;
+            before += t < blockIdx.x ? c : 0;
         }
     }
     uint32_t sum = all;  // of this digit and the lower ones
@@ -141,27 +162,44 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a) {
         at += c;
     }
     __syncthreads();
-    for (uint32_t i0 = first; i0 < end; i0 += 64) {
-        const uint32_t i = i0 + lane;
-        const bool there = i < end;
-        const uint32_t key = there ? sort_key(a, i) : 0, digit = key >> a.shift & mask;
-        uint64_t same = __ballot(there);
-        for (int b = 0; b < a.bits; ++b) {
-            const uint64_t set = __ballot(digit >> b & 1);
-            same &= digit >> b & 1 ? set : ~set;
+    for (uint32_t i0 = first; i0 < end; i0 += kBatch) {
+        if (!once) k.load(a, i0, end, true);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const bool there = i0 + u * 64 + lane < end;
+            const uint32_t digit = k.key[u] >> a.shift & mask;
+            uint64_t same = __ballot(there);
+            for (int b = 0; b < a.bits; ++b) {
+                const uint64_t set = __ballot(digit >> b & 1);
+                same &= digit >> b & 1 ? set : ~set;
+            }
+            const uint32_t rank = (uint32_t)__popcll(same & ((uint64_t(1) << lane) - 1)), many = (uint32_t)__popcll(same);
+            const uint32_t base = next[wave][digit];
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // all lanes have read
+            __builtin_amdgcn_wave_barrier();
+            if (there && rank == 0) next[wave][digit] = base + many;
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (!there) continue;
+            const uint32_t to = base + rank;
+            if (a.keys_out != nullptr) a.keys_out[to] = k.key[u];
+            a.from_out[to] = k.from[u];
+            if (a.place != nullptr) a.place[k.from[u]] = (int32_t)to;
         }
-        const uint32_t rank = (uint32_t)__popcll(same & ((uint64_t(1) << lane) - 1)), many = (uint32_t)__popcll(same);
-        const uint32_t base = next[wave][digit];
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // all lanes have read
-        __builtin_amdgcn_wave_barrier();
-        if (there && rank == 0) next[wave][digit] = base + many;
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (!there) continue;
-        const uint32_t to = base + rank, from = a.from == nullptr ? i : a.from[i];
-        if (a.keys_out != nullptr) a.keys_out[to] = key;
-        a.from_out[to] = from;
-        if (a.place != nullptr) a.place[from] = (int32_t)to;
+    }
+}
+
+// One pass over all tiles, or (passes) all passes of a single tile.
+struct SortPasses {
+    SortArgs pass[3];
+    int passes;
+};
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(SortPasses a) {
+    __shared__ uint32_t next[kSortWaves][kBins];  // of a wave and digit: how many, then the next one's place
+    __shared__ uint32_t meet[kSortWaves];
+    for (int p = 0; p < a.passes; ++p) {
+        if (p > 0) __syncthreads();  // the pass before is in memory
+        sort_pass(a.pass[p], next, meet);
     }
 }
 
@@ -198,6 +236,7 @@ int sort_ids(const Ids& ids, int64_t n, uint32_t* keys, uint32_t* from, int32_t*
     a.counts = scratch;
     uint32_t* const one = scratch + round_up(a.tiles > 1 ? (int64_t)a.tiles * kBins : 0, 64);
     uint32_t* const two = one + round_up(2 * n, 64);
+    SortPasses one_tile{};
     for (int p = 0; p < passes; ++p) {
         const bool last = p == passes - 1;
         uint32_t* const mid = p % 2 == 0 ? one : two;
@@ -207,12 +246,20 @@ int sort_ids(const Ids& ids, int64_t n, uint32_t* keys, uint32_t* from, int32_t*
         a.offsets = last && passes == 1 ? offsets : nullptr;
         a.shift = p * each;
         a.bits = each < bits - a.shift ? each : bits - a.shift;
-        if (a.tiles > 1 && (rc = launch(sort_count_kernel, dim3(a.tiles), kSortThreads, s, a, what)) != ZERO_OK) return rc;
-        if ((rc = launch(sort_kernel, dim3(a.tiles), kSortThreads, s, a, what)) != ZERO_OK) return rc;
+        if (a.tiles > 1) {
+            if ((rc = launch(sort_count_kernel, dim3(a.tiles), kSortThreads, s, a, what)) != ZERO_OK) return rc;
+            SortPasses one_pass{};
+            one_pass.pass[0] = a;
+            one_pass.passes = 1;
+            if ((rc = launch(sort_kernel, dim3(a.tiles), kSortThreads, s, one_pass, what)) != ZERO_OK) return rc;
+        } else {
+            one_tile.pass[p] = a;
+        }
         a.keys = a.keys_out;
         a.from = a.from_out;
     }
-    return ok();
+    one_tile.passes = passes;
+    return a.tiles > 1 ? ok() : launch(sort_kernel, dim3(1), kSortThreads, s, one_tile, what);
 }
 
 // The first place in keys[0 .. n) (sorted) whose key is `key` or more: a wave narrows the range
@@ -256,7 +303,7 @@ __global__ void __launch_bounds__(256) embedding_kernel(LookupArgs a) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         e[i].zero();
-        if (key[i] < a.ids.limit) e[i].load((const T*)a.table + (int64_t)key[i] * a.ldt, p[i].c, a.cols);
+        if (key[i] < a.ids.limit) e[i].fetch((const T*)a.table + (int64_t)key[i] * a.ldt, p[i].c, a.cols);
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -271,12 +318,12 @@ __global__ void __launch_bounds__(256) embedding_kernel(LookupArgs a) {
 
 // The gradient: row v is scale times the sum of dy over the tokens whose id is v, in their order,
 // in fp32, rounded once; zeros where there is none.  With the tokens sorted by id a row's tokens
-// are a run.  A workgroup takes kGradVectors vectors' worth of table rows, finds their runs, and
-// each thread sums its eight columns of a row: bound by writing the table's gradient, which is
-// nearly all zeros for a large vocabulary.  Runs of more than kRun tokens (a frequent word, or
-// padding with an id) are cut at multiples of kRun in the sorted order: further workgroups of the
-// same launch sum the pieces, a second launch adds the pieces in order.
-constexpr int kRun = 128, kGradVectors = 4096, kGradRows = 256;
+// are a run.  The sorted order is cut into pieces of kPiece tokens or more, so that a frequent word's
+// long run is as much work for a piece as many short ones: a piece sums each of its runs, writes
+// those that lie in it to their rows, and of the two that may leave it the sums so far; a second
+// launch adds what belongs together, in order.  Further workgroups of the first launch write
+// the zeros, which are nearly all of a large table's gradient.  Bound by memory.
+constexpr int kPiece = 16, kMostPieces = 4096, kZeroVectors = 16384, kZeroRows = 256, kZeroGroups = 1024;
 
 struct GradArgs {
     const uint32_t *keys, *from;  // sorted
@@ -286,130 +333,138 @@ struct GradArgs {
     float scale;
     void* out;
     int64_t ldo;
-    float* parts;       // [pieces][2][cols]
-    uint32_t rows;      // table rows of a workgroup
-    uint32_t groups;    // workgroups with table rows
-    uint32_t across;    // vectors in a row
-    uint32_t tiles;     // of 256 vectors in a row
-    Divider by;         // across
+    float* parts;             // [pieces][2][cols]: a run's sum in the piece where it goes on (0), starts and goes on (1)
+    uint32_t piece, pieces;   // tokens in a piece
+    uint32_t jobs, tiles;     // workgroups with pieces: for each 256 >> lanes pieces, of 256 vectors in a row
+    int lanes;                // log2 of the threads that share a piece
+    uint32_t rows;            // table rows of a workgroup that writes zeros
+    uint32_t across;          // vectors in a row
+    Divider by;               // across
 };
 
-// The sum of eight columns of dy over sorted places [s, e), in order.
 template <int DT>
-__device__ __forceinline__ void sum_run(const GradArgs& a, uint32_t s, uint32_t e, int64_t c, float* sum) {
+__device__ __forceinline__ void grad_piece(const GradArgs& a) {
     typedef typename Elem<DT>::type T;
     constexpr int kAhead = 8;
+    const uint32_t set = blockIdx.x / a.tiles, tile = blockIdx.x - set * a.tiles, lane = threadIdx.x & ((1u << a.lanes) - 1);
+    const uint32_t piece = set * (256u >> a.lanes) + (threadIdx.x >> a.lanes);
+    const int64_t c = ((int64_t)tile * 256 + lane) * 8;
+    if (piece >= a.pieces || c >= a.cols) return;
+    const uint32_t p0 = piece * a.piece, p1 = a.n - p0 < a.piece ? a.n : p0 + a.piece;
+    const uint32_t left = p0 > 0 ? a.keys[p0 - 1] : a.vocab, right = p1 < a.n ? a.keys[p1] : a.vocab;
+    uint32_t run = a.vocab;  // the id whose run is being summed, at first none
+    bool entered = false;    // it started before the piece
+    float sum[8];
+    auto done = [&](bool leaves) {
+        if (run >= a.vocab) return;
+        if (entered || leaves) {
+            put8<ZERO_F32>(a.parts + (int64_t)(2 * piece + !entered) * a.cols, c, a.cols, sum);
+        } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
-    uint32_t i = s;
-    for (; i + kAhead <= e; i += kAhead) {
+            for (int k = 0; k < 8; ++k) sum[k] *= a.scale;
+            put8<DT>((T*)a.out + (int64_t)run * a.ldo, c, a.cols, sum);
+        }
+    };
+    for (uint32_t i0 = p0; i0 < p1; i0 += kAhead) {
+        uint32_t key[kAhead], from[kAhead];
         Eight<DT> v[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) v[u].load((const T*)a.dy + (int64_t)a.from[i + u] * a.lddy, c, a.cols);
+        for (int u = 0; u < kAhead; ++u) {
+            key[u] = i0 + u < p1 ? a.keys[i0 + u] : a.vocab;
+            from[u] = i0 + u < p1 ? a.from[i0 + u] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (key[u] < a.vocab) v[u].fetch((const T*)a.dy + (int64_t)from[u] * a.lddy, c, a.cols);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
+            if (key[u] >= a.vocab) continue;  // sorted: nothing follows
+            if (key[u] != run) {
+                done(false);
+                run = key[u];
+                entered = i0 + u == p0 && left == run;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+            }
             float x[8];
             v[u].values(x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum[k] += x[k];
         }
     }
-    for (; i < e; ++i) {
-        Eight<DT> v;
-        v.load((const T*)a.dy + (int64_t)a.from[i] * a.lddy, c, a.cols);
-        float x[8];
-        v.values(x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += x[k];
-    }
+    done(right == run);
 }
 
 template <int DT>
 __global__ void __launch_bounds__(256) embedding_grad_kernel(GradArgs a) {
     typedef typename Elem<DT>::type T;
-    __shared__ uint32_t first[kGradRows], last[kGradRows], ends[4];
+    __shared__ uint8_t used[kZeroRows];
+    __shared__ uint32_t ends[2];
+    if (blockIdx.x < a.jobs) return grad_piece<DT>(a);
     const int tid = threadIdx.x, wave = tid >> 6;
-    if (blockIdx.x < a.groups) {
-        const uint32_t v0 = blockIdx.x * a.rows, v1 = a.vocab - v0 < a.rows ? a.vocab : v0 + a.rows;
-        if (wave < 2) {
-            const uint32_t at = first_place(a.keys, a.n, wave == 0 ? v0 : v1);
-            if ((tid & 63) == 0) ends[wave] = at;
-        }
-        first[tid] = last[tid] = 0;
-        __syncthreads();
-        const uint32_t lo = ends[0], hi = ends[1];
-        for (uint32_t i = lo + tid; i < hi; i += 256) {
-            const uint32_t key = a.keys[i];
-            if (i == lo || a.keys[i - 1] != key) first[key - v0] = i;
-            if (i + 1 == hi || a.keys[i + 1] != key) last[key - v0] = i + 1;
-        }
-        __syncthreads();
-        const uint32_t all = (v1 - v0) * a.across;
-        for (uint32_t f = tid; f < all; f += 256) {
-            const uint32_t r = a.by(f);
-            const int64_t c = (int64_t)(f - r * a.across) * 8;
-            const uint32_t s = first[r], e = last[r];
-            if (e - s > kRun) continue;
-            float sum[8];
-            sum_run<DT>(a, s, e, c, sum);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] *= a.scale;
-            put8<DT>((T*)a.out + (int64_t)(v0 + r) * a.ldo, c, a.cols, sum);
-        }
-        return;
+    const uint32_t v0 = (blockIdx.x - a.jobs) * a.rows, v1 = a.vocab - v0 < a.rows ? a.vocab : v0 + a.rows;
+    if (wave < 2) {
+        const uint32_t at = first_place(a.keys, a.n, wave == 0 ? v0 : v1);
+        if ((tid & 63) == 0) ends[wave] = at;
     }
-    // a piece of the sorted order: what of long runs lies in it, from its first and of its last key
-    const uint32_t job = blockIdx.x - a.groups, piece = job / a.tiles, tile = job - piece * a.tiles;
-    const uint32_t p0 = piece * kRun, p1 = a.n - p0 < kRun ? a.n : p0 + kRun;
-    const uint32_t k0 = a.keys[p0], k1 = a.keys[p1 - 1];
-    const uint32_t at = first_place(a.keys, a.n, (wave < 2 ? k0 : k1) + (wave & 1));
-    if ((tid & 63) == 0) ends[wave] = at;
+    used[tid] = 0;
     __syncthreads();
-    const int64_t c = ((int64_t)tile * 256 + tid) * 8;
-    if (c >= a.cols) return;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const uint32_t key = which == 0 ? k0 : k1, s = ends[2 * which], e = ends[2 * which + 1];
-        if (key >= a.vocab || e - s <= kRun || (which == 1 && k1 == k0)) continue;
-        float sum[8];
-        sum_run<DT>(a, s > p0 ? s : p0, e < p1 ? e : p1, c, sum);
-        put8<ZERO_F32>(a.parts + (int64_t)(2 * piece + which) * a.cols, c, a.cols, sum);
+    for (uint32_t i = ends[0] + tid; i < ends[1]; i += 256) used[a.keys[i] - v0] = 1;
+    __syncthreads();
+    const uint32_t all = (v1 - v0) * a.across;
+    const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (uint32_t f = tid; f < all; f += 256) {
+        const uint32_t r = a.by(f);
+        if (!used[r]) put8<DT>((T*)a.out + (int64_t)(v0 + r) * a.ldo, (int64_t)(f - r * a.across) * 8, a.cols, none);
     }
 }
 
-// The long run that starts in a piece, if one does (its last key's, at most one): its parts in order.
+// The runs that start in a piece and leave it (each piece's last key's, at most one): their parts, an
+// eighth of them in order by each of eight groups of 32 threads.  A workgroup looks at kJoin pieces,
+// most of which have none, for 256 columns.
+constexpr int kJoin = 8;
 template <int DT>
 __global__ void __launch_bounds__(256) embedding_join_kernel(GradArgs a) {
     typedef typename Elem<DT>::type T;
-    __shared__ uint32_t ends[2];
-    const int tid = threadIdx.x, wave = tid >> 6;
-    const uint32_t piece = blockIdx.x / a.tiles, tile = blockIdx.x - piece * a.tiles;
-    const uint32_t p0 = piece * kRun, p1 = a.n - p0 < kRun ? a.n : p0 + kRun;
-    const uint32_t key = a.keys[p1 - 1];
-    if (key >= a.vocab) return;
-    if (wave < 2) {
-        const uint32_t at = first_place(a.keys, a.n, key + wave);
-        if ((tid & 63) == 0) ends[wave] = at;
+    __shared__ float sums[8][256];
+    const uint32_t across = (uint32_t)((a.cols + 255) / 256), set = blockIdx.x / across, tile = blockIdx.x - set * across;
+    const int group = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t c = (int64_t)tile * 256 + lane * 8, col = (int64_t)tile * 256 + threadIdx.x;
+    // every wave finds out for itself which of the pieces have such a run
+    const uint32_t mine = set * kJoin + (threadIdx.x & (kJoin - 1));
+    const uint64_t m0 = (uint64_t)mine * a.piece, m1 = m0 + a.piece;
+    bool starts = m1 < a.n;
+    if (starts) {
+        const uint32_t key = a.keys[m1];
+        starts = key < a.vocab && a.keys[m1 - 1] == key && !(a.keys[m0] == key && m0 > 0 && a.keys[m0 - 1] == key);
     }
-    __syncthreads();
-    const uint32_t s = ends[0], e = ends[1];
-    const int64_t c = ((int64_t)tile * 256 + tid) * 8;
-    if (e - s <= kRun || s < p0 || c >= a.cols) return;
-    float sum[8];
-    Eight<ZERO_F32> v;
-    v.load(a.parts + (int64_t)(2 * piece + (a.keys[p0] != key)) * a.cols, c, a.cols);
-    v.values(sum);
-    const uint32_t to = (e - 1) / kRun;
-    for (uint32_t q = piece + 1; q <= to; ++q) {
-        float x[8];
-        v.load(a.parts + (int64_t)(2 * q) * a.cols, c, a.cols);
-        v.values(x);
+    for (uint32_t left = (uint32_t)__ballot(starts) & ((1u << kJoin) - 1); left != 0; left &= left - 1) {
+        const uint32_t piece = set * kJoin + (uint32_t)__builtin_ctz(left), key = a.keys[(piece + 1) * a.piece];
+        const uint32_t many = (first_place(a.keys, a.n, key + 1) - 1) / a.piece - piece + 1;
+        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (c < a.cols) {
+            const uint32_t each = (many + 7) / 8, to = (group + 1) * each < many ? (group + 1) * each : many;
+#pragma unroll 4
+            for (uint32_t q = group * each; q < to; ++q) {
+                Eight<ZERO_F32> v;
+                v.fetch(a.parts + (int64_t)(2 * (piece + q) + (q == 0)) * a.cols, c, a.cols);
+                float x[8];
+                v.values(x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += x[k];
+                for (int k = 0; k < 8; ++k) sum[k] += x[k];
+            }
+        }
+        __syncthreads();  // the run's before have been read
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sums[group][lane * 8 + k] = sum[k];
+        __syncthreads();
+        if (col < a.cols) {
+            float v = sums[0][threadIdx.x];
+#pragma unroll
+            for (int g = 1; g < 8; ++g) v += sums[g][threadIdx.x];
+            ((T*)a.out)[(int64_t)key * a.ldo + col] = from_float<DT>(v * a.scale);
+        }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] *= a.scale;
-    put8<DT>((T*)a.out + (int64_t)key * a.ldo, c, a.cols, sum);
 }
 
 // ---------------------------------------------------------------- tokens by expert
@@ -437,7 +492,7 @@ __global__ void __launch_bounds__(256) expert_rows_kernel(ExpertArgs a) {
     Eight<DT> e[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-        if (p[i].there) e[i].load((const T*)a.x + p[i].row * a.ldx, p[i].c, a.cols);
+        if (p[i].there) e[i].fetch((const T*)a.x + p[i].row * a.ldx, p[i].c, a.cols);
     const uint32_t used = (uint32_t)*a.used, slots = a.tokens * a.k;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -464,85 +519,98 @@ __device__ __forceinline__ float weight_of(const ExpertArgs& a, int64_t slot) {
     return to_float<DT>(((const typename Elem<DT>::type*)a.weights)[slot]);
 }
 
+// LANES lanes take a token, 64 or more, so that its places and weights are the same for a wave.
+template <int LANES>
+struct TokenOf {
+    static constexpr int kThreads = LANES < 256 ? 256 : LANES, kTokens = kThreads / LANES;
+    int64_t token;
+    int lane;
+    __device__ __forceinline__ TokenOf()
+        : token((int64_t)blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES)), lane(threadIdx.x % LANES) {}
+};
+
 // Tokens' rows from sorted rows: the weighted sum of a token's k rows, in fp32, in the slots' order.
-template <int DT>
-__global__ void __launch_bounds__(256) expert_combine_kernel(ExpertArgs a) {
+template <int DT, int LANES>
+__global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kernel(ExpertArgs a) {
     typedef typename Elem<DT>::type T;
-    Place8 p[kEach];
-    places8(a.v, p);
+    constexpr uint32_t kSlots = 8;
+    const TokenOf<LANES> t;
+    if (t.token >= a.tokens) return;
     const uint32_t used = (uint32_t)*a.used;
-    for (int i = 0; i < kEach; ++i) {
-        if (!p[i].there) break;
+    for (int64_t c = t.lane * 8; c < a.cols; c += LANES * 8) {
         float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        constexpr uint32_t kAhead = 8;
-        for (uint32_t j0 = 0; j0 < a.k; j0 += kAhead) {
-            Eight<DT> e[kAhead];
-            uint32_t from[kAhead];
+        for (uint32_t j0 = 0; j0 < a.k; j0 += kSlots) {
+            Eight<DT> e[kSlots];
+            uint32_t from[kSlots];
 #pragma unroll
-            for (uint32_t u = 0; u < kAhead; ++u) {
-                from[u] = j0 + u < a.k ? (uint32_t)a.place[p[i].row * a.k + j0 + u] : 0xFFFFFFFFu;
-                if (from[u] < used) e[u].load((const T*)a.x + (int64_t)from[u] * a.ldx, p[i].c, a.cols);
+            for (uint32_t u = 0; u < kSlots; ++u) {
+                from[u] = j0 + u < a.k ? (uint32_t)a.place[t.token * a.k + j0 + u] : 0xFFFFFFFFu;
+                if (from[u] < used) e[u].fetch((const T*)a.x + (int64_t)from[u] * a.ldx, c, a.cols);
             }
 #pragma unroll
-            for (uint32_t u = 0; u < kAhead; ++u) {
+            for (uint32_t u = 0; u < kSlots; ++u) {
                 if (from[u] >= used) continue;
-                const float w = weight_of<DT>(a, p[i].row * a.k + j0 + u);
+                const float w = weight_of<DT>(a, t.token * a.k + j0 + u);
                 float x[8];
                 e[u].values(x);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) sum[q] += w * x[q];
             }
         }
-        put8<DT>((T*)a.out + p[i].row * a.ldo, p[i].c, a.cols, sum);
+        put8<DT>((T*)a.out + t.token * a.ldo, c, a.cols, sum);
     }
 }
 
 // The gradients of that sum: of a sorted row its weight times dy of its token (zeros behind the
-// last), of a weight the product of its row with dy.  T lanes take a token.
+// last), of a weight the product of its row with dy.
 template <int DT, int LANES>
-__global__ void __launch_bounds__(256) expert_combine_grad_kernel(ExpertArgs a) {
+__global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_grad_kernel(ExpertArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t kSlots = 8;
-    __shared__ float meet[4][kSlots];
-    const int t = threadIdx.x % LANES;
-    const int64_t token = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-    if (token >= a.tokens) return;  // whole waves; with 256 lanes none
+    constexpr int kWaves = LANES / 64;
+    __shared__ float meet[kWaves][kSlots];
+    const TokenOf<LANES> t;
+    if (t.token >= a.tokens) return;  // whole waves; with more than 64 lanes none
     const uint32_t used = (uint32_t)*a.used, slots = a.tokens * a.k;
-    const T* const dy = (const T*)a.dy + token * a.lddy;
+    const T* const dy = (const T*)a.dy + t.token * a.lddy;
     for (uint32_t j0 = 0; j0 < a.k; j0 += kSlots) {
         uint32_t at[kSlots];
         float w[kSlots], dot[kSlots];
 #pragma unroll
         for (uint32_t u = 0; u < kSlots; ++u) {
-            at[u] = j0 + u < a.k ? (uint32_t)a.place[token * a.k + j0 + u] : 0xFFFFFFFFu;
-            w[u] = at[u] < used ? weight_of<DT>(a, token * a.k + j0 + u) : 0.0f;
+            at[u] = j0 + u < a.k ? (uint32_t)a.place[t.token * a.k + j0 + u] : 0xFFFFFFFFu;
+            w[u] = at[u] < used ? weight_of<DT>(a, t.token * a.k + j0 + u) : 0.0f;
             dot[u] = 0.0f;
         }
-        for (int64_t c = t * 8; c < a.cols; c += LANES * 8) {
+#pragma unroll 1
+        for (int64_t c = t.lane * 8; c < a.cols; c += LANES * 8) {
             Eight<DT> ey, e[kSlots];
-            ey.load(dy, c, a.cols);
+            ey.fetch(dy, c, a.cols);
             if (a.dw != nullptr) {
 #pragma unroll
                 for (uint32_t u = 0; u < kSlots; ++u)
-                    if (at[u] < used) e[u].load((const T*)a.x + (int64_t)at[u] * a.ldx, c, a.cols);
+                    if (at[u] < used) e[u].fetch((const T*)a.x + (int64_t)at[u] * a.ldx, c, a.cols);
             }
             float y[8];
             ey.values(y);
+            if (a.out != nullptr) {
 #pragma unroll
-            for (uint32_t u = 0; u < kSlots; ++u) {
-                if (at[u] >= slots) continue;
-                const bool there = at[u] < used;
-                if (there && a.dw != nullptr) {
+                for (uint32_t u = 0; u < kSlots; ++u) {
+                    if (at[u] >= slots) continue;
+                    float g[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) g[q] = at[u] < used ? w[u] * y[q] : 0.0f;
+                    put8<DT>((T*)a.out + (int64_t)at[u] * a.ldo, c, a.cols, g);
+                }
+            }
+            if (a.dw != nullptr) {
+#pragma unroll
+                for (uint32_t u = 0; u < kSlots; ++u) {
+                    if (at[u] >= used) continue;
                     float x[8];
                     e[u].values(x);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) dot[u] += x[q] * y[q];
-                }
-                if (a.out != nullptr) {
-                    float g[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) g[q] = there ? w[u] * y[q] : 0.0f;
-                    put8<DT>((T*)a.out + (int64_t)at[u] * a.ldo, c, a.cols, g);
                 }
             }
         }
@@ -551,26 +619,28 @@ __global__ void __launch_bounds__(256) expert_combine_grad_kernel(ExpertArgs a) 
         for (uint32_t u = 0; u < kSlots; ++u)
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) dot[u] += __shfl_xor(dot[u], d);
-        if constexpr (LANES > 64) {
+        if constexpr (kWaves > 1) {
             __syncthreads();  // the sums before have been read
             if ((threadIdx.x & 63) == 0) {
 #pragma unroll
                 for (uint32_t u = 0; u < kSlots; ++u) meet[threadIdx.x / 64][u] = dot[u];
             }
             __syncthreads();
-#pragma unroll
-            for (uint32_t u = 0; u < kSlots; ++u) dot[u] = meet[0][u] + meet[1][u] + meet[2][u] + meet[3][u];
         }
-        if (t == 0) {
+        if (t.lane < (int)kSlots && j0 + t.lane < a.k) {
+            float v = 0.0f;
+            if constexpr (kWaves > 1) {
+                v = meet[0][t.lane];
+                for (int i = 1; i < kWaves; ++i) v += meet[i][t.lane];
+            } else {
 #pragma unroll
-            for (uint32_t u = 0; u < kSlots; ++u) {
-                if (j0 + u >= a.k) break;
-                const int64_t slot = token * a.k + j0 + u;
-                if (a.weights_f32)
-                    ((float*)a.dw)[slot] = dot[u];
-                else
-                    ((T*)a.dw)[slot] = from_float<DT>(dot[u]);
+                for (uint32_t u = 0; u < kSlots; ++u) v = t.lane == (int)u ? dot[u] : v;
             }
+            const int64_t slot = t.token * a.k + j0 + t.lane;
+            if (a.weights_f32)
+                ((float*)a.dw)[slot] = v;
+            else
+                ((T*)a.dw)[slot] = from_float<DT>(v);
         }
     }
 }
@@ -598,6 +668,14 @@ int with_type(int32_t dt, F f) {
     }
 }
 
+// Lanes that share a token's row.
+template <class F>
+int with_lanes(int64_t cols, F f) {
+    if (cols <= 1024) return f(std::integral_constant<int, 64>());
+    if (cols <= 2048) return f(std::integral_constant<int, 256>());
+    return f(std::integral_constant<int, 512>());
+}
+
 int check_ids(const void* ids, int32_t bytes, int64_t n, int64_t limit, const char* what) {
     if (bytes != 4 && bytes != 8) return fail(ZERO_EINVAL, "%s: numbers of 4 or 8 bytes", what);
     if (n < 0 || n > kMaxSide || limit < 1 || limit > kMaxSide)
@@ -615,7 +693,11 @@ int check_space(const void* ws, size_t ws_bytes, size_t need, const char* what) 
     return ZERO_OK;
 }
 
-int64_t grad_parts(int64_t n, int64_t cols) { return n > kRun ? 2 * ceil_div(n, kRun) * cols : 0; }
+int64_t grad_piece_of(int64_t n) {
+    const int64_t p = round_up(ceil_div(n, kMostPieces), 8);
+    return p > kPiece ? p : kPiece;
+}
+int64_t grad_parts(int64_t n, int64_t cols) { return n > grad_piece_of(n) ? 2 * ceil_div(n, grad_piece_of(n)) * cols : 0; }
 
 // The checks shared by the calls on experts' rows; 1: nothing to do.
 int check_experts(const void* a, int64_t lda, const void* b, int64_t ldb, const void* place, const void* used, int32_t dtype,
@@ -682,21 +764,38 @@ int zero_embedding_grad(const void* ids, int32_t id_bytes, int64_t tokens, const
     uint32_t *const keys = (uint32_t*)ws, *const from = keys + tokens;
     uint32_t* const scratch = keys + round_up(2 * tokens, 64);
     const uint32_t across = (uint32_t)ceil_div(cols, 8);
-    GradArgs a{keys, from, (uint32_t)tokens, (uint32_t)vocab, dy, lddy, cols, scale, out, ldo,
-               (float*)(scratch + (tokens > 0 ? sort_words(tokens, (uint32_t)vocab) : 0)), 0, 0, across,
-               (uint32_t)ceil_div(across, 256), Divider(across)};
-    const int64_t rows = kGradVectors / across;
-    a.rows = (uint32_t)(rows < 1 ? 1 : rows < kGradRows ? rows : kGradRows);
-    a.groups = (uint32_t)ceil_div(vocab, a.rows);
-    const int64_t pieces = tokens > kRun ? ceil_div(tokens, kRun) : 0, jobs = pieces * a.tiles;
-    if (a.groups + jobs > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
+    GradArgs a{};
+    a.keys = keys;
+    a.from = from;
+    a.n = (uint32_t)tokens;
+    a.vocab = (uint32_t)vocab;
+    a.dy = dy;
+    a.lddy = lddy;
+    a.cols = cols;
+    a.scale = scale;
+    a.out = out;
+    a.ldo = ldo;
+    a.parts = (float*)(scratch + (tokens > 0 ? sort_words(tokens, (uint32_t)vocab) : 0));
+    a.piece = (uint32_t)grad_piece_of(tokens);
+    a.pieces = (uint32_t)ceil_div(tokens, a.piece);
+    a.across = across;
+    a.by = Divider(across);
+    a.tiles = (uint32_t)ceil_div(across, 256);
+    while ((1u << a.lanes) < across && a.lanes < 8) ++a.lanes;
+    a.jobs = (uint32_t)ceil_div(a.pieces, 256 >> a.lanes) * a.tiles;
+    // rows of zeros: a few writes a thread, but no fewer workgroups than fill the CUs
+    int64_t rows = kZeroVectors / across;
+    if (rows > ceil_div(vocab, kZeroGroups)) rows = ceil_div(vocab, kZeroGroups);
+    a.rows = (uint32_t)(rows < 1 ? 1 : rows < kZeroRows ? rows : kZeroRows);
+    const int64_t groups = ceil_div(vocab, a.rows), joins = a.pieces > 1 ? ceil_div(a.pieces, kJoin) * ceil_div(cols, 256) : 0;
+    if (a.jobs + groups > 0x7FFFFFFF || joins > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     if (tokens > 0 && (rc = sort_ids(Ids{ids, id_bytes == 8, (uint32_t)vocab}, tokens, keys, from, nullptr, nullptr, scratch, s,
                                      what)) != ZERO_OK)
         return rc;
     return with_type(dtype, [&](auto t) {
-        const int e = launch(embedding_grad_kernel<decltype(t)::value>, dim3((unsigned)(a.groups + jobs)), 256, s, a, what);
-        if (e != ZERO_OK || jobs == 0) return e;
-        return launch(embedding_join_kernel<decltype(t)::value>, dim3((unsigned)jobs), 256, s, a, what);
+        const int e = launch(embedding_grad_kernel<decltype(t)::value>, dim3((unsigned)(a.jobs + groups)), 256, s, a, what);
+        if (e != ZERO_OK || joins == 0) return e;
+        return launch(embedding_join_kernel<decltype(t)::value>, dim3((unsigned)joins), 256, s, a, what);
     });
 }
 
@@ -758,11 +857,14 @@ int zero_expert_combine(const void* rows, int32_t dtype, int64_t ldr, const int3
     if (overlap(to, values_at(rows, dtype, tokens * k, cols, ldr)) || overlap(to, Place(place, tokens * k * 4)) ||
         overlap(to, Place(used, 4)) || overlap(to, Place(weights, tokens * k * (int64_t)elem_bytes(weights_dtype))))
         return fail(ZERO_EINVAL, "%s: the result overlaps an input", what);
-    const ExpertArgs a{Vectors(tokens, cols), rows, nullptr, ldr, 0, place, used, weights, weights_dtype == ZERO_F32,
+    const ExpertArgs a{Vectors(1, 8), rows, nullptr, ldr, 0, place, used, weights, weights_dtype == ZERO_F32,
                        (uint32_t)tokens, (uint32_t)k, cols, y, nullptr, ldy};
-    if (a.v.workgroups() > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     return with_type(dtype, [&](auto t) {
-        return launch(expert_combine_kernel<decltype(t)::value>, dim3((unsigned)a.v.workgroups()), 256, (hipStream_t)stream, a, what);
+        return with_lanes(cols, [&](auto l) {
+            typedef TokenOf<decltype(l)::value> Token;
+            return launch(expert_combine_kernel<decltype(t)::value, decltype(l)::value>,
+                          dim3((unsigned)ceil_div(tokens, Token::kTokens)), Token::kThreads, (hipStream_t)stream, a, what);
+        });
     });
 }
 
@@ -791,10 +893,11 @@ int zero_expert_combine_grad(const void* dy, int64_t lddy, const void* rows, int
     const ExpertArgs a{Vectors(1, 8), rows, dy, ldr, lddy, place, used, weights, weights_dtype == ZERO_F32, (uint32_t)tokens,
                        (uint32_t)k, cols, drows, dweights, lddr};
     return with_type(dtype, [&](auto t) {
-        if (cols <= 2048)
-            return launch(expert_combine_grad_kernel<decltype(t)::value, 64>, dim3((unsigned)ceil_div(tokens, 4)), 256,
-                          (hipStream_t)stream, a, what);
-        return launch(expert_combine_grad_kernel<decltype(t)::value, 256>, dim3((unsigned)tokens), 256, (hipStream_t)stream, a, what);
+        return with_lanes(cols, [&](auto l) {
+            typedef TokenOf<decltype(l)::value> Token;
+            return launch(expert_combine_grad_kernel<decltype(t)::value, decltype(l)::value>,
+                          dim3((unsigned)ceil_div(tokens, Token::kTokens)), Token::kThreads, (hipStream_t)stream, a, what);
+        });
     });
 }
 
