@@ -114,6 +114,20 @@ struct Eight {
             for (int64_t i = cols - 1; i >= c; --i) up(row[i]);
         }
     }
+    // values() from whole dwords: two elements each, without 16-bit pieces in registers of their own.
+    __device__ __forceinline__ void floats(float* x) const {
+        if constexpr (DT == ZERO_BF16) {
+            uint32_t d[4];
+            __builtin_memcpy(d, v, sizeof(d));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __builtin_bit_cast(float, d[i] << 16);
+                x[2 * i + 1] = __builtin_bit_cast(float, d[i] & 0xFFFF0000u);
+            }
+        } else {
+            values(x);
+        }
+    }
     // The elements `by` (1 to 7) places lower, zeros behind them.
     __device__ __forceinline__ void down(int by) {
         if constexpr (kVecs == 1) {

@@ -15,6 +15,9 @@ namespace {
 constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p64f;
 __device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-80f ? kPreUp : 1.0f; }
 
+// Threads of a workgroup whose rows take T lanes each: four rows of a wave each, or one row.
+constexpr int row_block(int t) { return t == 64 ? 256 : t; }
+
 // The sums of N values over the T lanes of a row, T = 64 or a whole workgroup, the same bits in every lane.
 // One barrier each: consecutive calls take turns with the places in LDS.
 template <int T, int N>
@@ -81,10 +84,10 @@ __device__ __forceinline__ float rounded(float v) {
 // h of eight elements: from x, or from x and the residual, then also stored.
 template <int DX, int DR>
 __device__ __forceinline__ void sum8(const NormArgs& a, int64_t row, int64_t c, const Eight<DX>& ex, const Eight<DR>& er, float* h) {
-    ex.values(h);
+    ex.floats(h);
     if (a.residual != nullptr) {
         float r[8];
-        er.values(r);
+        er.floats(r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = rounded<DR>(h[i] + r[i]);
         put8<DR>((typename Elem<DR>::type*)a.h + row * a.ldh, c, a.cols, h);
@@ -104,10 +107,10 @@ __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int64_
 }
 
 template <int DX, int DR, int T, int V, bool MX>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    constexpr int kRows = T < 256 ? 256 / T : 1;
+    constexpr int kRows = row_block(T) / T;
     __shared__ RowSums<T, 1> meet;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
     if (row >= a.tokens) return;  // whole waves; with T > 64 none
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = 0.0f;
         } else {
-            ew[v].values(w);
+            ew[v].floats(w);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
             } else {
                 Eight<DR> eh;
                 eh.fetch(hr, c, a.cols);
-                eh.values(h);
+                eh.floats(h);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] *= pre;
@@ -217,15 +220,15 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
             if (a.residual == nullptr) {
                 Eight<DX> ex;
                 ex.fetch(x, c, a.cols);
-                ex.values(h);
+                ex.floats(h);
             } else {
                 Eight<DR> eh;
                 eh.fetch(hr, c, a.cols);
-                eh.values(h);
+                eh.floats(h);
             }
             Eight<DX> ew;
             ew.fetch((const X*)a.w, c, a.cols);
-            ew.values(w);
+            ew.floats(w);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * pre * w[i]) : 0.0f;
@@ -276,10 +279,10 @@ __device__ __forceinline__ void norm_sums8(const float* h, const float* y, const
 }
 
 template <int DX, int DR, int T, int V>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_grad_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(row_block(T)) norm_grad_kernel(NormGradArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    constexpr int kRows = T < 256 ? 256 / T : 1;
+    constexpr int kRows = row_block(T) / T;
     __shared__ RowSums<T, 2> meet;
     const int t = threadIdx.x % T;
     const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
@@ -307,21 +310,23 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_grad_kernel(NormGradAr
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
     }
+    constexpr bool kAhead = V == 1;  // the next row is on its way while this one's sums meet; with V = 2 registers run out
     Row next;
-    if (group < a.tokens) next.load(a, group, t);
+    if (kAhead && group < a.tokens) next.load(a, group, t);
     int turn = 0;
     for (int64_t row = group; row < a.tokens; row += a.groups) {
-        const Row e = next;  // the next row is on its way while this one's sums meet
-        if (row + a.groups < a.tokens) next.load(a, row + a.groups, t);
+        if (!kAhead) next.load(a, row, t);
+        const Row e = next;
+        if (kAhead && row + a.groups < a.tokens) next.load(a, row + a.groups, t);
         auto sums = [&](float pre, float (&s)[2]) {
             s[0] = s[1] = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if ((int64_t)(v * T + t) * 8 >= a.cols) break;
                 float h[8], y[8], w[8];
-                e.h[v].values(h);
-                e.y[v].values(y);
-                ew[v].values(w);
+                e.h[v].floats(h);
+                e.y[v].floats(y);
+                ew[v].floats(w);
                 norm_sums8(h, y, w, pre, s);
             }
             row_sums<T, 2>(s, meet, turn++);
@@ -340,10 +345,10 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_grad_kernel(NormGradAr
             const int64_t c = (int64_t)(v * T + t) * 8;
             if (c >= a.cols) break;
             float h[8], y[8], w[8], u[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            e.h[v].values(h);
-            e.y[v].values(y);
-            ew[v].values(w);
-            if (a.dh != nullptr) e.d[v].values(d);
+            e.h[v].floats(h);
+            e.y[v].floats(y);
+            ew[v].floats(w);
+            if (a.dh != nullptr) e.d[v].floats(d);
             norm_grad8(h, y, w, pre, r, m, u, d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[v][i] += y[i] * u[i];
@@ -381,9 +386,9 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
                 ey.fetch(dy, c, a.cols);
                 ew.fetch((const X*)a.w, c, a.cols);
                 float h[8], y[8], w[8];
-                eh.values(h);
-                ey.values(y);
-                ew.values(w);
+                eh.floats(h);
+                ey.floats(y);
+                ew.floats(w);
                 norm_sums8(h, y, w, pre, s);
             }
             row_sums<kWide, 2>(s, meet, turn++);
@@ -408,10 +413,10 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
             else
                 ed.zero();
             float h[8], y[8], w[8], u[8], d[8], p[8];
-            eh.values(h);
-            ey.values(y);
-            ew.values(w);
-            ed.values(d);
+            eh.floats(h);
+            ey.floats(y);
+            ew.floats(w);
+            ed.floats(d);
             float* const part = a.parts == nullptr ? nullptr : a.parts + (int64_t)blockIdx.x * a.cols;
             if (part != nullptr) {
 #pragma unroll
@@ -509,14 +514,14 @@ __global__ void __launch_bounds__(256) dropout_kernel(DropArgs a) {
         uint32_t w[4] = {group, (uint32_t)row, (uint32_t)offset, (uint32_t)(offset >> 32)};
         philox(w, a.key[0], a.key[1]);
         float x[8], r[8];
-        ex.values(x);
+        ex.floats(x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t bits = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFF;
             x[i] = bits >= a.limit ? x[i] * a.scale : 0.0f;
         }
         if (a.residual != nullptr) {
-            er.values(r);
+            er.floats(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] += r[i];
         }
@@ -544,8 +549,10 @@ int with_type(int32_t dt, F f) {
 template <int DX, int DR, bool MX>
 int norm_with(const NormArgs& a, hipStream_t s, const char* what) {
     const int64_t n = MX ? padded(a.cols) : a.cols;
-    const unsigned one = (unsigned)a.tokens;
-    if (n <= 1024) return launch(norm_kernel<DX, DR, 64, 2, MX>, dim3((unsigned)ceil_div(a.tokens, 4)), 256, s, a, what);
+    const unsigned one = (unsigned)a.tokens, four = (unsigned)ceil_div(a.tokens, 4);
+    if (n <= 512) return launch(norm_kernel<DX, DR, 64, 1, MX>, dim3(four), 256, s, a, what);
+    if (n <= 1024) return launch(norm_kernel<DX, DR, 64, 2, MX>, dim3(four), 256, s, a, what);
+    if (n <= 2048) return launch(norm_kernel<DX, DR, 256, 1, MX>, dim3(one), 256, s, a, what);
     if (n <= 4096) return launch(norm_kernel<DX, DR, 256, 2, MX>, dim3(one), 256, s, a, what);
     if (n <= 8192) return launch(norm_kernel<DX, DR, 512, 2, MX>, dim3(one), 512, s, a, what);
     if (n <= 16384) return launch(norm_kernel<DX, DR, 1024, 2, MX>, dim3(one), 1024, s, a, what);
@@ -580,15 +587,16 @@ int check_norm(const NormArgs& a, int32_t dx, int32_t dr, const char* what) {
 
 // Groups of rows that a gradient call sums dw over: workgroups, or waves where a wave takes a row.
 int64_t grad_groups(int64_t tokens, int64_t cols) {
-    const int64_t most = cols <= 1024 ? 4 * kGradGroups : kGradGroups;
+    const int64_t most = cols <= 512 ? 4 * kGradGroups : cols <= 2048 ? 2 * kGradGroups : kGradGroups;
     return tokens < most ? tokens : most;
 }
 
 template <int DX, int DR>
 int norm_grad_with(const NormGradArgs& a, hipStream_t s, const char* what) {
     const unsigned one = (unsigned)a.groups;
-    if (a.cols <= 1024)
-        return launch(norm_grad_kernel<DX, DR, 64, 2>, dim3((unsigned)ceil_div(a.groups, 4)), 256, s, a, what);
+    if (a.cols <= 512) return launch(norm_grad_kernel<DX, DR, 64, 1>, dim3((unsigned)ceil_div(a.groups, 4)), 256, s, a, what);
+    if (a.cols <= 1024) return launch(norm_grad_kernel<DX, DR, 128, 1>, dim3(one), 128, s, a, what);
+    if (a.cols <= 2048) return launch(norm_grad_kernel<DX, DR, 256, 1>, dim3(one), 256, s, a, what);
     if (a.cols <= 4096) return launch(norm_grad_kernel<DX, DR, 512, 1>, dim3(one), 512, s, a, what);
     if (a.cols <= 8192) return launch(norm_grad_kernel<DX, DR, 1024, 1>, dim3(one), 1024, s, a, what);
     if (a.cols <= 16384) return launch(norm_grad_kernel<DX, DR, 1024, 2>, dim3(one), 1024, s, a, what);

@@ -2,6 +2,7 @@
 // its gradient, and tokens sorted by expert and back.  Both rest on one stable sort of small
 // numbers; every sum is formed in a fixed order.
 #include "mx_common.h"
+#include <cstdlib>
 
 namespace {
 
@@ -309,10 +310,37 @@ __global__ void __launch_bounds__(256) embedding_kernel(LookupArgs a) {
     for (int i = 0; i < kEach; ++i) {
         if (!p[i].there) break;
         float x[8];
-        e[i].values(x);
+        e[i].floats(x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = key[i] < a.ids.limit ? x[k] * a.scale : 0.0f;
         put8<DT>((T*)a.out + p[i].row * a.ldo, p[i].c, a.cols, x);
+    }
+}
+
+// Long rows, a wave's vectors all of one token, whose id is then read once: kTokens tokens a
+// workgroup, their vectors kEach at a time.
+template <int DT>
+__global__ void __launch_bounds__(256) embedding_long_kernel(LookupArgs a) {
+    typedef typename Elem<DT>::type T;
+    const int64_t token = (int64_t)blockIdx.x;
+    const uint32_t key = a.ids(token);
+    for (int64_t c0 = threadIdx.x * 8; c0 < a.cols; c0 += 256 * 8 * kEach) {
+        Eight<DT> e[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int64_t c = c0 + i * 256 * 8;
+            if (c < a.cols && key < a.ids.limit) e[i].fetch((const T*)a.table + (int64_t)key * a.ldt, c, a.cols);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int64_t c = c0 + i * 256 * 8;
+            if (c >= a.cols) break;
+            float x[8];
+            e[i].floats(x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = key < a.ids.limit ? x[k] * a.scale : 0.0f;
+            put8<DT>((T*)a.out + token * a.ldo, c, a.cols, x);
+        }
     }
 }
 
@@ -387,7 +415,7 @@ __device__ __forceinline__ void grad_piece(const GradArgs& a) {
                 for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
             }
             float x[8];
-            v[u].values(x);
+            v[u].floats(x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum[k] += x[k];
         }
@@ -419,9 +447,9 @@ __global__ void __launch_bounds__(256) embedding_grad_kernel(GradArgs a) {
     }
 }
 
-// The runs that start in a piece and leave it (each piece's last key's, at most one): their parts, an
-// eighth of them in order by each of eight groups of 32 threads.  A workgroup looks at kJoin pieces,
-// most of which have none, for 256 columns.
+// The runs that start in a piece and leave it (each piece's last key's, at most one).  A workgroup
+// looks at kJoin pieces for 256 columns.  Most such runs end in the next piece: a thread a column
+// adds the two parts.  Of longer ones eight groups of 32 threads add an eighth of the parts each, in order.
 constexpr int kJoin = 8;
 template <int DT>
 __global__ void __launch_bounds__(256) embedding_join_kernel(GradArgs a) {
@@ -430,17 +458,34 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(GradArgs a) {
     const uint32_t across = (uint32_t)((a.cols + 255) / 256), set = blockIdx.x / across, tile = blockIdx.x - set * across;
     const int group = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t c = (int64_t)tile * 256 + lane * 8, col = (int64_t)tile * 256 + threadIdx.x;
-    // every wave finds out for itself which of the pieces have such a run
+    // every wave finds out for itself which of the pieces have such a run, and which of them a long one
     const uint32_t mine = set * kJoin + (threadIdx.x & (kJoin - 1));
-    const uint64_t m0 = (uint64_t)mine * a.piece, m1 = m0 + a.piece;
-    bool starts = m1 < a.n;
+    const uint64_t m0 = (uint64_t)mine * a.piece, m1 = m0 + a.piece, m2 = m1 + a.piece;
+    bool starts = m1 < a.n, goes_on = m2 < a.n;
     if (starts) {
-        const uint32_t key = a.keys[m1];
-        starts = key < a.vocab && a.keys[m1 - 1] == key && !(a.keys[m0] == key && m0 > 0 && a.keys[m0 - 1] == key);
+        const uint32_t key = a.keys[m1], before = a.keys[m1 - 1], first = a.keys[m0], left = m0 > 0 ? a.keys[m0 - 1] : a.vocab;
+        goes_on = goes_on && a.keys[goes_on ? m2 : m1] == key;
+        starts = key < a.vocab && before == key && !(first == key && left == key);
     }
-    for (uint32_t left = (uint32_t)__ballot(starts) & ((1u << kJoin) - 1); left != 0; left &= left - 1) {
-        const uint32_t piece = set * kJoin + (uint32_t)__builtin_ctz(left), key = a.keys[(piece + 1) * a.piece];
-        const uint32_t many = (first_place(a.keys, a.n, key + 1) - 1) / a.piece - piece + 1;
+    const uint32_t all = (uint32_t)__ballot(starts) & ((1u << kJoin) - 1), longs = all & (uint32_t)__ballot(goes_on);
+    const int64_t at = col < a.cols ? col : a.cols - 1;
+    float one[kJoin], two[kJoin];
+    uint32_t key[kJoin];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+        if (!((all & ~longs) >> i & 1)) continue;
+        const uint32_t piece = set * kJoin + i;
+        one[i] = a.parts[(int64_t)(2 * piece + 1) * a.cols + at];
+        two[i] = a.parts[(int64_t)(2 * piece + 2) * a.cols + at];
+        key[i] = a.keys[(piece + 1) * a.piece];
+    }
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i)
+        if (((all & ~longs) >> i & 1) && col < a.cols)
+            ((T*)a.out)[(int64_t)key[i] * a.ldo + col] = from_float<DT>((one[i] + two[i]) * a.scale);
+    for (uint32_t left = longs; left != 0; left &= left - 1) {
+        const uint32_t piece = set * kJoin + (uint32_t)__builtin_ctz(left), run = a.keys[(piece + 1) * a.piece];
+        const uint32_t many = (first_place(a.keys, a.n, run + 1) - 1) / a.piece - piece + 1;
         float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (c < a.cols) {
             const uint32_t each = (many + 7) / 8, to = (group + 1) * each < many ? (group + 1) * each : many;
@@ -449,7 +494,7 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(GradArgs a) {
                 Eight<ZERO_F32> v;
                 v.fetch(a.parts + (int64_t)(2 * (piece + q) + (q == 0)) * a.cols, c, a.cols);
                 float x[8];
-                v.values(x);
+                v.floats(x);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) sum[k] += x[k];
             }
@@ -462,7 +507,7 @@ __global__ void __launch_bounds__(256) embedding_join_kernel(GradArgs a) {
             float v = sums[0][threadIdx.x];
 #pragma unroll
             for (int g = 1; g < 8; ++g) v += sums[g][threadIdx.x];
-            ((T*)a.out)[(int64_t)key * a.ldo + col] = from_float<DT>(v * a.scale);
+            ((T*)a.out)[(int64_t)run * a.ldo + col] = from_float<DT>(v * a.scale);
         }
     }
 }
@@ -498,7 +543,7 @@ __global__ void __launch_bounds__(256) expert_rows_kernel(ExpertArgs a) {
     for (int i = 0; i < kEach; ++i) {
         if (!p[i].there) break;
         float x[8];
-        e[i].values(x);
+        e[i].floats(x);
         for (uint32_t j = 0; j < a.k; ++j) {
             const uint32_t to = (uint32_t)a.place[p[i].row * a.k + j];
             if (to >= slots) continue;
@@ -552,7 +597,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kerne
                 if (from[u] >= used) continue;
                 const float w = weight_of<DT>(a, t.token * a.k + j0 + u);
                 float x[8];
-                e[u].values(x);
+                e[u].floats(x);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) sum[q] += w * x[q];
             }
@@ -592,7 +637,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_grad_
                     if (at[u] < used) e[u].fetch((const T*)a.x + (int64_t)at[u] * a.ldx, c, a.cols);
             }
             float y[8];
-            ey.values(y);
+            ey.floats(y);
             if (a.out != nullptr) {
 #pragma unroll
                 for (uint32_t u = 0; u < kSlots; ++u) {
@@ -608,7 +653,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_grad_
                 for (uint32_t u = 0; u < kSlots; ++u) {
                     if (at[u] >= used) continue;
                     float x[8];
-                    e[u].values(x);
+                    e[u].floats(x);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) dot[u] += x[q] * y[q];
                 }
@@ -735,6 +780,8 @@ int zero_embedding(const void* ids, int32_t id_bytes, int64_t tokens, const void
     const LookupArgs a{{ids, id_bytes == 8, (uint32_t)vocab}, Vectors(tokens, cols), table, ldt, cols, scale, out, ldo};
     if (a.v.workgroups() > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     return with_type(dtype, [&](auto t) {
+        if (cols >= 2048 && !getenv("NOLONG"))
+            return launch(embedding_long_kernel<decltype(t)::value>, dim3((unsigned)tokens), 256, (hipStream_t)stream, a, what);
         return launch(embedding_kernel<decltype(t)::value>, dim3((unsigned)a.v.workgroups()), 256, (hipStream_t)stream, a, what);
     });
 }
