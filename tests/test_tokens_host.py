@@ -37,8 +37,8 @@ def test_sizes(Z):
     assert norm(0, 9) == 0 and norm(9, 0) == 0 and norm(BIG, 4) == 0 and norm(1, 9) == 36
     embed = lib.zero_embedding_grad_workspace_bytes
     assert embed(0, 9, 9) == 0 and embed(9, 9, 0) == 0 and embed(9, BIG, 9) == 0
-    assert embed(1, 9, 9) == 4 * 64 and embed(16, 9, 9) == 4 * 64  # ids and where they came from
-    assert embed(33, 9, 9) == 4 * (128 + 3 * 2 * 9)  # and two parts for each piece of the order
+    assert embed(1, 9, 9) == 4 * 64 and embed(8, 9, 9) == 4 * 64  # ids and where they came from
+    assert embed(33, 9, 9) == 4 * (128 + 5 * 2 * 9)  # and two parts for each piece of the order
     sort = lib.zero_expert_sort_workspace_bytes
     assert sort(0, 9) == 0 and sort(2048, 511) == 0 and sort(2049, 8) == 4 * 2 * 512 and sort(9, BIG) == 0
 

@@ -99,9 +99,11 @@ struct Eight {
         }
     }
     // The same with a row's last elements taken from its last whole vector, moved down: one load instead of
-    // eight, whose registers every kernel that holds several such vectors would pay for.
+    // eight, whose registers every kernel that holds several such vectors would pay for.  WHOLE: cols is a
+    // multiple of eight.
+    template <bool WHOLE = false>
     __device__ __forceinline__ void fetch(const T* row, int64_t c, int64_t cols) {
-        if (c + 8 <= cols) {
+        if (WHOLE || c + 8 <= cols) {
             __builtin_memcpy(v, row + c, sizeof(v));
         } else if (c >= cols) {
             zero();
@@ -196,13 +198,13 @@ struct Eight {
 };
 
 // Eight values, rounded to the type, to a row from column c on; nothing past the row's end.
-template <int DT>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void put8(typename Elem<DT>::type* row, int64_t c, int64_t cols, const float* x) {
     typedef typename Elem<DT>::type T;
     T v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = from_float<DT>(x[i]);
-    if (c + 8 <= cols) {  // whole vectors at any alignment
+    if (WHOLE || c + 8 <= cols) {  // whole vectors at any alignment
         u32x4 w[sizeof(v) / 16];
         __builtin_memcpy(w, v, sizeof(v));
 #pragma unroll

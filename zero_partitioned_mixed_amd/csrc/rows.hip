@@ -12,36 +12,65 @@ namespace {
 
 // 1 / sqrt(mean + eps) = r * pre: squares that leave fp32's range, or that its smallest numbers
 // would swallow, are summed again of elements times pre.
+constexpr int kMostThreads = 1024;
+constexpr int64_t kWaveCols = 512;
 constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p64f;
 __device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-80f ? kPreUp : 1.0f; }
 
-// Threads of a workgroup whose rows take T lanes each: four rows of a wave each, or one row.
-constexpr int row_block(int t) { return t == 64 ? 256 : t; }
-
-// The sums of N values over the T lanes of a row, T = 64 or a whole workgroup, the same bits in every lane.
-// One barrier each: consecutive calls take turns with the places in LDS.
-template <int T, int N>
-struct RowSums {
-    static constexpr int kWaves = T / 64;
-    float at[2][N][kWaves];
+// The lanes of a row: a wave (four rows a workgroup, for up to kWaveCols columns), or a workgroup
+// of as many waves as the row needs with V vectors a lane.
+template <bool WAVE>
+struct RowOf {
+    int64_t row;  // this row, or group of rows
+    int t, lanes;
+    __device__ __forceinline__ RowOf() {
+        if constexpr (WAVE) {
+            row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+            t = threadIdx.x % 64;
+            lanes = 64;
+        } else {
+            row = blockIdx.x;
+            t = threadIdx.x;
+            lanes = blockDim.x;
+        }
+    }
 };
-template <int T, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], RowSums<T, N>& meet, int turn) {
+
+// The sums of N values over the lanes of a row, the same bits in every lane.  One barrier each:
+// consecutive calls take turns with the places in LDS, of which there are sixteen, zeros where there
+// is no wave: four vectors, where a loop over the waves waits for each place in turn.
+constexpr int kMostWaves = kMostThreads / 64;
+template <int N>
+struct RowSums {
+    f32x4 at[2][N][kMostWaves / 4];
+    // before the first sums: the places without a wave
+    __device__ __forceinline__ void clear() {
+        if (threadIdx.x < kMostWaves && threadIdx.x >= blockDim.x / 64) {
+            for (int i = 0; i < 2 * N; ++i) (&((float*)at)[i * kMostWaves])[threadIdx.x] = 0.0f;
+        }
+    }
+};
+template <bool WAVE, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], RowSums<N>& meet, int turn) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
-    if constexpr (T > 64) {
+    if constexpr (!WAVE) {
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) meet.at[turn & 1][i][threadIdx.x / 64] = v[i];
+            for (int i = 0; i < N; ++i) ((float*)meet.at[turn & 1][i])[threadIdx.x / 64] = v[i];
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = meet.at[turn & 1][i][0];
+            f32x4 p[kMostWaves / 4];
 #pragma unroll
-            for (int w = 1; w < T / 64; ++w) v[i] += meet.at[turn & 1][i][w];
+            for (int w = 0; w < kMostWaves / 4; ++w) p[w] = meet.at[turn & 1][i][w];
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kMostWaves / 4; ++w) s += (p[w][0] + p[w][1]) + (p[w][2] + p[w][3]);
+            v[i] = s;
         }
     }
 }
@@ -82,7 +111,7 @@ __device__ __forceinline__ float rounded(float v) {
 }
 
 // h of eight elements: from x, or from x and the residual, then also stored.
-template <int DX, int DR>
+template <int DX, int DR, bool WHOLE>
 __device__ __forceinline__ void sum8(const NormArgs& a, int64_t row, int64_t c, const Eight<DX>& ex, const Eight<DR>& er, float* h) {
     ex.floats(h);
     if (a.residual != nullptr) {
@@ -90,11 +119,11 @@ __device__ __forceinline__ void sum8(const NormArgs& a, int64_t row, int64_t c, 
         er.floats(r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = rounded<DR>(h[i] + r[i]);
-        put8<DR>((typename Elem<DR>::type*)a.h + row * a.ldh, c, a.cols, h);
+        put8<DR, WHOLE>((typename Elem<DR>::type*)a.h + row * a.ldh, c, a.cols, h);
     }
 }
 
-template <int DX, bool MX>
+template <int DX, bool MX, bool WHOLE>
 __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int64_t c, const float* y) {
     if constexpr (MX) {
         const int64_t p = padded(a.cols);
@@ -102,19 +131,20 @@ __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int64_
         *(u32x2*)(a.codes + row * p + c) = codes8_e4m3(y, s);
         if ((threadIdx.x & 3) == 0) a.scales[row * (p / kMxBlock) + c / kMxBlock] = (uint8_t)s;
     } else {
-        put8<DX>((typename Elem<DX>::type*)a.y + row * a.ldy, c, a.cols, y);
+        put8<DX, WHOLE>((typename Elem<DX>::type*)a.y + row * a.ldy, c, a.cols, y);
     }
 }
 
-template <int DX, int DR, int T, int V, bool MX>
-__global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
+template <int DX, int DR, bool WAVE, int V, bool MX, bool WHOLE>
+__global__ void __launch_bounds__(WAVE ? 256 : kMostThreads) norm_kernel(NormArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    constexpr int kRows = row_block(T) / T;
-    __shared__ RowSums<T, 1> meet;
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
-    if (row >= a.tokens) return;  // whole waves; with T > 64 none
-    const int t = threadIdx.x % T;
+    __shared__ RowSums<1> meet;
+    const RowOf<WAVE> of;
+    if constexpr (!WAVE) meet.clear();
+    const int64_t row = of.row;
+    if (row >= a.tokens) return;  // whole waves; where a workgroup takes a row none
+    const int t = of.t, T = of.lanes;
     const int64_t end = MX ? padded(a.cols) : a.cols;
     Eight<DX> ex[V], ew[V];
     Eight<DR> er[V];
@@ -123,9 +153,9 @@ __global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
         if (c < a.cols) {
-            ex[v].fetch((const X*)a.x + row * a.ldx, c, a.cols);
-            if (a.residual != nullptr) er[v].fetch((const R*)a.residual + row * a.ldr, c, a.cols);
-            ew[v].fetch((const X*)a.w, c, a.cols);
+            ex[v].template fetch<WHOLE>((const X*)a.x + row * a.ldx, c, a.cols);
+            if (a.residual != nullptr) er[v].template fetch<WHOLE>((const R*)a.residual + row * a.ldr, c, a.cols);
+            ew[v].template fetch<WHOLE>((const X*)a.w, c, a.cols);
         }
     }
     float ss[1] = {0.0f};
@@ -133,7 +163,7 @@ __global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
         if (c < a.cols) {
-            sum8<DX, DR>(a, row, c, ex[v], er[v], h[v]);
+            sum8<DX, DR, WHOLE>(a, row, c, ex[v], er[v], h[v]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[v][i] = 0.0f;
@@ -141,7 +171,7 @@ __global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
         ss[0] += squares8(h[v]);
     }
     const float n = (float)a.cols;
-    row_sums<T, 1>(ss, meet, 0);
+    row_sums<WAVE>(ss, meet, 0);
     float q = ss[0] / n + a.eps;
     const float pre = pre_of(q);
     if (pre != 1.0f) {
@@ -152,7 +182,7 @@ __global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
             for (int i = 0; i < 8; ++i) h[v][i] *= pre;
             ss[0] += squares8(h[v]);
         }
-        row_sums<T, 1>(ss, meet, 1);
+        row_sums<WAVE>(ss, meet, 1);
         q = ss[0] / n + a.eps * pre * pre;
     }
     const Root root(q);
@@ -172,7 +202,7 @@ __global__ void __launch_bounds__(row_block(T)) norm_kernel(NormArgs a) {
             h[v][i] = root.times(h[v][i] * w[i]);
             if (MX && c + i >= a.cols) h[v][i] = 0.0f;  // also where r is not finite
         }
-        norm_out8<DX, MX>(a, row, c, h[v]);
+        norm_out8<DX, MX, WHOLE>(a, row, c, h[v]);
     }
 }
 
@@ -182,7 +212,7 @@ template <int DX, int DR, bool MX>
 __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    __shared__ RowSums<kWide, 1> meet;
+    __shared__ RowSums<1> meet;
     const int64_t row = blockIdx.x, end = MX ? padded(a.cols) : a.cols;
     const int64_t c0 = (int64_t)threadIdx.x * 8;
     const X* const x = (const X*)a.x + row * a.ldx;
@@ -196,7 +226,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
                 Eight<DR> er;
                 ex.fetch(x, c, a.cols);
                 if (a.residual != nullptr) er.fetch((const R*)a.residual + row * a.ldr, c, a.cols);
-                sum8<DX, DR>(a, row, c, ex, er, h);
+                sum8<DX, DR, false>(a, row, c, ex, er, h);
             } else {
                 Eight<DR> eh;
                 eh.fetch(hr, c, a.cols);
@@ -206,7 +236,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
             for (int i = 0; i < 8; ++i) h[i] *= pre;
             ss[0] += squares8(h);
         }
-        row_sums<kWide, 1>(ss, meet, first);
+        row_sums<false>(ss, meet, first);
         return ss[0];
     };
     const float n = (float)a.cols;
@@ -232,7 +262,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * pre * w[i]) : 0.0f;
-        norm_out8<DX, MX>(a, row, c, h);
+        norm_out8<DX, MX, false>(a, row, c, h);
     }
 }
 
@@ -240,7 +270,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
 //   dh' = (g - u mean(g u)) / root + dh,  dw = sum over tokens of dy u
 // dh' goes to the residual's gradient and, rounded to x's type, to x's.  root is computed again
 // from h, which has to be read anyway: nothing but h is kept for the backward pass.
-// A workgroup takes rows kGroups apart and holds its columns' part of dw in registers; the
+// A workgroup takes rows `groups` apart and holds its columns' part of dw in registers; the
 // parts are summed in order by a second launch.  Bound by memory.
 struct NormGradArgs {
     const void *dy, *h, *w, *dh;
@@ -253,8 +283,6 @@ struct NormGradArgs {
     void* dw;
     int groups;
 };
-
-constexpr int kGradGroups = 512;
 
 // dh' and u of eight elements.
 __device__ __forceinline__ void norm_grad8(const float* h, const float* y, const float* w, float pre, float r, float m, float* u,
@@ -278,46 +306,53 @@ __device__ __forceinline__ void norm_sums8(const float* h, const float* y, const
     s[1] += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
 }
 
-template <int DX, int DR, int T, int V>
-__global__ void __launch_bounds__(row_block(T)) norm_grad_kernel(NormGradArgs a) {
+template <int DX, int DR, bool WAVE, int V, bool WHOLE>
+__global__ void __launch_bounds__(WAVE ? 256 : kMostThreads) norm_grad_kernel(NormGradArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    constexpr int kRows = row_block(T) / T;
-    __shared__ RowSums<T, 2> meet;
-    const int t = threadIdx.x % T;
-    const int64_t group = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+    __shared__ RowSums<2> meet;
+    const RowOf<WAVE> of;
+    if constexpr (!WAVE) meet.clear();
+    const int64_t group = of.row;
+    const int t = of.t, T = of.lanes;
     const float n = (float)a.cols;
     struct Row {
         Eight<DX> y[V];
         Eight<DR> h[V], d[V];
-        __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int t) {
+        __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int t, int T) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int64_t c = (int64_t)(v * T + t) * 8;
                 if (c >= a.cols) break;
-                h[v].fetch((const R*)a.h + row * a.ldh, c, a.cols);
-                y[v].fetch((const X*)a.dy + row * a.lddy, c, a.cols);
-                if (a.dh != nullptr) d[v].fetch((const R*)a.dh + row * a.lddh, c, a.cols);
+                h[v].template fetch<WHOLE>((const R*)a.h + row * a.ldh, c, a.cols);
+                y[v].template fetch<WHOLE>((const X*)a.dy + row * a.lddy, c, a.cols);
+                if (a.dh != nullptr) d[v].template fetch<WHOLE>((const R*)a.dh + row * a.lddh, c, a.cols);
             }
         }
     };
+    constexpr bool kAhead = V == 1;  // the next row is on its way while this one's sums meet; with V = 2 registers run out,
+                                     // and the weights too are read again for each row
     Eight<DX> ew[V];
+    auto weights = [&](int v, float* w) {
+        const int64_t c = (int64_t)(v * T + t) * 8;
+        if (!kAhead) ew[v].template fetch<WHOLE>((const X*)a.w, c, a.cols);
+        ew[v].floats(w);
+    };
     float dw[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
-        if (c < a.cols) ew[v].fetch((const X*)a.w, c, a.cols);
+        if (kAhead && c < a.cols) ew[v].template fetch<WHOLE>((const X*)a.w, c, a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
     }
-    constexpr bool kAhead = V == 1;  // the next row is on its way while this one's sums meet; with V = 2 registers run out
     Row next;
-    if (kAhead && group < a.tokens) next.load(a, group, t);
+    if (kAhead && group < a.tokens) next.load(a, group, t, T);
     int turn = 0;
     for (int64_t row = group; row < a.tokens; row += a.groups) {
-        if (!kAhead) next.load(a, row, t);
+        if (!kAhead) next.load(a, row, t, T);
         const Row e = next;
-        if (kAhead && row + a.groups < a.tokens) next.load(a, row + a.groups, t);
+        if (kAhead && row + a.groups < a.tokens) next.load(a, row + a.groups, t, T);
         auto sums = [&](float pre, float (&s)[2]) {
             s[0] = s[1] = 0.0f;
 #pragma unroll
@@ -326,10 +361,10 @@ __global__ void __launch_bounds__(row_block(T)) norm_grad_kernel(NormGradArgs a)
                 float h[8], y[8], w[8];
                 e.h[v].floats(h);
                 e.y[v].floats(y);
-                ew[v].floats(w);
+                weights(v, w);
                 norm_sums8(h, y, w, pre, s);
             }
-            row_sums<T, 2>(s, meet, turn++);
+            row_sums<WAVE>(s, meet, turn++);
         };
         float s[2];
         sums(1.0f, s);
@@ -347,20 +382,20 @@ __global__ void __launch_bounds__(row_block(T)) norm_grad_kernel(NormGradArgs a)
             float h[8], y[8], w[8], u[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             e.h[v].floats(h);
             e.y[v].floats(y);
-            ew[v].floats(w);
+            weights(v, w);
             if (a.dh != nullptr) e.d[v].floats(d);
             norm_grad8(h, y, w, pre, r, m, u, d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[v][i] += y[i] * u[i];
-            if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
-            if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
+            if (a.dr != nullptr) put8<DR, WHOLE>((R*)a.dr + row * a.lddr, c, a.cols, d);
+            if (a.dx != nullptr) put8<DX, WHOLE>((X*)a.dx + row * a.lddx, c, a.cols, d);
         }
     }
     if (a.parts == nullptr || group >= a.groups) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
-        if (c < a.cols) put8<ZERO_F32>(a.parts + group * a.cols, c, a.cols, dw[v]);
+        if (c < a.cols) put8<ZERO_F32, WHOLE>(a.parts + group * a.cols, c, a.cols, dw[v]);
     }
 }
 
@@ -369,7 +404,7 @@ template <int DX, int DR>
 __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
-    __shared__ RowSums<kWide, 2> meet;
+    __shared__ RowSums<2> meet;
     const int64_t c0 = (int64_t)threadIdx.x * 8;
     const float n = (float)a.cols;
     bool first = true;
@@ -391,7 +426,7 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
                 ew.floats(w);
                 norm_sums8(h, y, w, pre, s);
             }
-            row_sums<kWide, 2>(s, meet, turn++);
+            row_sums<false>(s, meet, turn++);
         };
         float s[2];
         sums(1.0f, s);
@@ -546,17 +581,25 @@ int with_type(int32_t dt, F f) {
     return with_types(dt, dt, [&](auto x, auto) { return f(x); });
 }
 
-template <int DX, int DR, bool MX>
+// Threads for a row of n columns, v vectors each.
+int threads_for(int64_t n, int v) { return (int)round_up(ceil_div(n, 8 * v), 64); }
+
+template <int DX, int DR, bool MX, bool WHOLE>
 int norm_with(const NormArgs& a, hipStream_t s, const char* what) {
     const int64_t n = MX ? padded(a.cols) : a.cols;
-    const unsigned one = (unsigned)a.tokens, four = (unsigned)ceil_div(a.tokens, 4);
-    if (n <= 512) return launch(norm_kernel<DX, DR, 64, 1, MX>, dim3(four), 256, s, a, what);
-    if (n <= 1024) return launch(norm_kernel<DX, DR, 64, 2, MX>, dim3(four), 256, s, a, what);
-    if (n <= 2048) return launch(norm_kernel<DX, DR, 256, 1, MX>, dim3(one), 256, s, a, what);
-    if (n <= 4096) return launch(norm_kernel<DX, DR, 256, 2, MX>, dim3(one), 256, s, a, what);
-    if (n <= 8192) return launch(norm_kernel<DX, DR, 512, 2, MX>, dim3(one), 512, s, a, what);
-    if (n <= 16384) return launch(norm_kernel<DX, DR, 1024, 2, MX>, dim3(one), 1024, s, a, what);
-    return launch(norm_wide_kernel<DX, DR, MX>, dim3(one), kWide, s, a, what);
+    const dim3 one((unsigned)a.tokens);
+    if (n <= kWaveCols)
+        return launch(norm_kernel<DX, DR, true, 1, MX, WHOLE>, dim3((unsigned)ceil_div(a.tokens, 4)), 256, s, a, what);
+    if (n <= 2048) return launch(norm_kernel<DX, DR, false, 1, MX, WHOLE>, one, threads_for(n, 1), s, a, what);
+    if (n <= 16 * kMostThreads) return launch(norm_kernel<DX, DR, false, 2, MX, WHOLE>, one, threads_for(n, 2), s, a, what);
+    return launch(norm_wide_kernel<DX, DR, MX>, one, kWide, s, a, what);
+}
+template <bool MX>
+int norm_any(const NormArgs& a, int32_t dx, int32_t dr, hipStream_t s, const char* what) {
+    return with_types(dx, dr, [&](auto x, auto r) {
+        if (a.cols % 8 == 0) return norm_with<decltype(x)::value, decltype(r)::value, MX, true>(a, s, what);
+        return norm_with<decltype(x)::value, decltype(r)::value, MX, false>(a, s, what);
+    });
 }
 
 // The checks shared by the norm's two forms.
@@ -585,22 +628,23 @@ int check_norm(const NormArgs& a, int32_t dx, int32_t dr, const char* what) {
     return ZERO_OK;
 }
 
-// Groups of rows that a gradient call sums dw over: workgroups, or waves where a wave takes a row.
+// Groups of rows that a gradient call sums dw over: waves where a wave takes a row, else workgroups, as many
+// as are at work at once.
 int64_t grad_groups(int64_t tokens, int64_t cols) {
-    const int64_t most = cols <= 512 ? 4 * kGradGroups : cols <= 2048 ? 2 * kGradGroups : kGradGroups;
+    const int64_t most = cols <= kWaveCols ? 2048 : cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256;
     return tokens < most ? tokens : most;
 }
 
-template <int DX, int DR>
+template <int DX, int DR, bool WHOLE>
 int norm_grad_with(const NormGradArgs& a, hipStream_t s, const char* what) {
-    const unsigned one = (unsigned)a.groups;
-    if (a.cols <= 512) return launch(norm_grad_kernel<DX, DR, 64, 1>, dim3((unsigned)ceil_div(a.groups, 4)), 256, s, a, what);
-    if (a.cols <= 1024) return launch(norm_grad_kernel<DX, DR, 128, 1>, dim3(one), 128, s, a, what);
-    if (a.cols <= 2048) return launch(norm_grad_kernel<DX, DR, 256, 1>, dim3(one), 256, s, a, what);
-    if (a.cols <= 4096) return launch(norm_grad_kernel<DX, DR, 512, 1>, dim3(one), 512, s, a, what);
-    if (a.cols <= 8192) return launch(norm_grad_kernel<DX, DR, 1024, 1>, dim3(one), 1024, s, a, what);
-    if (a.cols <= 16384) return launch(norm_grad_kernel<DX, DR, 1024, 2>, dim3(one), 1024, s, a, what);
-    return launch(norm_grad_wide_kernel<DX, DR>, dim3(one), kWide, s, a, what);
+    const dim3 one((unsigned)a.groups);
+    if (a.cols <= kWaveCols)
+        return launch(norm_grad_kernel<DX, DR, true, 1, WHOLE>, dim3((unsigned)ceil_div(a.groups, 4)), 256, s, a, what);
+    if (a.cols <= 8 * kMostThreads)
+        return launch(norm_grad_kernel<DX, DR, false, 1, WHOLE>, one, threads_for(a.cols, 1), s, a, what);
+    if (a.cols <= 16 * kMostThreads)
+        return launch(norm_grad_kernel<DX, DR, false, 2, WHOLE>, one, threads_for(a.cols, 2), s, a, what);
+    return launch(norm_grad_wide_kernel<DX, DR>, one, kWide, s, a, what);
 }
 
 }  // namespace
@@ -625,9 +669,7 @@ int zero_rms_norm(const void* x, int32_t dtype, int64_t ldx, const void* residua
         (residual != nullptr && overlap(to, values_at(residual, dr, tokens, cols, ldr))) ||
         (h != nullptr && overlap(to, values_at(h, dr, tokens, cols, ldh))))
         return fail(ZERO_EINVAL, "%s: the result overlaps an input or the sum", what);
-    return with_types(dtype, dr, [&](auto dx, auto dr_) {
-        return norm_with<decltype(dx)::value, decltype(dr_)::value, false>(a, (hipStream_t)stream, what);
-    });
+    return norm_any<false>(a, dtype, dr, (hipStream_t)stream, what);
 }
 
 int zero_rms_norm_mx8(const void* x, int32_t dtype, int64_t ldx, const void* residual, int32_t residual_dtype, int64_t ldr,
@@ -647,9 +689,7 @@ int zero_rms_norm_mx8(const void* x, int32_t dtype, int64_t ldx, const void* res
             (residual != nullptr && (overlap(p, values_at(residual, dr, tokens, cols, ldr)) ||
                                      overlap(p, values_at(h, dr, tokens, cols, ldh)))))
             return fail(ZERO_EINVAL, "%s: codes or scales overlap an input or the sum", what);
-    return with_types(dtype, dr, [&](auto dx, auto dr_) {
-        return norm_with<decltype(dx)::value, decltype(dr_)::value, true>(a, (hipStream_t)stream, what);
-    });
+    return norm_any<true>(a, dtype, dr, (hipStream_t)stream, what);
 }
 
 size_t zero_rms_norm_grad_workspace_bytes(int64_t tokens, int64_t cols) {
@@ -695,7 +735,8 @@ int zero_rms_norm_grad(const void* dy, int64_t lddy, const void* h, int32_t h_dt
     }
     if (tokens > 0) {
         rc = with_types(dtype, h_dtype, [&](auto x, auto r) {
-            return norm_grad_with<decltype(x)::value, decltype(r)::value>(a, s, what);
+            if (cols % 8 == 0) return norm_grad_with<decltype(x)::value, decltype(r)::value, true>(a, s, what);
+            return norm_grad_with<decltype(x)::value, decltype(r)::value, false>(a, s, what);
         });
         if (rc != ZERO_OK) return rc;
     }

@@ -2,7 +2,6 @@
 // its gradient, and tokens sorted by expert and back.  Both rest on one stable sort of small
 // numbers; every sum is formed in a fixed order.
 #include "mx_common.h"
-#include <cstdlib>
 
 namespace {
 
@@ -346,12 +345,12 @@ __global__ void __launch_bounds__(256) embedding_long_kernel(LookupArgs a) {
 
 // The gradient: row v is scale times the sum of dy over the tokens whose id is v, in their order,
 // in fp32, rounded once; zeros where there is none.  With the tokens sorted by id a row's tokens
-// are a run.  The sorted order is cut into pieces of kPiece tokens or more, so that a frequent word's
+// are a run.  The sorted order is cut into pieces of 8 tokens or more, so that a frequent word's
 // long run is as much work for a piece as many short ones: a piece sums each of its runs, writes
 // those that lie in it to their rows, and of the two that may leave it the sums so far; a second
 // launch adds what belongs together, in order.  Further workgroups of the first launch write
 // the zeros, which are nearly all of a large table's gradient.  Bound by memory.
-constexpr int kPiece = 16, kMostPieces = 4096, kZeroVectors = 16384, kZeroRows = 256, kZeroGroups = 1024;
+constexpr int kZeroVectors = 16384, kZeroRows = 256, kZeroGroups = 1024;
 
 struct GradArgs {
     const uint32_t *keys, *from;  // sorted
@@ -587,19 +586,23 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kerne
         for (uint32_t j0 = 0; j0 < a.k; j0 += kSlots) {
             Eight<DT> e[kSlots];
             uint32_t from[kSlots];
+            float w[kSlots];
 #pragma unroll
             for (uint32_t u = 0; u < kSlots; ++u) {
                 from[u] = j0 + u < a.k ? (uint32_t)a.place[t.token * a.k + j0 + u] : 0xFFFFFFFFu;
+                w[u] = j0 + u < a.k ? weight_of<DT>(a, t.token * a.k + j0 + u) : 0.0f;
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kSlots; ++u) {
                 if (from[u] < used) e[u].fetch((const T*)a.x + (int64_t)from[u] * a.ldx, c, a.cols);
             }
 #pragma unroll
             for (uint32_t u = 0; u < kSlots; ++u) {
                 if (from[u] >= used) continue;
-                const float w = weight_of<DT>(a, t.token * a.k + j0 + u);
                 float x[8];
                 e[u].floats(x);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) sum[q] += w * x[q];
+                for (int q = 0; q < 8; ++q) sum[q] += w[u] * x[q];
             }
         }
         put8<DT>((T*)a.out + t.token * a.ldo, c, a.cols, sum);
@@ -738,9 +741,12 @@ int check_space(const void* ws, size_t ws_bytes, size_t need, const char* what) 
     return ZERO_OK;
 }
 
+// Tokens in a piece: few where there are few tokens, for their latency; 32 where the parts that pieces
+// leave would cost (32768 tokens of 4096 columns: 16 write and read 134 MB of them); no more than 4096 pieces.
 int64_t grad_piece_of(int64_t n) {
-    const int64_t p = round_up(ceil_div(n, kMostPieces), 8);
-    return p > kPiece ? p : kPiece;
+    int64_t p = n / 1024 < 8 ? 8 : n / 1024 < 32 ? n / 1024 : 32;
+    if (p < ceil_div(n, 4096)) p = ceil_div(n, 4096);
+    return round_up(p, 8);
 }
 int64_t grad_parts(int64_t n, int64_t cols) { return n > grad_piece_of(n) ? 2 * ceil_div(n, grad_piece_of(n)) * cols : 0; }
 
@@ -780,7 +786,7 @@ int zero_embedding(const void* ids, int32_t id_bytes, int64_t tokens, const void
     const LookupArgs a{{ids, id_bytes == 8, (uint32_t)vocab}, Vectors(tokens, cols), table, ldt, cols, scale, out, ldo};
     if (a.v.workgroups() > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     return with_type(dtype, [&](auto t) {
-        if (cols >= 2048 && !getenv("NOLONG"))
+        if (cols >= 2048)
             return launch(embedding_long_kernel<decltype(t)::value>, dim3((unsigned)tokens), 256, (hipStream_t)stream, a, what);
         return launch(embedding_kernel<decltype(t)::value>, dim3((unsigned)a.v.workgroups()), 256, (hipStream_t)stream, a, what);
     });
