@@ -472,16 +472,31 @@ int matmul_with(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what)
     });
 }
 
-typedef Mixed<256, 256, 128, 128, 3> Mixed256;
-typedef Mixed<128, 128, 64, 64, 3> Mixed128;
-typedef Mixed<64, 64, 32, 32, 4> Mixed64;
+// At 8192 x 8192 x 8192, us: eight waves with 64 x 128 each 474, four with 128 x 128 490 (without the
+// loads to LDS 404, without the matrix instructions 362: both keep the waves waiting for their turn to
+// issue).  First fragments read ahead of the barrier, or loads spread between the matrix instructions: no faster.
+typedef Mixed<256, 256, 64, 128, 3> Mixed256;
+typedef Mixed<128, 128, 64, 64, 3> Mixed128;  // two workgroups on a CU
+typedef Mixed<64, 64, 32, 32, 4> Mixed64;     // two or three
+
+// The shape that a product takes: microseconds a slab as measured (256 CUs, k = 4096) times the rounds that its tiles
+// need.  us at 128 x 4096 by tiles of 64, 128 and 256: 10, 19, 48; 512 x 4096: 23, 21, 50; 1024 x 4096: 42, 26, 52;
+// 300 x 11008: 42, 35, 53; 2048 x 11008: 206, 130, 112.
+int pick_mixed(int64_t t256, int64_t t128, int64_t t64) {
+    const double c256 = 1.55 * (double)ceil_div(t256, 256);
+    const double c128 = t128 <= 256 ? 0.75 : t128 <= 512 ? 0.75 + 0.65 * (double)t128 / 512 : 1.4 * (double)ceil_div(t128, 512);
+    const double c64 = t64 <= 256 ? 0.4 : 0.67 * (double)ceil_div(t64, 512);
+    return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+}
 
 // Values of A quantised in the product's own kernel.
 bool few_values(int64_t m, int64_t k) { return m <= 32 && m * padded(k) <= kFew8; }
 
 int matmul(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what) {
     g.vector = aligned(g.c, 4 * elem_bytes(c_dtype)) && g.ldc % 4 == 0;
-    if (g.m <= 32) {
+    // Few rows against tiles, us: 4096 x 4096, 8 rows 5.9 and 11.4, 32 rows 7.8 and 9.5; 11008 x 4096, where tiles too
+    // fill the CUs, 8 rows 9.2 and 10.3, 16 rows 10.7 and 10.2, 32 rows 14.3 and 10.6.
+    if (g.m <= 8 || (g.m <= 32 && g.n <= 64 * 128)) {
         const Few8Args f{g, nullptr, 0, 0};
         return with_dtype(c_dtype, [&](auto t) {
             return launch(mx8_few_kernel<ZERO_F32, decltype(t)::value, false>, dim3((unsigned)ceil_div(g.n, 32)),
@@ -489,9 +504,11 @@ int matmul(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what) {
         });
     }
     auto tiles = [&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); };
-    if (tiles(256) >= 256) return matmul_with<Mixed256>(g, c_dtype, s, what);
-    if (tiles(128) >= 256) return matmul_with<Mixed128>(g, c_dtype, s, what);
-    return matmul_with<Mixed64>(g, c_dtype, s, what);
+    switch (pick_mixed(tiles(256), tiles(128), tiles(64))) {
+        case 256: return matmul_with<Mixed256>(g, c_dtype, s, what);
+        case 128: return matmul_with<Mixed128>(g, c_dtype, s, what);
+        default: return matmul_with<Mixed64>(g, c_dtype, s, what);
+    }
 }
 
 int few_of_values(const Few8Args& f, int32_t a_dtype, int32_t c_dtype, hipStream_t s, const char* what) {
