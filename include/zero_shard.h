@@ -855,7 +855,8 @@ int zero_expert_sort(const void *ids_dev, int32_t id_bytes, int64_t slots, int64
                      size_t ws_bytes, void *stream);
 
 /* rows[place[slot]] = x[slot / k]; zeros at places from *used_dev on (used_dev =
- * offsets + experts).  rows: tokens k of them. */
+ * offsets + experts).  rows: tokens k of them.  In this call and the next two a place
+ * outside [0, tokens k) is left out. */
 int zero_expert_rows(const void *x_dev, int32_t dtype, int64_t ldx, const int32_t *place_dev,
                      const int32_t *used_dev, int64_t tokens, int64_t k, int64_t cols,
                      void *rows_dev, int64_t ldr, void *stream);

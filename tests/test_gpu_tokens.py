@@ -861,6 +861,144 @@ def test_two_streams_at_once(Z):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
 
 
+CODES = {F16: 1, BF16: 2, F32: 3}
+
+
+def c_call(Z, name, *args):
+    """A C call on the current stream: tensors by their pointers."""
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    rc = getattr(Z._lib, name)(*args, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0, Z.zero_last_error()
+
+
+def wide_like(x):
+    """Room for x's values in rows of a wider buffer, which holds 7 everywhere."""
+    return strided(torch.full_like(x, 7.0))
+
+
+def gaps_untouched(wide, cols, at=3):
+    assert (wide[:, :at] == 7).all() and (wide[:, at + cols:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,cols", [(5, 3), (40, 77), (33, 1024), (7, 5001), (2, 20001)])
+def test_strided_results_and_results_in_place(Z, tokens, cols, dtype):
+    """Results in rows of wider buffers, whose gaps stay as they were; results in their inputs' place."""
+    code, big = CODES[dtype], cols + 5
+    x, r, w = randn(tokens, cols, seed=1, dtype=dtype), randn(tokens, cols, seed=2), randn(cols, seed=3, dtype=dtype)
+    dy, dh = randn(tokens, cols, seed=4, dtype=dtype), randn(tokens, cols, seed=5)
+    y, h = Z.rms_norm(x, w, r)
+    eps = 1e-6
+    (yw, yb), (hw, hb) = wide_like(x), wide_like(r)
+    c_call(Z, "zero_rms_norm", x, code, cols, r, 3, cols, w, tokens, cols, eps, yw, big, hw, big)
+    assert torch.equal(yw, y) and torch.equal(hw, h)
+    gaps_untouched(yb, cols)
+    gaps_untouched(hb, cols)
+    xp, rp = x.clone(), r.clone()
+    c_call(Z, "zero_rms_norm", xp, code, cols, rp, 3, cols, w, tokens, cols, eps, xp, cols, rp, cols)
+    assert torch.equal(xp, y) and torch.equal(rp, h)
+    rp = r.clone()
+    q, qp = Z.rms_norm_mx8(x, w, r)[0], Z.MX8.alloc(tokens, cols, "cuda")
+    c_call(Z, "zero_rms_norm_mx8", x, code, cols, rp, 3, cols, w, tokens, cols, eps, *qp._places, rp, cols)
+    assert torch.equal(rp, h) and torch.equal(qp.codes, q.codes) and torch.equal(qp.scales, q.scales)
+
+    leaves = [t.clone().requires_grad_() for t in (x, w, r)]
+    dx, dw, dr = torch.autograd.grad(Z.rms_norm(*leaves), leaves, (dy, dh))
+    (xw, xb), (rw, rb), dwp = wide_like(x), wide_like(r), torch.empty_like(w)
+    size = Z._lib.zero_rms_norm_grad_workspace_bytes(tokens, cols)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    c_call(Z, "zero_rms_norm_grad", dy, cols, h, 3, cols, w, code, dh, cols, tokens, cols, eps, xw, big, rw, big, dwp, ws, size)
+    assert torch.equal(xw, dx) and torch.equal(rw, dr) and torch.equal(dwp, dw)
+    gaps_untouched(xb, cols)
+    gaps_untouched(rb, cols)
+
+    s = randn(tokens, cols, seed=6, dtype=dtype)
+    want = Z.dropout(x, 0.3, 5, 6, residual=s)
+    yw, yb = wide_like(x)
+    c_call(Z, "zero_dropout", x, code, cols, s, cols, tokens, cols, 0.3, 5, 6, None, yw, big)
+    assert torch.equal(yw, want)
+    gaps_untouched(yb, cols)
+    for place in (x.clone(), s.clone()):
+        a, b = (place, s) if torch.equal(place, x) else (x, place)
+        c_call(Z, "zero_dropout", a, code, cols, b, cols, tokens, cols, 0.3, 5, 6, None, place, cols)
+        assert torch.equal(place, want)
+
+    ids = torch.arange(tokens, device="cuda") * 3 % 7 - 1
+    table = randn(6, cols, seed=7, dtype=dtype).requires_grad_()
+    e = Z.embedding(ids, table, scale=3.0)
+    de, = torch.autograd.grad(e, table, dy)
+    (ew, eb), (gw, gb) = wide_like(x), wide_like(table.detach())
+    c_call(Z, "zero_embedding", ids, 8, tokens, table.detach(), code, cols, 6, cols, 3.0, ew, big)
+    size = Z._lib.zero_embedding_grad_workspace_bytes(tokens, 6, cols)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    c_call(Z, "zero_embedding_grad", ids, 8, tokens, dy, code, cols, 6, cols, 3.0, gw, big, ws, size)
+    assert torch.equal(ew, e) and torch.equal(gw, de)
+    gaps_untouched(eb, cols)
+    gaps_untouched(gb, cols)
+
+    plan = Z.expert_sort(choices(tokens, 2, 3, 8, 0.2), 3)
+    used = plan.offsets.data_ptr() + 12
+    rows = Z.expert_rows(x, plan)
+    g = torch.rand(tokens, 2, device="cuda", generator=gen(9)).requires_grad_()
+    z = randn(tokens * 2, cols, seed=10, dtype=dtype).requires_grad_()
+    c = Z.expert_combine(z, g, plan)
+    dz, dg = torch.autograd.grad(c, (z, g), dy)
+    (rw, rb), (cw, cb), (zw, zb), dgp = wide_like(rows), wide_like(x), wide_like(rows), torch.empty_like(dg)
+    c_call(Z, "zero_expert_rows", x, code, cols, plan.place, used, tokens, 2, cols, rw, big)
+    c_call(Z, "zero_expert_combine", z.detach(), code, cols, plan.place, used, g.detach(), 3, tokens, 2, cols, cw, big)
+    c_call(Z, "zero_expert_combine_grad", dy, cols, z.detach(), code, cols, plan.place, used, g.detach(), 3, tokens, 2, cols, zw, big, dgp)
+    assert torch.equal(rw, rows) and torch.equal(cw, c) and torch.equal(zw, dz) and torch.equal(dgp, dg)
+    for b in (rb, cb, zb):
+        gaps_untouched(b, cols)
+
+
+def test_expert_places_out_of_range(Z):
+    """A plan whose memory holds anything: places outside the rows are left out, and no more rows are used than there are."""
+    tokens, k, cols = 6, 2, 40
+    place = torch.tensor([[0, -1], [1, 99], [2, -(1 << 31)], [3, (1 << 31) - 1], [4, 12], [5, 6]], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, (1 << 31) - 1], dtype=torch.int32, device="cuda")
+    plan = Z.ExpertPlan(torch.zeros(12, dtype=torch.int32, device="cuda"), place, offsets, tokens, k, 1)
+    x, z, w, dy = randn(tokens, cols), randn(12, cols, seed=1), torch.rand(tokens, k, device="cuda") + 0.5, randn(tokens, cols, seed=2)
+    there = ((place >= 0) & (place < 12)).double()
+    at = place.clamp(0, 11).long()
+    want = (z.double()[at.view(-1)].view(tokens, k, cols) * (w.double() * there)[:, :, None]).sum(1)
+    z.requires_grad_()
+    w.requires_grad_()
+    y = Z.expert_combine(z, w, plan)
+    near(y.detach(), want, 4 * U * want.abs() + 4 * U)
+    dw, = torch.autograd.grad(y, w, dy)
+    assert not dw[there == 0].any() and dw[there == 1].all()
+    c_rows = torch.full((12, cols), 7.0, device="cuda")
+    c_call(Z, "zero_expert_rows", x, 3, cols, place, offsets.data_ptr() + 4, tokens, k, cols, c_rows, cols)
+    assert torch.equal(c_rows[:6], x) and torch.equal(c_rows[6], x[5]) and (c_rows[7:] == 7).all()
+
+
+def test_far_rows(Z):
+    """Rows more than 2^31 elements apart."""
+    far, rows, cols = (1 << 31) + 8, 3, 1001
+    base = torch.empty((rows - 1) * far + cols, dtype=F16, device="cuda")
+    x = base.as_strided((rows, cols), (far, 1))
+    x.copy_(randn(rows, cols))
+    near_x, w = x.contiguous(), randn(cols, seed=1, dtype=F16)
+    dy = randn(rows, cols, seed=2, dtype=F16)
+
+    def work(x):
+        leaf = x.detach().requires_grad_()
+        y = Z.rms_norm(leaf, w)
+        ids = torch.tensor([2, 0, 2, 1], device="cuda")
+        e = Z.embedding(ids, leaf)
+        plan = Z.expert_sort(torch.tensor([[1], [0], [1]], device="cuda"), 2)
+        gates = torch.ones(rows, 1, device="cuda").requires_grad_()
+        c = Z.expert_combine(leaf, gates, plan)
+        grad = torch.autograd.grad
+        with torch.no_grad():
+            q = Z.mx8_quantize(x)
+            more = [q.codes, q.scales, Z.mx8_matmul(x, Z.mx4_quantize(x)), Z.expert_rows(x, plan)]
+        return [y.detach(), grad(y, leaf, dy)[0], Z.dropout(x, 0.5, 1, residual=x), e.detach(), c.detach(), grad(c, gates, x)[0], *more]
+
+    assert all(torch.equal(a, b) for a, b in zip(work(x), work(near_x)))
+
+
 def test_without_gradients(Z):
     """Where torch records nothing, nothing is kept."""
     x, w = randn(4, 64).requires_grad_(), randn(64, seed=1)

@@ -527,6 +527,12 @@ struct ExpertArgs {
     int64_t ldo;
 };
 
+// Slots with an expert; places beyond are left out, whatever the plan's memory holds.
+__device__ __forceinline__ uint32_t used_of(const ExpertArgs& a) {
+    const uint32_t used = (uint32_t)*a.used, slots = a.tokens * a.k;
+    return used < slots ? used : slots;
+}
+
 // Sorted rows from tokens' rows: a token's row is read once and written k times; zeros behind the last.
 template <int DT>
 __global__ void __launch_bounds__(256) expert_rows_kernel(ExpertArgs a) {
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(256) expert_rows_kernel(ExpertArgs a) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
         if (p[i].there) e[i].fetch((const T*)a.x + p[i].row * a.ldx, p[i].c, a.cols);
-    const uint32_t used = (uint32_t)*a.used, slots = a.tokens * a.k;
+    const uint32_t used = used_of(a), slots = a.tokens * a.k;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         if (!p[i].there) break;
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kerne
     constexpr uint32_t kSlots = 8;
     const TokenOf<LANES> t;
     if (t.token >= a.tokens) return;
-    const uint32_t used = (uint32_t)*a.used;
+    const uint32_t used = used_of(a);
     for (int64_t c = t.lane * 8; c < a.cols; c += LANES * 8) {
         float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (uint32_t j0 = 0; j0 < a.k; j0 += kSlots) {
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_grad_
     __shared__ float meet[kWaves][kSlots];
     const TokenOf<LANES> t;
     if (t.token >= a.tokens) return;  // whole waves; with more than 64 lanes none
-    const uint32_t used = (uint32_t)*a.used, slots = a.tokens * a.k;
+    const uint32_t used = used_of(a), slots = a.tokens * a.k;
     const T* const dy = (const T*)a.dy + t.token * a.lddy;
     for (uint32_t j0 = 0; j0 < a.k; j0 += kSlots) {
         uint32_t at[kSlots];
