@@ -775,6 +775,78 @@ def test_a_block_of_them(Z):
         check_product(Z.mx8_matmul(rows8, qb, F32), rows8, qb)
 
 
+def load_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "experts_mx8.py")
+    spec = importlib.util.spec_from_file_location("experts_mx8", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_example_runs(Z):
+    m = load_example()
+    losses, p, ctrl = m.train(steps=3, ranks=2, width=128, tokens=100)
+    assert ctrl["t"] == 3 and all(math.isfinite(v) for v in losses)
+    ids, _ = m.batch(torch.Generator().manual_seed(1), 50)
+    served = m.serve(p, ids)
+    assert served.shape == (50, m.VOCAB) and torch.isfinite(served).all()
+
+
+class Plain:
+    """The calls that the example makes, from torch operations in the inputs' type, but for the products."""
+
+    def __init__(self, Z):
+        self.mx4_linear = Z.mx4_linear
+
+    def embedding(self, ids, table):
+        return table[ids]
+
+    def rms_norm(self, x, w, r=None):
+        h = x if r is None else x + r
+        y = h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-6) * w
+        return y if r is None else (y, h)
+
+    def dropout(self, x, p, seed, offset):
+        return torch.where(kept(*x.shape, p, seed, offset), x * (65536 / (65536 - round(p * 65536))), 0.0)
+
+    def expert_sort(self, chosen, experts):
+        class Plan:
+            pass
+        plan = Plan()
+        order, place, plan.offsets = plan_reference(chosen, experts)
+        plan.order, plan.place = order.long().cuda(), place.long().cuda()
+        return plan
+
+    def expert_rows(self, x, plan):
+        return x[plan.order // plan.place.shape[1]]
+
+    def expert_combine(self, rows, weights, plan):
+        return (rows[plan.place.view(-1)].view(*plan.place.shape, -1) * weights[:, :, None]).sum(1)
+
+
+def test_example_gradients(Z):
+    """The example's loss and gradients in fp32 against the same program on torch operations: equal but for fp32's
+    rounding, and for 4-bit codes next to a border that it moves to the neighbour."""
+    m = load_example()
+    places, psi = m.layout(64)
+    flat = randn(psi, seed=1) * 0.2
+    m.views(flat, places)["norms"].fill_(1.0)
+    ids, following = m.batch(torch.Generator().manual_seed(2), 80)
+    got = []
+    for calls in (Z, Plain(Z)):
+        m.Z = calls
+        leaf = flat.clone().requires_grad_()
+        loss = torch.nn.functional.cross_entropy(m.forward(ids, m.views(leaf, places), 0.3, 5, 6), following)
+        got.append((loss.detach(), torch.autograd.grad(loss, leaf)[0]))
+    (loss, grad), (want_loss, want) = got
+    assert abs(float(loss - want_loss)) <= 0.02 * float(want_loss)
+    for name in places:
+        a, b = m.views(grad, places)[name], m.views(want, places)[name]
+        assert float((a - b).norm()) <= 0.02 * float(b.norm()) and float(b.norm()) > 0, name
+
+
 def test_other_stream_and_graph(Z):
     """All calls on a side stream and in replayed graphs, with new values each time, equal the eager results."""
     tokens, cols, vocab, experts = 300, 200, 70, 5
