@@ -777,7 +777,7 @@ int zero_mx8_dequantize(const void *codes_dev, const void *scales_dev, int64_t r
 /* c[i][j] = sum over k of A[i][k] B[j][k] (+ c[i][j] when accumulate is 1 and c is
  * ZERO_F32): A m x k in MXFP8, B n x k in MXFP4, both along k.  The _rows form takes
  * A as values (a_dtype, row stride lda) and quantises them on the way in; up to m = 32
- * with m times the padded k up to 16384 in the product's own kernel, without a
+ * with m times the padded k up to 8192 in the product's own kernel, without a
  * workspace.  k = 0 gives zeros (or c unchanged). */
 int zero_mx8_matmul(const void *a_codes_dev, const void *a_scales_dev, const void *b_codes_dev,
                     const void *b_scales_dev, int64_t m, int64_t n, int64_t k, void *c_dev,

@@ -221,7 +221,8 @@ def test_mx8_product(Z, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(4096, 4096, 512), (2048, 5000, 640), (1000, 1100, 384), (8192, 130, 256), (1286, 5928, 384),
-                                   (657, 5969, 256), (657, 5395, 320), (400, 700, 4096)])
+                                   (657, 5969, 256), (657, 5395, 320), (400, 700, 4096),
+                                   (3000, 4000, 1536), (1000, 1100, 1024), (300, 500, 2560)])
 def test_mx8_product_large_tiles(Z, m, n, k):
     """Sizes that take the larger tiles; a sample of rows in 64 bits."""
     qa, qb = Z.mx8_quantize(randn(m, k, seed=1)), Z.mx4_quantize(randn(n, k, seed=2))

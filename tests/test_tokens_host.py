@@ -30,7 +30,7 @@ def test_sizes(Z):
     lib = Z._lib
     assert lib.zero_mx8_code_bytes(3, 129) == 3 * 256 and lib.zero_mx8_code_bytes(0, 5) == 0 == lib.zero_mx8_code_bytes(4, 0)
     rows = lib.zero_mx8_matmul_rows_workspace_bytes
-    assert rows(1, 9, 16384) == 0 and rows(32, 9, 512) == 0 and rows(0, 9, 9) == 0 and rows(9, BIG, 9) == 0
+    assert rows(1, 9, 8192) == 0 and rows(32, 9, 256) == 0 and rows(0, 9, 9) == 0 and rows(9, BIG, 9) == 0
     assert rows(33, 9, 128) == 33 * 128 + 128 + 256  # codes and scales, each to 256 bytes
     assert rows(2, 9, 16384) == 2 * 16384 + 1024
     norm = lib.zero_rms_norm_grad_workspace_bytes

@@ -130,7 +130,9 @@ using Step = std::integral_constant<int, K>;
 
 // A tile of TM x TN outputs by waves of WM x WN outputs each.  A slab is 128 elements of every
 // row: 128 bytes of A's and 64 of B's, and a dword of block scales; STAGES slabs in LDS,
-// copied by direct loads, STAGES - 1 on their way while one is used.  Piece q (16 bytes) of A's
+// copied by direct loads, STAGES - 1 on their way while one is used.  A dword of scales costs as much
+// of the memory pipeline as a line, so where their rows are multiples of 16 bytes (WIDE) those of four
+// slabs come together.  Piece q (16 bytes) of A's
 // row r sits in slot q ^ (r / 2 mod 8), of B's in q ^ (r / 4 mod 4): 16 lanes then read all banks.
 template <int TM_, int TN_, int WM_, int WN_, int STAGES_>
 struct Mixed {
@@ -139,15 +141,16 @@ struct Mixed {
     static constexpr int MT = WM / 32, NT = WN / 32;
     static constexpr int LA = TM / 8 / WAVES, LB = TN / 16 / WAVES;         // direct loads per wave and slab
     static constexpr int SETS = (TM + TN) / 64, LS = (SETS + WAVES - 1) / WAVES;  // and of scales
-    static constexpr int LOADS = LA + LB + LS;
-    static constexpr int B_AT = TM * 128, S_AT = B_AT + TN * 64, STAGE = S_AT + (TM + TN) * 4;
+    static constexpr int B_AT = TM * 128, STAGE = B_AT + TN * 64;
+    // behind the stages the scales: two groups of four slabs, or STAGES slabs
+    static constexpr int S_AT = STAGES * STAGE, SCALES = 2 * (TM + TN) * 16;
     static_assert(LA * 8 * WAVES == TM && LB * 16 * WAVES == TN && LA >= 1 && LB >= 1, "whole loads per wave");
-    static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
+    static_assert(S_AT + SCALES <= 160 * 1024 && STAGES * 4 <= 2 * 16, "LDS");
 };
 
-template <class S, int DT>
+template <class S, int DT, bool WIDE>
 __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
-    __shared__ __attribute__((aligned(16))) char lds[S::STAGES * S::STAGE];
+    __shared__ __attribute__((aligned(16))) char lds[S::S_AT + S::SCALES];
     int ti, tj;
     band_tile(xcd_tile(blockIdx.x, gridDim.x), g.tiles_m, g.tiles_n, ti, tj);
     const int64_t i0 = (int64_t)ti * S::TM, j0 = (int64_t)tj * S::TN;
@@ -192,9 +195,24 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
 #pragma unroll
             for (int i = 0; i < S::LB; ++i)
                 load_to_lds16(b + k / 2 + at_b[i], buf + S::B_AT + (L.wave * S::LB + i) * 1024);
+            if constexpr (WIDE) {
+                if (slab % 4 == 0) {
+                    char* const to = lds + S::S_AT + (slab / 4 & 1) * ((S::TM + S::TN) * 16);
 #pragma unroll
-            for (int i = 0; i < S::LS; ++i) load_to_lds4(from_s[i] + k / 32 + at_s[i], buf + S::S_AT + set_of(i) * 256);
+                    for (int i = 0; i < S::LS; ++i) load_to_lds16(from_s[i] + k / 32 + at_s[i], to + set_of(i) * 1024);
+                }
+            } else {
+                char* const to = lds + S::S_AT + slab % S::STAGES * ((S::TM + S::TN) * 4);
+#pragma unroll
+                for (int i = 0; i < S::LS; ++i) load_to_lds4(from_s[i] + k / 32 + at_s[i], to + set_of(i) * 256);
+            }
         }
+    };
+    auto scale = [&](int slab, int row) {  // of a row of A's, or of B's behind them
+        const uint32_t* const from = (const uint32_t*)(lds + S::S_AT);
+        const uint32_t v = WIDE ? from[(slab / 4 & 1) * ((S::TM + S::TN) * 4) + row * 4 + slab % 4]
+                                : from[slab % S::STAGES * (S::TM + S::TN) + row];
+        return (int)(v >> (8 * L.h));
     };
 
     f32x16 acc[S::MT][S::NT];
@@ -237,17 +255,18 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
     auto after = [&](char* x) { return x + S::STAGE == end ? lds : x + S::STAGE; };
     for (int t = 0; t < slabs; ++t) {
         // this slab has landed in every wave's part, and the buffer used before it is free
+        // (of the slabs after it those with scales have more loads: counted without, a few of them are waited for)
+        constexpr int kLoads = S::LA + S::LB + (WIDE ? 0 : S::LS);
         if (t + S::STAGES - 2 < slabs)
-            wait_and_meet<(S::STAGES - 2) * S::LOADS>();
+            wait_and_meet<(S::STAGES - 2) * kLoads>();
         else
             wait_and_meet<0>();
         const int next = t + S::STAGES - 1;
         const bool more = next < slabs;
-        const uint32_t* const scales = (const uint32_t*)(buf + S::S_AT);
 #pragma unroll
-        for (int i = 0; i < S::MT; ++i) va[i] = (int)(scales[wm * S::WM + 32 * i + L.c] >> (8 * L.h));
+        for (int i = 0; i < S::MT; ++i) va[i] = scale(t, wm * S::WM + 32 * i + L.c);
 #pragma unroll
-        for (int j = 0; j < S::NT; ++j) vb[j] = (int)(scales[S::TM + wn * S::WN + 32 * j + L.c] >> (8 * L.h));
+        for (int j = 0; j < S::NT; ++j) vb[j] = scale(t, S::TM + wn * S::WN + 32 * j + L.c);
         Frags f[2];
         fragments(buf, 0, f[0]);
         if (more) stage(next, fill, 0);
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
 // VALUES (m times the padded k up to kFew8): A comes as values, and every workgroup quantises all
 // of it to LDS first, which saves a launch.
 constexpr int kFewWaves = 8;
-constexpr int kFew8 = 16384;
+constexpr int kFew8 = 8192;  // two workgroups on a CU: one token 11008 x 4096 7.5 us with one
 constexpr int kFewSlabs = 2;  // slabs of a wave on their way at once
 
 struct Few8Args {
@@ -468,24 +487,28 @@ int matmul_with(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what)
     g.tiles_m = (int)tm;
     g.tiles_n = (int)tn;
     return with_dtype(c_dtype, [&](auto t) {
-        return launch(mx8_matmul_kernel<S, decltype(t)::value>, dim3((unsigned)(tm * tn)), S::THREADS, s, g, what);
+        const dim3 grid((unsigned)(tm * tn));
+        if (g.p % 512 == 0) return launch(mx8_matmul_kernel<S, decltype(t)::value, true>, grid, S::THREADS, s, g, what);
+        return launch(mx8_matmul_kernel<S, decltype(t)::value, false>, grid, S::THREADS, s, g, what);
     });
 }
 
-// At 8192 x 8192 x 8192, us: eight waves with 64 x 128 each 474, four with 128 x 128 490 (without the
-// loads to LDS 404, without the matrix instructions 362: both keep the waves waiting for their turn to
-// issue).  First fragments read ahead of the barrier, or loads spread between the matrix instructions: no faster.
+// At 8192 x 8192 x 8192, us: eight waves with 64 x 128 each 474, four with 128 x 128 490; with the scales of four
+// slabs at once 446 (2466 TFLOP/s; 4096 x 11008 x 4096 205 and 175).  Without the loads to LDS 404, without the
+// matrix instructions 362: both keep the waves waiting for their turn to issue, and together they lower the
+// clock.  Fragments read ahead of the barrier, loads spread between the matrix instructions, another first slab
+// for each row of tiles: no faster.
 typedef Mixed<256, 256, 64, 128, 3> Mixed256;
-typedef Mixed<128, 128, 64, 64, 3> Mixed128;  // two workgroups on a CU
-typedef Mixed<64, 64, 32, 32, 4> Mixed64;     // two or three
+typedef Mixed<128, 128, 64, 64, 3> Mixed128;  // up to two workgroups on a CU
+typedef Mixed<64, 64, 32, 32, 4> Mixed64;     // up to three
 
 // The shape that a product takes: microseconds a slab as measured (256 CUs, k = 4096) times the rounds that its tiles
-// need.  us at 128 x 4096 by tiles of 64, 128 and 256: 10, 19, 48; 512 x 4096: 23, 21, 50; 1024 x 4096: 42, 26, 52;
-// 300 x 11008: 42, 35, 53; 2048 x 11008: 206, 130, 112.
+// need.  us by tiles of 64, 128 and 256: 64 x 4096 10, 21, 50; 512 x 4096 18, 21, 50; 1024 x 4096 34, 23, 52;
+// 300 x 11008 30, 30, 53; 2048 x 11008 163, 114, 113; 4096 x 11008 288, 201, 175.
 int pick_mixed(int64_t t256, int64_t t128, int64_t t64) {
-    const double c256 = 1.55 * (double)ceil_div(t256, 256);
-    const double c128 = t128 <= 256 ? 0.75 : t128 <= 512 ? 0.75 + 0.65 * (double)t128 / 512 : 1.4 * (double)ceil_div(t128, 512);
-    const double c64 = t64 <= 256 ? 0.4 : 0.67 * (double)ceil_div(t64, 512);
+    const double c256 = t256 <= 256 ? 1.58 + 0.35 * (double)t256 / 256 : 1.85 * (double)ceil_div(t256, 256);
+    const double c128 = t128 <= 256 ? 0.72 : t128 <= 512 ? 0.72 + 0.45 * (double)t128 / 512 : 1.18 * (double)ceil_div(t128, 512);
+    const double c64 = t64 <= 256 ? 0.32 : 0.52 * (double)ceil_div(t64, 512);
     return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
 }
 
