@@ -222,7 +222,7 @@ def test_mx8_product(Z, m, n, k):
 
 @pytest.mark.parametrize("m,n,k", [(4096, 4096, 512), (2048, 5000, 640), (1000, 1100, 384), (8192, 130, 256), (1286, 5928, 384),
                                    (657, 5969, 256), (657, 5395, 320), (400, 700, 4096),
-                                   (3000, 4000, 1536), (1000, 1100, 1024), (300, 500, 2560)])
+                                   (3000, 4000, 1536), (1000, 1100, 1024), (300, 500, 2560), (1020, 4090, 512)])
 def test_mx8_product_large_tiles(Z, m, n, k):
     """Sizes that take the larger tiles; a sample of rows in 64 bits."""
     qa, qb = Z.mx8_quantize(randn(m, k, seed=1)), Z.mx4_quantize(randn(n, k, seed=2))
@@ -237,7 +237,7 @@ def test_mx8_product_of_values(Z, m, dtype):
     for n, k in ((33, 100), (1000, 640), (300, 1700), (2000, 4096)):
         x = (randn(m, k, seed=m) * torch.exp(randn(m, k, seed=5))).to(dtype)
         qb = Z.mx4_quantize(randn(n, k, seed=6))
-        for out in (F32, dtype):
+        for out in TYPES:
             check_product(Z.mx8_matmul(x, qb, out), Z.mx8_quantize(x), qb)
     wide = randn(m, 700, seed=9).to(dtype)
     qb = Z.mx4_quantize(randn(50, 129, seed=6))

@@ -26,13 +26,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_grads = torch.is_grad_enabled
+
+
 def _once(backward):
-    return staticmethod(torch.autograd.function.once_differentiable(backward))
-
-
-def _recorded(*tensors) -> bool:
-    """Whether torch records gradients for one of the tensors."""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """once_differentiable, without its own guard where torch records nothing, as in most backward passes."""
+    guarded = torch.autograd.function.once_differentiable(backward)
+    return staticmethod(lambda ctx, *g: guarded(ctx, *g) if _grads() else backward(ctx, *g))
 
 
 # ----------------------------------------------------------------------------- MXFP8
@@ -192,7 +192,7 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6):
     bf16 or fp32).  With a residual (x's type or fp32) it is the norm of h = x + residual, rounded
     to the residual's type, and (y, h) is returned.  Differentiable in all three; nothing but h (x
     without a residual) is kept for the gradients."""
-    if _recorded(x, weight, residual):
+    if _grads() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad):
         return _RmsNorm.apply(x, weight, residual, eps)
     y, h = _norm(x, weight, residual, eps, False)
     return y if h is None else (y, h)
@@ -212,17 +212,17 @@ def _rows_of(x):
 
 
 def _drop(x, residual, p, seed, offset, offset_dev):
-    shape, dev = x.shape, x.device
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     if not x.numel():
-        return torch.empty_like(x)
+        return y
     x, ldx = _rows_of(x)
-    ldr = 0
+    rows, cols = x.shape
+    at, ldr = None, 0
     if residual is not None:
         residual, ldr = _rows_of(residual)
-    y = _empty(shape, dtype=x.dtype, device=dev)
-    rows, cols = x.shape
-    _call(x.get_device(), "zero_dropout", x.data_ptr(), _DTYPES[x.dtype], ldx, _ptr(residual), ldr, rows, cols, p,
-          seed & _WORD, offset & _WORD, _ptr(offset_dev), y.data_ptr(), cols)
+        at = residual.data_ptr()
+    _call(x.get_device(), "zero_dropout", x.data_ptr(), _DTYPES[x.dtype], ldx, at, ldr, rows, cols, p, seed & _WORD, offset & _WORD,
+          None if offset_dev is None else offset_dev.data_ptr(), y.data_ptr(), cols)
     return y
 
 
@@ -231,16 +231,17 @@ _WORD = (1 << 64) - 1
 
 class _Dropout(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, residual, p, seed, offset, offset_dev):
-        ctx.how = (p, seed, offset)
-        ctx.save_for_backward(offset_dev)
-        return _drop(x, residual, p, seed, offset, offset_dev)
+    def forward(ctx, x, residual, how, offset_dev):
+        ctx.how = how
+        if offset_dev is not None:
+            ctx.save_for_backward(offset_dev)
+        return _drop(x, residual, *how, offset_dev)
 
     @_once
     def backward(ctx, dy):
-        offset_dev, = ctx.saved_tensors
-        dx = _drop(dy, None, *ctx.how, offset_dev) if ctx.needs_input_grad[0] else None
-        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None, None
+        need_x, need_r = ctx.needs_input_grad[:2]
+        dx = _drop(dy, None, *ctx.how, *(ctx.saved_tensors or (None,))) if need_x else None
+        return dx, dy if need_r else None, None, None
 
 
 def dropout(x, p: float, seed: int, offset=0, *, residual=None):
@@ -253,7 +254,7 @@ def dropout(x, p: float, seed: int, offset=0, *, residual=None):
     are different masks.  offset may be an int64 GPU tensor of one element, read when the kernels run:
     a captured graph then draws anew after the program has moved it.  It may not be moved between a
     forward pass and its backward pass."""
-    code = _code(x.dtype)  # noqa: F841
+    _code(x.dtype)
     if not 0.0 <= p <= 1.0:
         raise ValueError("p is not in [0, 1]")
     offset_dev = None
@@ -263,9 +264,12 @@ def dropout(x, p: float, seed: int, offset=0, *, residual=None):
         offset, offset_dev = 0, offset
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError("residual: another shape or type than x")
-    _gpu(x, *(t for t in (residual, offset_dev) if t is not None))
-    if _recorded(x, residual):
-        return _Dropout.apply(x, residual, p, seed, offset, offset_dev)
+    if residual is None and offset_dev is None:
+        _gpu(x)
+    else:
+        _gpu(x, *(t for t in (residual, offset_dev) if t is not None))
+    if _grads() and (x.requires_grad or residual is not None and residual.requires_grad):
+        return _Dropout.apply(x, residual, (p, seed, offset), offset_dev)
     return _drop(x, residual, p, seed, offset, offset_dev)
 
 
@@ -317,7 +321,7 @@ def embedding(tokens, table, *, scale: float = 1.0):
         raise ValueError("scale is not finite")
     _gpu(table, tokens)
     tokens = tokens.contiguous()
-    if _recorded(table):
+    if _grads() and table.requires_grad:
         return _Embedding.apply(tokens, table, scale)
     return _lookup(tokens, table, scale)
 
@@ -401,7 +405,7 @@ def expert_rows(x, plan: ExpertPlan):
     """The rows of x [tokens, cols] in the plan's order, [tokens k, cols]: expert e's are rows
     offsets[e] .. offsets[e + 1]; the rows behind the last are zeros.  Differentiable."""
     plan._check(x, plan.tokens, "x")
-    if _recorded(x):
+    if _grads() and x.requires_grad:
         return _ExpertRows.apply(x, plan)
     return _to_rows(x, plan)
 
@@ -442,6 +446,6 @@ def expert_combine(rows, weights, plan: ExpertPlan):
     if weights.get_device() != index:
         raise ValueError("rows and weights on one GPU")
     weights = weights.contiguous()
-    if _recorded(rows, weights):
+    if _grads() and (rows.requires_grad or weights.requires_grad):
         return _ExpertCombine.apply(rows, weights, plan)
     return _to_tokens(rows, weights, plan)
