@@ -70,7 +70,9 @@ __device__ __forceinline__ void places8(const Vectors& v, Place8 (&p)[kEach]) {
 // Stable, by at most 9 bits of the key a pass (least significant first).  A workgroup takes a
 // contiguous tile, each of its waves a contiguous part: counts per wave and digit give every
 // wave its first place for every digit, and within 64 keys the lanes with the same digit find
-// each other by one ballot per bit.  Integer counts alone are added atomically, in LDS.
+// each other by one ballot per bit.  Integer counts alone are added atomically, in LDS.  A single tile
+// (up to 2048 numbers) takes all its passes in one launch.  Bound by latency: 131072 numbers below 64
+// 15 us in two launches, 1024 below 50258 11 us in one.
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits, kSortWaves = 8, kSortThreads = 64 * kSortWaves;
 constexpr int64_t kMinTile = 2048, kMostTiles = 256;  // three passes at most: 24 bits of key
 
@@ -281,6 +283,8 @@ __device__ __forceinline__ uint32_t first_place(const uint32_t* keys, uint32_t n
 
 // ---------------------------------------------------------------- embedding
 //   out[t] = table[id[t]] * scale, rounded once; zeros for an id outside [0, vocab)
+// Bound by memory: 32768 rows of 4096 bf16 85 us for 451 MB.  Short rows share workgroups; those of 2048
+// columns or more have one each, whose id is read once (85 against 102 us).
 struct LookupArgs {
     Ids ids;
     Vectors v;
@@ -316,8 +320,7 @@ __global__ void __launch_bounds__(256) embedding_kernel(LookupArgs a) {
     }
 }
 
-// Long rows, a wave's vectors all of one token, whose id is then read once: kTokens tokens a
-// workgroup, their vectors kEach at a time.
+// Long rows: a workgroup takes a token, its vectors kEach at a time.
 template <int DT>
 __global__ void __launch_bounds__(256) embedding_long_kernel(LookupArgs a) {
     typedef typename Elem<DT>::type T;
@@ -349,7 +352,9 @@ __global__ void __launch_bounds__(256) embedding_long_kernel(LookupArgs a) {
 // long run is as much work for a piece as many short ones: a piece sums each of its runs, writes
 // those that lie in it to their rows, and of the two that may leave it the sums so far; a second
 // launch adds what belongs together, in order.  Further workgroups of the first launch write
-// the zeros, which are nearly all of a large table's gradient.  Bound by memory.
+// the zeros, which are nearly all of a large table's gradient.  Bound by memory: 131072 x 4096 bf16 from
+// 32768 tokens 247 us for 1.35 GB, 16 us for the join (1371 us with a row's tokens summed by the workgroup of
+// its row: a few frequent words kept a few workgroups busy).
 constexpr int kZeroVectors = 16384, kZeroRows = 256, kZeroGroups = 1024;
 
 struct GradArgs {
@@ -534,6 +539,7 @@ __device__ __forceinline__ uint32_t used_of(const ExpertArgs& a) {
 }
 
 // Sorted rows from tokens' rows: a token's row is read once and written k times; zeros behind the last.
+// Bound by memory: 16384 tokens of 4096 bf16, eight each, 204 us for 1.21 GB.
 template <int DT>
 __global__ void __launch_bounds__(256) expert_rows_kernel(ExpertArgs a) {
     typedef typename Elem<DT>::type T;
@@ -580,6 +586,8 @@ struct TokenOf {
 };
 
 // Tokens' rows from sorted rows: the weighted sum of a token's k rows, in fp32, in the slots' order.
+// Bound by memory: the same size 280 us for 1.21 GB, 246 with ones for weights.  A token's eight rows are on
+// their way at once; with the places read by each lane, and four tokens' vectors a lane, 512 us.
 template <int DT, int LANES>
 __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kernel(ExpertArgs a) {
     typedef typename Elem<DT>::type T;
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kerne
 }
 
 // The gradients of that sum: of a sorted row its weight times dy of its token (zeros behind the
-// last), of a weight the product of its row with dy.
+// last), of a weight the product of its row with dy.  Bound by memory: the same size 428 us for 2.29 GB.
 template <int DT, int LANES>
 __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_grad_kernel(ExpertArgs a) {
     typedef typename Elem<DT>::type T;
@@ -722,7 +730,7 @@ int with_type(int32_t dt, F f) {
     }
 }
 
-// Lanes that share a token's row.
+// Lanes that share a token's row: one to three vectors a lane, whole waves.
 template <class F>
 int with_lanes(int64_t cols, F f) {
     if (cols <= 1024) return f(std::integral_constant<int, 64>());
