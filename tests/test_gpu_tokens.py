@@ -419,6 +419,21 @@ def test_norm_range(Z, cols):
             assert torch.isnan(y[9]).all() if eps == 0.0 else (y[9] == 0).all()
 
 
+@pytest.mark.parametrize("cols", [40, 2000, 20000])
+def test_norm_weights_range(Z, cols):
+    """Weights whose products with the rows alone would leave fp32's range on either side; infinite ones and NaN."""
+    x = randn(4, cols, seed=1) * torch.tensor([1e15, 1e-15, 1.0, 3e37], device="cuda")[:, None]
+    x[:, 7] = 0.0
+    w = torch.ones(cols, device="cuda")
+    w[:5] = torch.tensor([1e30, 1e-30, 3e37, 1e-37, -1e33], device="cuda")
+    w[5:9] = torch.tensor([math.inf, -math.inf, math.inf, math.nan], device="cuda")
+    y = Z.rms_norm(x, w, eps=1e-36)
+    want = norm64(x.double(), w.double(), float(torch.tensor(1e-36)))[0]
+    fine = torch.isfinite(want)
+    near(y[fine], want[fine], (depth(cols) / 2 + 8) * U * want[fine].abs())
+    same(y[~fine], want[~fine].float())
+
+
 @pytest.mark.parametrize("stream", ["none", "same", "f32"])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,cols", [(1, 1), (3, 33), (2, 127), (5, 1024), (3, 1025), (1, 4096), (4, 5001), (2, 8191), (2, 9000),

@@ -95,7 +95,11 @@ struct Root {
         const float one = fmaf(p, r, -1.0f) + e * r;
         rest = q > 0.0f && q < 3.0e38f ? -0.5f * r * one : 0.0f;
     }
-    __device__ __forceinline__ float times(float x) const { return fmaf(x, r, x * rest); }
+    // h / sqrt(q) * w: h / sqrt(q), which is of moderate size, in two parts too (h w alone may leave fp32's range).
+    __device__ __forceinline__ float times(float h, float w) const {
+        const float u = h * r, low = fmaf(h, r, -u) + h * rest;
+        return fmaf(u, w, __builtin_isinf(w) ? 0.0f : low * w);
+    }
 };
 
 struct NormArgs {
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(WAVE ? 256 : kMostThreads) norm_kernel(NormArg
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            h[v][i] = root.times(h[v][i] * w[i]);
+            h[v][i] = root.times(h[v][i], w[i]);
             if (MX && c + i >= a.cols) h[v][i] = 0.0f;  // also where r is not finite
         }
         norm_out8<DX, MX, WHOLE>(a, row, c, h[v]);
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
             ew.floats(w);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * pre * w[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * pre, w[i]) : 0.0f;
         norm_out8<DX, MX, false>(a, row, c, h);
     }
 }
