@@ -26,6 +26,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_rows_like, _flat = torch.empty_like, torch.contiguous_format
+
+
+def _like(x):
+    """A new contiguous tensor of x's shape and type."""
+    return _rows_like(x, memory_format=_flat)
+
+
 _grads = torch.is_grad_enabled
 
 
@@ -141,13 +149,13 @@ def _norm_inputs(x, weight, residual, eps):
 def _norm(x, weight, residual, eps, packed):
     index, x, ldx, residual, ldr, weight, code, code_r = _norm_inputs(x, weight, residual, eps)
     tokens, cols = x.shape
-    h = None if residual is None else _empty(x.shape, dtype=residual.dtype, device=x.device)
+    h = None if residual is None else _like(residual)
     inputs = (x.data_ptr(), code, ldx, _ptr(residual), code_r, ldr, weight.data_ptr(), tokens, cols, eps)
     if packed:
         y = MX8.alloc(tokens, cols, x.device)
         _call(index, "zero_rms_norm_mx8", *inputs, *y._places, _ptr(h), cols)
     else:
-        y = _empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like(x)
         _call(index, "zero_rms_norm", *inputs, y.data_ptr(), cols, _ptr(h), cols)
     return y, h
 
@@ -172,13 +180,13 @@ class _RmsNorm(torch.autograd.Function):
         weight = weight.contiguous()
         dh, lddh = (None, 0) if dh is None else _matrix(dh)
         tokens, cols = h.shape
-        dev, one = h.device, h.dtype == ctx.dtype  # one: x's gradient is the residual's
-        dr = _empty(h.shape, dtype=h.dtype, device=dev) if need_r and not one else None
-        dx = _empty(h.shape, dtype=ctx.dtype, device=dev) if need_x or (need_r and one) else None
-        dw = torch.zeros_like(weight) if need_w and not tokens else _empty(weight.shape, dtype=ctx.dtype, device=dev) if need_w else None
+        one = h.dtype == ctx.dtype  # one: x's gradient is the residual's
+        dr = _like(h) if need_r and not one else None
+        dx = _like(dy) if need_x or (need_r and one) else None
+        dw = None if not need_w else _like(weight) if tokens else torch.zeros_like(weight)
         if tokens and cols:
             size = _lib.zero_rms_norm_grad_workspace_bytes(tokens, cols) if need_w else 0
-            ws = _empty(size, dtype=_bytes, device=dev) if size else None
+            ws = _empty(size, dtype=_bytes, device=h.device) if size else None
             _call(h.get_device(), "zero_rms_norm_grad", dy.data_ptr(), lddy, h.data_ptr(), _DTYPES[h.dtype], ldh,
                   weight.data_ptr(), _DTYPES[ctx.dtype], _ptr(dh), lddh, tokens, cols, ctx.eps, _ptr(dx), cols,
                   _ptr(dr), cols, _ptr(dw), _ptr(ws), size)
@@ -212,7 +220,7 @@ def _rows_of(x):
 
 
 def _drop(x, residual, p, seed, offset, offset_dev):
-    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    y = _like(x)
     if not x.numel():
         return y
     x, ldx = _rows_of(x)
@@ -427,7 +435,7 @@ class _ExpertCombine(torch.autograd.Function):
         drows = _empty((plan.tokens * plan.k, cols), dtype=dy.dtype, device=dev) if need_rows else None
         dweights = None
         if need_weights:
-            dweights = (_empty if cols else torch.zeros)(weights.shape, dtype=weights.dtype, device=dev)
+            dweights = _like(weights) if cols else torch.zeros_like(weights)
         _call(dy.get_device(), "zero_expert_combine_grad", dy.data_ptr(), lddy, _ptr(rows), _DTYPES[dy.dtype], ldr,
               *plan._places(), weights.data_ptr(), _DTYPES[weights.dtype], plan.tokens, plan.k, cols, _ptr(drows), cols,
               _ptr(dweights))
