@@ -230,3 +230,12 @@ def test_cpu_tensors_refused(Z):
         Z.MX8(torch.zeros(4, 127, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 4, 64)
     q = Z.MX8(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 4, 64)
     assert q.codes.shape == (4, 128) and ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_launches_past_32_bits_refused(Z):
+    # 2^24 rows of 256 threads; the addresses are far enough apart for rows of 4096 bytes
+    n, cols = 1 << 24, 2048
+    rows = dict(tokens=n, cols=cols)
+    assert call(Z, "zero_rms_norm", {**NORM, **OUT}, rdt=BF16, ldx=cols, ldr=cols, ldy=cols, ldh=cols, **rows) == ERANGE
+    assert call(Z, "zero_rms_norm_mx8", {**NORM, **OUT8}, rdt=BF16, ldx=cols, ldr=cols, ldh=cols, **rows) == ERANGE
+    assert call(Z, "zero_embedding", LOOKUP, ldt=cols, ldo=cols, **rows) == ERANGE

@@ -488,6 +488,8 @@ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 template <class Args>
 int launch(void (*kernel)(Args), dim3 grid, int block, hipStream_t s, const Args& args, const char* what) {
+    // the threads of a launch are counted in 32 bits
+    if ((uint64_t)grid.x * (uint64_t)block > 0xFFFFFFFFu) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     void* params[] = {const_cast<Args*>(&args)};
     const hipError_t e =
         hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(block), params, 0, s);

@@ -12,11 +12,11 @@ namespace {
 // Up to two vectors of eight a lane, and as many lanes as the row needs: with four vectors the registers
 // left four waves a SIMD, and 8192 columns took 66 us.  WHOLE: columns a multiple of eight, without the code for a
 // row's last elements, whose registers cost the gradient 6 of 57 us.
+constexpr int kMostThreads = 1024;
+constexpr int64_t kWaveCols = 512;
 
 // 1 / sqrt(mean + eps) = r * pre: squares that leave fp32's range, or that its smallest numbers
 // would swallow, are summed again of elements times pre.
-constexpr int kMostThreads = 1024;
-constexpr int64_t kWaveCols = 512;
 constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p64f;
 __device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-80f ? kPreUp : 1.0f; }
 
