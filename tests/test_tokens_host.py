@@ -219,7 +219,8 @@ def test_nothing_to_do(Z):
 def test_cpu_tensors_refused(Z):
     import torch
     x, w, ids = torch.zeros(4, 64), torch.zeros(64), torch.zeros(4, 2, dtype=torch.int64)
-    plan = Z.ExpertPlan(ids, ids, ids, 4, 2, 3)
+    numbers = torch.zeros(8, dtype=torch.int32)
+    plan = Z.ExpertPlan(numbers, numbers.view(4, 2), numbers[:4], 4, 2, 3)
     for call_ in (lambda: Z.mx8_quantize(x), lambda: Z.mx8_dequantize(Z.MX8.alloc(4, 64, "cpu")), lambda: Z.rms_norm(x, w),
                   lambda: Z.mx8_matmul(x, Z.MX4.alloc(4, 64, "cpu")), lambda: Z.rms_norm(x, w, x), lambda: Z.rms_norm_mx8(x, w),
                   lambda: Z.dropout(x, 0.5, 1), lambda: Z.embedding(ids, x), lambda: Z.expert_sort(ids, 3),
@@ -230,6 +231,16 @@ def test_cpu_tensors_refused(Z):
         Z.MX8(torch.zeros(4, 127, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 4, 64)
     q = Z.MX8(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 4, 64)
     assert q.codes.shape == (4, 128) and ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_plans_refused(Z):
+    import torch
+    n = torch.zeros(8, dtype=torch.int32)
+    Z.ExpertPlan(n, n.view(4, 2), n[:4], 4, 2, 3)
+    for order, place, offsets in ((n[:7], n, n[:4]), (n, n[:6], n[:4]), (n, n, n[:3]), (n.long(), n, n[:4]), (n, n.long(), n[:4]),
+                                  (n, n, n[:4].float()), (n, n.expand(2, 8)[:, :4], n[:4]), (n, n, n[::2])):
+        with pytest.raises(ValueError):
+            Z.ExpertPlan(order, place, offsets, 4, 2, 3)
 
 
 def test_launches_past_32_bits_refused(Z):

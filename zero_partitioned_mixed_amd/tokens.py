@@ -345,6 +345,9 @@ class ExpertPlan:
     __slots__ = ("order", "place", "offsets", "tokens", "k", "experts")
 
     def __init__(self, order, place, offsets, tokens: int, k: int, experts: int):
+        for t, n in ((order, tokens * k), (place, tokens * k), (offsets, experts + 1)):
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+                raise ValueError("order and place: tokens k contiguous int32 numbers, offsets: experts + 1")
         self.order, self.place, self.offsets = order, place, offsets
         self.tokens, self.k, self.experts = tokens, k, experts
 
