@@ -649,7 +649,8 @@ def choices(tokens, k, experts, seed, drop=0.1, dtype=torch.int64):
 
 
 SORTS = [(1, 1, 1), (3, 2, 4), (100, 2, 8), (333, 3, 5), (2048, 1, 64), (2049, 1, 64), (1500, 8, 256), (5000, 4, 511), (700, 2, 512),
-         (5000, 3, 1000), (40000, 8, 16), (9000, 2, 300000)]
+         (5000, 3, 1000), (40000, 8, 16), (9000, 2, 300000), (512, 1, 64), (513, 1, 600), (4096, 1, 64), (4097, 1, 600),
+         (1365, 3, 700), (2000, 2, 300000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])

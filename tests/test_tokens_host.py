@@ -40,7 +40,7 @@ def test_sizes(Z):
     assert embed(1, 9, 9) == 4 * 64 and embed(8, 9, 9) == 4 * 64  # ids and where they came from
     assert embed(33, 9, 9) == 4 * (128 + 5 * 2 * 9)  # and two parts for each piece of the order
     sort = lib.zero_expert_sort_workspace_bytes
-    assert sort(0, 9) == 0 and sort(2048, 511) == 0 and sort(2049, 8) == 4 * 2 * 512 and sort(9, BIG) == 0
+    assert sort(0, 9) == 0 and sort(4096, 511) == 0 and sort(4097, 8) == 4 * 3 * 512 and sort(9, BIG) == 0
 
 
 QUANT = dict(src=A, dt=BF16, rows=4, cols=64, ld=64, codes=B, scales=C)

@@ -71,10 +71,11 @@ __device__ __forceinline__ void places8(const Vectors& v, Place8 (&p)[kEach]) {
 // contiguous tile, each of its waves a contiguous part: counts per wave and digit give every
 // wave its first place for every digit, and within 64 keys the lanes with the same digit find
 // each other by one ballot per bit.  Integer counts alone are added atomically, in LDS.  A single tile
-// (up to 2048 numbers) takes all its passes in one launch.  Bound by latency: 131072 numbers below 64
-// 15 us in two launches, 1024 below 50258 11 us in one.
+// (up to 4096 numbers) takes all its passes in one launch.  Bound by latency: 131072 numbers below 64
+// 15 us in two launches, 1024 below 50258 11 us in one.  One tile against several, two passes within the embedding's
+// gradient (us, and the host's): 4096 numbers 25.7 (9) and 26.0 (19), 6000 31.6 and 28.4, 16384 64 and 31.
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits, kSortWaves = 8, kSortThreads = 64 * kSortWaves;
-constexpr int64_t kMinTile = 2048, kMostTiles = 256;  // three passes at most: 24 bits of key
+constexpr int64_t kOneTile = 4096, kMinTile = 2048, kMostTiles = 256;  // three passes at most: 24 bits of key
 
 struct SortArgs {
     Ids ids;                  // first pass
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(SortPasses a) {
 
 // Tile and number of tiles of a sort: enough tiles for the CUs, few enough for the sums over them.
 int64_t sort_tile(int64_t n) {
+    if (n <= kOneTile) return round_up(n, kSortThreads);
     const int64_t t = round_up(ceil_div(n, kMostTiles), kSortThreads);
     return t > kMinTile ? t : kMinTile;
 }
