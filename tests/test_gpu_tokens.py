@@ -220,6 +220,37 @@ def test_mx8_product(Z, m, n, k):
     assert (wide[:, :1] == 7).all() and (wide[:, n + 1:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 40, 128), (8, 70, 384), (32, 300, 512), (33, 70, 640), (300, 500, 1024), (3900, 4000, 384),
+                                   (1286, 5928, 384), (4096, 4096, 512)])
+def test_mx8_product_large_values_against_zeros(Z, m, n, k, dtype):
+    """A column of large values that meets a weight of zero, as 4-bit weights have many, takes nothing from its
+    neighbours: seven small products of eight, the smallest normal codes, the smallest below them, and ones."""
+    a = torch.empty(m, k, device="cuda")
+    b = torch.ones(n, k, device="cuda")
+    b[:, ::8] = 0.0
+    qb = Z.mx4_quantize(b)
+    for small in (2.0 ** -6, 2.0 ** -9, 1.0):
+        a.fill_(small)
+        a[:, ::8] = 448.0
+        want = float((k - -(-k // 8)) * small)
+        assert float(torch.tensor(want).to(dtype)) == want  # seven eighths of k: few bits
+        for x in (Z.mx8_quantize(a), a):
+            assert (Z.mx8_matmul(x, qb, dtype) == want).all(), (small, want)
+
+
+@pytest.mark.parametrize("m,n,k", PRODUCTS + [(4096, 4096, 512), (3900, 4000, 384), (1286, 5928, 384), (1000, 1100, 1024)])
+def test_mx8_product_sums(Z, m, n, k):
+    """Results of every type are fp32 sums, rounded once: rows with columns of much larger values, against 64 bits."""
+    a = randn(m, k, seed=1) * (1 + 60 * (torch.rand(k, device="cuda", generator=gen(3)) < 0.05))
+    qa, qb = Z.mx8_quantize(a), Z.mx4_quantize(randn(n, k, seed=2))
+    rows = torch.arange(0, m, max(1, m // 61))
+    a64, b64 = values8(qa)[rows], values4(qb)
+    want, slack = a64 @ b64.t(), (k + 1) * U * (a64.abs() @ b64.abs().t())
+    for dtype in TYPES:
+        near(Z.mx8_matmul(qa, qb, dtype)[rows.cuda()].cpu(), want, slack)
+
+
 @pytest.mark.parametrize("m,n,k", [(4096, 4096, 512), (2048, 5000, 640), (1000, 1100, 384), (8192, 130, 256), (1286, 5928, 384),
                                    (657, 5969, 256), (657, 5395, 320), (400, 700, 4096),
                                    (3000, 4000, 1536), (1000, 1100, 1024), (300, 500, 2560), (1020, 4090, 512)])

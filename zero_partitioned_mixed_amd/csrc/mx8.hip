@@ -103,26 +103,32 @@ struct Matmul8Args {
 //
 // The instruction adds eight neighbouring products on a grid of 2^(E - 13), E the largest sum of
 // their exponents, and cuts what lies below it (measured; a subnormal code counts with the smallest
-// normal exponent).  Activations leave 2e-5 of a result's norm that way: nothing beside the rounding
-// of 16-bit results, but not fp32.  So for those (EXACT) A is split by its codes' highest
-// exponent bit: products of codes from 2 on are multiples of 2^(E - 13), and those of the codes below
-// too, so that nothing is cut, at twice the instructions.
-template <bool EXACT, class K>
-__device__ __forceinline__ f32x16 mma8(const i32x4& a0, const i32x4& a1, const i32x4& b, f32x16 c, int sa, int sb, K) {
-    const i32x8 u = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+// normal exponent).  Sums have to be fp32 for results of 16 bits too: cut like that they are off by 2e-5 of
+// a result's norm for activations, and by more where few columns are large.  So A is split by its codes'
+// highest exponent bit: products of codes from 2 on are multiples of 2^(E - 13), and those of the codes below
+// too, so that nothing is cut, at twice the instructions (8192 x 8192 x 8192 418 us with one, 694 with two).
+template <class K>
+__device__ __forceinline__ f32x16 mma8(const i32x8& a, const i32x4& b, f32x16 c, int sa, int sb, K) {
     const i32x8 v = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    if constexpr (EXACT) {
-        i32x8 low, high;
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, v, c, 0, 4, K::value, sa, K::value, sb);
+}
+__device__ __forceinline__ i32x8 joined(const i32x4& a0, const i32x4& a1) {
+    return __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+// 255 in the bytes of codes from 2 on: the permutation takes the signs of 16-bit halves, to which the bits are moved.
+__device__ __forceinline__ uint32_t high_codes(int u) {
+    return __builtin_amdgcn_perm((uint32_t)u << 1, (uint32_t)u << 9, 0x0B090A08u);
+}
+template <class K>
+__device__ __forceinline__ f32x16 mma8_split(const i32x4& a0, const i32x4& a1, const i32x4& b, f32x16 c, int sa, int sb, K k) {
+    const i32x8 u = joined(a0, a1);
+    i32x8 low, high;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t bit = (uint32_t)u[i] << 1 & 0x80808080u, mask = bit | (bit - (bit >> 7));  // whole bytes
-            high[i] = u[i] & (int)mask;
-            low[i] = u[i] & (int)~mask;
-        }
-        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(low, v, c, 0, 4, K::value, sa, K::value, sb);
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(high, v, c, 0, 4, K::value, sa, K::value, sb);
+    for (int i = 0; i < 8; ++i) {
+        high[i] = u[i] & (int)high_codes(u[i]);
+        low[i] = u[i] ^ high[i];
     }
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(u, v, c, 0, 4, K::value, sa, K::value, sb);
+    return mma8(high, b, mma8(low, b, c, sa, sb, k), sa, sb, k);
 }
 
 template <int K>
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
 #pragma unroll
         for (int i = 0; i < S::MT; ++i)
 #pragma unroll
-            for (int j = 0; j < S::NT; ++j) acc[i][j] = mma8<DT == ZERO_F32>(f.a[i][0], f.a[i][1], f.b[j], acc[i][j], va[i], vb[j], kk);
+            for (int j = 0; j < S::NT; ++j) acc[i][j] = mma8_split(f.a[i][0], f.a[i][1], f.b[j], acc[i][j], va[i], vb[j], kk);
     };
 
 #pragma unroll
@@ -322,12 +328,14 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
         }
 }
 
-// Few rows (m <= 32, as single tokens bring): bound by reading B once (one token 11008 x 4096: 6.2 us,
+// Few rows (m <= 32, as single tokens bring): bound by reading B once (one token 11008 x 4096: 7.9 us a call,
 // where reading B takes 4.7; its waves wait for 58% of their cycles).  A workgroup takes 32 of B's
 // rows, its eight waves an eighth of k each: a wave brings slabs of 256 elements of them to its own
 // part of LDS in whole lines, waits for nobody, and the waves' sums meet in LDS.
 // VALUES (m times the padded k up to kFew8): A comes as values, and every workgroup quantises all
 // of it to LDS first, which saves a launch.
+// HALVES (m <= 16): the low codes of row i are the instruction's row 2i and the high ones its row 2i + 1, so
+// that one instruction is enough.
 constexpr int kFewWaves = 8;
 constexpr int kFew8 = 8192;  // two workgroups on a CU: one token 11008 x 4096 7.5 us with one
 constexpr int kFewSlabs = 2;  // slabs of a wave on their way at once
@@ -338,7 +346,7 @@ struct Few8Args {
     int64_t lda, k;
 };
 
-template <int DTA, int DT, bool VALUES>
+template <int DTA, int DT, bool VALUES, bool HALVES>
 __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
     const Matmul8Args& g = f.g;
     __shared__ __attribute__((aligned(16))) uint8_t codes[VALUES ? kFew8 : 16];
@@ -402,7 +410,9 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
     } else {
         if (any) fetch(L.wave);
     }
-    const uint32_t row = (uint32_t)(L.c < g.m ? L.c : g.m - 1);
+    const int of = HALVES ? L.c >> 1 : L.c;
+    const uint32_t other = HALVES && (L.c & 1) == 0 ? ~0u : 0u;  // even lanes take the low codes
+    const uint32_t row = (uint32_t)(of < g.m ? of : g.m - 1);
     const uint8_t* const a = (VALUES ? codes : g.a) + (int64_t)row * p + 16 * L.h;
     const uint8_t* const sa = (VALUES ? scales : g.sa) + (int64_t)row * scale_row;
     f32x16 acc;
@@ -411,7 +421,15 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
     // blocks q and q + apart (of the slab's) meet in a step
     auto step = [&](const uint8_t* at, int apart, const i32x4& bw, uint32_t as, uint32_t bs_, auto kk) {
         const int q = decltype(kk)::value;
-        acc = mma8<DT == ZERO_F32>(*(const i32x4*)(at + q * 32), *(const i32x4*)(at + (q + apart) * 32), bw, acc, (int)as, (int)bs_, kk);
+        const i32x4 a0 = *(const i32x4*)(at + q * 32), a1 = *(const i32x4*)(at + (q + apart) * 32);
+        if constexpr (HALVES) {
+            i32x8 part = joined(a0, a1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) part[i] &= (int)(high_codes(part[i]) ^ other);
+            acc = mma8(part, bw, acc, (int)as, (int)bs_, kk);
+        } else {
+            acc = mma8_split(a0, a1, bw, acc, (int)as, (int)bs_, kk);
+        }
     };
 
     for (int first = L.wave; first < slabs; first += kFewWaves * kFewSlabs) {
@@ -452,9 +470,12 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
         const int i = t / 32, c = t % 32;
         const int64_t col = (int64_t)blockIdx.x * 32 + c;
         if (col >= g.n) continue;
-        float v = sums[0][i][c];
+        constexpr int kRows = HALVES ? 2 : 1;  // of the sums
+        float v = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) v += sums[w][i][c];
+        for (int w = 0; w < kFewWaves; ++w)
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) v += sums[w][kRows * i + u][c];
         T* out = (T*)g.c + i * g.ldc + col;
         if constexpr (DT == ZERO_F32) {
             if (g.accumulate) v += *out;
@@ -494,37 +515,45 @@ int matmul_with(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what)
     });
 }
 
-// At 8192 x 8192 x 8192, us: eight waves with 64 x 128 each 474, four with 128 x 128 490; with the scales of four
-// slabs at once 446 (2466 TFLOP/s; 4096 x 11008 x 4096 205 and 175).  Without the loads to LDS 404, without the
-// matrix instructions 362: both keep the waves waiting for their turn to issue, and together they lower the
-// clock.  Fragments read ahead of the barrier, loads spread between the matrix instructions, another first slab
-// for each row of tiles: no faster.
+// 8192 x 8192 x 8192 690 us (1600 TFLOP/s, 3200 of instructions; from registers they reach 4212), 4096 x 11008 x 4096 262.
+// Chosen with one instruction a step, 8192 x 8192 x 8192, us: eight waves with 64 x 128 each 474, four with 128 x 128
+// 490; with the scales of four slabs at once 446.  Without the loads to LDS 404, without the matrix instructions 362:
+// both keep the waves waiting for their turn to issue, and together they lower the clock.  Fragments read ahead of the
+// barrier, loads spread between the matrix instructions, another first slab for each row of tiles: no faster.
 typedef Mixed<256, 256, 64, 128, 3> Mixed256;
 typedef Mixed<128, 128, 64, 64, 3> Mixed128;  // up to two workgroups on a CU
 typedef Mixed<64, 64, 32, 32, 4> Mixed64;     // up to three
 
-// The shape that a product takes: microseconds a slab as measured (256 CUs, k = 4096) times the rounds that its tiles
-// need.  us by tiles of 64, 128 and 256: 64 x 4096 10, 21, 50; 512 x 4096 18, 21, 50; 1024 x 4096 34, 23, 52;
-// 300 x 11008 30, 30, 53; 2048 x 11008 163, 114, 113; 4096 x 11008 288, 201, 175.
+// The shape that a product takes: microseconds a slab as measured (256 CUs, k = 4096), a part of it however few the
+// tiles and a part for each tile that the busiest CU gets.  us by tiles of 64, 128 and 256: 64 x 4096 15, 33, 83; 512 x
+// 4096 23, 33, 84; 1024 x 4096 41, 36, 87; 300 x 11008 41, 55, 89; 1024 x 11008 103, 83, 93; 2048 x 11008 201, 152, 175;
+// 4096 x 4096 148, 105, 93; 4096 x 11008 391, 278, 262.
 int pick_mixed(int64_t t256, int64_t t128, int64_t t64) {
-    const double c256 = t256 <= 256 ? 1.58 + 0.35 * (double)t256 / 256 : 1.85 * (double)ceil_div(t256, 256);
-    const double c128 = t128 <= 256 ? 0.72 : t128 <= 512 ? 0.72 + 0.45 * (double)t128 / 512 : 1.18 * (double)ceil_div(t128, 512);
-    const double c64 = t64 <= 256 ? 0.32 : 0.52 * (double)ceil_div(t64, 512);
+    const double c256 = 0.10 + 2.70 * (double)ceil_div(t256, 256);
+    const double c128 = 0.20 + 0.79 * (double)ceil_div(t128, 256);
+    const double c64 = 0.20 + 0.28 * (double)ceil_div(t64, 256);
     return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
 }
 
 // Values of A quantised in the product's own kernel.
 bool few_values(int64_t m, int64_t k) { return m <= 32 && m * padded(k) <= kFew8; }
 
+template <class F>
+int with_halves(int64_t m, F f) {
+    return m <= 16 ? f(std::true_type()) : f(std::false_type());
+}
+
 int matmul(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what) {
     g.vector = aligned(g.c, 4 * elem_bytes(c_dtype)) && g.ldc % 4 == 0;
-    // Few rows against tiles, us: 4096 x 4096, 8 rows 5.9 and 11.4, 32 rows 7.8 and 9.5; 11008 x 4096, where tiles too
-    // fill the CUs, 8 rows 9.2 and 10.3, 16 rows 10.7 and 10.2, 32 rows 14.3 and 10.6.
-    if (g.m <= 8 || (g.m <= 32 && g.n <= 64 * 128)) {
+    // Few rows against tiles, us: 4096 x 4096, 8 rows 5.8 and 15.2, 32 rows 7.6 and 15.3; 11008 x 4096, 8 rows 8.9 and
+    // 16.2, 24 rows 12.8 and 15.5, 32 rows 15.7 and 15.5.
+    if (g.m <= 32) {
         const Few8Args f{g, nullptr, 0, 0};
-        return with_dtype(c_dtype, [&](auto t) {
-            return launch(mx8_few_kernel<ZERO_F32, decltype(t)::value, false>, dim3((unsigned)ceil_div(g.n, 32)),
-                          kFewWaves * 64, s, f, what);
+        return with_halves(g.m, [&](auto h) {
+            return with_dtype(c_dtype, [&](auto t) {
+                return launch(mx8_few_kernel<ZERO_F32, decltype(t)::value, false, decltype(h)::value>,
+                              dim3((unsigned)ceil_div(g.n, 32)), kFewWaves * 64, s, f, what);
+            });
         });
     }
     auto tiles = [&](int64_t t) { return ceil_div(g.m, t) * ceil_div(g.n, t); };
@@ -536,10 +565,12 @@ int matmul(Matmul8Args g, int32_t c_dtype, hipStream_t s, const char* what) {
 }
 
 int few_of_values(const Few8Args& f, int32_t a_dtype, int32_t c_dtype, hipStream_t s, const char* what) {
-    return with_dtype(a_dtype, [&](auto ta) {
-        return with_dtype(c_dtype, [&](auto tc) {
-            return launch(mx8_few_kernel<decltype(ta)::value, decltype(tc)::value, true>, dim3((unsigned)ceil_div(f.g.n, 32)),
-                          kFewWaves * 64, s, f, what);
+    return with_halves(f.g.m, [&](auto h) {
+        return with_dtype(a_dtype, [&](auto ta) {
+            return with_dtype(c_dtype, [&](auto tc) {
+                return launch(mx8_few_kernel<decltype(ta)::value, decltype(tc)::value, true, decltype(h)::value>,
+                              dim3((unsigned)ceil_div(f.g.n, 32)), kFewWaves * 64, s, f, what);
+            });
         });
     });
 }

@@ -85,8 +85,8 @@ def mx8_dequantize(q: MX8, dtype=torch.bfloat16, out=None):
 def mx8_matmul(a, b: MX4, out_dtype=torch.bfloat16, *, out=None, accumulate: bool = False, ws=None):
     """a b^T: a an MX8 (rms_norm_mx8 and mx8_quantize make them), or a matrix of values that is
     quantised along its rows (in the product's own kernel for few rows); b an MX4 over the same
-    columns.  accumulate adds into ``out`` (fp32).  out shares no element with a or b.  Sums are fp32 for
-    an fp32 result; for 16-bit ones they lose 2e-5 of the results' norm.  Not differentiable."""
+    columns.  accumulate adds into ``out`` (fp32).  out shares no element with a or b.  Results are sums in
+    fp32, rounded once to their type.  Not differentiable."""
     values = not isinstance(a, MX8)
     if values and isinstance(a, _Blocks):
         raise TypeError("a is neither an MX8 nor a matrix of values")
