@@ -391,8 +391,9 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
             const uint32_t r = (uint32_t)t / (p / 8), c = ((uint32_t)t - r * (p / 8)) * 8;
             quantize8<DTA>(e, codes + r * p + c, scales + r * scale_row + c / kMxBlock);
         };
-        // loads return in order: the first of A go out before B's, so that A is ready while B is on its way
-        constexpr int kFirst = 2;
+        // loads return in order: A's go out before B's, so that A is ready while B is on its way
+        constexpr int kFirst = kFew8 / (8 * kFewWaves * 64);  // pieces a lane
+        static_assert(kFirst * 8 * kFewWaves * 64 == kFew8, "all of A");
         const int tid = threadIdx.x;
         Eight<DTA> e[kFirst];
 #pragma unroll
@@ -402,10 +403,6 @@ __global__ void __launch_bounds__(kFewWaves * 64) mx8_few_kernel(Few8Args f) {
 #pragma unroll
         for (int i = 0; i < kFirst; ++i)
             if (tid + i * kFewWaves * 64 < pieces) put(tid + i * kFewWaves * 64, e[i]);
-        for (int t = tid + kFirst * kFewWaves * 64; t < pieces; t += kFewWaves * 64) {
-            read(t, e[0]);
-            put(t, e[0]);
-        }
         __syncthreads();
     } else {
         if (any) fetch(L.wave);
