@@ -250,3 +250,27 @@ def test_launches_past_32_bits_refused(Z):
     assert call(Z, "zero_rms_norm", {**NORM, **OUT}, rdt=BF16, ldx=cols, ldr=cols, ldy=cols, ldh=cols, **rows) == ERANGE
     assert call(Z, "zero_rms_norm_mx8", {**NORM, **OUT8}, rdt=BF16, ldx=cols, ldr=cols, ldh=cols, **rows) == ERANGE
     assert call(Z, "zero_embedding", LOOKUP, ldt=cols, ldo=cols, **rows) == ERANGE
+
+
+def test_tangents_are_not_lost(Z, monkeypatch):
+    """In forward mode, where no input requires a gradient, the calls raise as torch's own do without a formula,
+    rather than return a result without its tangent.  The C calls stubbed out."""
+    import torch
+    import torch.autograd.forward_ad as forward_ad
+    from zero_partitioned_mixed_amd import tokens as M
+    monkeypatch.setattr(M, "_gpu", lambda *t: 0)
+    monkeypatch.setattr(M, "_call", lambda *a: None)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    x, w, numbers = torch.ones(8, 64), torch.ones(64), torch.zeros(8, dtype=torch.int32)
+    plan, ids, gates = Z.ExpertPlan(numbers, numbers.view(8, 1), numbers[:4], 8, 1, 3), torch.zeros(5, dtype=torch.int64), torch.ones(8, 1)
+    calls = [(lambda t: Z.rms_norm(t, w), x), (lambda t: Z.rms_norm(x, t), w), (lambda t: Z.rms_norm(x, w, t), x),
+             (lambda t: Z.dropout(t, 0.5, 1), x), (lambda t: Z.dropout(x, 0.5, 1, residual=t), x), (lambda t: Z.embedding(ids, t), x),
+             (lambda t: Z.expert_rows(t, plan), x), (lambda t: Z.expert_combine(t, gates, plan), x),
+             (lambda t: Z.expert_combine(x, t, plan), gates)]
+    for call_, t in calls:
+        with forward_ad.dual_level():
+            call_(t)  # without a tangent as ever
+            for recorded in (torch.enable_grad, torch.no_grad):
+                with recorded(), pytest.raises(RuntimeError, match="jvp"):
+                    call_(forward_ad.make_dual(t, torch.ones_like(t)))
+        call_(t)

@@ -8,11 +8,13 @@ of the tensors' device.  Rows of unit stride are taken where they are, others ar
 
 Forward and backward can be captured into a HIP graph.  As with every autograd function, no
 eager result of the same leaves may be alive then: torch would accumulate their gradients on
-that result's stream, inside the capture.
+that result's stream, inside the capture.  Gradients are those of backward passes: tensors with a
+tangent of forward mode are refused.
 """
 from __future__ import annotations
 
 import torch
+import torch.autograd.forward_ad as _forward
 
 from . import F32, _lib
 from .matrices import (MX4, _Blocks, _bytes, _call, _code, _DTYPES, _empty, _gpu, _laid_out,
@@ -35,6 +37,12 @@ def _like(x):
 
 
 _grads = torch.is_grad_enabled
+
+
+def _dual() -> bool:
+    """Whether a level of forward mode is open: a tensor may have a tangent then without requiring a gradient, which
+    the autograd functions, that have no formula for it, refuse."""
+    return getattr(_forward, "_current_level", 0) >= 0
 
 
 def _once(backward):
@@ -201,7 +209,7 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6):
     bf16 or fp32).  With a residual (x's type or fp32) it is the norm of h = x + residual, rounded
     to the residual's type, and (y, h) is returned.  Differentiable in all three; nothing but h (x
     without a residual) is kept for the gradients."""
-    if _grads() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad):
+    if _dual() or _grads() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad):
         return _RmsNorm.apply(x, weight, residual, eps)
     y, h = _norm(x, weight, residual, eps, False)
     return y if h is None else (y, h)
@@ -277,7 +285,7 @@ def dropout(x, p: float, seed: int, offset=0, *, residual=None):
         _gpu(x)
     else:
         _gpu(x, *(t for t in (residual, offset_dev) if t is not None))
-    if _grads() and (x.requires_grad or residual is not None and residual.requires_grad):
+    if _dual() or _grads() and (x.requires_grad or residual is not None and residual.requires_grad):
         return _Dropout.apply(x, residual, (p, seed, offset), offset_dev)
     return _drop(x, residual, p, seed, offset, offset_dev)
 
@@ -330,7 +338,7 @@ def embedding(tokens, table, *, scale: float = 1.0):
         raise ValueError("scale is not finite")
     _gpu(table, tokens)
     tokens = tokens.contiguous()
-    if _grads() and table.requires_grad:
+    if _dual() or _grads() and table.requires_grad:
         return _Embedding.apply(tokens, table, scale)
     return _lookup(tokens, table, scale)
 
@@ -417,7 +425,7 @@ def expert_rows(x, plan: ExpertPlan):
     """The rows of x [tokens, cols] in the plan's order, [tokens k, cols]: expert e's are rows
     offsets[e] .. offsets[e + 1]; the rows behind the last are zeros.  Differentiable."""
     plan._check(x, plan.tokens, "x")
-    if _grads() and x.requires_grad:
+    if _dual() or _grads() and x.requires_grad:
         return _ExpertRows.apply(x, plan)
     return _to_rows(x, plan)
 
@@ -458,6 +466,6 @@ def expert_combine(rows, weights, plan: ExpertPlan):
     if weights.get_device() != index:
         raise ValueError("rows and weights on one GPU")
     weights = weights.contiguous()
-    if _grads() and (rows.requires_grad or weights.requires_grad):
+    if _dual() or _grads() and (rows.requires_grad or weights.requires_grad):
         return _ExpertCombine.apply(rows, weights, plan)
     return _to_tokens(rows, weights, plan)
