@@ -1172,3 +1172,20 @@ def test_refusals_of_tensors(Z):
             (TypeError, lambda: Z.expert_combine(randn(16, 5), torch.ones(8, 2, device="cuda").half(), plan))]:
         with pytest.raises(error):
             call()
+
+
+def test_calls_without_gradients_refuse_them(Z):
+    """Calls that are not differentiable and return a tensor say so instead of returning it without its graph."""
+    import torch.autograd.forward_ad as forward_ad
+    x, r, w, b = randn(4, 64), randn(4, 64, seed=1), randn(64, seed=2), Z.mx4_quantize(randn(8, 64))
+    leaf = x.clone().requires_grad_()
+    for call in (lambda t: Z.rms_norm_mx8(t, w, r), lambda t: Z.rms_norm_mx8(x, w, t), lambda t: Z.mx8_matmul(t, b)):
+        with pytest.raises(RuntimeError, match="not differentiable"):
+            call(leaf)
+        with forward_ad.dual_level():
+            with pytest.raises(RuntimeError, match="not differentiable"):
+                call(forward_ad.make_dual(x, torch.ones_like(x)))
+            call(x)
+        with torch.no_grad():
+            call(leaf)
+        call(leaf.detach())

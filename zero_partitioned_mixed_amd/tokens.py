@@ -28,6 +28,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _constant(what: str, *tensors) -> None:
+    """Refuses tensors whose derivative a call that has none would drop."""
+    for t in tensors:
+        if t is not None and (_grads() and t.requires_grad or _dual() and _forward.unpack_dual(t).tangent is not None):
+            raise RuntimeError(f"{what} is not differentiable: detach its inputs, or call it under torch.no_grad()")
+
+
 _rows_like, _flat = torch.empty_like, torch.contiguous_format
 
 
@@ -94,10 +101,12 @@ def mx8_matmul(a, b: MX4, out_dtype=torch.bfloat16, *, out=None, accumulate: boo
     """a b^T: a an MX8 (rms_norm_mx8 and mx8_quantize make them), or a matrix of values that is
     quantised along its rows (in the product's own kernel for few rows); b an MX4 over the same
     columns.  accumulate adds into ``out`` (fp32).  out shares no element with a or b.  Results are sums in
-    fp32, rounded once to their type.  Not differentiable."""
+    fp32, rounded once to their type.  Not differentiable: values that require a gradient are refused."""
     values = not isinstance(a, MX8)
-    if values and isinstance(a, _Blocks):
-        raise TypeError("a is neither an MX8 nor a matrix of values")
+    if values:
+        if isinstance(a, _Blocks):
+            raise TypeError("a is neither an MX8 nor a matrix of values")
+        _constant("mx8_matmul", a)
     if not isinstance(b, MX4):
         raise TypeError("b is not an MX4")
     m, k = a.shape if values else (a.rows, a.cols)
@@ -217,7 +226,10 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6):
 
 def rms_norm_mx8(x, weight, residual=None, *, eps: float = 1e-6):
     """rms_norm whose result is left as MX8 rows, from its fp32 values, for mx8_matmul: MX8, or
-    (MX8, h) with a residual.  Not differentiable."""
+    (MX8, h) with a residual.  Not differentiable: with a residual, x and residual that require
+    a gradient are refused, since h, a tensor that goes on, would come back without its graph."""
+    if residual is not None:
+        _constant("rms_norm_mx8", x, residual)
     y, h = _norm(x, weight, residual, eps, True)
     return y if h is None else (y, h)
 
