@@ -465,6 +465,23 @@ def test_norm_weights_range(Z, cols):
     same(y[~fine], want[~fine].float())
 
 
+@pytest.mark.parametrize("cols", [40, 2000, 5000, 20000, 40000])
+def test_norm_smallest_rows(Z, cols):
+    """Rows of numbers below the normal ones, without an eps: elements of about one, not infinities."""
+    for dtype in (F32, BF16):
+        least = float(2 * last(dtype))
+        x = torch.randint(-3, 4, (6, cols), device="cuda", generator=gen(1)).double() * least
+        x[1] *= 100.0
+        x[2], x[3] = 0.0, 0.0
+        x[2, cols // 2], x[3, cols - 1] = least, -2.0 * least
+        x[4, 0] = 2.0 ** -60  # and beside a much larger one
+        x[:, 1] = least
+        x, w = x.to(dtype), randn(cols, seed=2).to(dtype)
+        y = Z.rms_norm(x, w, eps=0.0)
+        want = norm64(x.double(), w.double(), 0.0)[0]
+        near(y, want, (depth(cols) / 2 + 8) * U * want.abs())
+
+
 @pytest.mark.parametrize("stream", ["none", "same", "f32"])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,cols", [(1, 1), (3, 33), (2, 127), (5, 1024), (3, 1025), (1, 4096), (4, 5001), (2, 8191), (2, 9000),

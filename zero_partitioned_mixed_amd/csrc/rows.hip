@@ -16,9 +16,10 @@ constexpr int kMostThreads = 1024;
 constexpr int64_t kWaveCols = 512;
 
 // 1 / sqrt(mean + eps) = r * pre: squares that leave fp32's range, or that its smallest numbers
-// would swallow, are summed again of elements times pre.
-constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p64f;
-__device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-80f ? kPreUp : 1.0f; }
+// would swallow, are summed again of elements times pre.  Up: a mean of squares below 2^-100 leaves sums below 2^124
+// for up to 2^24 elements, and the square of the smallest number, 2^-149, becomes 2^-98.
+constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p100f;
+__device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-100f ? kPreUp : 1.0f; }
 
 // The lanes of a row: a wave (four rows a workgroup, for up to kWaveCols columns), or a workgroup
 // of as many waves as the row needs with V vectors a lane.
