@@ -482,6 +482,19 @@ def test_norm_smallest_rows(Z, cols):
         near(y, want, (depth(cols) / 2 + 8) * U * want.abs())
 
 
+@pytest.mark.parametrize("cols", [40, 2000, 5000, 20000, 40000])
+def test_norm_small_elements_of_large_rows(Z, cols):
+    """Where a row's squares leave fp32's range, each of its elements still has all its bits."""
+    x = randn(3, cols, seed=1) * torch.tensor([2.0 ** -45, 2.0 ** -30, 1.0], device="cuda")[:, None]
+    x[:, 3] = torch.tensor([2.0 ** 66, 2.0 ** 90, -2.0 ** 127], device="cuda")
+    w = randn(cols, seed=2)
+    y = Z.rms_norm(x, w)
+    want = norm64(x.double(), w.double())[0]
+    # h / root is kept in two parts; the lower one of a result near the smallest numbers is itself below the normal ones:
+    # rounded when it is made, by half of the smallest number, then times w, and so is their product
+    near(y, want, (depth(cols) / 2 + 8) * U * want.abs() + (1 + w.double().abs()) * last(F32))
+
+
 @pytest.mark.parametrize("stream", ["none", "same", "f32"])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,cols", [(1, 1), (3, 33), (2, 127), (5, 1024), (3, 1025), (1, 4096), (4, 5001), (2, 8191), (2, 9000),

@@ -20,6 +20,10 @@ constexpr int64_t kWaveCols = 512;
 // for up to 2^24 elements, and the square of the smallest number, 2^-149, becomes 2^-98.
 constexpr float kPreDown = 0x1p-96f, kPreUp = 0x1p100f;
 __device__ __forceinline__ float pre_of(float q) { return !(q <= 0x1p120f) ? kPreDown : q < 0x1p-100f ? kPreUp : 1.0f; }
+// The results' elements take pre in two parts, h times the one and r times the other, so that those far below a
+// large row's keep their bits: h 2^-96 would leave the normal numbers where h 2^-48 does not.
+__device__ __forceinline__ float pre_of_h(float pre) { return pre == kPreDown ? 0x1p-48f : pre; }
+__device__ __forceinline__ float pre_of_r(float pre) { return pre == kPreDown ? 0x1p-48f : 1.0f; }
 
 // The lanes of a row: a wave (four rows a workgroup, for up to kWaveCols columns), or a workgroup
 // of as many waves as the row needs with V vectors a lane.
@@ -85,18 +89,19 @@ __device__ __forceinline__ float squares8(const float* h) {
            ((h[4] * h[4] + h[5] * h[5]) + (h[6] * h[6] + h[7] * h[7]));
 }
 
-// 1 / sqrt(q) as the sum of two fp32 numbers: results rounded to 8 bits next to a border, and the
+// by / sqrt(q), by a power of two, as the sum of two fp32 numbers: results rounded to 8 bits next to a border, and the
 // last bits of fp32 ones, show the rounding of one.
 struct Root {
     float r, rest;
-    __device__ __forceinline__ explicit Root(float q) {
+    __device__ __forceinline__ Root(float q, float by) {
         r = 1.0f / sqrtf(q);
         // one Newton step: r (1 - q r^2) / 2, q r^2 - 1 with its rounding undone by fused products
         const float p = q * r, e = fmaf(q, r, -p);
         const float one = fmaf(p, r, -1.0f) + e * r;
-        rest = q > 0.0f && q < 3.0e38f ? -0.5f * r * one : 0.0f;
+        rest = q > 0.0f && q < 3.0e38f ? -0.5f * r * one * by : 0.0f;
+        r *= by;
     }
-    // h / sqrt(q) * w: h / sqrt(q), which is of moderate size, in two parts too (h w alone may leave fp32's range).
+    // h by / sqrt(q) * w: h by / sqrt(q), which is of moderate size, in two parts too (h w alone may leave fp32's range).
     __device__ __forceinline__ float times(float h, float w) const {
         const float u = h * r, low = fmaf(h, r, -u) + h * rest;
         return fmaf(u, w, __builtin_isinf(w) ? 0.0f : low * w);
@@ -186,14 +191,18 @@ __global__ void __launch_bounds__(WAVE ? 256 : kMostThreads) norm_kernel(NormArg
         ss[0] = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            float p[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[v][i] *= pre;
-            ss[0] += squares8(h[v]);
+            for (int i = 0; i < 8; ++i) {
+                p[i] = h[v][i] * pre;
+                h[v][i] *= pre_of_h(pre);
+            }
+            ss[0] += squares8(p);
         }
         row_sums<WAVE>(ss, meet, 1);
         q = ss[0] / n + a.eps * pre * pre;
     }
-    const Root root(q);
+    const Root root(q, pre_of_r(pre));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = (int64_t)(v * T + t) * 8;
@@ -251,7 +260,8 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
     float q = sum_of(1.0f, true) / n + a.eps;
     const float pre = pre_of(q);
     if (pre != 1.0f) q = sum_of(pre, false) / n + a.eps * pre * pre;
-    const Root root(q);
+    const Root root(q, pre_of_r(pre));
+    const float of_h = pre_of_h(pre);
     for (int64_t c = c0; c < end; c += kWide * 8) {
         float h[8], w[8];
         if (c < a.cols) {
@@ -269,7 +279,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
             ew.floats(w);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * pre, w[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) h[i] = c + i < a.cols ? root.times(h[i] * of_h, w[i]) : 0.0f;
         norm_out8<DX, MX, false>(a, row, c, h);
     }
 }
