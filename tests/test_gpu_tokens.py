@@ -495,6 +495,49 @@ def test_norm_small_elements_of_large_rows(Z, cols):
     near(y, want, (depth(cols) / 2 + 8) * U * want.abs() + (1 + w.double().abs()) * last(F32))
 
 
+@pytest.mark.parametrize("stream", ["none", "f32"])
+@pytest.mark.parametrize("cols", [40, 2000, 5000, 20000, 40000])
+def test_norm_gradient_range(Z, cols, stream):
+    """Gradients of rows and weights whose products, or sums of products, leave fp32's range on either side."""
+    scale = torch.tensor([1e37, 1e30, 1e15, 1.0, 1e-15, 1e-30, 1e-40], device="cuda")[:, None]
+    for dtype in (F32, BF16):
+        kind = dtype if stream == "none" else F32
+        h = (randn(7, cols, seed=1) * scale).to(kind)
+        dy = randn(7, cols, seed=3).to(dtype)
+        for weights in ([3e37, 1e30, 1e-30, 1e-37, -1e33], [1.0] * 5, [1e-37] * 5):
+            w = randn(cols, seed=2) if weights[0] > 1e-3 else randn(cols, seed=2) * 1e-30
+            w[:5] = torch.tensor(weights)
+            w = w.to(dtype)
+            for eps in (1e-6, 0.0):
+                e64, lw = float(torch.tensor(eps)), w.clone().requires_grad_()
+                if stream == "none":
+                    leaf = h.clone().requires_grad_()
+                    dx, dw = torch.autograd.grad(Z.rms_norm(leaf, lw, eps=eps), (leaf, lw), dy)
+                    check_norm_gradients(h.double(), w.double(), dy.double(), None, dx, None, dw, eps=e64)
+                    continue
+                zero, leaf, dh = torch.zeros(7, cols, dtype=dtype, device="cuda").requires_grad_(), h.clone().requires_grad_(), randn(7, cols, seed=5)
+                dx, dw, dr = torch.autograd.grad(Z.rms_norm(zero, lw, leaf, eps=eps), (zero, lw, leaf), (dy, dh))
+                check_norm_gradients(h.double(), w.double(), dy.double(), dh.double(), dx, dr, dw, eps=e64)
+
+
+@pytest.mark.parametrize("cols", [40, 2000, 20000, 40000])
+def test_norm_gradient_infinities(Z, cols):
+    """Infinities and NaN in one row's gradient or values leave the other rows' gradients alone."""
+    x, w, dy = randn(6, cols, seed=1), randn(cols, seed=2), randn(6, cols, seed=3)
+    dy[1, 5], dy[2, cols - 1], x[4, 7] = math.inf, math.nan, -math.inf
+    leaf, lw = x.clone().requires_grad_(), w.clone().requires_grad_()
+    dx, dw = torch.autograd.grad(Z.rms_norm(leaf, lw), (leaf, lw), dy)
+    fine = [0, 3, 5]
+    check_norm_gradients(x.double()[fine], w.double(), dy.double()[fine], None, dx[fine], None, None)
+    # (g - u m) / root with m infinite: NaN in the infinity's own place, infinities of -u's sign (times m's) elsewhere
+    u = norm64(x[1:2].double(), 1.0)[0][0]
+    want = -u * torch.sign(w[5].double() * u[5]) * math.inf
+    want[5] = math.nan
+    same(dx[1], want.float())
+    assert torch.isnan(dx[2]).all() and torch.isnan(dx[4]).all()
+    assert torch.isinf(dw[5]) and torch.isnan(dw[cols - 1]) and torch.isnan(dw[7])
+
+
 @pytest.mark.parametrize("stream", ["none", "same", "f32"])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,cols", [(1, 1), (3, 33), (2, 127), (5, 1024), (3, 1025), (1, 4096), (4, 5001), (2, 8191), (2, 9000),

@@ -30,10 +30,11 @@ __device__ __forceinline__ float pre_of_r(float pre) { return pre == kPreDown ? 
 template <bool WAVE>
 struct RowOf {
     int64_t row;  // this row, or group of rows
-    int t, lanes;
+    int t, lanes, wave = 0;  // wave: this row's in the workgroup
     __device__ __forceinline__ RowOf() {
         if constexpr (WAVE) {
-            row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+            wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+            row = (int64_t)blockIdx.x * 4 + wave;
             t = threadIdx.x % 64;
             lanes = 64;
         } else {
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
 // parts are summed in order by a second launch.  Bound by memory: 8192 x 4096 bf16 47 us for 276 MB
 // and 4.5 us for dw.  The next row is read while this one's sums meet (without that, and two barriers a
 // sum, 83 us).
+constexpr int64_t kWaveGroups = 2048, kLeastGroups = 256;
 struct NormGradArgs {
     const void *dy, *h, *w, *dh;
     int64_t lddy, ldh, lddh;
@@ -305,25 +307,103 @@ struct NormGradArgs {
 };
 
 // dh' and u of eight elements.
-__device__ __forceinline__ void norm_grad8(const float* h, const float* y, const float* w, float pre, float r, float m, float* u,
-                                           float* d) {
+__device__ __forceinline__ void norm_grad8(const float* h, const float* y, const float* w, float r, float m, float* u, float* d) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        u[i] = h[i] * pre * r;
-        d[i] = (y[i] * w[i] - u[i] * m) * r * pre + d[i];
+        u[i] = h[i] * r;
+        d[i] = (y[i] * w[i] - u[i] * m) * r + d[i];
     }
 }
 
-// The sums of squares and of g h over eight elements times pre.
-__device__ __forceinline__ void norm_sums8(const float* h, const float* y, const float* w, float pre, float (&s)[2]) {
-    float p[8], g[8];
+// The sums of squares and of g h over eight elements.
+__device__ __forceinline__ void norm_sums8(const float* h, const float* y, const float* w, float (&s)[2]) {
+    float g[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        p[i] = h[i] * pre;
-        g[i] = y[i] * w[i] * p[i];
-    }
-    s[0] += squares8(p);
+    for (int i = 0; i < 8; ++i) g[i] = y[i] * w[i] * h[i];
+    s[0] += squares8(h);
     s[1] += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
+}
+
+// Whether fp32 holds a row's sums and what is made of them: its mean square q, and its sum of g h.
+__device__ __forceinline__ bool norm_in_fp32(float q, float gh) {
+    const float size = __builtin_fabsf(gh);
+    return q >= 0x1p-60f && q <= 0x1p120f && size <= 0x1p90f && (size >= 0x1p-90f || size == 0.0f);
+}
+
+// The sum over a row's lanes in 64 bits, the same bits in every lane; consecutive calls take turns, as above.
+typedef double RowSum64[2][kMostWaves];
+template <bool WAVE>
+__device__ __forceinline__ double row_sum64(double v, RowSum64& meet, int turn) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    if constexpr (!WAVE) {
+        if ((threadIdx.x & 63) == 0) meet[turn][threadIdx.x / 64] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll 1
+        for (uint32_t w = 0; w < blockDim.x / 64; ++w) v += meet[turn][w];
+    }
+    return v;
+}
+
+// Which of a group's rows are left for norm_grad_row64 when the others are done (among them it costs registers that
+// every row pays for: 2048 x 16384 bf16 with an fp32 stream 148 us, behind them 128, without it 118): a bit each, for the most rows in
+// the fewest groups.
+template <bool WAVE>
+struct LeftRows {
+    static constexpr int kWords = (int)(kMaxSide / (WAVE ? kWaveGroups : kLeastGroups) / 32);
+    uint32_t* bits;
+    __device__ __forceinline__ LeftRows(uint32_t* all, int wave) : bits(all + (WAVE ? wave * kWords : 0)) {}
+    __device__ __forceinline__ void meet() {
+        if constexpr (WAVE) {
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ void clear(int t, int T) {
+        for (int i = t; i < kWords; i += T) bits[i] = 0;
+        meet();
+    }
+    __device__ __forceinline__ void add(int t, int i) {
+        if (t == 0) bits[i / 32] |= 1u << (i % 32);
+    }
+    __device__ __forceinline__ bool has(int i) const { return bits[i / 32] >> (i % 32) & 1; }
+};
+
+// The other rows (below 1e-9 or above 1e18, weights or gradients of such sizes, infinities and NaN): dr and dx
+// in 64 bits, which hold every product and sum here, an element at a time, read again.  Leaves u = h by * r.
+struct UnitOf {
+    float by, r;
+    __device__ __forceinline__ float operator()(float h) const { return h * by * r; }
+};
+template <int DX, int DR, bool WAVE>
+__device__ __forceinline__ UnitOf norm_grad_row64(const NormGradArgs& a, int64_t row, int t, int T, RowSum64& meet) {
+    typedef typename Elem<DX>::type X;
+    typedef typename Elem<DR>::type R;
+    const X *const dy = (const X*)a.dy + row * a.lddy, *const w = (const X*)a.w;
+    const R *const h = (const R*)a.h + row * a.ldh, *const dh = (const R*)a.dh + row * a.lddh;
+    const double n = (double)a.cols;
+    double ss = 0.0, gu = 0.0;
+#pragma unroll 1
+    for (int64_t c = t; c < a.cols; c += T) {
+        const double v = to_float<DR>(h[c]);
+        ss += v * v;
+    }
+    const double q = row_sum64<WAVE>(ss, meet, 0) / n + a.eps, r = 1.0 / sqrt(q);
+#pragma unroll 1
+    for (int64_t c = t; c < a.cols; c += T) gu += (double)to_float<DX>(dy[c]) * to_float<DX>(w[c]) * (to_float<DR>(h[c]) * r);
+    const double m = row_sum64<WAVE>(gu, meet, 1) / n;
+#pragma unroll 1
+    for (int64_t c = t; c < a.cols; c += T) {
+        const double g = (double)to_float<DX>(dy[c]) * to_float<DX>(w[c]), u = to_float<DR>(h[c]) * r;
+        const float d = (float)((g - u * m) * r + (a.dh != nullptr ? to_float<DR>(dh[c]) : 0.0f));
+        if (a.dr != nullptr) ((R*)a.dr)[row * a.lddr + c] = from_float<DR>(d);
+        if (a.dx != nullptr) ((X*)a.dx)[row * a.lddx + c] = from_float<DX>(d);
+    }
+    const float by = q > 0x1p120 ? 0x1p-48f : q < 0x1p-100 ? 0x1p100f : 1.0f;
+    return UnitOf{by, (float)(r / by)};
 }
 
 template <int DX, int DR, bool WAVE, int V, bool WHOLE>
@@ -331,6 +411,8 @@ __global__ void __launch_bounds__(WAVE ? 256 : kMostThreads) norm_grad_kernel(No
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
     __shared__ RowSums<2> meet;
+    __shared__ RowSum64 meet64;
+    __shared__ uint32_t left[WAVE ? 4 * LeftRows<WAVE>::kWords : LeftRows<WAVE>::kWords];
     const RowOf<WAVE> of;
     if constexpr (!WAVE) meet.clear();
     const int64_t group = of.row;
@@ -369,46 +451,66 @@ __global__ void __launch_bounds__(WAVE ? 256 : kMostThreads) norm_grad_kernel(No
     Row next;
     if (kAhead && group < a.tokens) next.load(a, group, t, T);
     int turn = 0;
+    bool any = false;  // the same in all lanes of a row
+    LeftRows<WAVE> rest(left, of.wave);
     for (int64_t row = group; row < a.tokens; row += a.groups) {
         if (!kAhead) next.load(a, row, t, T);
         const Row e = next;
         if (kAhead && row + a.groups < a.tokens) next.load(a, row + a.groups, t, T);
-        auto sums = [&](float pre, float (&s)[2]) {
-            s[0] = s[1] = 0.0f;
+        // f(v, c, h, y, w) for this lane's vectors
+        auto each = [&](auto f) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if ((int64_t)(v * T + t) * 8 >= a.cols) break;
+                const int64_t c = (int64_t)(v * T + t) * 8;
+                if (c >= a.cols) break;
                 float h[8], y[8], w[8];
                 e.h[v].floats(h);
                 e.y[v].floats(y);
                 weights(v, w);
-                norm_sums8(h, y, w, pre, s);
+                f(v, c, h, y, w);
             }
-            row_sums<WAVE>(s, meet, turn++);
         };
-        float s[2];
-        sums(1.0f, s);
-        float q = s[0] / n + a.eps;
-        const float pre = pre_of(q);
-        if (pre != 1.0f) {
-            sums(pre, s);
-            q = s[0] / n + a.eps * pre * pre;
+        float s[2] = {0.0f, 0.0f};
+        each([&](int, int64_t, const float* h, const float* y, const float* w) { norm_sums8(h, y, w, s); });
+        row_sums<WAVE>(s, meet, turn++);
+        const float q = s[0] / n + a.eps;
+        if (!norm_in_fp32(q, s[1])) {
+            if (!any) rest.clear(t, T);
+            any = true;
+            rest.add(t, turn - 1);
+            continue;
         }
         const float r = 1.0f / sqrtf(q), m = s[1] * r / n;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t c = (int64_t)(v * T + t) * 8;
-            if (c >= a.cols) break;
-            float h[8], y[8], w[8], u[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            e.h[v].floats(h);
-            e.y[v].floats(y);
-            weights(v, w);
+        each([&](int v, int64_t c, const float* h, const float* y, const float* w) {
+            float u[8], d[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (a.dh != nullptr) e.d[v].floats(d);
-            norm_grad8(h, y, w, pre, r, m, u, d);
+            norm_grad8(h, y, w, r, m, u, d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[v][i] += y[i] * u[i];
             if (a.dr != nullptr) put8<DR, WHOLE>((R*)a.dr + row * a.lddr, c, a.cols, d);
             if (a.dx != nullptr) put8<DX, WHOLE>((X*)a.dx + row * a.lddx, c, a.cols, d);
+        });
+    }
+    if (any) {
+        rest.meet();
+        int64_t row = group;
+        for (int k = 0; row < a.tokens; ++k, row += a.groups) {
+            if (!rest.has(k)) continue;
+            const UnitOf u = norm_grad_row64<DX, DR, WAVE>(a, row, t, T, meet64);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int64_t c = (int64_t)(v * T + t) * 8;
+                if (c >= a.cols) break;
+                Eight<DX> ey;
+                Eight<DR> eh;
+                ey.template fetch<WHOLE>((const X*)a.dy + row * a.lddy, c, a.cols);
+                eh.template fetch<WHOLE>((const R*)a.h + row * a.ldh, c, a.cols);
+                float y[8], h[8];
+                ey.floats(y);
+                eh.floats(h);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dw[v][i] += y[i] * u(h[i]);
+            }
         }
     }
     if (a.parts == nullptr || group >= a.groups) return;
@@ -425,6 +527,7 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
     typedef typename Elem<DX>::type X;
     typedef typename Elem<DR>::type R;
     __shared__ RowSums<2> meet;
+    __shared__ RowSum64 meet64;
     const int64_t c0 = (int64_t)threadIdx.x * 8;
     const float n = (float)a.cols;
     bool first = true;
@@ -432,8 +535,8 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
     for (int64_t row = blockIdx.x; row < a.tokens; row += a.groups) {
         const X* const dy = (const X*)a.dy + row * a.lddy;
         const R* const hr = (const R*)a.h + row * a.ldh;
-        auto sums = [&](float pre, float (&s)[2]) {
-            s[0] = s[1] = 0.0f;
+        // f(c, h, y, w) for this lane's vectors
+        auto each = [&](auto f) {
             for (int64_t c = c0; c < a.cols; c += kWide * 8) {
                 Eight<DX> ey, ew;
                 Eight<DR> eh;
@@ -444,45 +547,44 @@ __global__ void __launch_bounds__(kWide) norm_grad_wide_kernel(NormGradArgs a) {
                 eh.floats(h);
                 ey.floats(y);
                 ew.floats(w);
-                norm_sums8(h, y, w, pre, s);
+                f(c, h, y, w);
             }
-            row_sums<false>(s, meet, turn++);
         };
-        float s[2];
-        sums(1.0f, s);
-        float q = s[0] / n + a.eps;
-        const float pre = pre_of(q);
-        if (pre != 1.0f) {
-            sums(pre, s);
-            q = s[0] / n + a.eps * pre * pre;
-        }
-        const float r = 1.0f / sqrtf(q), m = s[1] * r / n;
-        for (int64_t c = c0; c < a.cols; c += kWide * 8) {
-            Eight<DX> ey, ew;
-            Eight<DR> eh, ed;
-            eh.fetch(hr, c, a.cols);
-            ey.fetch(dy, c, a.cols);
-            ew.fetch((const X*)a.w, c, a.cols);
-            if (a.dh != nullptr)
-                ed.fetch((const R*)a.dh + row * a.lddh, c, a.cols);
-            else
-                ed.zero();
-            float h[8], y[8], w[8], u[8], d[8], p[8];
-            eh.floats(h);
-            ey.floats(y);
-            ew.floats(w);
-            ed.floats(d);
-            float* const part = a.parts == nullptr ? nullptr : a.parts + (int64_t)blockIdx.x * a.cols;
-            if (part != nullptr) {
+        float* const part = a.parts == nullptr ? nullptr : a.parts + (int64_t)blockIdx.x * a.cols;
+        auto add_part = [&](int64_t c, const float* y, const float* u) {
+            if (part == nullptr) return;
+            float p[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = first || c + i >= a.cols ? 0.0f : part[c + i];
-            }
-            norm_grad8(h, y, w, pre, r, m, u, d);
+            for (int i = 0; i < 8; ++i) p[i] = (first || c + i >= a.cols ? 0.0f : part[c + i]) + y[i] * u[i];
+            put8<ZERO_F32>(part, c, a.cols, p);
+        };
+        float s[2] = {0.0f, 0.0f};
+        each([&](int64_t, const float* h, const float* y, const float* w) { norm_sums8(h, y, w, s); });
+        row_sums<false>(s, meet, turn++);
+        const float q = s[0] / n + a.eps;
+        if (norm_in_fp32(q, s[1])) {
+            const float r = 1.0f / sqrtf(q), m = s[1] * r / n;
+            each([&](int64_t c, const float* h, const float* y, const float* w) {
+                Eight<DR> ed;
+                if (a.dh != nullptr)
+                    ed.fetch((const R*)a.dh + row * a.lddh, c, a.cols);
+                else
+                    ed.zero();
+                float u[8], d[8];
+                ed.floats(d);
+                norm_grad8(h, y, w, r, m, u, d);
+                add_part(c, y, u);
+                if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
+                if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
+            });
+        } else {
+            const UnitOf of = norm_grad_row64<DX, DR, false>(a, row, (int)threadIdx.x, kWide, meet64);
+            each([&](int64_t c, const float* h, const float* y, const float*) {
+                float u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] += y[i] * u[i];
-            if (part != nullptr) put8<ZERO_F32>(part, c, a.cols, p);
-            if (a.dr != nullptr) put8<DR>((R*)a.dr + row * a.lddr, c, a.cols, d);
-            if (a.dx != nullptr) put8<DX>((X*)a.dx + row * a.lddx, c, a.cols, d);
+                for (int i = 0; i < 8; ++i) u[i] = of(h[i]);
+                add_part(c, y, u);
+            });
         }
         first = false;
     }
@@ -653,7 +755,7 @@ int check_norm(const NormArgs& a, int32_t dx, int32_t dr, const char* what) {
 // Groups of rows that a gradient call sums dw over: waves where a wave takes a row, else workgroups, as many
 // as are at work at once.
 int64_t grad_groups(int64_t tokens, int64_t cols) {
-    const int64_t most = cols <= kWaveCols ? 2048 : cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256;
+    const int64_t most = cols <= kWaveCols ? kWaveGroups : cols <= 2048 ? 1024 : cols <= 4096 ? 512 : kLeastGroups;
     return tokens < most ? tokens : most;
 }
 
