@@ -520,6 +520,20 @@ def test_norm_gradient_range(Z, cols, stream):
                 check_norm_gradients(h.double(), w.double(), dy.double(), dh.double(), dx, dr, dw, eps=e64)
 
 
+@pytest.mark.parametrize("tokens,cols", [(9000, 96), (5000, 1500), (2500, 3000), (1500, 5000), (1500, 12000), (700, 20000)])
+def test_norm_gradient_rows_of_all_sizes(Z, tokens, cols):
+    """Ordinary rows and others among those of a group, of which there are several for each."""
+    power = torch.randint(0, 5, (tokens, 1), device="cuda", generator=gen(4))
+    scale = torch.tensor([1.0, 1.0, 1e30, 1e-30, 1e-12], device="cuda")[power]
+    x, w, dy = randn(tokens, cols, seed=1) * scale, randn(cols, seed=2), randn(tokens, cols, seed=3)
+    for eps in (1e-6, 0.0):
+        leaf, lw = x.clone().requires_grad_(), w.clone().requires_grad_()
+        dx, dw = torch.autograd.grad(Z.rms_norm(leaf, lw, eps=eps), (leaf, lw), dy)
+        check_norm_gradients(x.double(), w.double(), dy.double(), None, dx, None, dw, eps=float(torch.tensor(eps)))
+        again, = torch.autograd.grad(Z.rms_norm(leaf, lw, eps=eps), lw, dy)
+        assert torch.equal(again, dw)
+
+
 @pytest.mark.parametrize("cols", [40, 2000, 20000, 40000])
 def test_norm_gradient_infinities(Z, cols):
     """Infinities and NaN in one row's gradient or values leave the other rows' gradients alone."""

@@ -373,7 +373,8 @@ struct LeftRows {
 };
 
 // The other rows (below 1e-9 or above 1e18, weights or gradients of such sizes, infinities and NaN): dr and dx
-// in 64 bits, which hold every product and sum here, an element at a time, read again.  Leaves u = h by * r.
+// in 64 bits, which hold every product and sum here, an element at a time, read again (8192 x 4096 bf16 of such rows
+// alone 191 us, of others 44).  Leaves u = h by * r.
 struct UnitOf {
     float by, r;
     __device__ __forceinline__ float operator()(float h) const { return h * by * r; }
