@@ -836,6 +836,29 @@ def test_expert_rows_and_back(Z, tokens, k, experts, cols, dtype, drop):
         assert torch.equal(torch.autograd.grad(Z.expert_combine(z.detach(), w, plan), w, dy)[0], dw)
 
 
+@pytest.mark.parametrize("tokens,cols", [((1 << 23) + 5, 2056), (1 << 24, 1032)])
+def test_expert_calls_on_many_tokens(Z, tokens, cols):
+    """As many tokens as expert_rows takes, there, back and backward: more than one launch of a workgroup a token."""
+    if torch.cuda.mem_get_info()[0] < 190 << 30:
+        pytest.skip("needs 190 GB of free GPU memory")
+    slots = torch.arange(tokens, device="cuda")
+    x = (slots % 13).to(BF16)[:, None].expand(tokens, cols).contiguous().requires_grad_()
+    plan = Z.expert_sort((slots % 3)[:, None], 3)
+    rows = Z.expert_rows(x, plan)
+    assert torch.equal(rows[:, 0].float(), (plan.order % 13).float())
+    dx, = torch.autograd.grad(rows, x, rows.detach())
+    assert torch.equal(dx, x)
+    del dx
+    rows, w = rows.detach().requires_grad_(), torch.ones(tokens, 1, device="cuda").requires_grad_()
+    y = Z.expert_combine(rows, w, plan)
+    assert torch.equal(y, x)
+    drows, dw = torch.autograd.grad(y, (rows, w), x.detach())
+    assert torch.equal(drows, rows)
+    assert torch.equal(dw[:, 0], (slots % 13).float() ** 2 * cols)  # whole numbers below 2^24
+    del x, rows, y, drows
+    torch.cuda.empty_cache()
+
+
 def test_expert_strides(Z):
     tokens, k, experts, cols = 50, 3, 6, 77
     plan = Z.expert_sort(choices(tokens, k, experts, 1).t().contiguous().t(), experts)

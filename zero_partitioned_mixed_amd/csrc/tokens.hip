@@ -532,6 +532,7 @@ struct ExpertArgs {
     int64_t cols;
     void *out, *dw;
     int64_t ldo;
+    uint32_t first;  // token of the launch
 };
 
 // Slots with an expert; places beyond are left out, whatever the plan's memory holds.
@@ -583,8 +584,9 @@ struct TokenOf {
     static constexpr int kThreads = LANES < 256 ? 256 : LANES, kTokens = kThreads / LANES;
     int64_t token;
     int lane;
-    __device__ __forceinline__ TokenOf()
-        : token((int64_t)blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES)), lane(threadIdx.x % LANES) {}
+    __device__ __forceinline__ explicit TokenOf(uint32_t first)
+        : token((int64_t)first + blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(threadIdx.x / LANES)),
+          lane(threadIdx.x % LANES) {}
 };
 
 // Tokens' rows from sorted rows: the weighted sum of a token's k rows, in fp32, in the slots' order.
@@ -594,7 +596,7 @@ template <int DT, int LANES>
 __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_kernel(ExpertArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t kSlots = 8;
-    const TokenOf<LANES> t;
+    const TokenOf<LANES> t(a.first);
     if (t.token >= a.tokens) return;
     const uint32_t used = used_of(a);
     for (int64_t c = t.lane * 8; c < a.cols; c += LANES * 8) {
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(TokenOf<LANES>::kThreads) expert_combine_grad_
     constexpr uint32_t kSlots = 8;
     constexpr int kWaves = LANES / 64;
     __shared__ float meet[kWaves][kSlots];
-    const TokenOf<LANES> t;
+    const TokenOf<LANES> t(a.first);
     if (t.token >= a.tokens) return;  // whole waves; with more than 64 lanes none
     const uint32_t used = used_of(a), slots = a.tokens * a.k;
     const T* const dy = (const T*)a.dy + t.token * a.lddy;
@@ -738,6 +740,18 @@ int with_lanes(int64_t cols, F f) {
     if (cols <= 1024) return f(std::integral_constant<int, 64>());
     if (cols <= 2048) return f(std::integral_constant<int, 256>());
     return f(std::integral_constant<int, 512>());
+}
+
+// launch_of(arguments, tokens) for 2^22 tokens at a time: with up to 512 threads each, 2^31 in a launch.
+constexpr int64_t kTokensAtOnce = int64_t(1) << 22;
+template <class F>
+int in_launches(ExpertArgs a, F launch_of) {
+    int rc = ZERO_OK;
+    for (int64_t first = 0; first < a.tokens && rc == ZERO_OK; first += kTokensAtOnce) {
+        a.first = (uint32_t)first;
+        rc = launch_of(a, a.tokens - first < kTokensAtOnce ? a.tokens - first : kTokensAtOnce);
+    }
+    return rc;
 }
 
 int check_ids(const void* ids, int32_t bytes, int64_t n, int64_t limit, const char* what) {
@@ -905,7 +919,7 @@ int zero_expert_rows(const void* x, int32_t dtype, int64_t ldx, const int32_t* p
     if (overlap(to, values_at(x, dtype, tokens, cols, ldx)) || overlap(to, Place(place, tokens * k * 4)) || overlap(to, Place(used, 4)))
         return fail(ZERO_EINVAL, "%s: the rows overlap an input", what);
     const ExpertArgs a{Vectors(tokens, cols), x, nullptr, ldx, 0, place, used, nullptr, 0, (uint32_t)tokens, (uint32_t)k, cols,
-                       rows, nullptr, ldr};
+                       rows, nullptr, ldr, 0};
     if (a.v.workgroups() > 0x7FFFFFFF) return fail(ZERO_ERANGE, "%s: too many elements for one launch", what);
     return with_type(dtype, [&](auto t) {
         return launch(expert_rows_kernel<decltype(t)::value>, dim3((unsigned)a.v.workgroups()), 256, (hipStream_t)stream, a, what);
@@ -927,12 +941,14 @@ int zero_expert_combine(const void* rows, int32_t dtype, int64_t ldr, const int3
         overlap(to, Place(used, 4)) || overlap(to, Place(weights, tokens * k * (int64_t)elem_bytes(weights_dtype))))
         return fail(ZERO_EINVAL, "%s: the result overlaps an input", what);
     const ExpertArgs a{Vectors(1, 8), rows, nullptr, ldr, 0, place, used, weights, weights_dtype == ZERO_F32,
-                       (uint32_t)tokens, (uint32_t)k, cols, y, nullptr, ldy};
+                       (uint32_t)tokens, (uint32_t)k, cols, y, nullptr, ldy, 0};
     return with_type(dtype, [&](auto t) {
         return with_lanes(cols, [&](auto l) {
             typedef TokenOf<decltype(l)::value> Token;
-            return launch(expert_combine_kernel<decltype(t)::value, decltype(l)::value>,
-                          dim3((unsigned)ceil_div(tokens, Token::kTokens)), Token::kThreads, (hipStream_t)stream, a, what);
+            return in_launches(a, [&](const ExpertArgs& part, int64_t many) {
+                return launch(expert_combine_kernel<decltype(t)::value, decltype(l)::value>,
+                              dim3((unsigned)ceil_div(many, Token::kTokens)), Token::kThreads, (hipStream_t)stream, part, what);
+            });
         });
     });
 }
@@ -960,12 +976,14 @@ int zero_expert_combine_grad(const void* dy, int64_t lddy, const void* rows, int
             (dweights != nullptr && overlap(p, values_at(rows, dtype, tokens * k, cols, ldr))))
             return fail(ZERO_EINVAL, "%s: a gradient overlaps an input", what);
     const ExpertArgs a{Vectors(1, 8), rows, dy, ldr, lddy, place, used, weights, weights_dtype == ZERO_F32, (uint32_t)tokens,
-                       (uint32_t)k, cols, drows, dweights, lddr};
+                       (uint32_t)k, cols, drows, dweights, lddr, 0};
     return with_type(dtype, [&](auto t) {
         return with_lanes(cols, [&](auto l) {
             typedef TokenOf<decltype(l)::value> Token;
-            return launch(expert_combine_grad_kernel<decltype(t)::value, decltype(l)::value>,
-                          dim3((unsigned)ceil_div(tokens, Token::kTokens)), Token::kThreads, (hipStream_t)stream, a, what);
+            return in_launches(a, [&](const ExpertArgs& part, int64_t many) {
+                return launch(expert_combine_grad_kernel<decltype(t)::value, decltype(l)::value>,
+                              dim3((unsigned)ceil_div(many, Token::kTokens)), Token::kThreads, (hipStream_t)stream, part, what);
+            });
         });
     });
 }
