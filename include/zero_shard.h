@@ -769,7 +769,8 @@ int zero_mx4_linear_grad(const void *dy_dev, int64_t lddy, int32_t dtype, int64_
  * holding inf or NaN has s = 255 (NaN) and codes 0.  codes: [rows][P] bytes, P as
  * above; scales: [rows][P / 32] (zero_mx4_scale_bytes); both 16-byte aligned.
  * Errors of all calls: EINVAL, EALIGN (rows to their elements, codes, scales and
- * workspaces to 16 bytes), ERANGE, ESPACE. */
+ * workspaces to 16 bytes), ERANGE, ESPACE.  Results share no memory with inputs, with one
+ * another or with the workspace (EINVAL) but where a call allows it. */
 size_t zero_mx8_code_bytes(int64_t rows, int64_t cols);
 int zero_mx8_quantize(const void *src_dev, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                       void *codes_dev, void *scales_dev, void *stream);

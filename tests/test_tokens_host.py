@@ -274,3 +274,26 @@ def test_tangents_are_not_lost(Z, monkeypatch):
                 with recorded(), pytest.raises(RuntimeError, match="jvp"):
                     call_(forward_ad.make_dual(t, torch.ones_like(t)))
         call_(t)
+
+
+@pytest.mark.parametrize("name,defaults,kw", [
+    ("zero_mx8_quantize", QUANT, dict(scales=B)), ("zero_mx8_quantize", QUANT, dict(codes=C - 496)),
+    ("zero_rms_norm_mx8", {**NORM, **OUT8}, dict(scales=D + 496)),
+    ("zero_rms_norm_grad", GRAD, dict(dr=E)), ("zero_rms_norm_grad", GRAD, dict(dw=E + 256)),
+    ("zero_rms_norm_grad", GRAD, dict(dw=E + (1 << 40) + 64)), ("zero_rms_norm_grad", GRAD, dict(dx=W)),
+    ("zero_rms_norm_grad", GRAD, dict(dr=W + 1020)), ("zero_rms_norm_grad", GRAD, dict(dw=W + 16)),
+    ("zero_rms_norm_grad", GRAD, dict(ws=A)), ("zero_rms_norm_grad", GRAD, dict(ws=B + 16)), ("zero_rms_norm_grad", GRAD, dict(ws=C)),
+    ("zero_rms_norm_grad", GRAD, dict(ws=D - 1008)),
+    ("zero_mx8_matmul_rows", dict(a=A, adt=BF16, lda=4096, b=B, sb=C, m=8, n=8, k=4096, c=D, cdt=BF16, ldc=8, acc=0, ws=D, wsb=1 << 40), {}),
+    ("zero_mx8_matmul_rows", dict(a=A, adt=BF16, lda=4096, b=B, sb=C, m=8, n=8, k=4096, c=D, cdt=BF16, ldc=8, acc=0, ws=A + 16, wsb=1 << 40), {}),
+    ("zero_mx8_matmul_rows", dict(a=A, adt=BF16, lda=4096, b=B, sb=C, m=8, n=8, k=4096, c=D, cdt=BF16, ldc=8, acc=0, ws=B, wsb=1 << 40), {}),
+    ("zero_mx8_matmul_rows", dict(a=A, adt=BF16, lda=4096, b=B, sb=C, m=8, n=8, k=4096, c=D, cdt=BF16, ldc=8, acc=0, ws=C, wsb=1 << 40), {}),
+    ("zero_embedding_grad", LOOKUP_GRAD, dict(ws=A)), ("zero_embedding_grad", LOOKUP_GRAD, dict(ws=B)),
+    ("zero_embedding_grad", LOOKUP_GRAD, dict(ws=C + 2544)),
+    ("zero_expert_sort", SORT, dict(order=C)), ("zero_expert_sort", SORT, dict(place=D + 4)), ("zero_expert_sort", SORT, dict(offsets=B + 400)),
+    ("zero_expert_sort", SORT, dict(ws=A)), ("zero_expert_sort", SORT, dict(ws=B)), ("zero_expert_sort", SORT, dict(ws=C + 19984)),
+    ("zero_expert_sort", SORT, dict(offsets=W + 4)),
+    ("zero_expert_combine_grad", COMBINE_GRAD, dict(dw=E)), ("zero_expert_combine_grad", COMBINE_GRAD, dict(dw=E + 1276))])
+def test_results_and_workspaces_share_nothing(Z, name, defaults, kw):
+    """Two results of a call, or its workspace and anything else of its, in the same memory."""
+    assert call(Z, name, defaults, **kw) == EINVAL

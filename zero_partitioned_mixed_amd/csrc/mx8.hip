@@ -612,6 +612,8 @@ int zero_mx8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols
     const Place from = values_at(src, dtype, rows, cols, ld);
     if (overlap(from, codes8_at(codes, rows, cols)) || overlap(from, scales_at(scales, rows, cols)))
         return fail(ZERO_EINVAL, "%s: codes or scales overlap the values", what);
+    if (overlap(codes8_at(codes, rows, cols), scales_at(scales, rows, cols)))
+        return fail(ZERO_EINVAL, "%s: codes and scales overlap", what);
     return quantize(Quant8Args{src, rows, cols, ld, (uint8_t*)codes, (uint8_t*)scales}, dtype, (hipStream_t)stream, what);
 }
 
@@ -677,6 +679,8 @@ int zero_mx8_matmul_rows(const void* a, int32_t a_dtype, int64_t lda, const void
     }
     const Place to = values_at(c, c_dtype, m, n, ldc);
     if (overlap(to, values_at(a, a_dtype, m, k, lda))) return fail(ZERO_EINVAL, "%s: the result overlaps an operand", what);
+    if (need > 0 && meets(Place(ws, (int64_t)need), {to, values_at(a, a_dtype, m, k, lda), codes_at(b, n, k), scales_at(sb, n, k)}))
+        return fail(ZERO_EINVAL, "%s: the workspace overlaps the result or an operand", what);
     const hipStream_t s = (hipStream_t)stream;
     Matmul8Args g{nullptr, nullptr, (const uint8_t*)b, (const uint8_t*)sb, m, n, padded(k), c, ldc, 0, 0, accumulate, 0};
     if (few_values(m, k)) return few_of_values(Few8Args{g, a, lda, k}, a_dtype, c_dtype, s, what);

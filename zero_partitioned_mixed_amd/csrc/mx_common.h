@@ -2,6 +2,8 @@
 // tokens.hip): sizes, eight elements of a row at a time, block scales, places.
 #pragma once
 
+#include <initializer_list>
+
 #include "matrix_common.h"
 
 namespace {
@@ -266,5 +268,12 @@ inline Place values_at(const void* p, int32_t dtype, int64_t rows, int64_t cols,
 inline Place codes_at(const void* p, int64_t rows, int64_t cols) { return Place(p, rows * (padded(cols) / 2)); }
 inline Place codes8_at(const void* p, int64_t rows, int64_t cols) { return Place(p, rows * padded(cols)); }
 inline Place scales_at(const void* p, int64_t rows, int64_t cols) { return Place(p, rows * (padded(cols) / kMxBlock)); }
+
+// Whether a place shares memory with one of the others.
+inline bool meets(const Place& p, std::initializer_list<Place> others) {
+    for (const Place& o : others)
+        if (overlap(p, o)) return true;
+    return false;
+}
 
 }  // namespace

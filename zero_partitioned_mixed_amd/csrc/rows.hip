@@ -814,6 +814,7 @@ int zero_rms_norm_mx8(const void* x, int32_t dtype, int64_t ldx, const void* res
             (residual != nullptr && (overlap(p, values_at(residual, dr, tokens, cols, ldr)) ||
                                      overlap(p, values_at(h, dr, tokens, cols, ldh)))))
             return fail(ZERO_EINVAL, "%s: codes or scales overlap an input or the sum", what);
+    if (overlap(to[0], to[1])) return fail(ZERO_EINVAL, "%s: codes and scales overlap", what);
     return norm_any<true>(a, dtype, dr, (hipStream_t)stream, what);
 }
 
@@ -847,6 +848,7 @@ int zero_rms_norm_grad(const void* dy, int64_t lddy, const void* h, int32_t h_dt
     for (const Place& p : to)
         for (const Place& f : from)
             if (overlap(p, f)) return fail(ZERO_EINVAL, "%s: a gradient overlaps an input", what);
+    if (meets(to[0], {to[1], to[2]}) || overlap(to[1], to[2])) return fail(ZERO_EINVAL, "%s: gradients overlap", what);
     NormGradArgs a{dy, h, w, dh, lddy, ldh, lddh, tokens, cols, eps, dx, dr, lddx, lddr, (float*)ws, dw,
                    (int)grad_groups(tokens, cols)};
     const hipStream_t s = (hipStream_t)stream;
@@ -855,6 +857,8 @@ int zero_rms_norm_grad(const void* dy, int64_t lddy, const void* h, int32_t h_dt
         if (need > 0 && ws == nullptr) return fail(ZERO_EINVAL, "%s: null workspace", what);
         if (!aligned(ws, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", what);
         if (ws_bytes < need) return fail(ZERO_ESPACE, "%s: workspace %zu bytes, needs %zu", what, ws_bytes, need);
+        if (need > 0 && meets(Place(ws, (int64_t)need), {from[0], from[1], from[2], from[3], to[0], to[1], to[2]}))
+            return fail(ZERO_EINVAL, "%s: the workspace overlaps an input or a gradient", what);
     } else {
         a.parts = nullptr;
     }

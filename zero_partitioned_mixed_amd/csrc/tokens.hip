@@ -843,6 +843,9 @@ int zero_embedding_grad(const void* ids, int32_t id_bytes, int64_t tokens, const
     const Place to = values_at(out, dtype, vocab, cols, ldo);
     if (overlap(to, values_at(dy, dtype, tokens, cols, lddy)) || overlap(to, Place(ids, tokens * id_bytes)))
         return fail(ZERO_EINVAL, "%s: the gradient overlaps an input", what);
+    if (meets(Place(ws, (int64_t)zero_embedding_grad_workspace_bytes(tokens, vocab, cols)),
+              {to, values_at(dy, dtype, tokens, cols, lddy), Place(ids, tokens * id_bytes)}))
+        return fail(ZERO_EINVAL, "%s: the workspace overlaps an input or the gradient", what);
     const hipStream_t s = (hipStream_t)stream;
     uint32_t *const keys = (uint32_t*)ws, *const from = keys + tokens;
     uint32_t* const scratch = keys + round_up(2 * tokens, 64);
@@ -895,9 +898,11 @@ int zero_expert_sort(const void* ids, int32_t id_bytes, int64_t slots, int64_t e
     if (offsets == nullptr || (slots > 0 && (order == nullptr || place == nullptr))) return fail(ZERO_EINVAL, "%s: null result", what);
     if (!aligned(order, 4) || !aligned(place, 4) || !aligned(offsets, 4)) return fail(ZERO_EALIGN, "%s: results not aligned", what);
     if ((rc = check_space(ws, ws_bytes, zero_expert_sort_workspace_bytes(slots, experts), what)) != ZERO_OK) return rc;
-    const Place from(ids, slots * id_bytes);
-    if (overlap(from, Place(order, slots * 4)) || overlap(from, Place(place, slots * 4)) || overlap(from, Place(offsets, (experts + 1) * 4)))
-        return fail(ZERO_EINVAL, "%s: a result overlaps the numbers", what);
+    const Place from(ids, slots * id_bytes), to[3] = {Place(order, slots * 4), Place(place, slots * 4), Place(offsets, (experts + 1) * 4)};
+    if (meets(from, {to[0], to[1], to[2]})) return fail(ZERO_EINVAL, "%s: a result overlaps the numbers", what);
+    if (meets(to[0], {to[1], to[2]}) || overlap(to[1], to[2])) return fail(ZERO_EINVAL, "%s: results overlap", what);
+    if (meets(Place(ws, (int64_t)zero_expert_sort_workspace_bytes(slots, experts)), {from, to[0], to[1], to[2]}))
+        return fail(ZERO_EINVAL, "%s: the workspace overlaps the numbers or a result", what);
     const hipStream_t s = (hipStream_t)stream;
     const Ids numbers{ids, id_bytes == 8, (uint32_t)experts};
     const bool one = sort_passes((uint32_t)experts) == 1;
@@ -975,6 +980,7 @@ int zero_expert_combine_grad(const void* dy, int64_t lddy, const void* rows, int
             overlap(p, Place(used, 4)) || overlap(p, Place(weights, wbytes)) ||
             (dweights != nullptr && overlap(p, values_at(rows, dtype, tokens * k, cols, ldr))))
             return fail(ZERO_EINVAL, "%s: a gradient overlaps an input", what);
+    if (overlap(to[0], to[1])) return fail(ZERO_EINVAL, "%s: gradients overlap", what);
     const ExpertArgs a{Vectors(1, 8), rows, dy, ldr, lddy, place, used, weights, weights_dtype == ZERO_F32, (uint32_t)tokens,
                        (uint32_t)k, cols, drows, dweights, lddr, 0};
     return with_type(dtype, [&](auto t) {
