@@ -297,3 +297,24 @@ def test_tangents_are_not_lost(Z, monkeypatch):
 def test_results_and_workspaces_share_nothing(Z, name, defaults, kw):
     """Two results of a call, or its workspace and anything else of its, in the same memory."""
     assert call(Z, name, defaults, **kw) == EINVAL
+
+
+def test_plans_are_guarded(Z, monkeypatch):
+    """A plan's memory may not be written between a forward pass and its backward pass.  The C calls stubbed out."""
+    import torch
+    from zero_partitioned_mixed_amd import tokens as M
+    monkeypatch.setattr(M, "_gpu", lambda *t: 0)
+    monkeypatch.setattr(M, "_call", lambda *a: None)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    x, gates = torch.ones(8, 64).requires_grad_(), torch.ones(8, 1).requires_grad_()
+    for call_ in (lambda p: Z.expert_rows(x, p), lambda p: Z.expert_combine(x, gates, p)):
+        for touched in (None, "place", "offsets"):
+            n = torch.zeros(8, dtype=torch.int32)
+            plan = Z.ExpertPlan(n, n.clone().view(8, 1), n[:4].clone(), 8, 1, 3)
+            y = call_(plan)
+            if touched is None:
+                torch.autograd.grad(y, x, torch.ones_like(y))
+                continue
+            getattr(plan, touched).add_(1)
+            with pytest.raises(RuntimeError, match="inplace"):
+                torch.autograd.grad(y, x, torch.ones_like(y))

@@ -377,6 +377,14 @@ class ExpertPlan:
             raise ValueError(f"{what}: expected [{rows}, cols]")
         return _gpu(t, self.place, self.offsets)
 
+    def _versions(self):
+        """How often torch has written the memory that the calls read; forward and backward passes read the same."""
+        return tuple(None if t.is_inference() else t._version for t in (self.place, self.offsets))
+
+    def _again(self, versions) -> None:
+        if versions != self._versions():
+            raise RuntimeError("the plan was modified by an inplace operation between a forward pass and its backward pass")
+
     def _places(self):
         return self.place.data_ptr(), self.offsets.data_ptr() + 4 * self.experts
 
@@ -425,11 +433,12 @@ def _to_tokens(rows, weights, plan):
 class _ExpertRows(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, plan):
-        ctx.plan = plan
+        ctx.plan, ctx.versions = plan, plan._versions()
         return _to_rows(x, plan)
 
     @_once
     def backward(ctx, drows):
+        ctx.plan._again(ctx.versions)
         return _to_tokens(drows, None, ctx.plan), None
 
 
@@ -445,7 +454,7 @@ def expert_rows(x, plan: ExpertPlan):
 class _ExpertCombine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, plan):
-        ctx.plan = plan
+        ctx.plan, ctx.versions = plan, plan._versions()
         ctx.save_for_backward(rows if ctx.needs_input_grad[1] else None, weights)
         return _to_tokens(rows, weights, plan)
 
@@ -453,6 +462,7 @@ class _ExpertCombine(torch.autograd.Function):
     def backward(ctx, dy):
         rows, weights = ctx.saved_tensors
         plan, (need_rows, need_weights) = ctx.plan, ctx.needs_input_grad[:2]
+        plan._again(ctx.versions)
         dy, lddy = _matrix(dy)
         cols, dev = dy.shape[1], dy.device
         rows, ldr = (None, 0) if rows is None else _matrix(rows)
