@@ -421,6 +421,16 @@ def test_norm_gradient_by_differences(Z):
         assert abs(slope - float((g.double() * step).sum())) < 1e-5 * float((g.double() * step).abs().sum())
 
 
+@pytest.mark.parametrize("tokens,cols,groups", [(9000, 96, 2048), (5000, 1500, 1024), (2500, 3000, 512), (2500, 9000, 256), (300, 20000, 256)])
+def test_norm_weight_gradient_sums(Z, tokens, cols, groups):
+    """The weights' gradient against the additions that a term goes through: a group's rows one after the other, at most
+    32 groups a run, 64 runs."""
+    x, w, dy = randn(tokens, cols, seed=1), randn(cols, seed=2).requires_grad_(), randn(tokens, cols, seed=3)
+    dw, = torch.autograd.grad(Z.rms_norm(x, w), w, dy)
+    terms = dy.double() * norm64(x.double(), 1.0)[0]
+    near(dw, terms.sum(0), (math.ceil(tokens / groups) + 32 + 64 + depth(cols)) * U * terms.abs().sum(0))
+
+
 @pytest.mark.parametrize("cols", [40, 2000, 5000, 20000, 40000])
 def test_norm_range(Z, cols):
     """Rows whose squares leave fp32's range or fall below it; zeros; infinities and NaN in one row alone."""
@@ -713,6 +723,33 @@ def test_embedding_runs(Z, runs):
     table, dy = randn(vocab, cols).requires_grad_(), randn(len(ids), cols, seed=1)
     y = Z.embedding(ids, table)
     check_embedding(Z, ids, table.detach(), 1.0, dy, y.detach(), torch.autograd.grad(y, table, dy)[0])
+
+
+def piece_of(n):
+    """Tokens of the sorted order that are summed together: 8 to 32, more where there are more than 4096 pieces."""
+    return -(-max(min(max(n // 1024, 8), 32), math.ceil(n / 4096)) // 8) * 8
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [3000, 17000, 25000, 33000, 140000, 270001])
+def test_embedding_gradient_at_the_cuts(Z, n, dtype):
+    """Runs that end one before, at and one past the cuts of the sorted order, within a piece, over exactly two and
+    three, and over many, for pieces of 8, 16, 24, 32 and more; the bound from the additions that a term goes through."""
+    piece, cols = piece_of(n), 40
+    ends = sorted({piece * a + d for a in (1, 2, 3, 5, 8, 9, 20, 150) for d in (-1, 0, 1)} | {piece * 30 + piece // 2, piece * 32, n})
+    runs = torch.tensor(ends).diff(prepend=torch.tensor([0]))
+    ids = torch.repeat_interleave(torch.arange(1, len(ends) + 1), runs)
+    ids = ids[torch.randperm(n, generator=torch.Generator().manual_seed(1))].cuda()
+    table, dy = randn(len(ends) + 2, cols, dtype=dtype).requires_grad_(), randn(n, cols, seed=1, dtype=dtype)
+    d, = torch.autograd.grad(Z.embedding(ids, table, scale=0.5), table, dy)
+    sums, sizes = (torch.zeros(table.shape, dtype=torch.float64, device="cuda") for _ in range(2))
+    sums.index_add_(0, ids, dy.double())
+    sizes.index_add_(0, ids, dy.double().abs())
+    many = torch.nn.functional.pad(runs, (1, 1)).double().cuda()
+    # in a piece one after the other; of the pieces an eighth each, and eight of these
+    adds = many.clamp(max=piece) + torch.where(many > piece, torch.ceil((many / piece + 2) / 8) + 8, 2.0) + 1
+    near(d, sums * 0.5, 0.5 * adds[:, None] * U * sizes)
+    assert not d[0].any() and not d[-1].any()
 
 
 def test_embedding_order_and_shapes(Z):
