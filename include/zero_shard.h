@@ -812,7 +812,8 @@ int zero_rms_norm_mx8(const void *x_dev, int32_t dtype, int64_t ldx, const void 
  * too, its gradient dh (h_dtype; may be NULL).  With u = h / sqrt(mean(h^2) + eps), g = dy w:
  *     dr = (g - u mean(g u)) / sqrt(mean(h^2) + eps) + dh    the residual's, h_dtype
  *     dx = dr rounded to dtype;   dw = sum over tokens of dy u, dtype
- * Each of dx, dr and dw may be NULL; the workspace is for dw. */
+ * Each of dx, dr and dw may be NULL; the workspace is for dw.  Rows whose sums or
+ * products leave fp32's range are computed in 64 bits. */
 size_t zero_rms_norm_grad_workspace_bytes(int64_t tokens, int64_t cols);
 int zero_rms_norm_grad(const void *dy_dev, int64_t lddy, const void *h_dev, int32_t h_dtype,
                        int64_t ldh, const void *w_dev, int32_t dtype, const void *dh_dev,

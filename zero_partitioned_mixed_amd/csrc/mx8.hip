@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
         }
 }
 
-// Few rows (m <= 32, as single tokens bring): bound by reading B once (one token 11008 x 4096: 7.9 us a call,
-// where reading B takes 4.7; its waves wait for 58% of their cycles).  A workgroup takes 32 of B's
+// Few rows (m <= 32, as single tokens bring): bound by reading B once (one token 11008 x 4096: 7.5 us,
+// where reading B takes 4.7; its waves wait for 53% of their cycles).  A workgroup takes 32 of B's
 // rows, its eight waves an eighth of k each: a wave brings slabs of 256 elements of them to its own
 // part of LDS in whole lines, waits for nobody, and the waves' sums meet in LDS.
 // VALUES (m times the padded k up to kFew8): A comes as values, and every workgroup quantises all
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(S::THREADS) mx8_matmul_kernel(Matmul8Args g) {
 // HALVES (m <= 16): the low codes of row i are the instruction's row 2i and the high ones its row 2i + 1, so
 // that one instruction is enough.
 constexpr int kFewWaves = 8;
-constexpr int kFew8 = 8192;  // two workgroups on a CU: one token 11008 x 4096 7.5 us with one
+constexpr int kFew8 = 8192;  // two workgroups on a CU: one token 11008 x 4096 6.2 us, 7.5 with one, with codes unsplit
 constexpr int kFewSlabs = 2;  // slabs of a wave on their way at once
 
 struct Few8Args {

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kWide) norm_wide_kernel(NormArgs a) {
 // dh' goes to the residual's gradient and, rounded to x's type, to x's.  root is computed again
 // from h, which has to be read anyway: nothing but h is kept for the backward pass.
 // A workgroup takes rows `groups` apart and holds its columns' part of dw in registers; the
-// parts are summed in order by a second launch.  Bound by memory: 8192 x 4096 bf16 47 us for 276 MB
+// parts are summed in order by a second launch.  Bound by memory: 8192 x 4096 bf16 46 us for 276 MB
 // and 4.5 us for dw.  The next row is read while this one's sums meet (without that, and two barriers a
 // sum, 83 us).
 constexpr int64_t kWaveGroups = 2048, kLeastGroups = 256;
@@ -346,9 +346,9 @@ __device__ __forceinline__ double row_sum64(double v, RowSum64& meet, int turn) 
     return v;
 }
 
-// Which of a group's rows are left for norm_grad_row64 when the others are done (among them it costs registers that
-// every row pays for: 2048 x 16384 bf16 with an fp32 stream 148 us, behind them 128, without it 118): a bit each, for the most rows in
-// the fewest groups.
+// Which of a group's rows are left for norm_grad_row64 when the others are done: a bit each, for the most rows in the
+// fewest groups.  Among them it costs registers that every row pays for: 2048 x 16384 bf16 with an fp32 stream 148 us,
+// behind them 128, without it 118.
 template <bool WAVE>
 struct LeftRows {
     static constexpr int kWords = (int)(kMaxSide / (WAVE ? kWaveGroups : kLeastGroups) / 32);
