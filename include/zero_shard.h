@@ -760,7 +760,8 @@ int zero_mx4_linear_grad(const void *dy_dev, int64_t lddy, int32_t dtype, int64_
  * ZERO_F16, ZERO_BF16 or ZERO_F32; rows and columns go up to 2^24 unless a call
  * says otherwise.  What would take a launch of 2^32 threads or more is refused
  * (ERANGE): the norm has one for 8 or 16 columns of a row, the lookup 256 for a token
- * of 2048 columns or more.  Sums are fp32, in an order that depends on sizes alone.
+ * of 2048 columns or more.  Sums are fp32 or wider, in an order that depends on sizes
+ * alone, but for rows that a call computes in 64 bits: those come last.
  *
  * MXFP8 rows: blocks of 32 along a row as in the part above, with 8-bit codes
  * (E4M3, largest 448).  A block's scale 2^(s - 127) is the smallest power of two

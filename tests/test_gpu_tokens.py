@@ -280,6 +280,24 @@ def test_mx8_product_of_values(Z, m, dtype):
     check_product(out, qa, qb, extra=before)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 40, 128), (20, 70, 384), (50, 70, 640), (300, 500, 1024)])
+def test_mx8_product_range(Z, m, n, k):
+    """Rows of every size against weights of the opposite one, the types' smallest and largest scales among them."""
+    e = torch.linspace(-140, 119, m, device="cuda").round()[:, None]
+    a = (randn(m, k, seed=1).double() * torch.pow(2.0, e.double())).float()
+    for f in (-118.0, -60.0, 0.0, 60.0, 124.0):
+        b = (randn(n, k, seed=2).double().clamp(-3, 3) * 2.0 ** f).float()
+        qa, qb = Z.mx8_quantize(a), Z.mx4_quantize(b)
+        a64, b64 = values8(qa), values4(qb)
+        want = a64 @ b64.t()
+        rows = (want.abs().amax(1) < 2.0 ** 120)
+        # the smallest results: products and sums below the normal numbers, each off by half of the smallest one
+        slack = (k + 1) * U * (a64.abs() @ b64.abs().t()) + 2 * k * last(F32)
+        for x in (qa, a):
+            got = Z.mx8_matmul(x, qb, F32).cpu()
+            near(got[rows], want[rows], slack[rows])
+
+
 def test_mx8_product_places(Z):
     """Every place of a block in k and every row meet their own scale: one element at a time against ones whose
     blocks' scales differ."""
